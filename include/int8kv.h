@@ -53,6 +53,30 @@
  *                  No prefill chunk.  group_size is validated but no store
  *                  uses it.
  *
+ * Block-scaled variants: both stores hold 8-bit codes with one fp32 scale for
+ * each block of group_size consecutive positions (16, 32, 64 or 128, at most a
+ * page) of a kv head, all head_dim values of them; value = code * scale.
+ *     INT8KV_K8V8_BLOCK  int8 codes;   qmax 127, fits 127.5
+ *     INT8KV_F8_BLOCK    e4m3 codes;   qmax 448, fits 464
+ * kv_quant_append, with a = the largest magnitude among the call's new values of
+ * a block:
+ *     a block whose first position is among the new ones, or whose scale is 0:
+ *         s = fp32(a / qmax)                            (IEEE division)
+ *     else s = s_old * 2^k, the smallest k >= 0 with a <= fp32(fits * s_old) * 2^k;
+ *         for k > 0 the codes of the block's earlier positions become
+ *         round_half_even(c * 2^-k)
+ *     new codes: round_half_even(fp32(x / s)) saturated to +-qmax, 0 where s = 0
+ * so a code is off by at most half a step of its block's scale, or one step in a
+ * block that grew.  A position that is written again (after a sequence was cut
+ * back) keeps the block's scale.  Decode, query windows and the fused append
+ * serve them at every head_dim, page size and group size; prefill chunks and
+ * saved images return UNSUPPORTED.  Blocks behind a sequence's end are neither
+ * read nor written.
+ *
+ * Pages: with reference counts in device memory, sequences share pages, and the
+ * kv_pages_* calls give pages out, take them back, fork sequences and compact
+ * the pool without the host seeing a length (every variant).
+ *
  * Pool layout in device memory (caller-allocated; the library never
  * allocates device memory):
  *     int8 store   int8    [n_layers][n_pages][n_kv_heads][page_size][head_dim]
@@ -60,6 +84,8 @@
  *     4-bit store  uint8   [n_layers][n_pages][n_kv_heads][page_size][head_dim/2]
  *     scales       fp16    [n_layers][n_pages][n_kv_heads][page_size][head_dim/group_size]
  *                          (of the 4-bit store: [...][head_dim/32])
+ *     block-scaled codes   [n_layers][n_pages][n_kv_heads][page_size][head_dim], 1 byte each
+ *     block scales   fp32  [n_layers][n_pages][n_kv_heads][page_size/group_size]
  * Position p of sequence b lives on physical page page_table[b*max_pages + p/page_size],
  * slot p % page_size.
  *
@@ -110,13 +136,17 @@ extern "C" {
 #define INT8KV_DEVERR_PAGE_ID     1  /* page-table entry outside [0, n_pages) */
 #define INT8KV_DEVERR_LENGTH      2  /* position beyond max_pages_per_seq * page_size */
 #define INT8KV_DEVERR_TIMEOUT     4  /* an mbarrier wait on an async copy hit its iteration cap */
+#define INT8KV_DEVERR_NO_PAGE     8  /* kv_pages_*: no free page was left for an entry */
+#define INT8KV_DEVERR_FORK       16  /* kv_pages_fork: a fork that cannot take place was left out */
 
 typedef enum {
   INT8KV_K8V8 = 0,
   INT8KV_K8V16 = 1,
   INT8KV_K16V8 = 2,
   INT8KV_K8V4 = 3,
-  INT8KV_Q4_0 = 4
+  INT8KV_Q4_0 = 4,
+  INT8KV_K8V8_BLOCK = 8,
+  INT8KV_F8_BLOCK = 9
 } int8kv_variant;
 
 /* Regions of a pool, for int8kv_pool_region_bytes. */
@@ -144,7 +174,9 @@ int int8kv_pool_region_bytes(int n_layers, int n_kv_heads, int head_dim, int gro
  * query's head_dim).
  *   head_dim    64, 128 or 256
  *   group_size  values per scale: head_dim (one scale per (position, kv head))
- *               or 16/32/64/128 dividing head_dim (64 = Strata's grouping)
+ *               or 16/32/64/128 dividing head_dim (64 = Strata's grouping);
+ *               block-scaled variants: positions per scale, 16/32/64/128, at most
+ *               page_size (their scales regions are fp32)
  *   page_size   positions per page: 16, 32, 64 or 128
  *   k_store, v_store   device, 16-byte aligned, region bytes as queried
  *   k_scales, v_scales device, 16-byte aligned; required for an int8 store,
@@ -402,6 +434,83 @@ int kv_pool_save(const int8kv_pool* pool, int n_seqs, const int32_t* seq_lens,
 int kv_pool_load(const int8kv_pool* pool, const void* image, size_t image_bytes, int n_seqs,
                  const int32_t* page_table, int max_pages_per_seq, void* staging,
                  size_t staging_bytes, int32_t* seq_lens, void* stream);
+
+/* ---- pages ---------------------------------------------------------------
+ * A page table is device int32 [n_seqs][max_pages_per_seq]: entry k of a row is
+ * the page of positions k * page_size .., negative where the row has none.
+ * page_refs is device int32 [n_pages]: how many entries name the page; 0 is a
+ * free page.  All rows that use a pool belong to one table.  Every layer of the
+ * pool shares the table, so the calls below handle all layers of a page.
+ *
+ * Pages are given out in ascending order of id, to rows in ascending order, so
+ * the result of a call depends on its inputs alone.  An entry beyond the pool, or
+ * one that would take a page's count below 0, is flagged
+ * (INT8KV_DEVERR_PAGE_ID) and dropped; so is a length beyond the row
+ * (INT8KV_DEVERR_LENGTH), which counts as the row's whole.  Calls whose
+ * tables, counts or workspaces are the same must not overlap on the device. */
+
+/* Bytes of the workspace of kv_pages_resize, kv_pages_fork and
+ * kv_pages_compact for a table of n_seqs rows.  Errors: NULL_PTR, INVALID_ARG. */
+int kv_pages_workspace_bytes(const int8kv_pool* pool, int n_seqs, size_t* out_bytes);
+
+/* Copy pages: codes and scales of page src[i] of every layer to page dst[i].
+ *   src, dst   device int32 [n]; a pair with a negative entry, or of one page
+ *              twice, is no copy; one with an entry beyond the pool is flagged and
+ *              left out
+ * The destinations must differ from each other and from all sources.
+ * Errors: NULL_PTR, INVALID_ARG, CUDA. */
+int kv_pages_copy(const int8kv_pool* pool, int n, const int32_t* src, const int32_t* dst,
+                  void* stream);
+
+/* Give every row of the table the pages that seq_lens[row] positions need: entries
+ * behind them are given back (their counts fall by one; a page at 0 is free and may
+ * be given out by the same call), entries among them that are negative get
+ * a free page, counted 1.  So a length of 0 frees a sequence, a new sequence starts
+ * from a row of -1, and a step's growth is one call for the whole batch.
+ *   page_refs   device int32 [n_pages], updated
+ *   page_table  device int32 [n_seqs][max_pages_per_seq], updated
+ *   seq_lens    device int32 [n_seqs]
+ *   workspace   device, >= kv_pages_workspace_bytes, 16-byte aligned, any contents
+ * Entries for which no page is left stay -1 (INT8KV_DEVERR_NO_PAGE).  A page that
+ * is still shared is not copied: cut a sequence back into a shared page only with
+ * a fork or copy of it.  Contents of pages are not touched.
+ * Errors: NULL_PTR, INVALID_ARG, WORKSPACE, ALIGNMENT, CUDA. */
+int kv_pages_resize(const int8kv_pool* pool, int32_t* page_refs, int32_t* page_table, int n_seqs,
+                    int max_pages_per_seq, const int32_t* seq_lens, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* Fork sequences: row children[i] becomes a copy of row parents[i].  What the child
+ * held is given back, the parent's full pages are shared (counted one more), and
+ * the page that the parent's length ends inside is copied, in every layer,
+ * into a free page for the child, so that both may append.  Entries of the parent
+ * behind its length are not inherited.
+ *   seq_lens           device int32 [n_seqs]; seq_lens[child] = seq_lens[parent]
+ *   parents, children  device int32 [n_forks], n_forks <= n_seqs
+ * A fork with a negative entry is no fork.  A row may be the parent of several
+ * forks but the child of one, and not both parent and child in one call: of forks
+ * with the same child the first takes place; the others, a fork
+ * whose child is a parent, and one with a row outside the table are flagged
+ * (INT8KV_DEVERR_FORK) and left out.  Where no page is left for the copy
+ * (INT8KV_DEVERR_NO_PAGE) the child ends behind the shared pages.
+ * Errors: NULL_PTR, INVALID_ARG, WORKSPACE, ALIGNMENT, CUDA. */
+int kv_pages_fork(const int8kv_pool* pool, int32_t* page_refs, int32_t* page_table, int n_seqs,
+                  int max_pages_per_seq, int32_t* seq_lens, int n_forks, const int32_t* parents,
+                  const int32_t* children, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Compact the pool: with U pages in use, the used pages from id U on move, in
+ * ascending order, into the free pages below U, and the table and the counts follow.
+ *   page_refs, page_table          device, as they are
+ *   page_refs_out, page_table_out  device, the same shapes: as they are afterwards
+ *                                  (either may be the input array itself)
+ *   n_used                         device int32: U; pages from there on are free
+ * The moved pages keep their old contents too, so work that still reads through
+ * the old table may overlap the call while nothing is appended or given out.  An
+ * entry that names a free page is flagged and becomes -1.
+ * Errors: NULL_PTR, INVALID_ARG, WORKSPACE, ALIGNMENT, CUDA. */
+int kv_pages_compact(const int8kv_pool* pool, const int32_t* page_refs, const int32_t* page_table,
+                     int n_seqs, int max_pages_per_seq, int32_t* page_refs_out,
+                     int32_t* page_table_out, int32_t* n_used, void* workspace,
+                     size_t workspace_bytes, void* stream);
 
 /* Diagnostic for the device-side timeout report (genie-ai-runtime release
  * v0.1.0-alpha.11, "--int8-kv triage": a path that fell back silently ended in

@@ -18,9 +18,12 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libint8kv.so")
 
 K8V8, K8V16, K16V8, K8V4, Q4_0 = 0, 1, 2, 3, 4
-VARIANTS = {"k8v8": K8V8, "k8v16": K8V16, "k16v8": K16V8, "k8v4": K8V4, "q4_0": Q4_0}
+K8V8_BLOCK, F8_BLOCK = 8, 9     # one fp32 scale per (group_size positions, kv head)
+VARIANTS = {"k8v8": K8V8, "k8v16": K8V16, "k16v8": K16V8, "k8v4": K8V4, "q4_0": Q4_0,
+            "k8v8_block": K8V8_BLOCK, "f8_block": F8_BLOCK}
 REGION_K_STORE, REGION_V_STORE, REGION_K_SCALES, REGION_V_SCALES = 0, 1, 2, 3
 DEVERR_PAGE_ID, DEVERR_LENGTH, DEVERR_TIMEOUT = 1, 2, 4
+DEVERR_NO_PAGE, DEVERR_FORK = 8, 16
 ERR_FORMAT = -9
 DECODE_AUTO, DECODE_WARP_MMA, DECODE_SIMT = 0, 1, 3
 
@@ -51,6 +54,13 @@ _SIGS = {
     "kv_pool_image_bytes": (_c_int, [_vp, _c_int, _vp, ctypes.POINTER(_c_size)]),
     "kv_pool_test_expire_waits": (_c_int, [_vp, ctypes.c_uint32]),
     "kv_pool_save": (_c_int, [_vp, _c_int, _vp, _vp, _c_int, _vp, _c_size, _vp, _c_size, _vp]),
+    "kv_pages_workspace_bytes": (_c_int, [_vp, _c_int, ctypes.POINTER(_c_size)]),
+    "kv_pages_copy": (_c_int, [_vp, _c_int, _vp, _vp, _vp]),
+    "kv_pages_resize": (_c_int, [_vp, _vp, _vp, _c_int, _c_int, _vp, _vp, _c_size, _vp]),
+    "kv_pages_fork": (_c_int, [_vp, _vp, _vp, _c_int, _c_int, _vp, _c_int, _vp, _vp, _vp,
+                               _c_size, _vp]),
+    "kv_pages_compact": (_c_int, [_vp, _vp, _vp, _c_int, _c_int, _vp, _vp, _vp, _vp, _c_size,
+                                  _vp]),
     "kv_pool_load": (_c_int, [_vp, _vp, _c_size, _c_int, _vp, _c_int, _vp, _c_size, _vp, _vp]),
 }
 
@@ -112,6 +122,11 @@ def _dev(t, dtype, name):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _shape(t, shape, name):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+
+
 def int8kv_pool_region_bytes(n_layers, n_kv_heads, head_dim, group_size, page_size, n_pages,
                              variant, region):
     out = _c_size(0)
@@ -140,6 +155,8 @@ def kv_quant_append(pool, layer, k_new, v_new, seq_pos, page_table, stream=None)
     """k_new, v_new: fp16 [n_seqs][n_new][Hkv][D]; seq_pos int32 [n_seqs];
     page_table int32 [n_seqs][max_pages]."""
     n_seqs, n_new = k_new.shape[0], k_new.shape[1]
+    _block_rows(pool, k_new, (n_seqs, n_new), "k_new")
+    _block_rows(pool, v_new, (n_seqs, n_new), "v_new")
     _check(lib().kv_quant_append(pool.handle, layer, _dev(k_new, torch.float16, "k_new"),
                                  _dev(v_new, torch.float16, "v_new"), n_seqs, n_new,
                                  _dev(seq_pos, torch.int32, "seq_pos"),
@@ -166,6 +183,7 @@ def attn_decode_int8(pool, layer, q, seq_lens, page_table, out, workspace=None, 
     """q fp16 [B][H][D]; seq_lens int32 [B]; page_table int32 [B][max_pages];
     out fp32 [B][H][D]; workspace uint8 tensor (any contents) or None."""
     B, H = q.shape[0], q.shape[1]
+    _block_call(pool, q, seq_lens, page_table, out)
     ws = _dev(workspace, torch.uint8, "workspace") if workspace is not None else None
     nbytes = workspace.numel() if workspace is not None else 0
     _check(lib().attn_decode_int8(pool.handle, layer, _dev(q, torch.float16, "q"), B, H,
@@ -181,6 +199,7 @@ def attn_decode_int8_noalloc(pool, layer, q, seq_lens, page_table, out, window=0
     """attn_decode_int8 without a workspace: the partials use the library's own
     fixed scratch (for callers that cannot allocate device memory)."""
     B, H = q.shape[0], q.shape[1]
+    _block_call(pool, q, seq_lens, page_table, out)
     _check(lib().attn_decode_int8_noalloc(pool.handle, layer, _dev(q, torch.float16, "q"), B, H,
                                           _dev(seq_lens, torch.int32, "seq_lens"),
                                           _dev(page_table, torch.int32, "page_table"),
@@ -193,6 +212,9 @@ def attn_decode_append_int8(pool, layer, q, k_new, v_new, seq_lens, page_table, 
                             workspace=None, window=0, softmax_scale=0.0, n_splits=0, stream=None):
     """Append k_new, v_new (fp16 [B][Hkv][D]) at position seq_lens[b] - 1, then decode."""
     B, H = q.shape[0], q.shape[1]
+    _block_rows(pool, k_new, (B,), "k_new")
+    _block_rows(pool, v_new, (B,), "v_new")
+    _block_call(pool, q, seq_lens, page_table, out)
     ws = _dev(workspace, torch.uint8, "workspace") if workspace is not None else None
     nbytes = workspace.numel() if workspace is not None else 0
     _check(lib().attn_decode_append_int8(pool.handle, layer, _dev(q, torch.float16, "q"),
@@ -213,6 +235,7 @@ def attn_decode_multi_int8(pool, layer, q, seq_lens, page_table, out, workspace=
     seq_lens[b] - q_len + i.  out: fp32 [B][q_len][H][D].  The workspace is sized
     by attn_decode_workspace_bytes(B * q_len, H, ...)."""
     B, Q, H = q.shape[0], q.shape[1], q.shape[2]
+    _block_call(pool, q, seq_lens, page_table, out)
     ws = _dev(workspace, torch.uint8, "workspace") if workspace is not None else None
     nbytes = workspace.numel() if workspace is not None else 0
     _check(lib().attn_decode_multi_int8(pool.handle, layer, _dev(q, torch.float16, "q"), B, Q, H,
@@ -253,6 +276,21 @@ def attn_prefill_chunk_int8(pool, layer, q, start_pos, page_table, out, workspac
 def kv_pool_set_decode_kernel(pool, kind):
     """kind: DECODE_AUTO, DECODE_WARP_MMA or DECODE_SIMT."""
     _check(lib().kv_pool_set_decode_kernel(pool.handle, int(kind)), "kv_pool_set_decode_kernel")
+
+
+def _block_rows(pool, t, lead, name):
+    """A block-scaled pool's K/V rows have the shape lead + [n_kv_heads][head_dim]."""
+    if getattr(pool, "block", False):
+        _shape(t, tuple(lead) + (pool.n_kv_heads, pool.head_dim), name)
+
+
+def _block_call(pool, q, seq_lens, page_table, out):
+    """Shapes of a decode call on a block-scaled pool."""
+    if getattr(pool, "block", False):
+        _shape(q, q.shape[:-1] + (pool.head_dim,), "q")
+        _shape(out, q.shape, "out")
+        _shape(seq_lens, q.shape[:1], "seq_lens")
+        _shape(page_table, (q.shape[0], page_table.shape[-1]), "page_table")
 
 
 def _host_lens(seq_lens):
@@ -303,6 +341,65 @@ def kv_pool_load(pool, image, page_table, staging=None, stream=None):
     return lens[:n_seqs].tolist()
 
 
+def kv_pages_workspace_bytes(pool, n_seqs):
+    out = _c_size(0)
+    _check(lib().kv_pages_workspace_bytes(pool.handle, n_seqs, ctypes.byref(out)),
+           "kv_pages_workspace_bytes")
+    return out.value
+
+
+def kv_pages_copy(pool, src, dst, stream=None):
+    """Copy page src[i] of every layer, codes and scales, to page dst[i] (int32 [n])."""
+    s, d = _dev(src, torch.int32, "src"), _dev(dst, torch.int32, "dst")
+    _shape(dst, (src.numel(),), "dst")
+    _check(lib().kv_pages_copy(pool.handle, src.numel(), s, d, _stream(stream)), "kv_pages_copy")
+
+
+def kv_pages_resize(pool, page_refs, page_table, seq_lens, workspace, stream=None):
+    """Give every row of page_table (int32 [n_seqs][max_pages]) the pages that seq_lens (int32
+    [n_seqs]) needs and take back the others; page_refs: int32 [n_pages]."""
+    r, t = _dev(page_refs, torch.int32, "page_refs"), _dev(page_table, torch.int32, "page_table")
+    n = _dev(seq_lens, torch.int32, "seq_lens")
+    w = _dev(workspace, torch.uint8, "workspace")
+    _shape(page_refs, (pool.n_pages,), "page_refs")
+    _shape(seq_lens, (page_table.shape[0],), "seq_lens")
+    _check(lib().kv_pages_resize(pool.handle, r, t, page_table.shape[0], page_table.shape[1], n,
+                                 w, workspace.numel(), _stream(stream)), "kv_pages_resize")
+
+
+def kv_pages_fork(pool, page_refs, page_table, seq_lens, parents, children, workspace,
+                  stream=None):
+    """Row children[i] of page_table becomes a fork of row parents[i] (int32 [n_forks] each):
+    full pages are shared, the page that the length ends inside is copied."""
+    r, t = _dev(page_refs, torch.int32, "page_refs"), _dev(page_table, torch.int32, "page_table")
+    n = _dev(seq_lens, torch.int32, "seq_lens")
+    p, c = _dev(parents, torch.int32, "parents"), _dev(children, torch.int32, "children")
+    w = _dev(workspace, torch.uint8, "workspace")
+    _shape(page_refs, (pool.n_pages,), "page_refs")
+    _shape(seq_lens, (page_table.shape[0],), "seq_lens")
+    _shape(children, (parents.numel(),), "children")
+    _check(lib().kv_pages_fork(pool.handle, r, t, page_table.shape[0], page_table.shape[1], n,
+                               parents.numel(), p, c, w, workspace.numel(), _stream(stream)),
+           "kv_pages_fork")
+
+
+def kv_pages_compact(pool, page_refs, page_table, page_refs_out, page_table_out, n_used,
+                     workspace, stream=None):
+    """Move the used pages to ids 0 .. n_used - 1 (int32 [1] on the device); the counts and the
+    table afterwards go to page_refs_out and page_table_out (which may be the inputs)."""
+    r, t = _dev(page_refs, torch.int32, "page_refs"), _dev(page_table, torch.int32, "page_table")
+    ro = _dev(page_refs_out, torch.int32, "page_refs_out")
+    to = _dev(page_table_out, torch.int32, "page_table_out")
+    u = _dev(n_used, torch.int32, "n_used")
+    w = _dev(workspace, torch.uint8, "workspace")
+    _shape(page_refs, (pool.n_pages,), "page_refs")
+    _shape(page_refs_out, (pool.n_pages,), "page_refs_out")
+    _shape(page_table_out, page_table.shape, "page_table_out")
+    _check(lib().kv_pages_compact(pool.handle, r, t, page_table.shape[0], page_table.shape[1], ro,
+                                  to, u, w, workspace.numel(), _stream(stream)),
+           "kv_pages_compact")
+
+
 def kv_pool_test_expire_waits(pool, max_polls):
     """Diagnostic: later decode calls arm their copy waits so that they expire after
     max_polls polls and report INT8KV_DEVERR_TIMEOUT (0 switches it off)."""
@@ -326,8 +423,34 @@ class KVPool:
             variant = VARIANTS[variant]
         dev = torch.device("cuda", torch.cuda.current_device() if device is None else device)
         shape = (n_layers, n_pages, n_kv_heads, page_size, head_dim)
-        ng = head_dim // group_size
-        sshape = (n_layers, n_pages, n_kv_heads, page_size, ng)
+        self.block = variant in (K8V8_BLOCK, F8_BLOCK)
+        if self.block:
+            codes = torch.int8 if variant == K8V8_BLOCK else torch.float8_e4m3fn
+            self.k_store = torch.zeros(shape, dtype=torch.int8, device=dev).view(codes)
+            self.v_store = torch.zeros(shape, dtype=torch.int8, device=dev).view(codes)
+            self.k_scales = torch.zeros(shape[:-2] + (page_size // max(group_size, 1),),
+                                        dtype=torch.float32, device=dev)
+            self.v_scales = torch.zeros_like(self.k_scales)
+        else:
+            self._rows_with_scales(shape, group_size, variant, dev)
+        self.dev_error = torch.zeros(4, dtype=torch.int32, device=dev)
+        for region, t in ((REGION_K_STORE, self.k_store), (REGION_V_STORE, self.v_store),
+                          (REGION_K_SCALES, self.k_scales), (REGION_V_SCALES, self.v_scales)):
+            want = int8kv_pool_region_bytes(n_layers, n_kv_heads, head_dim, group_size,
+                                            page_size, n_pages, variant, region)
+            have = 0 if t is None else t.numel() * t.element_size()
+            assert want == have, (region, want, have)
+        self.n_layers, self.n_kv_heads, self.head_dim = n_layers, n_kv_heads, head_dim
+        self.group_size, self.page_size, self.n_pages, self.variant = (group_size, page_size,
+                                                                       n_pages, variant)
+        with torch.cuda.device(dev):     # the descriptor belongs to the device that is current
+            self.handle = kv_pool_create(n_layers, n_kv_heads, head_dim, group_size, page_size,
+                                         n_pages, variant, self.k_store, self.v_store,
+                                         self.k_scales, self.v_scales, self.dev_error)
+
+    def _rows_with_scales(self, shape, group_size, variant, dev):
+        head_dim = shape[-1]
+        sshape = shape[:-1] + (head_dim // group_size,)
         k8 = variant in (K8V8, K8V16, K8V4)
         v8 = variant in (K8V8, K16V8)
         k4 = variant == Q4_0
@@ -344,19 +467,6 @@ class KVPool:
             self.v_store = torch.zeros(shape[:-1] + (head_dim // 2,), dtype=torch.uint8, device=dev)
             self.v_scales = torch.zeros(shape[:-1] + (head_dim // 32,), dtype=torch.float16,
                                         device=dev)
-        self.dev_error = torch.zeros(4, dtype=torch.int32, device=dev)
-        for region, t in ((REGION_K_STORE, self.k_store), (REGION_V_STORE, self.v_store),
-                          (REGION_K_SCALES, self.k_scales), (REGION_V_SCALES, self.v_scales)):
-            want = int8kv_pool_region_bytes(n_layers, n_kv_heads, head_dim, group_size,
-                                            page_size, n_pages, variant, region)
-            have = 0 if t is None else t.numel() * t.element_size()
-            assert want == have, (region, want, have)
-        self.n_layers, self.n_kv_heads, self.head_dim = n_layers, n_kv_heads, head_dim
-        self.group_size, self.page_size, self.n_pages, self.variant = (group_size, page_size,
-                                                                       n_pages, variant)
-        self.handle = kv_pool_create(n_layers, n_kv_heads, head_dim, group_size, page_size,
-                                     n_pages, variant, self.k_store, self.v_store,
-                                     self.k_scales, self.v_scales, self.dev_error)
 
     def __del__(self):
         h = getattr(self, "handle", None)
@@ -370,3 +480,8 @@ class KVPool:
     def decode_workspace(self, batch, n_heads, n_splits):
         n = attn_decode_workspace_bytes(batch, n_heads, self.n_kv_heads, self.head_dim, n_splits)
         return torch.zeros(max(n, 16), dtype=torch.uint8, device=self.k_store.device)
+
+    def pages_workspace(self, n_seqs):
+        """Workspace of kv_pages_resize, kv_pages_fork and kv_pages_compact for n_seqs rows."""
+        return torch.zeros(kv_pages_workspace_bytes(self, n_seqs), dtype=torch.uint8,
+                           device=self.k_store.device)

@@ -10,6 +10,7 @@
 
 #include <cuda_runtime.h>
 
+#include "block_common.cuh"
 #include "decode_common.cuh"
 #include "internal.h"
 
@@ -39,8 +40,19 @@ bool variant_stores(int variant, bool* k8, bool* v8, bool* k4, bool* v4) {
     case INT8KV_K16V8: *k8 = false; *v8 = true; return true;
     case INT8KV_K8V4: *k8 = true; *v8 = false; *v4 = true; return true;
     case INT8KV_Q4_0: *k8 = false; *v8 = false; *k4 = true; *v4 = true; return true;
+    case INT8KV_K8V8_BLOCK:
+    case INT8KV_F8_BLOCK: *k8 = true; *v8 = true; return true;   // one byte a value
     default: return false;
   }
+}
+
+bool block_variant(int variant) {
+  return variant == INT8KV_K8V8_BLOCK || variant == INT8KV_F8_BLOCK;
+}
+
+// group_size of a block-scaled pool: positions that share a scale.
+bool valid_block(int page_size, int gs) {
+  return (gs == 16 || gs == 32 || gs == 64 || gs == 128) && gs <= page_size;
 }
 
 bool variant_int8(int variant, bool* k8, bool* v8) {
@@ -55,7 +67,9 @@ int shape_status(int n_layers, int n_kv_heads, int head_dim, int group_size, int
   if (n_layers <= 0 || n_kv_heads <= 0 || n_pages <= 0) return INT8KV_ERR_INVALID_ARG;
   if (!valid_head_dim(head_dim)) return INT8KV_ERR_UNSUPPORTED;
   if (!valid_page_size(page_size)) return INT8KV_ERR_UNSUPPORTED;
-  if (!valid_group(head_dim, group_size)) return INT8KV_ERR_GROUP;
+  if (block_variant(variant) ? !valid_block(page_size, group_size)
+                             : !valid_group(head_dim, group_size))
+    return INT8KV_ERR_GROUP;
   return INT8KV_OK;
 }
 
@@ -173,9 +187,42 @@ int decode_splits_heuristic(const int8kv_pool* pool, long long units, int max_ct
   return n;
 }
 
+// Splits of a block-scaled pool's decode call: the balanced schedule runs up to
+// units * (n - 1) + 1 blocks, so n is the least that fills the device.  A context
+// of one tile per warp is left to one block per unit: it needs no combine.
+static int block_splits(const int8kv_pool* pool, long long units, int max_ctx) {
+  if (max_ctx <= kBlockSingle) return 1;
+  const long long n = (pool->block_resident - 1 + units - 1) / units + 1;
+  return (int)(n < 2 ? 2 : n > kMaxSplits ? kMaxSplits : n);
+}
+
+// Blocks of the balanced schedule: one share each.  Unit u's piece in share c is
+// partial u + c, so units + shares - 1 partials of `width` rows must fit the
+// workspace's batch * q_len * n_heads * n_splits rows.
+static int block_shares(const int8kv_pool* pool, long long units, int width, long long rows,
+                        int n_splits) {
+  if (n_splits == 1) return 0;
+  long long n = units * (n_splits - 1) + 1;
+  const long long fit = rows / width - units + 1;
+  if (n > fit) n = fit;
+  if (n > pool->block_resident) n = pool->block_resident;
+  return (int)(n < 1 ? 1 : n);
+}
+
 int decode_auto_splits(const int8kv_pool* pool, int batch, int q_len, int G, int max_pages,
                        int window, size_t max_workspace) {
   const int n_cg = (q_len * G + 7) / 8;   // blocks per (sequence, kv head) sharing the columns
+  if (pool->block) {
+    const long long cap = (long long)max_pages * pool->page_size;
+    int n = block_splits(pool, (long long)batch * n_cg * pool->n_kv_heads,
+                         (int)(window > 0 && window < cap ? window : cap < INT32_MAX ? cap : INT32_MAX));
+    if (max_workspace > 0)
+      while (n > 1 && decode_workspace_layout(batch * q_len, G * pool->n_kv_heads,
+                                              pool->n_kv_heads, pool->head_dim, n, nullptr,
+                                              nullptr) > max_workspace)
+        --n;
+    return n;
+  }
   int ctx = max_pages * pool->page_size;
   if (window > 0 && window + pool->page_size < ctx) ctx = window + pool->page_size;
   int top = kMaxSplits;
@@ -185,6 +232,11 @@ int decode_auto_splits(const int8kv_pool* pool, int batch, int q_len, int G, int
                                               nullptr) > max_workspace)
       --top;
   return decode_splits_heuristic(pool, (long long)batch * n_cg * pool->n_kv_heads, ctx, top);
+}
+
+static int launch_status(cudaError_t e) {
+  if (e == cudaErrorNotSupported) return INT8KV_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? INT8KV_OK : INT8KV_ERR_CUDA;
 }
 
 }  // namespace int8kv
@@ -217,6 +269,11 @@ int int8kv_pool_region_bytes(int n_layers, int n_kv_heads, int head_dim, int gro
   bool k8, v8, k4, v4;
   variant_stores(variant, &k8, &v8, &k4, &v4);
   const size_t rows = (size_t)n_layers * n_pages * n_kv_heads * page_size;
+  if (block_variant(variant) &&
+      (region == INT8KV_REGION_K_SCALES || region == INT8KV_REGION_V_SCALES)) {
+    *out_bytes = rows / group_size * sizeof(float);
+    return INT8KV_OK;
+  }
   switch (region) {
     case INT8KV_REGION_K_STORE:
       *out_bytes = k4 ? rows * head_dim / 2 : rows * head_dim * (k8 ? 1 : 2);
@@ -262,7 +319,10 @@ int kv_pool_create(int8kv_pool** out, int n_layers, int n_kv_heads, int head_dim
   p->n_kv_heads = n_kv_heads;
   p->head_dim = head_dim;
   p->group_size = group_size;
-  p->n_groups = head_dim / group_size;
+  p->block = block_variant(variant);
+  p->f8 = variant == INT8KV_F8_BLOCK;
+  p->block_resident = 0;
+  p->n_groups = p->block ? 1 : head_dim / group_size;
   p->page_size = page_size;
   p->n_pages = n_pages;
   p->variant = variant;
@@ -281,6 +341,15 @@ int kv_pool_create(int8kv_pool** out, int n_layers, int n_kv_heads, int head_dim
   p->decode_kernel = INT8KV_DECODE_AUTO;
   for (int k = 0; k < 4; ++k) p->resident[k] = 0;
   p->expire_polls = 0;
+  if (p->block) {
+    p->block_resident = block_decode_resident(head_dim, p->f8);
+    if (p->block_resident <= 0) {
+      delete p;
+      return INT8KV_ERR_CUDA;
+    }
+    *out = p;
+    return INT8KV_OK;
+  }
   // TMA descriptors for the tensor-core kernels; a 4-bit store is mapped as
   // rows of head_dim / 2 bytes (head_dim 256 only: one 128-byte box a row)
   if (page_size == 64 && (head_dim == 128 || head_dim == 256) && (!v4 || head_dim == 256)) {
@@ -308,6 +377,9 @@ int kv_quant_append(const int8kv_pool* pool, int layer, const uint16_t* k_new,
   if ((long long)n_seqs * n_new == 0) return INT8KV_OK;
   if (!k_new || !v_new || !seq_pos || !page_table) return INT8KV_ERR_NULL_PTR;
   if (!aligned16(k_new) || !aligned16(v_new)) return INT8KV_ERR_ALIGNMENT;
+  if (pool->block) return launch_status(launch_block_append(
+      block_view(pool, layer), pool->head_dim, pool->f8, k_new, v_new, n_seqs, n_new, seq_pos, 0,
+      page_table, max_pages_per_seq, (cudaStream_t)stream));
   const cudaError_t e = launch_quant_append(layer_view(pool, layer), k_new, v_new, n_seqs, n_new,
                                             seq_pos, page_table, max_pages_per_seq, pool->k_int8,
                                             pool->v_int8, (cudaStream_t)stream);
@@ -318,6 +390,8 @@ int kv_pool_set_decode_kernel(int8kv_pool* pool, int kind) {
   if (!pool) return INT8KV_ERR_NULL_PTR;
   if (kind != INT8KV_DECODE_AUTO && kind != INT8KV_DECODE_WARP_MMA && kind != INT8KV_DECODE_SIMT)
     return INT8KV_ERR_INVALID_ARG;
+  if (pool->block)     // one kernel serves these pools
+    return kind == INT8KV_DECODE_AUTO ? INT8KV_OK : INT8KV_ERR_UNSUPPORTED;
   const PoolView v = layer_view(pool, 0);
   if (kind == INT8KV_DECODE_WARP_MMA && !(pool->has_tmaps && decode_mma_supported(v, 1)))
     return INT8KV_ERR_UNSUPPORTED;
@@ -328,6 +402,7 @@ int kv_pool_set_decode_kernel(int8kv_pool* pool, int kind) {
 int attn_decode_n_splits(const int8kv_pool* pool, int batch, int max_ctx) {
   if (!pool) return INT8KV_ERR_NULL_PTR;
   if (batch <= 0 || max_ctx < 0) return INT8KV_ERR_INVALID_ARG;
+  if (pool->block) return block_splits(pool, (long long)batch * pool->n_kv_heads, max_ctx);
   return decode_splits_heuristic(pool, (long long)batch * pool->n_kv_heads, max_ctx, kMaxSplits);
 }
 
@@ -393,7 +468,7 @@ static int decode_entry(const int8kv_pool* pool, int layer, const uint16_t* q,
   const int G = n_heads / pool->n_kv_heads;
   if (G > 8) return INT8KV_ERR_UNSUPPORTED;
   // a query window runs on the warp-level tensor-core kernel only
-  if (q_len > 1 && decode_kernel_for(pool, G) != INT8KV_DECODE_WARP_MMA)
+  if (q_len > 1 && !pool->block && decode_kernel_for(pool, G) != INT8KV_DECODE_WARP_MMA)
     return INT8KV_ERR_UNSUPPORTED;
   if (batch == 0) return INT8KV_OK;
   if (!q || !seq_lens || !page_table || !out) return INT8KV_ERR_NULL_PTR;
@@ -410,6 +485,36 @@ static int decode_entry(const int8kv_pool* pool, int layer, const uint16_t* q,
     if (!workspace || workspace_bytes < need) return INT8KV_ERR_WORKSPACE;
     if (!aligned16(workspace)) return INT8KV_ERR_ALIGNMENT;
   }
+  const float scale = softmax_scale != 0.f ? softmax_scale : 1.0f / std::sqrt((float)pool->head_dim);
+  if (pool->block) {
+    cudaStream_t s = (cudaStream_t)stream;
+    if (k_new) {
+      const cudaError_t e = launch_block_append(block_view(pool, layer), pool->head_dim, pool->f8,
+                                                k_new, v_new, batch, 1, seq_lens, -1, page_table,
+                                                max_pages_per_seq, s);
+      if (e != cudaSuccess) return launch_status(e);
+    }
+    BlockDecodeArgs d;
+    d.pool = block_view(pool, layer);
+    d.q = q;
+    d.seq_lens = seq_lens;
+    d.page_table = page_table;
+    d.out = out;
+    d.part_o = a.ws.part_o;
+    d.part_lse = (float*)a.ws.part_ml;
+    d.B = batch;
+    d.H = n_heads;
+    d.G = G;
+    d.Q = q_len;
+    d.max_pages = max_pages_per_seq;
+    d.window = window;
+    d.n_cg = n_cg;
+    d.width = (q_len * G + n_cg - 1) / n_cg;
+    d.shares = block_shares(pool, (long long)batch * pool->n_kv_heads * n_cg, d.width,
+                            (long long)batch * q_len * n_heads * n_splits, n_splits);
+    d.scale_log2 = scale * 1.4426950408889634f;
+    return launch_status(launch_block_decode(d, pool->head_dim, pool->f8, s));
+  }
   a.pool = layer_view(pool, layer);
   a.q = q;
   a.k_new = k_new;
@@ -423,7 +528,6 @@ static int decode_entry(const int8kv_pool* pool, int layer, const uint16_t* q,
   a.max_pages = max_pages_per_seq;
   a.window = window;
   a.n_splits = n_splits;
-  const float scale = softmax_scale != 0.f ? softmax_scale : 1.0f / std::sqrt((float)pool->head_dim);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.expire_polls = pool->expire_polls;
   const cudaError_t e = launch_decode(pool, layer, a, (cudaStream_t)stream);
@@ -436,7 +540,7 @@ int attn_prefill_n_splits(const int8kv_pool* pool, int n_new, int n_heads, int s
   if (n_new <= 0 || n_heads <= 0 || start_pos < 0 || n_heads % pool->n_kv_heads != 0)
     return INT8KV_ERR_INVALID_ARG;
   const int G = n_heads / pool->n_kv_heads;
-  if (G > 8) return INT8KV_ERR_UNSUPPORTED;
+  if (G > 8 || pool->block) return INT8KV_ERR_UNSUPPORTED;
   // One block per SM at a time: (query tiles of 128 rows) x kv heads x splits
   // blocks run in ceil(blocks / SMs) waves of ceil(pages / splits) pages each.
   // Take the split count with the shortest such chain, counting two pages of
@@ -511,6 +615,7 @@ int attn_prefill_chunk_int8(const int8kv_pool* pool, int layer, const uint16_t* 
 
 int kv_pool_test_expire_waits(int8kv_pool* pool, uint32_t max_polls) {
   if (!pool) return INT8KV_ERR_NULL_PTR;
+  if (max_polls != 0 && pool->block) return INT8KV_ERR_UNSUPPORTED;
   if (max_polls != 0 && decode_kernel_for(pool, 1) != INT8KV_DECODE_WARP_MMA)
     return INT8KV_ERR_UNSUPPORTED;
   pool->expire_polls = max_polls;

@@ -1,0 +1,562 @@
+// Pages of a pool on the device: copying them, forking sequences, giving rows of a
+// page table the pages their lengths need, and compacting the pool.
+//
+// page_refs[p] counts the page-table entries that name page p; 0 is a free page.
+// Pages are taken in ascending order of id by the rows (forks) in ascending order,
+// so results do not depend on timing: counts change by integer atomics whose order
+// does not matter, everything that is ranked is ranked by prefix sums.
+//
+// The bookkeeping of one call runs in one cluster of thread blocks (the calls read
+// a few hundred KB: a grid-wide barrier would cost more than the other SMs bring).
+// A range of entries or pages is cut into one contiguous run per thread; a rank is
+// the prefix sum over the runs before it, exchanged through distributed shared
+// memory.  The bytes of pages move in a second, grid-wide kernel, which reads its
+// list of (source, destination) pairs from device memory.
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace int8kv {
+namespace {
+
+constexpr int kBlocks = 8;        // blocks of the bookkeeping cluster
+constexpr int kThreads = 512;     // threads of each
+constexpr int kRuns = kBlocks * kThreads;
+
+// ---- copies -----------------------------------------------------------------
+constexpr int kCopyThreads = 256;
+constexpr int kChunk = 16384;     // bytes a block copies at a time
+
+struct Regions {
+  char* base[4];             // stores and scales, all layers (null: the pool has none)
+  unsigned bytes[4];         // of one page of one layer
+  int chunks[4];             // per page and layer, summed up to and including this region
+  int n_layers, n_pages;
+  int32_t* err;
+};
+
+// Pages (src[i], dst[i]) of every layer and region, i < n (or *n_dev).  A negative
+// entry on either side is no copy.
+__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const Regions r, const int32_t* src,
+                                                                 const int32_t* dst, int n,
+                                                                 const int32_t* n_dev) {
+  ptx::grid_launch_dependents();
+  ptx::grid_dependency_wait();
+  if (n_dev) n = *n_dev;
+  const int per = r.chunks[3];                         // chunks of a page and layer
+  const long long total = (long long)n * r.n_layers * per;
+  for (long long w = blockIdx.x; w < total; w += gridDim.x) {
+    const int c = (int)(w % per);
+    const long long il = w / per;
+    const int layer = (int)(il % r.n_layers), i = (int)(il / r.n_layers);
+    const int s = src[i], d = dst[i];
+    if (s < 0 || d < 0 || s >= r.n_pages || d >= r.n_pages) {
+      if ((s >= r.n_pages || d >= r.n_pages) && threadIdx.x == 0)
+        flag_error(r.err, INT8KV_DEVERR_PAGE_ID);
+      continue;
+    }
+    if (s == d) continue;
+    int k = 0;
+    while (c >= r.chunks[k]) ++k;
+    const unsigned bytes = r.bytes[k];
+    const unsigned at = (unsigned)(c - (k ? r.chunks[k - 1] : 0)) * kChunk;
+    const unsigned len = min(bytes - at, (unsigned)kChunk);
+    const char* from = r.base[k] + ((size_t)layer * r.n_pages + s) * bytes + at;
+    char* to = r.base[k] + ((size_t)layer * r.n_pages + d) * bytes + at;
+    if (bytes % 16 == 0) {
+      uint4 x[kChunk / 16 / kCopyThreads];
+#pragma unroll
+      for (int j = 0; j < kChunk / 16 / kCopyThreads; ++j) {
+        const unsigned o = (threadIdx.x + j * kCopyThreads) * 16;
+        if (o < len) x[j] = *reinterpret_cast<const uint4*>(from + o);
+      }
+#pragma unroll
+      for (int j = 0; j < kChunk / 16 / kCopyThreads; ++j) {
+        const unsigned o = (threadIdx.x + j * kCopyThreads) * 16;
+        if (o < len) *reinterpret_cast<uint4*>(to + o) = x[j];
+      }
+    } else {     // scales of a few blocks: a multiple of 4 bytes
+      for (unsigned o = threadIdx.x * 4; o < len; o += kCopyThreads * 4)
+        *reinterpret_cast<uint32_t*>(to + o) = *reinterpret_cast<const uint32_t*>(from + o);
+    }
+  }
+}
+
+// ---- bookkeeping ------------------------------------------------------------
+struct Ranks {
+  int warp[kThreads / 32];
+  int block[2];       // this block's sum, double-buffered over calls
+};
+
+// Exclusive prefix sum of v over the cluster's threads, in order; *total its sum.
+// Every thread of the cluster calls it the same number of times.
+__device__ __forceinline__ int cluster_rank(int v, int& total, Ranks& sh, int& phase) {
+  cg::cluster_group cl = cg::this_cluster();
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  int inc = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, inc, off);
+    if (lane >= off) inc += o;
+  }
+  if (lane == 31) sh.warp[wid] = inc;
+  __syncthreads();
+  int before = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < wid) before += sh.warp[w];
+    sum += sh.warp[w];
+  }
+  if (threadIdx.x == 0) sh.block[phase] = sum;
+  cl.sync();     // (also: sh.warp may be written again)
+  total = 0;
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b) {
+    const int o = *cl.map_shared_rank(&sh.block[phase], b);
+    if (b < (int)cl.block_rank()) before += o;
+    total += o;
+  }
+  phase ^= 1;    // the other slot was read before the last cluster barrier
+  return before + inc - v;
+}
+
+// This thread's run [a, z) of n items.
+__device__ __forceinline__ void run_of(long long n, long long& a, long long& z) {
+  const long long per = (n + kRuns - 1) / kRuns;
+  a = per * (blockIdx.x * kThreads + threadIdx.x);
+  z = a + per < n ? a + per : n;
+}
+
+// One reference less.  A page that has none stays at 0 (flagged).
+__device__ __forceinline__ void give_back(int32_t* refs, int page, int32_t* err) {
+  if (atomicAdd(refs + page, -1) <= 0) {
+    atomicAdd(refs + page, 1);
+    flag_error(err, INT8KV_DEVERR_PAGE_ID);
+  }
+}
+
+// The `want` first free pages in ascending order -> list; returns how many there are.
+__device__ __forceinline__ int free_pages(const int32_t* refs, int n_pages, int want, int32_t* list,
+                                          Ranks& sh, int& phase) {
+  long long a, z;
+  run_of(n_pages, a, z);
+  int mine = 0;
+  for (long long i = a; i < z; ++i) mine += __ldcg(refs + i) == 0;
+  int n;
+  int at = cluster_rank(mine, n, sh, phase);
+  if (mine && at < want)
+    for (long long i = a; i < z && at < want; ++i)
+      if (__ldcg(refs + i) == 0) list[at++] = (int)i;
+  cg::this_cluster().sync();
+  return n;
+}
+
+struct PagesArgs {
+  int32_t* refs;
+  int32_t* table;          // [n_seqs][max_pages]
+  int n_seqs, max_pages, n_pages, page_size;
+  int32_t* err;
+  int32_t* list;           // workspace: free pages, [n_pages]
+  int32_t* src;            // workspace: pages to copy, [max(n_pages, n_seqs)] each
+  int32_t* dst;
+  int32_t* map;            // workspace: [max(n_pages, 2 n_seqs)]
+  int32_t* count;          // workspace: pairs to copy
+};
+
+// Pages that `len` positions need, at most what a row holds (more is flagged).
+__device__ __forceinline__ int pages_needed(int len, const PagesArgs& a) {
+  if (len <= 0) return 0;
+  const int n = (len - 1) / a.page_size + 1;
+  if (n > a.max_pages) {
+    flag_error(a.err, INT8KV_DEVERR_LENGTH);
+    return a.max_pages;
+  }
+  return n;
+}
+
+__global__ void __launch_bounds__(kThreads) resize_kernel(const PagesArgs a,
+                                                          const int32_t* __restrict__ lens) {
+  __shared__ Ranks sh;
+  int phase = 0;
+  ptx::grid_launch_dependents();
+  ptx::grid_dependency_wait();
+  long long lo, hi;
+  run_of((long long)a.n_seqs * a.max_pages, lo, hi);
+  int missing = 0;
+  if (lo < hi) {
+    int row = (int)(lo / a.max_pages), p = (int)(lo % a.max_pages), need = pages_needed(lens[row], a);
+    for (long long i = lo; i < hi; ++i) {
+      const int e = a.table[i];
+      if (e >= a.n_pages) {
+        flag_error(a.err, INT8KV_DEVERR_PAGE_ID);
+        a.table[i] = -1;
+      }
+      const bool has = e >= 0 && e < a.n_pages;
+      if (p < need) {
+        missing += !has;
+      } else if (has) {
+        give_back(a.refs, e, a.err);
+        a.table[i] = -1;
+      }
+      if (++p == a.max_pages && i + 1 < hi) {
+        p = 0;
+        need = pages_needed(lens[++row], a);
+      }
+    }
+  }
+  int want;
+  int at = cluster_rank(missing, want, sh, phase);
+  if (want == 0) {            // the same for the whole cluster
+    cg::this_cluster().sync();   // the others may still read this block's sum
+    return;
+  }
+  const int n = free_pages(a.refs, a.n_pages, want, a.list, sh, phase);
+  if (missing) {
+    int row = (int)(lo / a.max_pages), p = (int)(lo % a.max_pages), need = pages_needed(lens[row], a);
+    for (long long i = lo; i < hi; ++i) {
+      if (p < need && a.table[i] < 0) {
+        if (at < n) {
+          const int page = __ldcg(a.list + at);
+          a.table[i] = page;
+          a.refs[page] = 1;
+        } else {
+          flag_error(a.err, INT8KV_DEVERR_NO_PAGE);
+        }
+        ++at;
+      }
+      if (++p == a.max_pages && i + 1 < hi) {
+        p = 0;
+        need = pages_needed(lens[++row], a);
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) fork_kernel(const PagesArgs a, int32_t* lens, int n,
+                                                        const int32_t* __restrict__ parents,
+                                                        const int32_t* __restrict__ children) {
+  __shared__ Ranks sh;
+  int phase = 0;
+  cg::cluster_group cl = cg::this_cluster();
+  const int me = blockIdx.x * kThreads + threadIdx.x;
+  ptx::grid_launch_dependents();
+  ptx::grid_dependency_wait();
+  int32_t* first = a.map;              // lowest fork that names a row as its child
+  int32_t* parent = a.map + a.n_seqs;  // whether a row is some fork's parent
+  for (int i = me; i < a.n_seqs; i += kRuns) {
+    first[i] = INT32_MAX;
+    parent[i] = 0;
+  }
+  cl.sync();
+  for (int i = me; i < n; i += kRuns) {
+    const int p = parents[i], c = children[i];
+    if (p < 0 || c < 0 || p >= a.n_seqs || c >= a.n_seqs) continue;
+    atomicMin(first + c, i);
+    atomicExch(parent + p, 1);
+  }
+  cl.sync();
+  // whether fork i takes place; one that names no two rows (-1) is left out silently
+  auto takes = [&](int i, int& p, int& c) {
+    p = parents[i];
+    c = children[i];
+    if (p < 0 || c < 0) return false;
+    return p < a.n_seqs && c < a.n_seqs && __ldcg(first + c) == i && __ldcg(parent + c) == 0;
+  };
+  // children's rows: what they held goes back, the parent's full pages are shared
+  const long long entries = (long long)n * a.max_pages;
+  for (long long w = me; w < entries; w += kRuns) {
+    const int i = (int)(w / a.max_pages), k = (int)(w % a.max_pages);
+    int p, c;
+    if (!takes(i, p, c)) {
+      if (k == 0 && p >= 0 && c >= 0) flag_error(a.err, INT8KV_DEVERR_FORK);
+      continue;
+    }
+    const long long cap = (long long)a.max_pages * a.page_size;
+    const int len = (int)min((long long)max(lens[p], 0), cap);
+    if (k == 0 && lens[p] > cap) flag_error(a.err, INT8KV_DEVERR_LENGTH);
+    int e = -1;
+    if (k < len / a.page_size) {
+      e = a.table[(size_t)p * a.max_pages + k];
+      if (e < 0 || e >= a.n_pages) {
+        flag_error(a.err, INT8KV_DEVERR_PAGE_ID);
+        e = -1;
+      } else {
+        atomicAdd(a.refs + e, 1);
+      }
+    }
+    int32_t* mine = a.table + (size_t)c * a.max_pages + k;
+    const int was = *mine;
+    if (was >= 0) {
+      if (was < a.n_pages) give_back(a.refs, was, a.err);
+      else flag_error(a.err, INT8KV_DEVERR_PAGE_ID);
+    }
+    *mine = e;
+  }
+  // forks whose parent ends inside a page need a page of their own for its copy
+  long long lo, hi;
+  run_of(n, lo, hi);
+  int need = 0;
+  for (long long i = lo; i < hi; ++i) {
+    int p, c, page = -1;
+    if (takes((int)i, p, c)) {
+      const int len = (int)min((long long)max(lens[p], 0), (long long)a.max_pages * a.page_size);
+      if (len % a.page_size) {
+        page = a.table[(size_t)p * a.max_pages + len / a.page_size];
+        if (page < 0 || page >= a.n_pages) {
+          flag_error(a.err, INT8KV_DEVERR_PAGE_ID);
+          page = -1;
+        }
+      }
+    }
+    a.src[i] = page;
+    need += page >= 0;
+  }
+  int want;
+  int at = cluster_rank(need, want, sh, phase);
+  int got = 0;
+  if (want) got = free_pages(a.refs, a.n_pages, want, a.list, sh, phase);
+  else cl.sync();     // the others may still read this block's sum
+  for (long long i = lo; i < hi; ++i) {
+    int p, c, page = -1;
+    if (takes((int)i, p, c)) {
+      int len = (int)min((long long)max(lens[p], 0), (long long)a.max_pages * a.page_size);
+      if (a.src[i] >= 0) {
+        if (at < got) {
+          page = __ldcg(a.list + at);
+          a.refs[page] = 1;
+          a.table[(size_t)c * a.max_pages + len / a.page_size] = page;
+        } else {     // no page for the rest: the child ends with the shared ones
+          flag_error(a.err, INT8KV_DEVERR_NO_PAGE);
+          len -= len % a.page_size;
+        }
+        ++at;
+      }
+      lens[c] = len;
+    }
+    a.dst[i] = page;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) compact_kernel(const PagesArgs a, int32_t* refs_out,
+                                                           int32_t* table_out, int32_t* n_used) {
+  __shared__ Ranks sh;
+  int phase = 0;
+  cg::cluster_group cl = cg::this_cluster();
+  ptx::grid_launch_dependents();
+  ptx::grid_dependency_wait();
+  long long lo, hi;
+  run_of(a.n_pages, lo, hi);
+  int mine = 0;
+  for (long long i = lo; i < hi; ++i) mine += a.refs[i] > 0;
+  int used;
+  const int below = cluster_rank(mine, used, sh, phase);     // used pages before the run
+  // pages [0, used) are to be the used ones: free ids there are filled, in order, with
+  // the used pages from there on.  Used pages before `used` number used - movers.
+  long long cut = used < lo ? lo : used > hi ? hi : used;     // run's first id >= used
+  int holes = 0;
+  for (long long i = lo; i < cut; ++i) holes += a.refs[i] <= 0;
+  int n;
+  int hole = cluster_rank(holes, n, sh, phase);               // n: pages to move
+  // of the run's used pages, those from `cut` on move
+  int low = 0;
+  for (long long i = lo; i < cut; ++i) low += a.refs[i] > 0;
+  int mover = below + low - (used - n);                       // rank of the run's first mover
+  const int first_mover = mover;
+  for (long long i = lo; i < cut; ++i) {
+    const int r = a.refs[i];
+    a.map[i] = r > 0 ? (int)i : -1;
+    if (r > 0) refs_out[i] = r;      // (a hole's count comes with the page that fills it)
+    else a.dst[hole++] = (int)i;
+  }
+  for (long long i = cut; i < hi; ++i)
+    if (a.refs[i] > 0) a.src[mover++] = (int)i;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *n_used = used;
+    *a.count = n;
+  }
+  cl.sync();
+  mover = first_mover;
+  for (long long i = cut; i < hi; ++i) {
+    const int r = a.refs[i];
+    int to = -1;
+    if (r > 0) {
+      to = __ldcg(a.dst + mover++);
+      refs_out[to] = r;
+    }
+    a.map[i] = to;
+    refs_out[i] = 0;
+  }
+  cl.sync();
+  const long long entries = (long long)a.n_seqs * a.max_pages;
+  for (long long i = blockIdx.x * kThreads + threadIdx.x; i < entries; i += kRuns) {
+    int e = a.table[i];
+    if (e >= 0) {
+      e = e < a.n_pages ? __ldcg(a.map + e) : -1;
+      if (e < 0) flag_error(a.err, INT8KV_DEVERR_PAGE_ID);
+    }
+    table_out[i] = e;
+  }
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+size_t workspace(const int8kv_pool* p, int n_seqs, PagesArgs* a, void* base) {
+  const size_t pages = p->n_pages, seqs = n_seqs;
+  const size_t list = up256(pages * 4), pair = up256((pages > seqs ? pages : seqs) * 4),
+               map = up256((pages > 2 * seqs ? pages : 2 * seqs) * 4);
+  if (a) {
+    char* w = (char*)base;
+    a->count = (int32_t*)w;
+    a->list = (int32_t*)(w + 256);
+    a->src = (int32_t*)(w + 256 + list);
+    a->dst = (int32_t*)(w + 256 + list + pair);
+    a->map = (int32_t*)(w + 256 + list + 2 * pair);
+  }
+  return 256 + list + 2 * pair + map;
+}
+
+template <class... A>
+cudaError_t launch_cluster(void (*kernel)(A...), cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kBlocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kBlocks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// most: pairs at most (the grid); n_dev: their number on the device, or null.
+cudaError_t launch_copy(const int8kv_pool* p, const int32_t* src, const int32_t* dst, int most,
+                        const int32_t* n_dev, cudaStream_t stream) {
+  Regions r;
+  void* base[4] = {p->k_store, p->v_store, p->k_scales, p->v_scales};
+  int sum = 0;
+  for (int k = 0; k < 4; ++k) {
+    size_t bytes = 0;
+    int8kv_pool_region_bytes(1, p->n_kv_heads, p->head_dim, p->group_size, p->page_size, 1,
+                             p->variant, k, &bytes);
+    if (bytes > 0x7fffffff) return cudaErrorNotSupported;
+    r.base[k] = (char*)base[k];
+    r.bytes[k] = (unsigned)bytes;
+    sum += (int)((bytes + kChunk - 1) / kChunk);
+    r.chunks[k] = sum;
+  }
+  r.n_layers = p->n_layers;
+  r.n_pages = p->n_pages;
+  r.err = p->dev_error;
+  const long long total = (long long)most * p->n_layers * sum, full = 8LL * p->num_sms;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(total < full ? total : full));
+  cfg.blockDim = dim3(kCopyThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, copy_pages_kernel, r, src, dst, most, n_dev);
+}
+
+// The checks that the bookkeeping calls share, and their kernels' arguments.
+int prepare(const int8kv_pool* pool, const int32_t* refs, const int32_t* table, int n_seqs,
+            int max_pages, void* ws, size_t ws_bytes, PagesArgs* a) {
+  if (!pool) return INT8KV_ERR_NULL_PTR;
+  if (n_seqs < 0 || max_pages <= 0) return INT8KV_ERR_INVALID_ARG;
+  if (!refs || (n_seqs > 0 && !table)) return INT8KV_ERR_NULL_PTR;
+  if (!ws || ws_bytes < workspace(pool, n_seqs, nullptr, nullptr)) return INT8KV_ERR_WORKSPACE;
+  if (((uintptr_t)ws & 15) != 0) return INT8KV_ERR_ALIGNMENT;
+  a->refs = const_cast<int32_t*>(refs);
+  a->table = const_cast<int32_t*>(table);
+  a->n_seqs = n_seqs;
+  a->max_pages = max_pages;
+  a->n_pages = pool->n_pages;
+  a->page_size = pool->page_size;
+  a->err = pool->dev_error;
+  workspace(pool, n_seqs, a, ws);
+  return INT8KV_OK;
+}
+
+int status(cudaError_t e) {
+  if (e == cudaErrorNotSupported) return INT8KV_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? INT8KV_OK : INT8KV_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace int8kv
+
+using namespace int8kv;
+
+extern "C" {
+
+int kv_pages_workspace_bytes(const int8kv_pool* pool, int n_seqs, size_t* out_bytes) {
+  if (!pool || !out_bytes) return INT8KV_ERR_NULL_PTR;
+  if (n_seqs < 0) return INT8KV_ERR_INVALID_ARG;
+  *out_bytes = workspace(pool, n_seqs, nullptr, nullptr);
+  return INT8KV_OK;
+}
+
+int kv_pages_copy(const int8kv_pool* pool, int n, const int32_t* src, const int32_t* dst,
+                  void* stream) {
+  if (!pool) return INT8KV_ERR_NULL_PTR;
+  if (n < 0) return INT8KV_ERR_INVALID_ARG;
+  if (n == 0) return INT8KV_OK;
+  if (!src || !dst) return INT8KV_ERR_NULL_PTR;
+  return status(launch_copy(pool, src, dst, n, nullptr, (cudaStream_t)stream));
+}
+
+int kv_pages_resize(const int8kv_pool* pool, int32_t* page_refs, int32_t* page_table, int n_seqs,
+                    int max_pages_per_seq, const int32_t* seq_lens, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  PagesArgs a;
+  const int st = prepare(pool, page_refs, page_table, n_seqs, max_pages_per_seq, workspace,
+                         workspace_bytes, &a);
+  if (st != INT8KV_OK) return st;
+  if (n_seqs == 0) return INT8KV_OK;
+  if (!seq_lens) return INT8KV_ERR_NULL_PTR;
+  return status(launch_cluster(resize_kernel, (cudaStream_t)stream, (const PagesArgs)a, seq_lens));
+}
+
+int kv_pages_fork(const int8kv_pool* pool, int32_t* page_refs, int32_t* page_table, int n_seqs,
+                  int max_pages_per_seq, int32_t* seq_lens, int n_forks, const int32_t* parents,
+                  const int32_t* children, void* workspace, size_t workspace_bytes, void* stream) {
+  PagesArgs a;
+  const int st = prepare(pool, page_refs, page_table, n_seqs, max_pages_per_seq, workspace,
+                         workspace_bytes, &a);
+  if (st != INT8KV_OK) return st;
+  if (n_forks < 0 || n_forks > n_seqs) return INT8KV_ERR_INVALID_ARG;
+  if (n_forks == 0) return INT8KV_OK;
+  if (!seq_lens || !parents || !children) return INT8KV_ERR_NULL_PTR;
+  const cudaStream_t s = (cudaStream_t)stream;
+  const cudaError_t e = launch_cluster(fork_kernel, s, (const PagesArgs)a, seq_lens, n_forks,
+                                       parents, children);
+  if (e != cudaSuccess) return status(e);
+  return status(launch_copy(pool, a.src, a.dst, n_forks, nullptr, s));
+}
+
+int kv_pages_compact(const int8kv_pool* pool, const int32_t* page_refs, const int32_t* page_table,
+                     int n_seqs, int max_pages_per_seq, int32_t* page_refs_out,
+                     int32_t* page_table_out, int32_t* n_used, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  PagesArgs a;
+  const int st = prepare(pool, page_refs, page_table, n_seqs, max_pages_per_seq, workspace,
+                         workspace_bytes, &a);
+  if (st != INT8KV_OK) return st;
+  if (!page_refs_out || (n_seqs > 0 && !page_table_out) || !n_used) return INT8KV_ERR_NULL_PTR;
+  const cudaStream_t s = (cudaStream_t)stream;
+  const cudaError_t e = launch_cluster(compact_kernel, s, (const PagesArgs)a, page_refs_out,
+                                       page_table_out, n_used);
+  if (e != cudaSuccess) return status(e);
+  return status(launch_copy(pool, a.src, a.dst, pool->n_pages / 2 + 1, a.count, s));
+}
+
+}  // extern "C"

@@ -1,0 +1,389 @@
+"""Block-scaled pools on the GPU: append bit for bit, attention against fp64."""
+
+import numpy as np
+import pytest
+import torch
+
+from int8_kv_cache_02_gb300 import inputs
+from tests import block_util as bu
+
+pytestmark = pytest.mark.gpu
+
+KINDS = ["int8", "e4m3"]
+
+
+def _rows(gen, n_seqs, n_new, Hkv, D, outliers=False):
+    k = torch.randn((n_seqs, n_new, Hkv, D), generator=gen)
+    if outliers:
+        k[..., :4] *= 20
+    return k.half(), torch.randn((n_seqs, n_new, Hkv, D), generator=gen).half()
+
+
+# ---- append ----------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,Hkv,gs,ps", [(64, 3, 16, 16), (64, 1, 16, 128), (128, 2, 64, 64),
+                                         (256, 2, 32, 64), (256, 1, 128, 128), (128, 1, 16, 32)])
+def test_append_is_bit_exact(kind, D, Hkv, gs, ps):
+    """Prompts of ragged lengths, then single tokens, then a chunk behind an odd position."""
+    g = torch.Generator().manual_seed(D + gs)
+    lens = [1, gs - 1, 2 * gs + 3]
+    room = [n + 3 * gs + 12 for n in lens]
+    pt, n_pages = inputs.page_table(room, ps, seed=1)
+    dev, orc = bu.make_pools(kind, Hkv, D, gs, ps, n_pages)
+    for b, n in enumerate(lens):
+        k, v = _rows(g, 1, n, Hkv, D, outliers=True)
+        bu.append(dev, orc, 0, k, v, [0], pt[b:b + 1])
+    bu.assert_same(dev, orc, "prompts")
+    pos = list(lens)
+    for step in range(6):         # magnitudes that rise make blocks grow, one of them steeply
+        k, v = _rows(g, 3, 1, Hkv, D)
+        k, v = (k * 2.0 ** step).half(), (v * 9.0 ** (step == 3)).half()
+        bu.append(dev, orc, 0, k, v, pos, pt)
+        pos = [p + 1 for p in pos]
+        bu.assert_same(dev, orc, f"step {step}")
+    k, v = _rows(g, 3, 3 * gs + 1, Hkv, D)
+    bu.append(dev, orc, 0, (300 * k).half(), v, pos, pt)
+    bu.assert_same(dev, orc, "chunk")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n_new", [1, 2, 5, 17, 64])
+def test_append_sizes(kind, n_new):
+    """Every launch shape of the kernel, in the second layer, at even and odd positions."""
+    g = torch.Generator().manual_seed(n_new)
+    pos = [0, 7, 64, 100]
+    for D in (64, 128, 256):
+        pt, n_pages = inputs.page_table([p + n_new for p in pos], 64, seed=2)
+        dev, orc = bu.make_pools(kind, 2, D, 64, 64, n_pages, n_layers=2)
+        for b, p in enumerate(pos):
+            if p:
+                bu.append(dev, orc, 1, *_rows(g, 1, p, 2, D), [0], pt[b:b + 1])
+        bu.append(dev, orc, 1, *_rows(g, 4, n_new, 2, D, outliers=True), pos, pt)
+        bu.assert_same(dev, orc, f"D {D}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_append_rounds_ties_and_extremes_like_the_oracle(kind):
+    """Quotients at and next to the codes' rounding boundaries; the largest and the smallest
+    fp16 values; zeros."""
+    D, gs = 256, 16
+    q = 127.0 if kind == "int8" else 448.0
+    if kind == "int8":
+        y = np.arange(D) - 128 + 0.5                                  # half-integers
+    else:
+        t = np.sort(bu.oblock._POS)
+        y = np.resize((t[1:] + t[:-1]) / 2, D)                        # midpoints of codes
+    rows = []
+    for s in (1.0, 0.25, 0.0078125):
+        x = (y * s).astype(np.float16)
+        x[0] = q * s                                                  # the scale is s exactly
+        bits = x.view(np.int16)
+        rows += [x, (bits + 1).view(np.float16), (bits - 1).view(np.float16)]
+        rows[-1][0] = rows[-2][0] = q * s
+    tiny = np.zeros(D, np.float16)
+    tiny[:3] = [6e-8, -6e-8, 1.2e-7]
+    rows += [tiny, np.full(D, 65504, np.float16), -np.full(D, 65504, np.float16),
+             np.zeros(D, np.float16)]
+    x = torch.tensor(np.stack(rows)).reshape(1, len(rows), 1, D)
+    pt = torch.arange(len(rows), dtype=torch.int32).reshape(1, -1)
+    dev, orc = bu.make_pools(kind, 1, D, gs, 16, len(rows))
+    for i in range(len(rows)):                                        # a block for each row
+        bu.append(dev, orc, 0, x[:, i:i + 1], x[:, i:i + 1].flip(3).contiguous(), [16 * i], pt)
+    bu.assert_same(dev, orc)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_append_leaves_everything_else_alone(kind):
+    from int8_kv_cache_02_gb300 import binding as b
+    g = torch.Generator().manual_seed(3)
+    dev, orc = bu.make_pools(kind, 2, 64, 16, 32, 6)
+    for t in (dev.k_store, dev.v_store, orc.k_store, orc.v_store):
+        (t.view(torch.uint8) if isinstance(t, torch.Tensor) else t.view(np.uint8))[...] = 0x35
+    for t in (dev.k_scales, dev.v_scales, orc.k_scales, orc.v_scales):
+        t[...] = 0.5
+    pt = torch.tensor([[4, 1, -1], [0, 9, 2]], dtype=torch.int32)
+    bu.append(dev, orc, 0, *_rows(g, 2, 20, 2, 64), [5, 0], pt)
+    bu.assert_same(dev, orc)
+    assert b.kv_pool_read_device_error(dev) == 0
+    # a page that is not there, one beyond the pool, positions beyond the row and below 0
+    bu.append(dev, orc, 0, *_rows(g, 2, 70, 2, 64), [40, 10], pt)
+    bu.assert_same(dev, orc)
+    assert b.kv_pool_read_device_error(dev) == b.DEVERR_PAGE_ID | b.DEVERR_LENGTH
+    bu.append(dev, orc, 0, *_rows(g, 2, 4, 2, 64), [-2, 2 ** 31 - 2], pt)
+    bu.assert_same(dev, orc)
+    assert b.kv_pool_read_device_error(dev) == b.DEVERR_LENGTH
+
+
+# ---- decode ----------------------------------------------------------------
+
+def _filled(kind, seed, lens, Hkv, G, D, gs, ps, Q=1, outliers=False):
+    g = torch.Generator().manual_seed(seed)
+    pt, n_pages = inputs.page_table(lens, ps, seed=seed)
+    dev, orc = bu.make_pools(kind, Hkv, D, gs, ps, n_pages)
+    for b, n in enumerate(lens):
+        if n:
+            bu.append(dev, orc, 0, *_rows(g, 1, n, Hkv, D, outliers), [0], pt[b:b + 1])
+    return torch.randn((len(lens), Q, Hkv * G, D), generator=g).half(), pt, dev, orc
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,Hkv,G,gs,ps", [(64, 2, 4, 16, 16), (64, 1, 8, 32, 128),
+                                           (128, 2, 8, 64, 64), (128, 3, 1, 16, 32),
+                                           (256, 2, 8, 64, 64), (256, 1, 3, 128, 128)])
+def test_decode_against_fp64(kind, D, Hkv, G, gs, ps):
+    from int8_kv_cache_02_gb300 import binding as b
+    lens = [0, 1, 15, 16, 17, 63, 64, 65, 257, 700]
+    q, pt, dev, orc = _filled(kind, D + G, lens, Hkv, G, D, gs, ps)
+    ref = bu.reference(orc, 0, q, lens, pt)
+    for n_splits in (0, 1, 2, 5, 33):
+        out = bu.decode(dev, 0, q, lens, pt, n_splits=n_splits)
+        bu.assert_close(out, ref, what=f"splits {n_splits}")
+    assert b.kv_pool_read_device_error(dev) == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("window", [1, 2, 16, 17, 100, 5000])
+def test_decode_windows(kind, window):
+    lens = [0, 1, 16, 130, 1003]
+    q, pt, dev, orc = _filled(kind, window, lens, 2, 4, 128, 32, 64)
+    ref = bu.reference(orc, 0, q, lens, pt, window)
+    free = pt.clone()        # pages behind the window may be gone
+    for b, n in enumerate(lens):
+        free[b, :max(0, n - window) // 64] = -1
+    for n_splits in (0, 1, 7):
+        bu.assert_close(bu.decode(dev, 0, q, lens, free, window, n_splits), ref)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,Hkv,G,Q", [(64, 2, 4, 2), (128, 2, 3, 3), (128, 1, 8, 5),
+                                       (256, 2, 8, 2), (64, 1, 1, 64), (256, 1, 5, 7)])
+def test_query_windows(kind, D, Hkv, G, Q):
+    lens = [0, 1, Q, 70, 403]        # queries at negative positions get zero rows
+    q, pt, dev, orc = _filled(kind, D + Q, lens, Hkv, G, D, 16, 32, Q)
+    ref = bu.reference(orc, 0, q, lens, pt)
+    for n_splits in (0, 1, 2, 9):
+        bu.assert_close(bu.decode(dev, 0, q, lens, pt, n_splits=n_splits), ref,
+                        what=f"splits {n_splits}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_decode_outliers_and_large_scores(kind):
+    """Four K channels of 20 times the others' size: scores up to about 100 in base 2."""
+    lens = [777, 64]
+    q, pt, dev, orc = _filled(kind, 5, lens, 2, 8, 256, 64, 64, outliers=True)
+    ref = bu.reference(orc, 0, q, lens, pt)
+    bu.assert_close(bu.decode(dev, 0, q, lens, pt), ref, z_max=128)
+    assert np.abs(bu.decode(dev, 0, q, lens, pt, scale=0.0) - ref).max() < 2e-3
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rising", [True, False])
+def test_decode_v_scales_of_any_range(kind, rising):
+    """V magnitudes over 2^24 along the sequence, and a query that attends the small ones."""
+    D, ps, n = 128, 16, 16 * 25
+    g = torch.Generator().manual_seed(8)
+    k, v = _rows(g, 1, n, 1, D)
+    size = 2.0 ** -torch.arange(25).repeat_interleave(16).float()
+    size = size.flip(0) if rising else size
+    v = (v.float() * 64 * size[None, :, None, None]).half()
+    small = size < 2.0 ** -12
+    k[:, :, 0, 0] = torch.where(small, 9.0, -9.0).half()[None]
+    q = torch.randn((1, 1, 4, D), generator=g).half()
+    q[..., 0] = 24.0                         # scores of the small blocks win by 2^50
+    pt, n_pages = inputs.page_table([n], ps, seed=8)
+    dev, orc = bu.make_pools(kind, 1, D, 16, ps, n_pages)
+    bu.append(dev, orc, 0, k, v, [0], pt)
+    ref = bu.reference(orc, 0, q, [n], pt)
+    for n_splits in (0, 1, 3):
+        bu.assert_close(bu.decode(dev, 0, q, [n], pt, n_splits=n_splits), ref, z_max=64)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_decode_ignores_what_lies_behind_the_sequence(kind):
+    """NaN codes, NaN and infinite scales in rows and blocks that are not attended."""
+    lens = [37, 64, 5]
+    q, pt, dev, orc = _filled(kind, 9, lens, 2, 4, 64, 16, 64)
+    ref = bu.reference(orc, 0, q, lens, pt)
+    for b, n in enumerate(lens):
+        for t in (dev.k_store, dev.v_store):
+            t.view(torch.uint8)[0, int(pt[b, 0]), :, n:] = 0x7F
+        for t, x in ((dev.k_scales, float("nan")), (dev.v_scales, float("inf"))):
+            t[0, int(pt[b, 0]), :, -(-n // 16):] = x
+    for n_splits in (0, 1, 4):
+        bu.assert_close(bu.decode(dev, 0, q, lens, pt, n_splits=n_splits), ref)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_zero_values_and_one_zero_block(kind):
+    lens = [40]
+    g = torch.Generator().manual_seed(10)
+    k, v = _rows(g, 1, 40, 1, 64)
+    v[:, :16] = 0
+    k[:, 16:32] = 0
+    pt, n_pages = inputs.page_table(lens, 16, seed=1)
+    dev, orc = bu.make_pools(kind, 1, 64, 16, 16, n_pages)
+    q = torch.randn((1, 1, 8, 64), generator=g).half()
+    bu.append(dev, orc, 0, k, v, [0], pt)
+    bu.assert_close(bu.decode(dev, 0, q, lens, pt), bu.reference(orc, 0, q, lens, pt))
+    bu.append(dev, orc, 0, k, 0 * v, [0], pt)
+    assert not bu.decode(dev, 0, q, lens, pt).any()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_bad_pages_and_lengths_are_flagged_and_left_out(kind):
+    from int8_kv_cache_02_gb300 import binding as b
+    lens = [64, 64]
+    q, pt, dev, orc = _filled(kind, 11, lens, 1, 2, 64, 16, 32)
+    bad = pt.clone()
+    bad[0, 1], bad[1, 0] = -1, 10 ** 6
+    out = bu.decode(dev, 0, q, lens, bad)
+    assert b.kv_pool_read_device_error(dev) == b.DEVERR_PAGE_ID
+    bu.assert_close(out[:1], bu.reference(orc, 0, q[:1], [32], pt))
+    kh, vh = orc.gather(0, pt[1].numpy(), 64)
+    bu.assert_close(out[1, 0], bu.oatt.decode(q[1, 0].numpy(), kh[32:], vh[32:], 32))
+    out = bu.decode(dev, 0, q, [10 ** 9, -5], pt)
+    assert b.kv_pool_read_device_error(dev) == b.DEVERR_LENGTH
+    bu.assert_close(out[:1], bu.reference(orc, 0, q[:1], [64], pt))
+    assert not out[1].any()
+
+
+def test_long_ragged_batches_against_fp64_on_the_device():
+    """Up to 40,000 positions: many shares per unit and many units per share."""
+    from int8_kv_cache_02_gb300 import binding as b
+    for kind, D, Hkv, G, lens in (("e4m3", 128, 4, 2, [40000, 3, 0, 12345, 1, 7777]),
+                                  ("int8", 256, 1, 8, [33333]),
+                                  ("int8", 64, 2, 5, [100] * 300 + [20000])):
+        g = torch.Generator().manual_seed(len(lens))
+        pt, n_pages = inputs.page_table(lens, 64, seed=4)
+        dev, _ = bu.make_pools(kind, Hkv, D, 64, 64, n_pages)
+        c = torch.randint(-127, 127, dev.k_store.shape, generator=g).to(torch.int8)
+        if kind == "e4m3":
+            c = c.view(torch.uint8).clamp(max=0x70).view(torch.int8)
+        for t in (dev.k_store, dev.v_store):
+            t.view(torch.int8).copy_(c)
+            c = c.flip(3)
+        m = 60.0 if kind == "int8" else 40.0
+        dev.k_scales.copy_(torch.rand(dev.k_scales.shape, generator=g) / m)
+        dev.v_scales.copy_(torch.rand(dev.v_scales.shape, generator=g) / m)
+        q = torch.randn((len(lens), 1, Hkv * G, D), generator=g).half()
+        out = torch.from_numpy(bu.decode(dev, 0, q, lens, pt))
+        assert b.kv_pool_read_device_error(dev) == 0
+        ref = torch.zeros(out.shape, dtype=torch.float64)
+        for i, n in enumerate(lens):
+            if n:
+                ids = pt[i, :-(-n // 64)].long().cuda()
+                x = []
+                for t, s in ((dev.k_store, dev.k_scales), (dev.v_store, dev.v_scales)):
+                    y = t.view(torch.uint8)[0][ids].view(t.dtype).float().double()
+                    y = y * s[0][ids].double().repeat_interleave(64, 2)[..., None]
+                    x.append(y.transpose(0, 1).reshape(Hkv, -1, D)[:, :n])
+                z = q[i, 0].double().cuda().reshape(Hkv, G, D) @ x[0].transpose(1, 2) / D ** 0.5
+                ref[i, 0] = (torch.softmax(z, -1) @ x[1]).reshape(-1, D).cpu()
+        bu.assert_close(out.numpy(), ref.numpy(), z_max=64, what=kind)
+
+
+# ---- calls together --------------------------------------------------------
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n_splits", [0, 1, 3])
+def test_fused_append_is_append_then_decode(kind, n_splits):
+    from int8_kv_cache_02_gb300 import binding as b
+    lens = [0, 16, 100, 64]
+    q, pt, dev, orc = _filled(kind, 12, [n + 1 for n in lens], 2, 4, 128, 16, 64)
+    g = torch.Generator().manual_seed(1)
+    k, v = _rows(g, 4, 1, 2, 128, outliers=True)
+    n = torch.tensor([x + 1 for x in lens], dtype=torch.int32, device="cuda")
+    out = torch.full((4, 8, 128), float("nan"), device="cuda")
+    ws = dev.decode_workspace(4, 8, n_splits or 256)
+    b.attn_decode_append_int8(dev, 0, q[:, 0].contiguous().cuda(), k[:, 0].contiguous().cuda(),
+                              v[:, 0].contiguous().cuda(), n, pt.cuda(), out, ws,
+                              n_splits=n_splits)
+    orc.append(0, k.numpy(), v.numpy(), lens, pt.numpy())
+    bu.assert_same(dev, orc)
+    two = bu.decode(dev, 0, q, [x + 1 for x in lens], pt, n_splits=n_splits)
+    assert np.array_equal(out.cpu().numpy(), two[:, 0])
+    bu.assert_close(two, bu.reference(orc, 0, q, [x + 1 for x in lens], pt), z_max=64)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_captured_steps_replay_as_lengths_grow(kind):
+    from int8_kv_cache_02_gb300 import binding as b
+    B, H, Hkv, D, start, steps = 2, 8, 2, 128, [30, 61], 20
+    g = torch.Generator().manual_seed(13)
+    pt, n_pages = inputs.page_table([n + steps for n in start], 32, seed=3)
+    dev, orc = bu.make_pools(kind, Hkv, D, 32, 32, n_pages)
+    for i, n in enumerate(start):
+        bu.append(dev, orc, 0, *_rows(g, 1, n, Hkv, D), [0], pt[i:i + 1])
+    q = torch.zeros((B, H, D), dtype=torch.float16, device="cuda")
+    k, v = (torch.zeros((B, Hkv, D), dtype=torch.float16, device="cuda") for _ in range(2))
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")       # empty while it is captured
+    ptd, out = pt.cuda(), torch.empty((B, H, D), device="cuda")
+    ws = dev.decode_workspace(B, H, 8)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.attn_decode_append_int8(dev, 0, q, k, v, lens, ptd, out, ws, n_splits=8)
+    for s in range(steps):
+        ks, vs = _rows(g, B, 1, Hkv, D, outliers=s == 7)
+        qs = torch.randn((B, 1, H, D), generator=g).half()
+        q.copy_(qs[:, 0])
+        k.copy_(ks[:, 0])
+        v.copy_(vs[:, 0])
+        pos = [n + s for n in start]
+        lens.copy_(torch.tensor([p + 1 for p in pos], dtype=torch.int32))
+        graph.replay()
+        orc.append(0, ks.numpy(), vs.numpy(), pos, pt.numpy())
+        ref = bu.reference(orc, 0, qs, [p + 1 for p in pos], pt)
+        bu.assert_close(out.cpu().numpy(), ref[:, 0], z_max=64)
+    bu.assert_same(dev, orc)
+    assert b.kv_pool_read_device_error(dev) == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_results_do_not_depend_on_the_run_or_the_stream(kind):
+    lens = [5000, 17, 900]
+    q, pt, dev, orc = _filled(kind, 14, lens, 2, 4, 128, 64, 64)
+    one = bu.decode(dev, 0, q, lens, pt)
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(other):
+        two = bu.decode(dev, 0, q, lens, pt)
+    assert np.array_equal(one, two)
+
+
+def test_noalloc_decode_and_refusals():
+    import ctypes
+
+    from int8_kv_cache_02_gb300 import binding as b
+    lens = [900, 31]
+    q, pt, dev, orc = _filled("int8", 15, lens, 2, 4, 128, 32, 64)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out = torch.empty((2, 8, 128), device="cuda")
+    qd, ptd = q[:, 0].contiguous().cuda(), pt.cuda()
+    b.attn_decode_int8_noalloc(dev, 0, qd, n, ptd, out)
+    bu.assert_close(out.cpu().numpy(), bu.reference(orc, 0, q, lens, pt)[:, 0])
+    status = lambda f: pytest.raises(b.Int8KVError, match=f)   # noqa: E731
+    with status("-8"):
+        b.attn_decode_int8(dev, 0, qd, n, ptd, out, None, n_splits=4)
+    with status("-6"):
+        b.kv_pool_set_decode_kernel(dev, b.DECODE_SIMT)
+    with status("-6"):
+        b.kv_pool_set_decode_kernel(dev, b.DECODE_WARP_MMA)
+    b.kv_pool_set_decode_kernel(dev, b.DECODE_AUTO)
+    with status("-6"):
+        b.attn_prefill_chunk_int8(dev, 0, qd, 0, ptd[0], out)
+    with status("-6"):
+        b.attn_prefill_n_splits(dev, 2, 8, 0)
+    with status("-6"):
+        b.kv_pool_save(dev, lens, ptd)
+    with status("-6"):
+        b.kv_pool_load(dev, b"I8KV" + bytes(60), ptd)
+    with status("-6"):
+        b.kv_pool_test_expire_waits(dev, 5)
+    with status("-1"):
+        b.attn_decode_int8(dev, 1, qd, n, ptd, out, None, n_splits=1)
+    with status("-6"):
+        b.attn_decode_int8(dev, 0, torch.zeros((2, 18, 128), dtype=torch.float16, device="cuda"),
+                           n, ptd, torch.empty((2, 18, 128), device="cuda"), None, n_splits=1)
+    assert b.lib().kv_quant_append(dev.handle, 0, ctypes.c_void_p(8), ctypes.c_void_p(16), 1, 1,
+                                   ctypes.c_void_p(16), ctypes.c_void_p(16), 1, None) == -3
