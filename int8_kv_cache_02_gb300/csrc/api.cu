@@ -192,7 +192,8 @@ int decode_splits_heuristic(const int8kv_pool* pool, long long units, int max_ct
 // of one tile per warp is left to one block per unit: it needs no combine.
 static int block_splits(const int8kv_pool* pool, long long units, int max_ctx) {
   if (max_ctx <= kBlockSingle) return 1;
-  const long long n = (pool->block_resident - 1 + units - 1) / units + 1;
+  // (query windows may take 16 columns to a unit: up to twice the splits per unit)
+  const long long n = (pool->head_dim <= 128 ? 2 : 1) * ((pool->block_resident + units - 2) / units) + 1;
   return (int)(n < 2 ? 2 : n > kMaxSplits ? kMaxSplits : n);
 }
 
@@ -508,9 +509,10 @@ static int decode_entry(const int8kv_pool* pool, int layer, const uint16_t* q,
     d.Q = q_len;
     d.max_pages = max_pages_per_seq;
     d.window = window;
-    d.n_cg = n_cg;
-    d.width = (q_len * G + n_cg - 1) / n_cg;
-    d.shares = block_shares(pool, (long long)batch * pool->n_kv_heads * n_cg, d.width,
+    const int cols = q_len * G, per = pool->head_dim <= 128 && cols > 8 ? 16 : 8;
+    d.n_cg = (cols + per - 1) / per;
+    d.width = (cols + d.n_cg - 1) / d.n_cg;
+    d.shares = block_shares(pool, (long long)batch * pool->n_kv_heads * d.n_cg, d.width,
                             (long long)batch * q_len * n_heads * n_splits, n_splits);
     d.scale_log2 = scale * 1.4426950408889634f;
     return launch_status(launch_block_decode(d, pool->head_dim, pool->f8, s));

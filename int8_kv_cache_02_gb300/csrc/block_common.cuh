@@ -94,10 +94,19 @@ __device__ __forceinline__ uint32_t codes_to_h2(uint32_t x) {
   }
 }
 
-// The pair behind the one that codes_to_h2 takes from the same word.
+// The pair behind the one that codes_to_h2 takes from the same word: int8 bytes 1 and 3, e4m3 the
+// two high bytes.
 template <bool F8>
-__device__ __forceinline__ uint32_t codes_behind(uint32_t x) {
-  return F8 ? x >> 16 : x >> 8;
+__device__ __forceinline__ uint32_t codes_behind_to_h2(uint32_t x) {
+  if constexpr (F8) {
+    uint32_t h;
+    asm("{ .reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, u;\n\t}"
+        : "=r"(h)
+        : "r"(x));
+    return h;
+  } else {
+    return codes_to_h2<F8>(x >> 8);
+  }
 }
 
 // Two words as words of pairs: the first and second byte of a beside those of b
@@ -130,7 +139,7 @@ __device__ __forceinline__ uint32_t round_codes(const float (&y)[4]) {
 // Four code bytes as fp32 values in units of the scale.
 template <bool F8>
 __device__ __forceinline__ void code_values(uint32_t w, float (&y)[4]) {
-  const uint32_t a = codes_to_h2<F8>(w), b = codes_to_h2<F8>(codes_behind<F8>(w));
+  const uint32_t a = codes_to_h2<F8>(w), b = codes_behind_to_h2<F8>(w);
   const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
   const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&b));
   y[0] = fa.x;

@@ -1,0 +1,701 @@
+// The decode kernel over block-scaled pools (one fp32 scale per T positions and kv
+// head; int8 or e4m3 codes), for the translation units that instantiate it.
+//
+//   z_i = (q . ck_i) sk(block of i) scale,  o = sum_i 2^(z_i) sv(block of i) cv_i / sum_i 2^(z_i)
+// in base-2 exponents, ck and cv the codes: a scale multiplies 16 scores at once
+// instead of every row's, so dequantizing is a bare conversion of codes to fp16,
+// which is exact.
+//
+// Tiles of 16 positions (T and the page size are multiples of 16, so a tile has
+// one page and one scale of each store).  A warp owns its tiles alone:
+//   S^T[16 x 8] = K[16 x D] q^T[D x 8]            mma.sync m16n8k16, heads on N
+//   O^T[D x 8] += V^T[D x 16] W^T[16 x 8]         W = 2^(z - M) sv, as fp16 hi + lo
+// A tile's rows are contiguous in the pool; the warp copies them with cp.async, whole
+// 128-byte lines at a time, into a ring of its own (no barrier but the warp's), with
+// zeros in place of rows outside the context.  (Lanes that fetched just the 64 bytes of
+// a row that they use read HBM at 5.5 TB/s, whole lines at 7.4: requests of half a line
+// halve what the L2 can ask for.)  The D index of the first product, the row order of
+// the second and the order of a tile's positions are permuted, and 16-byte pieces
+// swizzled, so that an operand is a 16-byte shared-memory load without bank conflicts
+// (D = 64: V two-way).
+//
+// Two references per head: m for the softmax sum and M for the weights times their
+// V scales, both the running maximum of what they scale (moved only when exceeded by
+// 2^8), so the fp16 pair of W keeps ~22 bits of the largest weight whatever
+// the scales' range.
+//
+// A column is a (query, head) pair of the kv head.  With at most four of them
+// (kPair) columns 4 - 7 hold the same queries again: there W is the lo part, and one
+// product brings both (the halves are added at the end).  More than eight take two
+// groups of columns per pass where the registers hold them (NC = 2, D <= 128), so
+// that a page is read and converted once for 16 columns.
+//
+// Schedule: all tiles of all (sequence, kv head, column group) units in one line,
+// cut into equal shares, one per resident block (a.shares); a unit that a share
+// boundary cuts leaves partials, numbered unit + share, which the combine kernel
+// joins.  With a.shares = 0 every block takes one whole unit and writes it out.
+//
+// Bound by HBM: 2 D bytes per position and kv head.
+#pragma once
+
+#include "block_common.cuh"
+#include "decode_common.cuh"
+
+namespace int8kv {
+namespace block {
+
+constexpr int kTile = 16;
+constexpr float kUnset = -1e30f;      // reference of a head that has seen nothing
+constexpr float kLazy = 8.f;          // a reference moves when exceeded by 2^8
+constexpr float kWeightShift = 6.f;   // W is scaled by 2^6: at most 2^14 in fp16
+
+template <int D>
+struct Shape {
+  static constexpr int NW = 4;                        // warps per block
+  static constexpr int TPI = 256 / D;                 // tiles a warp takes at a time
+  static constexpr int NS = D == 256 ? 3 : 3;         // ring stages per warp
+  static constexpr int BLOCKS = 2;                    // per SM
+  static constexpr int LEAST = NW * TPI * (NS - 1);   // tiles of a share at least: its rings' first fill
+  static constexpr int KP = D / 64;                   // 16-byte K pieces per lane and row
+  static constexpr int ROWS = kTile * D;              // bytes of a tile's K rows, or V rows
+  static constexpr int TILE = 2 * ROWS;               // bytes of a tile in the ring: K, then V
+  static constexpr int STAGE = TPI * TILE;
+  static constexpr int RING = NW * NS * STAGE;        // (the warps' outputs are joined over it)
+};
+
+// Variants of the kernel by columns of a unit.
+enum Columns { kPair = 0, kEight = 1, kSixteen = 2 };
+template <int V>
+struct Cols {
+  static constexpr int NC = V == kSixteen ? 2 : 1;
+  static constexpr int N = 8 * NC;                    // columns of the products
+};
+
+template <bool FULL>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool valid) {
+  if constexpr (FULL) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  } else {
+    const int n = valid ? 16 : 0;    // 0: zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+                 : "memory");
+  }
+}
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The positions of sequence b that some query of it attends: [lo, hi).
+__device__ __forceinline__ void unit_range(const BlockDecodeArgs& a, int b, int& lo, int& hi) {
+  hi = block_length(__ldg(a.seq_lens + b), a.max_pages, a.pool);
+  lo = a.window > 0 && hi > a.window ? hi - a.window : 0;
+}
+__device__ __forceinline__ int unit_tiles(int lo, int hi) {
+  return hi > lo ? (hi - 1) / kTile - lo / kTile + 1 : 0;
+}
+
+// Tiles of the whole batch.  Every thread sums a run of sequences; `mine` is the
+// number of tiles before its run.
+template <int NT>
+__device__ __forceinline__ long long batch_tiles(const BlockDecodeArgs& a, int per_seq,
+                                                 long long* warp_sums, long long& mine) {
+  const int run = (a.B + NT - 1) / NT;
+  long long sum = 0;
+  for (int i = 0; i < run; ++i) {
+    const int b = threadIdx.x * run + i;
+    if (b >= a.B) break;
+    int lo, hi;
+    unit_range(a, b, lo, hi);
+    sum += (long long)unit_tiles(lo, hi) * per_seq;
+  }
+  long long inc = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, inc, off);
+    if ((threadIdx.x & 31) >= off) inc += o;
+  }
+  if ((threadIdx.x & 31) == 31) warp_sums[threadIdx.x >> 5] = inc;
+  __syncthreads();
+  long long total = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < (int)(threadIdx.x >> 5)) before += warp_sums[w];
+    total += warp_sums[w];
+  }
+  mine = before + inc - sum;
+  return total;
+}
+
+__device__ __forceinline__ long long share_tiles(long long total, int shares, int least) {
+  const long long per = (total + shares - 1) / shares;
+  return per > least ? per : least;
+}
+
+// ---- one warp's tiles -------------------------------------------------------
+template <int D, int V>
+struct Warp {
+  static constexpr int NC = Cols<V>::NC;
+  float acc[NC][D / 16][4];    // O^T: rows in out_dim's order, columns 2t, 2t + 1
+  float m[NC][2], M[NC][2], l[NC][2];
+  uint32_t q[NC][D / 8];       // q^T fragments
+
+  __device__ __forceinline__ void reset() {
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j)
+        acc[n][j][0] = acc[n][j][1] = acc[n][j][2] = acc[n][j][3] = 0.f;
+      m[n][0] = m[n][1] = M[n][0] = M[n][1] = kUnset;
+      l[n][0] = l[n][1] = 0.f;
+    }
+  }
+};
+
+// A tile in shared memory: rows of D bytes, the 16-byte pieces of row r permuted by an
+// xor with bits of r so that the loads below meet no bank twice.
+template <int D>
+__device__ __forceinline__ int piece(int r, int c) {
+  return r * D + ((D == 64 ? c ^ (r >> 1 & 3) : c ^ (r & 7)) << 4);
+}
+
+// Position of a tile that row x of the fragments stands for (x and x + 8 alike): rows
+// 2i and 2i + 1 differ in bits 0 and 2 of it, which the K loads need, and the even (odd)
+// rows take all values of bits 1 and 2, which the V loads need.
+__device__ __forceinline__ int position_of(int x) { return x ^ ((x & 1) << 2); }
+
+// What of a tile a lane copies and loads: byte offsets within K or V rows.
+template <int D>
+struct Lane {
+  uint32_t to;        // its first copied piece
+  uint32_t k;         // row g, piece t
+  uint32_t v[2];      // rows 2t and 2t + 1, its piece (D = 64: half a piece)
+  __device__ __forceinline__ Lane(int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    to = piece<D>(lane * 16 / D, lane * 16 % D / 16);
+    k = piece<D>(position_of(g), t);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+      v[n] = D == 64 ? piece<D>(position_of(2 * t + n), g >> 1) + 8 * (g & 1)
+                     : piece<D>(position_of(2 * t + n), g);
+  }
+};
+
+// Issue the copies of one tile from its rows at k and v (at the lane's 16 bytes):
+// zeros for rows outside [a, z).  Copy i takes bytes 512 i + 16 lane of the rows.
+template <int D, bool FULL>
+__device__ __forceinline__ void copy_tile(const uint8_t* k, const uint8_t* v, uint32_t tile,
+                                          const Lane<D>& ln, int a, int z, int lane) {
+  using S = Shape<D>;
+#pragma unroll
+  for (int i = 0; i < S::ROWS / 512; ++i) {
+    const int r = (512 * i + 16 * lane) / D;
+    const bool ok = r >= a && r < z;
+    // rows 512 i / D further: their low bits flip bits of the piece
+    const uint32_t to = 512 * i + (D == 64 ? ln.to : ln.to ^ ((512 * i / D & 7) << 4));
+    copy_async<FULL>(tile + to, k + 512 * i, ok);
+    copy_async<FULL>(tile + S::ROWS + to, v + 512 * i, ok);
+  }
+}
+
+// The lane's words of its four V tokens and 16 values (D = 64: 8), of O^T rows g (a) and
+// g + 8 (b); h: which 128 of D = 256.
+template <int D>
+__device__ __forceinline__ void v_words(uint32_t tile, const Lane<D>& ln, int h,
+                                        uint32_t (&a)[4][2], uint32_t (&b)[4][2]) {
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const uint32_t at = tile + Shape<D>::ROWS + ln.v[n & 1] + (n >> 1) * 8 * D + h * 128;
+    if constexpr (D == 64) {
+      const uint2 x = ptx::lds64(at);
+      a[n][0] = x.x;
+      b[n][0] = x.y;
+    } else {
+      const uint4 x = ptx::lds128(at);
+      a[n][0] = x.x;
+      a[n][1] = x.y;
+      b[n][0] = x.z;
+      b[n][1] = x.w;
+    }
+  }
+}
+
+// S^T of one tile: z[n][2r + c] is row g + 8r, column 2t + c of group n.
+template <int D, bool F8, int V>
+__device__ __forceinline__ void score_tile(const Warp<D, V>& w, uint32_t tile, const Lane<D>& ln,
+                                           float (&z)[Cols<V>::NC][4]) {
+  using S = Shape<D>;
+  constexpr int NC = Cols<V>::NC;
+  float s[2][NC][4] = {};
+#pragma unroll
+  for (int c = 0; c < S::KP; ++c) {
+    // piece 4c + t of rows g and g + 8
+    const uint32_t at = tile + (ln.k ^ ((c & 1) << 6)) + (c >> 1) * 128;
+    const uint4 x = ptx::lds128(at), y = ptx::lds128(at + 8 * D);
+    const uint32_t* xw = reinterpret_cast<const uint32_t*>(&x);
+    const uint32_t* yw = reinterpret_cast<const uint32_t*>(&y);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t a[4] = {codes_to_h2<F8>(xw[u]), codes_to_h2<F8>(yw[u]),
+                             codes_behind_to_h2<F8>(xw[u]), codes_behind_to_h2<F8>(yw[u])};
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+        ptx::mma_f16(s[u & 1][n], a, w.q[n][8 * c + 2 * u], w.q[n][8 * c + 2 * u + 1]);
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NC; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z[n][i] = s[0][n][i] + s[1][n][i];
+}
+
+// The TPI tiles of one stage.  f: K scale * softmax scale * log2(e) of each tile; lv: log2 of
+// its V scale; lim: last position that each column attends; masked: whether lim, lo
+// or a tile that is not there (bit i of `none`) cut the stage.
+template <int D, bool F8, int V>
+__device__ __forceinline__ void take_stage(Warp<D, V>& w, uint32_t stage, int pos,
+                                           const float (&f)[Shape<D>::TPI],
+                                           const float (&lv)[Shape<D>::TPI], bool masked,
+                                           uint32_t none, int lo, const int (&lim)[Cols<V>::NC][2],
+                                           const Lane<D>& ln, int g, int t) {
+  using S = Shape<D>;
+  constexpr int NC = Cols<V>::NC, TPI = S::TPI;
+  float z[TPI][NC][4];
+  float top[NC][2], topM[NC][2];
+#pragma unroll
+  for (int i = 0; i < TPI; ++i) {
+    score_tile<D, F8, V>(w, stage + i * S::TILE, ln, z[i]);
+#pragma unroll
+    for (int n = 0; n < NC; ++n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) z[i][n][k] *= f[i];
+  }
+  if (masked) {
+#pragma unroll
+    for (int i = 0; i < TPI; ++i)
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int at = pos + i * kTile + position_of(g) + 8 * (k >> 1);
+          if (at < lo || at > lim[n][k & 1] || (none >> i & 1)) z[i][n][k] = -INFINITY;
+        }
+  }
+  bool over = false;
+#pragma unroll
+  for (int n = 0; n < NC; ++n)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int i = 0; i < TPI; ++i) {
+        const float x = fmaxf(z[i][n][c], z[i][n][2 + c]);
+        top[n][c] = i ? fmaxf(top[n][c], x) : x;
+        topM[n][c] = i ? fmaxf(topM[n][c], x + lv[i]) : x + lv[i];
+      }
+      over |= top[n][c] > w.m[n][c] + kLazy || topM[n][c] > w.M[n][c] + kLazy;
+    }
+  if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+      float r[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float x = top[n][c], y = topM[n][c];
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
+        }
+        const float nm = fmaxf(w.m[n][c], x), nM = fmaxf(w.M[n][c], y);
+        w.l[n][c] *= ptx::ex2(w.m[n][c] - nm);
+        r[c] = ptx::ex2(w.M[n][c] - nM);
+        w.m[n][c] = nm;
+        w.M[n][c] = nM;
+      }
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        w.acc[n][j][0] *= r[0];
+        w.acc[n][j][1] *= r[1];
+        w.acc[n][j][2] *= r[0];
+        w.acc[n][j][3] *= r[1];
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < TPI; ++i) {
+    uint32_t hi[NC][2], lw[NC][2];      // W^T fragments, hi and lo parts
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+      float wt[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        w.l[n][k & 1] += ptx::ex2(z[i][n][k] - w.m[n][k & 1]);
+        wt[k] = ptx::ex2(z[i][n][k] + (lv[i] + kWeightShift - w.M[n][k & 1]));
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        uint32_t h = ptx::pack_f16x2(wt[2 * r], wt[2 * r + 1]);
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        const uint32_t o = ptx::pack_f16x2(wt[2 * r] - x.x, wt[2 * r + 1] - x.y);
+        if constexpr (V == kPair) {
+          hi[n][r] = ptx::movmatrix_trans(t < 2 ? h : o);
+        } else {
+          hi[n][r] = ptx::movmatrix_trans(h);
+          lw[n][r] = ptx::movmatrix_trans(o);
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < (D == 256 ? 2 : 1); ++h) {
+      constexpr int N = D == 64 ? 1 : 2;              // words
+      uint32_t a[4][2], b[4][2];
+      v_words<D>(stage + i * S::TILE, ln, h, a, b);
+#pragma unroll
+      for (int x = 0; x < N; ++x) {
+        uint32_t pa[2][2], pb[2][2];      // [k half][first / second pair word]
+#pragma unroll
+        for (int kh = 0; kh < 2; ++kh) {
+          pair_words<F8>(a[2 * kh][x], a[2 * kh + 1][x], pa[kh][0], pa[kh][1]);
+          pair_words<F8>(b[2 * kh][x], b[2 * kh + 1][x], pb[kh][0], pb[kh][1]);
+        }
+        uint32_t fr[4][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int kh = 0; kh < 2; ++kh) {
+            const uint32_t wa = pa[kh][e >> 1], wb = pb[kh][e >> 1];
+            fr[e][2 * kh] = e & 1 ? codes_behind_to_h2<F8>(wa) : codes_to_h2<F8>(wa);
+            fr[e][2 * kh + 1] = e & 1 ? codes_behind_to_h2<F8>(wb) : codes_to_h2<F8>(wb);
+          }
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            ptx::mma_f16(w.acc[n][(h * N + x) * 4 + e], fr[e], hi[n][0], hi[n][1]);
+          if constexpr (V != kPair)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              ptx::mma_f16(w.acc[n][(h * N + x) * 4 + e], fr[e], lw[n][0], lw[n][1]);
+        }
+      }
+    }
+  }
+}
+
+// d index of row (g + 8 r) of O^T tile j.
+template <int D>
+__device__ __forceinline__ int out_dim(int j, int r, int g) {
+  if constexpr (D == 64) return 8 * g + 4 * r + j;
+  return (j >> 3) * 128 + 16 * g + 8 * r + (j & 7);
+}
+
+template <int D, bool F8, int V>
+__global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
+    decode_block_kernel(const BlockDecodeArgs a) {
+  using S = Shape<D>;
+  constexpr int NT = S::NW * 32, NC = Cols<V>::NC, N = Cols<V>::N, TPI = S::TPI;
+  static_assert(S::NW * N * (D + 4) * 4 <= S::RING, "the warps' outputs are joined over the ring");
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ long long warp_sums[S::NW];
+  __shared__ long long place_start;
+  __shared__ int place_b;
+  __shared__ float stat[3][S::NW][N];     // m, M, l of each warp and column
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const uint32_t ring = ptx::smem_u32(smem) + warp * S::NS * S::STAGE;
+  const Lane<D> ln(lane);
+  const BlockView& p = a.pool;
+  const int per_seq = p.Hkv * a.n_cg;      // units of a sequence
+  ptx::grid_launch_dependents();
+  ptx::grid_dependency_wait();
+
+  long long at, end, seq_start;
+  int b;
+  if (a.shares == 0) {
+    b = blockIdx.x / per_seq;
+    int lo, hi;
+    unit_range(a, b, lo, hi);
+    const int nt = unit_tiles(lo, hi), u = blockIdx.x % per_seq;
+    seq_start = 0;
+    at = (long long)u * nt;
+    end = at + nt;
+    if (nt == 0) end = at + 1;    // run the unit's (empty) segment once: zero rows
+  } else {
+    long long mine;
+    const long long total = batch_tiles<NT>(a, per_seq, warp_sums, mine);
+    const long long per = share_tiles(total, a.shares, S::LEAST);
+    at = per * blockIdx.x;
+    end = min(at + per, total);
+    if (at >= end) return;
+    const int run = (a.B + NT - 1) / NT;
+    for (int i = 0; i < run; ++i) {
+      const int s = threadIdx.x * run + i;
+      if (s >= a.B) break;
+      int lo, hi;
+      unit_range(a, s, lo, hi);
+      const long long n = (long long)unit_tiles(lo, hi) * per_seq;
+      if (at >= mine && at < mine + n) {
+        place_b = s;
+        place_start = mine;
+      }
+      mine += n;
+    }
+    __syncthreads();
+    b = place_b;
+    seq_start = place_start;
+  }
+
+  Warp<D, V> w;
+  while (at < end) {
+    int lo, hi;
+    unit_range(a, b, lo, hi);
+    const int nt = unit_tiles(lo, hi);
+    const int u = a.shares == 0 ? blockIdx.x % per_seq : (nt ? (int)((at - seq_start) / nt) : per_seq);
+    if (u >= per_seq) {           // past this sequence's units
+      seq_start += (long long)nt * per_seq;
+      ++b;
+      continue;
+    }
+    const int kvh = u / a.n_cg, cg = u % a.n_cg;
+    const int first = nt ? (int)(at - seq_start - (long long)u * nt) : 0;   // tiles of the unit: [first, last)
+    const int last = (int)min((long long)nt, first + (end - at));
+    const int tile0 = lo / kTile;
+
+    // columns 2t, 2t + 1 of the fragments and the lane's q rows (column g)
+    const int cols = min(a.width, a.G * a.Q - cg * a.width);
+    int lim[NC][2];
+#pragma unroll
+    for (int n = 0; n < NC; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int col = V == kPair ? (2 * t + c) & 3 : 8 * n + 2 * t + c;
+        lim[n][c] = col < cols ? hi - a.Q + (cg * a.width + col) / a.G : -1;
+      }
+    const int least = hi - a.Q + (cg * a.width) / a.G;   // positions <= least: no column masks
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+      const int mine = V == kPair ? g & 3 : 8 * n + g;
+      const int col = cg * a.width + min(mine, cols - 1);
+      const uint16_t* q =
+          a.q + (((size_t)b * a.Q + col / a.G) * a.H + kvh * a.G + col % a.G) * D + 16 * t;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        const uint4 x = ptx::ldg128(q + 64 * c), y = ptx::ldg128(q + 64 * c + 8);
+        const uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {     // values 4k .. 4k + 3 of the lane's 16
+          uint32_t lo2 = v[2 * k], hi2 = v[2 * k + 1];
+          if (mine >= cols) lo2 = hi2 = 0;
+          w.q[n][8 * c + 2 * k] = F8 ? lo2 : ptx::prmt(lo2, hi2, 0x5410);
+          w.q[n][8 * c + 2 * k + 1] = F8 ? hi2 : ptx::prmt(lo2, hi2, 0x7632);
+        }
+      }
+    }
+    w.reset();
+
+    // the warp's stages of the segment: TPI tiles each, from first + TPI * (warp + NW * i)
+    const int mine0 = first + warp * TPI;
+    const int n = last > mine0 ? (last - mine0 + S::NW * TPI - 1) / (S::NW * TPI) : 0;
+    const int32_t* table = a.page_table + (size_t)b * a.max_pages;
+    constexpr int BATCH = 32 / TPI;       // stages whose pages and scales the lanes hold
+    int pages = -1;                       // lane TPI * i + j: tile j of stage (issue index & ~(BATCH - 1)) + i
+    float fs = 0.f, ls = 0.f;
+    int pages_now = -1;                   // the same for the stage being taken
+    float fs_now = 0.f, ls_now = 0.f;
+    int slot_in = 0, slot_out = 0;        // stages' bytes in the ring
+    auto issue = [&](int i) {
+      if ((i & (BATCH - 1)) == 0) {
+        const int tile = mine0 + (i + lane / TPI) * (S::NW * TPI) + lane % TPI;
+        pages = -1;
+        fs = ls = 0.f;
+        if (tile < last) {
+          const int pos = (tile0 + tile) * kTile;
+          pages = block_page(table, pos >> p.ps_log2, p);
+          if (pages >= 0) {
+            const size_t blk = (((size_t)pages * p.Hkv + kvh) << (p.ps_log2 - p.t_log2)) +
+                               ((pos & ((1 << p.ps_log2) - 1)) >> p.t_log2);
+            fs = __ldg(p.ks + blk) * a.scale_log2;
+            ls = log2f(__ldg(p.vs + blk));
+          }
+        }
+      }
+      if (i < n) {
+#pragma unroll
+        for (int j = 0; j < TPI; ++j) {
+          const int page = __shfl_sync(0xffffffffu, pages, (i & (BATCH - 1)) * TPI + j);
+          const int pos = (tile0 + mine0 + i * (S::NW * TPI) + j) * kTile;
+          const size_t row = ((((size_t)(page < 0 ? 0 : page) * p.Hkv + kvh) << p.ps_log2) +
+                              (pos & ((1 << p.ps_log2) - 1))) * D + 16 * lane;
+          const uint32_t to = ring + slot_in + j * S::TILE;
+          if (page >= 0 && pos >= lo && pos + kTile <= hi)
+            copy_tile<D, true>(p.k + row, p.v + row, to, ln, 0, kTile, lane);
+          else      // rows behind the context, or of no page, become zeros
+            copy_tile<D, false>(p.k + row, p.v + row, to, ln, page < 0 ? kTile : lo - pos, hi - pos,
+                                lane);
+        }
+      }
+      commit_copies();
+      slot_in = slot_in == (S::NS - 1) * S::STAGE ? 0 : slot_in + S::STAGE;
+    };
+#pragma unroll
+    for (int i = 0; i < S::NS - 1; ++i) issue(i);
+    for (int i = 0; i < n; ++i) {
+      if ((i & (BATCH - 1)) == 0) {
+        pages_now = pages;
+        fs_now = fs;
+        ls_now = ls;
+      }
+      wait_copies<S::NS - 2>();
+      __syncwarp();     // stage i is there for all lanes, and none still reads the one before
+      issue(i + S::NS - 1);
+      float f[TPI], lv[TPI];
+      const uint32_t none =
+          __ballot_sync(0xffffffffu, pages_now < 0) >> ((i & (BATCH - 1)) * TPI) & ((1u << TPI) - 1);
+#pragma unroll
+      for (int j = 0; j < TPI; ++j) {
+        f[j] = __shfl_sync(0xffffffffu, fs_now, (i & (BATCH - 1)) * TPI + j);
+        lv[j] = __shfl_sync(0xffffffffu, ls_now, (i & (BATCH - 1)) * TPI + j);
+      }
+      const int pos = (tile0 + mine0 + i * (S::NW * TPI)) * kTile;
+      const bool masked = none || pos < lo || pos + TPI * kTile - 1 > least;
+      take_stage<D, F8, V>(w, ring + slot_out, pos, f, lv, masked, none, lo, lim, ln, g, t);
+      slot_out = slot_out == (S::NS - 1) * S::STAGE ? 0 : slot_out + S::STAGE;
+    }
+    wait_copies<0>();
+
+    // join the warps
+    __syncthreads();
+    float* merge = reinterpret_cast<float*>(smem);
+    const int live = min(S::NW, (last - first + TPI - 1) / TPI);     // warps that had tiles
+#pragma unroll
+    for (int k = 0; k < NC; ++k)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int col = 8 * k + 2 * t + c;
+        if (warp < live)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int j = 0; j < D / 16; j += 4)
+              *reinterpret_cast<float4*>(merge + (warp * N + col) * (D + 4) + out_dim<D>(j, r, g)) =
+                  make_float4(w.acc[k][j][2 * r + c], w.acc[k][j + 1][2 * r + c],
+                              w.acc[k][j + 2][2 * r + c], w.acc[k][j + 3][2 * r + c]);
+        float l = w.l[k][c];
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+        if (g == 0) {
+          stat[0][warp][col] = w.m[k][c];
+          stat[1][warp][col] = w.M[k][c];
+          stat[2][warp][col] = l;
+        }
+      }
+    __syncthreads();
+    const bool whole = first == 0 && last == nt;
+    const long long slot = (long long)b * per_seq + u + blockIdx.x;
+    for (int i = threadIdx.x; i < cols * (D / 4); i += NT) {
+      const int col = i / (D / 4), d = i % (D / 4) * 4;
+      float m = kUnset, M = kUnset;
+      for (int k = 0; k < live; ++k) {
+        m = fmaxf(m, stat[0][k][col]);
+        M = fmaxf(M, stat[1][k][col]);
+      }
+      float l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < live; ++k) {
+        l += stat[2][k][col] * ptx::ex2(stat[0][k][col] - m);
+        const float r = ptx::ex2(stat[1][k][col] - M);
+        float4 x = *reinterpret_cast<const float4*>(merge + (k * N + col) * (D + 4) + d);
+        if constexpr (V == kPair) {      // hi and lo parts
+          const float4 y = *reinterpret_cast<const float4*>(merge + (k * N + col + 4) * (D + 4) + d);
+          x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+        }
+        o.x = fmaf(r, x.x, o.x);
+        o.y = fmaf(r, x.y, o.y);
+        o.z = fmaf(r, x.z, o.z);
+        o.w = fmaf(r, x.w, o.w);
+      }
+      const float inv = l > 0.f ? ptx::ex2(M - m - kWeightShift) / l : 0.f;
+      o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+      if (whole) {
+        const int gc = cg * a.width + col;
+        float* out = a.out + (((size_t)b * a.Q + gc / a.G) * a.H + kvh * a.G + gc % a.G) * D + d;
+        *reinterpret_cast<float4*>(out) = o;
+      } else {
+        *reinterpret_cast<float4*>(a.part_o + (slot * a.width + col) * D + d) = o;
+        if (d == 0) a.part_lse[slot * a.width + col] = l > 0.f ? m + log2f(l) : -INFINITY;
+      }
+    }
+    if (a.shares == 0) return;
+    at += last - first;
+    __syncthreads();      // the next segment's copies overwrite the merge buffer
+  }
+}
+
+template <int D, bool F8, int V>
+cudaError_t launch_variant(const BlockDecodeArgs& a, cudaStream_t stream) {
+  const long long units = (long long)a.B * a.pool.Hkv * a.n_cg;
+  const long long grid = a.shares ? a.shares : units;
+  if (grid > 0x7fffffffLL) return cudaErrorNotSupported;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(Shape<D>::NW * 32);
+  cfg.dynamicSmemBytes = Shape<D>::RING;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_block_kernel<D, F8, V>, a);
+}
+
+// Blocks per SM of one variant, with its shared-memory attribute set.
+template <int D, bool F8, int V>
+int variant_blocks() {
+  int per_sm = 0;
+  if (cudaFuncSetAttribute(decode_block_kernel<D, F8, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Shape<D>::RING) != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, decode_block_kernel<D, F8, V>,
+                                                    Shape<D>::NW * 32, Shape<D>::RING) != cudaSuccess)
+    return -1;
+  return per_sm;
+}
+
+template <int D, bool F8>
+cudaError_t launch_codes(const BlockDecodeArgs& a, cudaStream_t stream) {
+  if (a.width <= 4) return launch_variant<D, F8, kPair>(a, stream);
+  if (a.width <= 8) return launch_variant<D, F8, kEight>(a, stream);
+  if constexpr (D <= 128) return launch_variant<D, F8, kSixteen>(a, stream);
+  return cudaErrorNotSupported;
+}
+
+template <int D, bool F8>
+int codes_blocks() {
+  int n = variant_blocks<D, F8, kPair>(), x = variant_blocks<D, F8, kEight>();
+  if (x < n) n = x;
+  if constexpr (D <= 128) {
+    x = variant_blocks<D, F8, kSixteen>();
+    if (x < n) n = x;
+  }
+  return n;
+}
+
+}  // namespace block
+
+// One head_dim's kernels, each in a translation unit of its own.
+#define INT8KV_DECODE_BLOCK_INSTANCE(D)                                                          \
+  cudaError_t launch_block_decode_##D(const BlockDecodeArgs& a, bool f8, cudaStream_t stream) {  \
+    return f8 ? block::launch_codes<D, true>(a, stream) : block::launch_codes<D, false>(a, stream); \
+  }                                                                                              \
+  int block_decode_blocks_##D(bool f8) {                                                         \
+    return f8 ? block::codes_blocks<D, true>() : block::codes_blocks<D, false>();                \
+  }
+
+cudaError_t launch_block_decode_64(const BlockDecodeArgs& a, bool f8, cudaStream_t stream);
+cudaError_t launch_block_decode_128(const BlockDecodeArgs& a, bool f8, cudaStream_t stream);
+cudaError_t launch_block_decode_256(const BlockDecodeArgs& a, bool f8, cudaStream_t stream);
+int block_decode_blocks_64(bool f8);
+int block_decode_blocks_128(bool f8);
+int block_decode_blocks_256(bool f8);
+
+}  // namespace int8kv
