@@ -503,6 +503,9 @@ static int decode_entry(const int8kv_pool* pool, int layer, const uint16_t* q,
     d.out = out;
     d.part_o = a.ws.part_o;
     d.part_lse = (float*)a.ws.part_ml;
+    // (the region holds two floats a row; the units' words follow the first of them)
+    const size_t rows = (size_t)batch * q_len * n_heads * n_splits;
+    d.part_units = (int2*)((char*)a.ws.part_ml + (rows * sizeof(float) + 7) / 8 * 8);
     d.B = batch;
     d.H = n_heads;
     d.G = G;
@@ -512,8 +515,11 @@ static int decode_entry(const int8kv_pool* pool, int layer, const uint16_t* q,
     const int cols = q_len * G, per = pool->head_dim <= 128 && cols > 8 ? 16 : 8;
     d.n_cg = (cols + per - 1) / per;
     d.width = (cols + d.n_cg - 1) / d.n_cg;
-    d.shares = block_shares(pool, (long long)batch * pool->n_kv_heads * d.n_cg, d.width,
-                            (long long)batch * q_len * n_heads * n_splits, n_splits);
+    const long long units = (long long)batch * pool->n_kv_heads * d.n_cg;
+    d.shares = block_shares(pool, units, d.width, (long long)rows, n_splits);
+    // the kernels count the line of tiles in 32 bits; one block per unit needs no line
+    const long long most = ((long long)max_pages_per_seq * pool->page_size + 15) / 16 + 64;
+    if (units * most > INT32_MAX / 2) d.shares = 0;
     d.scale_log2 = scale * 1.4426950408889634f;
     return launch_status(launch_block_decode(d, pool->head_dim, pool->f8, s));
   }

@@ -156,6 +156,7 @@ struct BlockDecodeArgs {
   float* out;                 // [B][Q][H][D]
   float* part_o;              // [slots][width][D] normalised partial outputs
   float* part_lse;            // [slots][width] their log2-sum-exp
+  int2* part_units;           // [units] first partial and number of them (1: none, it is in out)
   int B, H, G, Q, max_pages, window;
   int n_cg, width;            // column groups per (sequence, kv head), columns of each
   int shares;                 // blocks of the balanced schedule, or 0: one block per unit

@@ -8,59 +8,61 @@ using namespace block;
 
 // Join the partials of units that a share boundary cut; zero rows of empty units:
 //   out = sum_i o_i 2^(lse_i - M) / sum_i 2^(lse_i - M).
-// One block per (sequence, query, head) and 64 values of it; its warps share the
-// partials, a lane two values.  The first kAhead rows of each warp are requested
-// before the weights are known, so that the two trips to L2 overlap.
-constexpr int kJoinWarps = 8;
-constexpr int kAhead = 8;
+// One block per (sequence, query, head) and 128 values of it; a warp takes every 16th
+// partial, a lane four values (D = 64: two).  The decode blocks left each unit's first
+// partial and their number.  The first kAhead rows of each warp are requested before
+// the weights are known, so that the two trips to L2 overlap.
+constexpr int kJoinWarps = 16;
+constexpr int kAhead = 6;
 
+template <int PER>
+__device__ __forceinline__ void load_row(const float* from, float (&x)[PER]) {
+  if constexpr (PER == 4) {
+    const float4 v = from ? *reinterpret_cast<const float4*>(from) : make_float4(0.f, 0.f, 0.f, 0.f);
+    x[0] = v.x;
+    x[1] = v.y;
+    x[2] = v.z;
+    x[3] = v.w;
+  } else {
+    const float2 v = from ? *reinterpret_cast<const float2*>(from) : make_float2(0.f, 0.f);
+    x[0] = v.x;
+    x[1] = v.y;
+  }
+}
+
+template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) decode_block_combine_kernel(
-    const BlockDecodeArgs a, int D, int least) {
-  constexpr int NT = kJoinWarps * 32;
+    const BlockDecodeArgs a) {
+  constexpr int NT = kJoinWarps * 32, DIMS = D < 128 ? D : 128, PER = DIMS / 32;
   extern __shared__ float weight[];         // [partials of the unit]
-  __shared__ long long warp_sums[kJoinWarps];
-  __shared__ long long place;
   __shared__ float red[kJoinWarps];
-  __shared__ float2 sums[kJoinWarps][32];
+  __shared__ float sums[kJoinWarps][DIMS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   ptx::grid_launch_dependents();
-  ptx::grid_dependency_wait();
   const int row = blockIdx.x, h = row % a.H, bq = row / a.H, b = bq / a.Q;
   const int kvh = h / a.G, gc = (bq % a.Q) * a.G + h % a.G, cg = gc / a.width, col = gc % a.width;
-  const int per_seq = a.pool.Hkv * a.n_cg;
-  const int d = blockIdx.y * 64 + 2 * lane;
-  long long mine;
-  const long long total = batch_tiles<NT>(a, per_seq, warp_sums, mine);
-  int lo, hi;
-  const int run = (a.B + NT - 1) / NT;
-  if (b / run == (int)threadIdx.x) {
-    for (int s = threadIdx.x * run; s < b; ++s) {
-      unit_range(a, s, lo, hi);
-      mine += (long long)unit_tiles(lo, hi) * per_seq;
-    }
-    place = mine;
-  }
-  __syncthreads();
-  unit_range(a, b, lo, hi);
-  const int nt = unit_tiles(lo, hi), u = kvh * a.n_cg + cg;
+  const int per_seq = a.pool.Hkv * a.n_cg, u = kvh * a.n_cg + cg;
+  const int d = blockIdx.y * DIMS + PER * lane;
   float* out = a.out + (size_t)row * D + d;
-  if (nt == 0) {
-    if (warp == 0) *reinterpret_cast<float2*>(out) = make_float2(0.f, 0.f);
+  ptx::grid_dependency_wait();
+  const int2 unit = a.part_units[b * per_seq + u];      // (of no meaning where the unit is empty)
+  int lo, hi;
+  unit_range(a, b, lo, hi);
+  if (unit_tiles(lo, hi) == 0) {
+    if (warp == 0)
+#pragma unroll
+      for (int k = 0; k < PER; ++k) out[k] = 0.f;
     return;
   }
-  const long long per = share_tiles(total, a.shares, least);
-  const long long start = place + (long long)u * nt;
-  const long long c0 = start / per, c1 = (start + nt - 1) / per;
-  if (c0 == c1) return;      // one block had the whole unit and wrote it
-  const int n = (int)(c1 - c0 + 1);
-  const size_t first = ((size_t)b * per_seq + u + c0) * a.width + col;
+  const int n = unit.y;
+  if (n == 1) return;      // one block had the whole unit and wrote it
+  const size_t first = (size_t)unit.x * a.width + col, stride = (size_t)a.width * D;
   const float* o = a.part_o + first * D + d;
-  const size_t stride = (size_t)a.width * D;
-  float2 x[kAhead];
+  float x[kAhead][PER];
 #pragma unroll
   for (int k = 0; k < kAhead; ++k) {
     const int i = warp + k * kJoinWarps;
-    x[k] = i < n ? *reinterpret_cast<const float2*>(o + i * stride) : make_float2(0.f, 0.f);
+    load_row<PER>(i < n ? o + i * stride : nullptr, x[k]);
   }
   float M = -INFINITY;
   for (int i = threadIdx.x; i < n; i += NT) {
@@ -73,37 +75,111 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_block_combine_kernel(
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, red[w]);
+  if (M == -INFINITY) M = 0.f;      // nothing attended: all weights are 0
   float l = 0.f;
-  for (int i = lane; i < n; i += 32) l += M > -INFINITY ? ptx::ex2(weight[i] - M) : 0.f;
+  for (int i = lane; i < n; i += 32) l += ptx::ex2(weight[i] - M);
   l = warp_sum(l);       // every warp the same sum
-  float2 acc = make_float2(0.f, 0.f);
+  float acc[PER] = {};
 #pragma unroll
   for (int k = 0; k < kAhead; ++k) {
     const int i = warp + k * kJoinWarps;
-    if (i < n && l > 0.f) {
+    if (i < n) {
       const float r = ptx::ex2(weight[i] - M);
-      acc.x = fmaf(r, x[k].x, acc.x);
-      acc.y = fmaf(r, x[k].y, acc.y);
+#pragma unroll
+      for (int e = 0; e < PER; ++e) acc[e] = fmaf(r, x[k][e], acc[e]);
     }
   }
 #pragma unroll 4
   for (int i = warp + kAhead * kJoinWarps; i < n; i += kJoinWarps) {
-    const float2 y = *reinterpret_cast<const float2*>(o + i * stride);
-    const float r = l > 0.f ? ptx::ex2(weight[i] - M) : 0.f;
-    acc.x = fmaf(r, y.x, acc.x);
-    acc.y = fmaf(r, y.y, acc.y);
-  }
-  sums[warp][lane] = acc;
-  __syncthreads();
-  if (warp == 0) {
+    float y[PER];
+    load_row<PER>(o + i * stride, y);
+    const float r = ptx::ex2(weight[i] - M);
 #pragma unroll
-    for (int w = 1; w < kJoinWarps; ++w) {
-      acc.x += sums[w][lane].x;
-      acc.y += sums[w][lane].y;
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    *reinterpret_cast<float2*>(out) = make_float2(acc.x * inv, acc.y * inv);
+    for (int e = 0; e < PER; ++e) acc[e] = fmaf(r, y[e], acc[e]);
   }
+#pragma unroll
+  for (int e = 0; e < PER; ++e) sums[warp][PER * lane + e] = acc[e];
+  __syncthreads();
+  if (threadIdx.x < DIMS) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) v += sums[w][threadIdx.x];
+    a.out[(size_t)row * D + blockIdx.y * DIMS + threadIdx.x] = l > 0.f ? v / l : 0.f;
+  }
+}
+
+// The same for units of few partials: one warp per row and 128 values.
+constexpr int kFewWarps = 4;
+template <int D>
+__global__ void __launch_bounds__(kFewWarps * 32) decode_block_combine_few_kernel(
+    const BlockDecodeArgs a, int rows) {
+  constexpr int DIMS = D < 128 ? D : 128, PER = DIMS / 32, CHUNKS = D / DIMS, K = 4;
+  const int lane = threadIdx.x & 31;
+  const int job = blockIdx.x * kFewWarps + (threadIdx.x >> 5);
+  const int row = job / CHUNKS, d = job % CHUNKS * DIMS + PER * lane;
+  ptx::grid_launch_dependents();
+  const int h = row % a.H, bq = row / a.H, b = bq / a.Q;
+  const int kvh = h / a.G, gc = (bq % a.Q) * a.G + h % a.G, cg = gc / a.width, col = gc % a.width;
+  ptx::grid_dependency_wait();
+  if (row >= rows) return;
+  const int2 unit = a.part_units[(b * a.pool.Hkv + kvh) * a.n_cg + cg];
+  int lo, hi;
+  unit_range(a, b, lo, hi);
+  const bool empty = unit_tiles(lo, hi) == 0;
+  const int n = empty ? 0 : unit.y;
+  if (n == 1) return;      // one block had the whole unit and wrote it
+  const size_t first = (size_t)unit.x * a.width + col, stride = (size_t)a.width * D;
+  float M = kUnset, l = 0.f, acc[PER] = {};
+  for (int i0 = 0; i0 < n; i0 += K) {
+    float v[K], x[K][PER], top = M;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const bool in = i0 + k < n;
+      v[k] = in ? a.part_lse[first + (size_t)(i0 + k) * a.width] : -INFINITY;
+      load_row<PER>(in ? a.part_o + first * D + (i0 + k) * stride + d : nullptr, x[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) top = fmaxf(top, v[k]);
+    const float r = ptx::ex2(M - top);
+    M = top;
+    l *= r;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] *= r;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const float f = ptx::ex2(v[k] - M);
+      l += f;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) acc[e] = fmaf(f, x[k][e], acc[e]);
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) a.out[(size_t)row * D + d + e] = acc[e] * inv;
+}
+
+template <int D>
+cudaError_t launch_combine(const BlockDecodeArgs& a, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  const int rows = a.B * a.Q * a.H, chunks = D > 128 ? D / 128 : 1;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // Up to 8 shares a unit: most rows have one to nine partials, and blocks of 16 warps
+  // would mostly start to find nothing to do (12 sequences of up to 8K, 4 queries, 32
+  // heads: 13 us against FEW us).
+  if (a.shares <= 8LL * a.B * a.pool.Hkv * a.n_cg) {
+    cfg.gridDim = dim3((unsigned)(((long long)rows * chunks + kFewWarps - 1) / kFewWarps));
+    cfg.blockDim = dim3(kFewWarps * 32);
+    return cudaLaunchKernelEx(&cfg, decode_block_combine_few_kernel<D>, a, rows);
+  }
+  cfg.gridDim = dim3(rows, chunks);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.dynamicSmemBytes = a.shares * sizeof(float);     // a unit has at most a piece in every share
+  return cudaLaunchKernelEx(&cfg, decode_block_combine_kernel<D>, a);
 }
 
 }  // namespace
@@ -126,25 +202,18 @@ cudaError_t launch_block_decode(const BlockDecodeArgs& a, int head_dim, bool f8,
   const long long rows = (long long)a.B * a.Q * a.H;
   if (rows > 0x7fffffffLL) return cudaErrorNotSupported;
   cudaError_t e;
-  int least;      // as the decode kernel's
   switch (head_dim) {
-    case 64: e = launch_block_decode_64(a, f8, stream); least = Shape<64>::LEAST; break;
-    case 128: e = launch_block_decode_128(a, f8, stream); least = Shape<128>::LEAST; break;
-    case 256: e = launch_block_decode_256(a, f8, stream); least = Shape<256>::LEAST; break;
+    case 64:
+      e = launch_block_decode_64(a, f8, stream);
+      return e != cudaSuccess || a.shares == 0 ? e : launch_combine<64>(a, stream);
+    case 128:
+      e = launch_block_decode_128(a, f8, stream);
+      return e != cudaSuccess || a.shares == 0 ? e : launch_combine<128>(a, stream);
+    case 256:
+      e = launch_block_decode_256(a, f8, stream);
+      return e != cudaSuccess || a.shares == 0 ? e : launch_combine<256>(a, stream);
     default: return cudaErrorNotSupported;
   }
-  if (e != cudaSuccess || a.shares == 0) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)rows, head_dim / 64);
-  cfg.blockDim = dim3(kJoinWarps * 32);
-  cfg.dynamicSmemBytes = a.shares * sizeof(float);     // a unit has at most a piece in every share
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_block_combine_kernel, a, head_dim, least);
 }
 
 }  // namespace int8kv

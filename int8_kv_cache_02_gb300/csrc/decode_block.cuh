@@ -30,10 +30,13 @@
 // groups of columns per pass where the registers hold them (NC = 2, D <= 128), so
 // that a page is read and converted once for 16 columns.
 //
-// Schedule: all tiles of all (sequence, kv head, column group) units in one line,
-// cut into equal shares, one per resident block (a.shares); a unit that a share
-// boundary cuts leaves partials, numbered unit + share, which the combine kernel
-// joins.  With a.shares = 0 every block takes one whole unit and writes it out.
+// Schedule: all (sequence, kv head, column group) units in one line, each as long as
+// its tiles plus a start of kStart (what a block spends on a unit besides its tiles:
+// fetching q, the first wait, joining its warps), cut into equal shares, one per
+// resident block (a.shares).  A unit that a share boundary cuts leaves partials,
+// numbered unit + share, which the combine kernel joins.  The first copies of a
+// block's next unit are under way while its warps are joined for the last one.  With
+// a.shares = 0 every block takes one whole unit and writes it out.
 //
 // Bound by HBM: 2 D bytes per position and kv head.
 #pragma once
@@ -55,12 +58,13 @@ struct Shape {
   static constexpr int TPI = 256 / D;                 // tiles a warp takes at a time
   static constexpr int NS = D == 256 ? 3 : 3;         // ring stages per warp
   static constexpr int BLOCKS = 2;                    // per SM
-  static constexpr int LEAST = NW * TPI * (NS - 1);   // tiles of a share at least: its rings' first fill
+  static constexpr int START = 2 * NW * TPI;          // a unit's start, in tiles
+  static constexpr int LEAST = START + NW * TPI * (NS - 1);   // a share at least: its rings' first fill
   static constexpr int KP = D / 64;                   // 16-byte K pieces per lane and row
   static constexpr int ROWS = kTile * D;              // bytes of a tile's K rows, or V rows
   static constexpr int TILE = 2 * ROWS;               // bytes of a tile in the ring: K, then V
   static constexpr int STAGE = TPI * TILE;
-  static constexpr int RING = NW * NS * STAGE;        // (the warps' outputs are joined over it)
+  static constexpr int RING = NW * NS * STAGE;
 };
 
 // Variants of the kernel by columns of a unit.
@@ -96,41 +100,89 @@ __device__ __forceinline__ int unit_tiles(int lo, int hi) {
   return hi > lo ? (hi - 1) / kTile - lo / kTile + 1 : 0;
 }
 
-// Tiles of the whole batch.  Every thread sums a run of sequences; `mine` is the
-// number of tiles before its run.
-template <int NT>
-__device__ __forceinline__ long long batch_tiles(const BlockDecodeArgs& a, int per_seq,
-                                                 long long* warp_sums, long long& mine) {
-  const int run = (a.B + NT - 1) / NT;
-  long long sum = 0;
-  for (int i = 0; i < run; ++i) {
-    const int b = threadIdx.x * run + i;
-    if (b >= a.B) break;
-    int lo, hi;
-    unit_range(a, b, lo, hi);
-    sum += (long long)unit_tiles(lo, hi) * per_seq;
-  }
-  long long inc = sum;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, inc, off);
-    if ((threadIdx.x & 31) >= off) inc += o;
-  }
-  if ((threadIdx.x & 31) == 31) warp_sums[threadIdx.x >> 5] = inc;
-  __syncthreads();
-  long long total = 0, before = 0;
-#pragma unroll
-  for (int w = 0; w < NT / 32; ++w) {
-    if (w < (int)(threadIdx.x >> 5)) before += warp_sums[w];
-    total += warp_sums[w];
-  }
-  mine = before + inc - sum;
-  return total;
+// Length of sequence b's units in the line.
+__device__ __forceinline__ int line_length(const BlockDecodeArgs& a, int b, int per_seq, int start) {
+  int lo, hi;
+  unit_range(a, b, lo, hi);
+  const int nt = unit_tiles(lo, hi);
+  return nt ? (nt + start) * per_seq : 0;
 }
 
-__device__ __forceinline__ long long share_tiles(long long total, int shares, int least) {
-  const long long per = (total + shares - 1) / shares;
-  return per > least ? per : least;
+// What a share's place in the line is made of: sequence b's units begin at `base`.
+// Every warp finds it by itself: a lane sums a run of sequences, and the lane whose
+// run holds the place walks it.  (The whole line is shorter than 2^31.)
+struct Place {
+  int at, end, b, base, per;
+};
+__device__ __forceinline__ Place find_share(const BlockDecodeArgs& a, int per_seq, int start,
+                                            int least) {
+  const int lane = threadIdx.x & 31, run = (a.B + 31) / 32;
+  int sum = 0;
+  for (int i = 0; i < run; ++i)
+    if (lane * run + i < a.B) sum += line_length(a, lane * run + i, per_seq, start);
+  int inc = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, inc, off);
+    if (lane >= off) inc += o;
+  }
+  const int total = __shfl_sync(0xffffffffu, inc, 31);
+  const int even = (int)(((unsigned)total + a.shares - 1) / (unsigned)a.shares);
+  const int per = even > least ? even : least;
+  Place p;
+  p.per = per;
+  const long long at = (long long)per * blockIdx.x;
+  if (at >= total) {
+    p.at = p.end = total;
+    p.b = a.B;
+    p.base = total;
+    return p;
+  }
+  p.at = (int)at;
+  p.end = (int)min(at + per, (long long)total);
+  int base = inc - sum, b = lane * run;
+  const bool mine = p.at >= base && p.at < inc;
+  if (mine && run > 1)
+    for (;;) {
+      const int n = line_length(a, b, per_seq, start);
+      if (p.at < base + n) break;
+      base += n;
+      ++b;
+    }
+  const int from = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+  p.b = __shfl_sync(0xffffffffu, b, from);
+  p.base = __shfl_sync(0xffffffffu, base, from);
+  return p;
+}
+
+// The part of a unit that one block takes: tiles [first, last) of unit u of sequence b.
+// pieces: how many shares the unit lies in, from this one on.
+struct Segment {
+  int b, u, lo, hi, nt, first, last, pieces;
+};
+
+// The segment at p.at, and p behind it; false at the share's end.
+__device__ __forceinline__ bool next_segment(const BlockDecodeArgs& a, Place& p, int per_seq,
+                                             int start, Segment& s) {
+  while (p.at < p.end) {
+    unit_range(a, p.b, s.lo, s.hi);
+    s.nt = unit_tiles(s.lo, s.hi);
+    const int len = s.nt + start;
+    s.u = s.nt ? (int)((unsigned)(p.at - p.base) / (unsigned)len) : per_seq;
+    if (s.u >= per_seq) {     // past this sequence's units
+      p.base += s.nt ? len * per_seq : 0;
+      ++p.b;
+      continue;
+    }
+    s.b = p.b;
+    const int unit = p.base + s.u * len + start;      // where its tiles begin
+    s.first = max(0, p.at - unit);
+    s.last = min(s.nt, p.end - unit);
+    p.at = min(p.end, unit + s.nt);
+    s.pieces = (int)((unsigned)(unit + s.nt - 1) / (unsigned)p.per) - blockIdx.x + 1;
+    if (s.last > s.first) return true;                // (else the share ends in the unit's start)
+  }
+  return false;
 }
 
 // ---- one warp's tiles -------------------------------------------------------
@@ -390,16 +442,58 @@ __device__ __forceinline__ int out_dim(int j, int r, int g) {
   return (j >> 3) * 128 + 16 * g + 8 * r + (j & 7);
 }
 
+// The lane's pieces of the queries of a unit's columns, 16 values of every 64: requested
+// before the unit's copies, which would delay them ...
+template <int D, int V>
+__device__ __forceinline__ void load_queries(Warp<D, V>& w, const BlockDecodeArgs& a,
+                                             const Segment& s, int g, int t) {
+  const int kvh = s.u / a.n_cg, cg = s.u % a.n_cg, cols = min(a.width, a.G * a.Q - cg * a.width);
+#pragma unroll
+  for (int n = 0; n < Cols<V>::NC; ++n) {
+    const int mine = V == kPair ? g & 3 : 8 * n + g;
+    const int col = cg * a.width + min(mine, cols - 1);
+    const uint16_t* q =
+        a.q + (((size_t)s.b * a.Q + col / a.G) * a.H + kvh * a.G + col % a.G) * D + 16 * t;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      const uint4 x = ptx::ldg128(q + 64 * (c >> 1) + 8 * (c & 1));
+      w.q[n][4 * c] = x.x;
+      w.q[n][4 * c + 1] = x.y;
+      w.q[n][4 * c + 2] = x.z;
+      w.q[n][4 * c + 3] = x.w;
+    }
+  }
+}
+
+// ... and as fragments: columns that are none get zeros, int8 the order of codes_to_h2.
+template <int D, bool F8, int V>
+__device__ __forceinline__ void order_queries(Warp<D, V>& w, int cols, int g) {
+#pragma unroll
+  for (int n = 0; n < Cols<V>::NC; ++n) {
+    const bool none = (V == kPair ? g & 3 : 8 * n + g) >= cols;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {     // four values each
+      const uint32_t x = none ? 0 : w.q[n][2 * k], y = none ? 0 : w.q[n][2 * k + 1];
+      w.q[n][2 * k] = F8 ? x : ptx::prmt(x, y, 0x5410);
+      w.q[n][2 * k + 1] = F8 ? y : ptx::prmt(x, y, 0x7632);
+    }
+  }
+}
+
+// Joining the warps: where a warp's output (column, d) lies in its region of D * N floats.
+// The xor spreads the four columns and the pieces of 16 that a warp writes at once.
+template <int D>
+__device__ __forceinline__ int joined(int col, int d) {
+  return col * D + (d ^ ((col >> 1 & 3) << 2));
+}
+
 template <int D, bool F8, int V>
 __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
     decode_block_kernel(const BlockDecodeArgs a) {
   using S = Shape<D>;
-  constexpr int NT = S::NW * 32, NC = Cols<V>::NC, N = Cols<V>::N, TPI = S::TPI;
-  static_assert(S::NW * N * (D + 4) * 4 <= S::RING, "the warps' outputs are joined over the ring");
+  constexpr int NC = Cols<V>::NC, N = Cols<V>::N, TPI = S::TPI;
+  static_assert(N * D * 4 <= S::STAGE, "a warp's output fits one stage of its ring");
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ long long warp_sums[S::NW];
-  __shared__ long long place_start;
-  __shared__ int place_b;
   __shared__ float stat[3][S::NW][N];     // m, M, l of each warp and column
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const uint32_t ring = ptx::smem_u32(smem) + warp * S::NS * S::STAGE;
@@ -409,141 +503,92 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
   ptx::grid_launch_dependents();
   ptx::grid_dependency_wait();
 
-  long long at, end, seq_start;
-  int b;
+  Place place;
+  Segment seg;
   if (a.shares == 0) {
-    b = blockIdx.x / per_seq;
-    int lo, hi;
-    unit_range(a, b, lo, hi);
-    const int nt = unit_tiles(lo, hi), u = blockIdx.x % per_seq;
-    seq_start = 0;
-    at = (long long)u * nt;
-    end = at + nt;
-    if (nt == 0) end = at + 1;    // run the unit's (empty) segment once: zero rows
+    seg.b = blockIdx.x / per_seq;
+    seg.u = blockIdx.x % per_seq;
+    unit_range(a, seg.b, seg.lo, seg.hi);
+    seg.nt = seg.last = unit_tiles(seg.lo, seg.hi);    // (none: zero rows)
+    seg.first = 0;
+    seg.pieces = 1;
+    place.at = place.end = 0;
   } else {
-    long long mine;
-    const long long total = batch_tiles<NT>(a, per_seq, warp_sums, mine);
-    const long long per = share_tiles(total, a.shares, S::LEAST);
-    at = per * blockIdx.x;
-    end = min(at + per, total);
-    if (at >= end) return;
-    const int run = (a.B + NT - 1) / NT;
-    for (int i = 0; i < run; ++i) {
-      const int s = threadIdx.x * run + i;
-      if (s >= a.B) break;
-      int lo, hi;
-      unit_range(a, s, lo, hi);
-      const long long n = (long long)unit_tiles(lo, hi) * per_seq;
-      if (at >= mine && at < mine + n) {
-        place_b = s;
-        place_start = mine;
-      }
-      mine += n;
-    }
-    __syncthreads();
-    b = place_b;
-    seq_start = place_start;
+    place = find_share(a, per_seq, S::START, S::LEAST);
+    if (!next_segment(a, place, per_seq, S::START, seg)) return;
   }
 
-  Warp<D, V> w;
-  while (at < end) {
-    int lo, hi;
-    unit_range(a, b, lo, hi);
-    const int nt = unit_tiles(lo, hi);
-    const int u = a.shares == 0 ? blockIdx.x % per_seq : (nt ? (int)((at - seq_start) / nt) : per_seq);
-    if (u >= per_seq) {           // past this sequence's units
-      seq_start += (long long)nt * per_seq;
-      ++b;
-      continue;
-    }
-    const int kvh = u / a.n_cg, cg = u % a.n_cg;
-    const int first = nt ? (int)(at - seq_start - (long long)u * nt) : 0;   // tiles of the unit: [first, last)
-    const int last = (int)min((long long)nt, first + (end - at));
-    const int tile0 = lo / kTile;
-
-    // columns 2t, 2t + 1 of the fragments and the lane's q rows (column g)
-    const int cols = min(a.width, a.G * a.Q - cg * a.width);
-    int lim[NC][2];
-#pragma unroll
-    for (int n = 0; n < NC; ++n)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int col = V == kPair ? (2 * t + c) & 3 : 8 * n + 2 * t + c;
-        lim[n][c] = col < cols ? hi - a.Q + (cg * a.width + col) / a.G : -1;
-      }
-    const int least = hi - a.Q + (cg * a.width) / a.G;   // positions <= least: no column masks
-#pragma unroll
-    for (int n = 0; n < NC; ++n) {
-      const int mine = V == kPair ? g & 3 : 8 * n + g;
-      const int col = cg * a.width + min(mine, cols - 1);
-      const uint16_t* q =
-          a.q + (((size_t)b * a.Q + col / a.G) * a.H + kvh * a.G + col % a.G) * D + 16 * t;
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        const uint4 x = ptx::ldg128(q + 64 * c), y = ptx::ldg128(q + 64 * c + 8);
-        const uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {     // values 4k .. 4k + 3 of the lane's 16
-          uint32_t lo2 = v[2 * k], hi2 = v[2 * k + 1];
-          if (mine >= cols) lo2 = hi2 = 0;
-          w.q[n][8 * c + 2 * k] = F8 ? lo2 : ptx::prmt(lo2, hi2, 0x5410);
-          w.q[n][8 * c + 2 * k + 1] = F8 ? hi2 : ptx::prmt(lo2, hi2, 0x7632);
+  // The warp's stages of a segment: TPI tiles each, from first + TPI * (warp + NW * i).
+  constexpr int BATCH = 32 / TPI;       // stages whose pages and scales the lanes hold
+  int pages = -1;                       // lane TPI * i + j: tile j of stage (issue index & ~(BATCH - 1)) + i
+  float ks = 0.f, vs = 0.f;
+  int slot_in = 0, slot_out = 0;        // stages' bytes in the ring
+  int mine0, n;
+  auto issue = [&](int i) {
+    const int kvh = seg.u / a.n_cg;
+    if ((i & (BATCH - 1)) == 0) {
+      const int tile = mine0 + (i + lane / TPI) * (S::NW * TPI) + lane % TPI;
+      pages = -1;
+      if (tile < seg.last) {
+        const int pos = (seg.lo / kTile + tile) * kTile;
+        pages = block_page(a.page_table + (size_t)seg.b * a.max_pages, pos >> p.ps_log2, p);
+        if (pages >= 0) {
+          const size_t blk = (((size_t)pages * p.Hkv + kvh) << (p.ps_log2 - p.t_log2)) +
+                             ((pos & ((1 << p.ps_log2) - 1)) >> p.t_log2);
+          ks = __ldg(p.ks + blk);
+          vs = __ldg(p.vs + blk);
         }
       }
     }
-    w.reset();
-
-    // the warp's stages of the segment: TPI tiles each, from first + TPI * (warp + NW * i)
-    const int mine0 = first + warp * TPI;
-    const int n = last > mine0 ? (last - mine0 + S::NW * TPI - 1) / (S::NW * TPI) : 0;
-    const int32_t* table = a.page_table + (size_t)b * a.max_pages;
-    constexpr int BATCH = 32 / TPI;       // stages whose pages and scales the lanes hold
-    int pages = -1;                       // lane TPI * i + j: tile j of stage (issue index & ~(BATCH - 1)) + i
-    float fs = 0.f, ls = 0.f;
-    int pages_now = -1;                   // the same for the stage being taken
-    float fs_now = 0.f, ls_now = 0.f;
-    int slot_in = 0, slot_out = 0;        // stages' bytes in the ring
-    auto issue = [&](int i) {
-      if ((i & (BATCH - 1)) == 0) {
-        const int tile = mine0 + (i + lane / TPI) * (S::NW * TPI) + lane % TPI;
-        pages = -1;
-        fs = ls = 0.f;
-        if (tile < last) {
-          const int pos = (tile0 + tile) * kTile;
-          pages = block_page(table, pos >> p.ps_log2, p);
-          if (pages >= 0) {
-            const size_t blk = (((size_t)pages * p.Hkv + kvh) << (p.ps_log2 - p.t_log2)) +
-                               ((pos & ((1 << p.ps_log2) - 1)) >> p.t_log2);
-            fs = __ldg(p.ks + blk) * a.scale_log2;
-            ls = log2f(__ldg(p.vs + blk));
-          }
-        }
-      }
-      if (i < n) {
+    if (i < n) {
 #pragma unroll
-        for (int j = 0; j < TPI; ++j) {
-          const int page = __shfl_sync(0xffffffffu, pages, (i & (BATCH - 1)) * TPI + j);
-          const int pos = (tile0 + mine0 + i * (S::NW * TPI) + j) * kTile;
-          const size_t row = ((((size_t)(page < 0 ? 0 : page) * p.Hkv + kvh) << p.ps_log2) +
-                              (pos & ((1 << p.ps_log2) - 1))) * D + 16 * lane;
-          const uint32_t to = ring + slot_in + j * S::TILE;
-          if (page >= 0 && pos >= lo && pos + kTile <= hi)
-            copy_tile<D, true>(p.k + row, p.v + row, to, ln, 0, kTile, lane);
-          else      // rows behind the context, or of no page, become zeros
-            copy_tile<D, false>(p.k + row, p.v + row, to, ln, page < 0 ? kTile : lo - pos, hi - pos,
-                                lane);
-        }
+      for (int j = 0; j < TPI; ++j) {
+        const int page = __shfl_sync(0xffffffffu, pages, (i & (BATCH - 1)) * TPI + j);
+        const int pos = (seg.lo / kTile + mine0 + i * (S::NW * TPI) + j) * kTile;
+        const size_t row = ((((size_t)(page < 0 ? 0 : page) * p.Hkv + kvh) << p.ps_log2) +
+                            (pos & ((1 << p.ps_log2) - 1))) * D + 16 * lane;
+        const uint32_t to = ring + slot_in + j * S::TILE;
+        if (page >= 0 && pos >= seg.lo && pos + kTile <= seg.hi)
+          copy_tile<D, true>(p.k + row, p.v + row, to, ln, 0, kTile, lane);
+        else      // rows behind the context, or of no page, become zeros
+          copy_tile<D, false>(p.k + row, p.v + row, to, ln, page < 0 ? kTile : seg.lo - pos,
+                              seg.hi - pos, lane);
       }
-      commit_copies();
-      slot_in = slot_in == (S::NS - 1) * S::STAGE ? 0 : slot_in + S::STAGE;
-    };
+    }
+    commit_copies();
+    slot_in = slot_in == (S::NS - 1) * S::STAGE ? 0 : slot_in + S::STAGE;
+  };
+  auto begin = [&]() {       // the first copies of a segment
+    mine0 = seg.first + warp * TPI;
+    n = seg.last > mine0 ? (seg.last - mine0 + S::NW * TPI - 1) / (S::NW * TPI) : 0;
 #pragma unroll
     for (int i = 0; i < S::NS - 1; ++i) issue(i);
+  };
+
+  Warp<D, V> w;
+  load_queries(w, a, seg, g, t);
+  begin();
+  for (;;) {
+    const int kvh = seg.u / a.n_cg, cg = seg.u % a.n_cg;
+    const int cols = min(a.width, a.G * a.Q - cg * a.width);
+    order_queries<D, F8, V>(w, cols, g);
+    w.reset();
+    int lim[NC][2];           // columns 2t, 2t + 1 of the fragments
+#pragma unroll
+    for (int k = 0; k < NC; ++k)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int col = V == kPair ? (2 * t + c) & 3 : 8 * k + 2 * t + c;
+        lim[k][c] = col < cols ? seg.hi - a.Q + (cg * a.width + col) / a.G : -1;
+      }
+    const int least = seg.hi - a.Q + (cg * a.width) / a.G;   // positions <= least: no column masks
+    int pages_now = -1;       // pages and scales of the stage being taken
+    float fs_now = 0.f, ls_now = 0.f;
     for (int i = 0; i < n; ++i) {
       if ((i & (BATCH - 1)) == 0) {
         pages_now = pages;
-        fs_now = fs;
-        ls_now = ls;
+        fs_now = pages < 0 ? 0.f : ks * a.scale_log2;
+        ls_now = pages < 0 ? 0.f : log2f(vs);
       }
       wait_copies<S::NS - 2>();
       __syncwarp();     // stage i is there for all lanes, and none still reads the one before
@@ -556,17 +601,24 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
         f[j] = __shfl_sync(0xffffffffu, fs_now, (i & (BATCH - 1)) * TPI + j);
         lv[j] = __shfl_sync(0xffffffffu, ls_now, (i & (BATCH - 1)) * TPI + j);
       }
-      const int pos = (tile0 + mine0 + i * (S::NW * TPI)) * kTile;
-      const bool masked = none || pos < lo || pos + TPI * kTile - 1 > least;
-      take_stage<D, F8, V>(w, ring + slot_out, pos, f, lv, masked, none, lo, lim, ln, g, t);
+      const int pos = (seg.lo / kTile + mine0 + i * (S::NW * TPI)) * kTile;
+      const bool masked = none || pos < seg.lo || pos + TPI * kTile - 1 > least;
+      take_stage<D, F8, V>(w, ring + slot_out, pos, f, lv, masked, none, seg.lo, lim, ln, g, t);
       slot_out = slot_out == (S::NS - 1) * S::STAGE ? 0 : slot_out + S::STAGE;
     }
-    wait_copies<0>();
+    __syncwarp();
 
-    // join the warps
-    __syncthreads();
-    float* merge = reinterpret_cast<float*>(smem);
-    const int live = min(S::NW, (last - first + TPI - 1) / TPI);     // warps that had tiles
+    // the next segment's first copies, into stages 1 and on: stage 0 joins the warps
+    const Segment done = seg;
+    const bool more = next_segment(a, place, per_seq, S::START, seg);
+    slot_in = slot_out = S::STAGE;
+    if (more) {
+      load_queries(w, a, seg, g, t);
+      begin();
+    }
+
+    const int live = min(S::NW, (done.last - done.first + TPI - 1) / TPI);     // warps that had tiles
+    float* mine = reinterpret_cast<float*>(smem + warp * S::NS * S::STAGE);
 #pragma unroll
     for (int k = 0; k < NC; ++k)
 #pragma unroll
@@ -577,7 +629,7 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
           for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int j = 0; j < D / 16; j += 4)
-              *reinterpret_cast<float4*>(merge + (warp * N + col) * (D + 4) + out_dim<D>(j, r, g)) =
+              *reinterpret_cast<float4*>(mine + joined<D>(col, out_dim<D>(j, r, g))) =
                   make_float4(w.acc[k][j][2 * r + c], w.acc[k][j + 1][2 * r + c],
                               w.acc[k][j + 2][2 * r + c], w.acc[k][j + 3][2 * r + c]);
         float l = w.l[k][c];
@@ -590,44 +642,53 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
         }
       }
     __syncthreads();
-    const bool whole = first == 0 && last == nt;
-    const long long slot = (long long)b * per_seq + u + blockIdx.x;
-    for (int i = threadIdx.x; i < cols * (D / 4); i += NT) {
-      const int col = i / (D / 4), d = i % (D / 4) * 4;
-      float m = kUnset, M = kUnset;
-      for (int k = 0; k < live; ++k) {
-        m = fmaxf(m, stat[0][k][col]);
-        M = fmaxf(M, stat[1][k][col]);
-      }
-      float l = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k = 0; k < live; ++k) {
-        l += stat[2][k][col] * ptx::ex2(stat[0][k][col] - m);
-        const float r = ptx::ex2(stat[1][k][col] - M);
-        float4 x = *reinterpret_cast<const float4*>(merge + (k * N + col) * (D + 4) + d);
-        if constexpr (V == kPair) {      // hi and lo parts
-          const float4 y = *reinterpret_cast<const float4*>(merge + (k * N + col + 4) * (D + 4) + d);
-          x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+    const bool whole = done.first == 0 && done.last == done.nt;
+    const int unit = done.b * per_seq + done.u, slot = unit + blockIdx.x;
+    if (a.shares && done.first == 0 && threadIdx.x == 0)     // for the combine
+      a.part_units[unit] = make_int2(slot, done.pieces);
+    for (int col = warp; col < cols; col += S::NW) {
+      float m = kUnset, M = kUnset, l = 0.f, r[S::NW];
+#pragma unroll
+      for (int k = 0; k < S::NW; ++k)
+        if (k < live) {
+          m = fmaxf(m, stat[0][k][col]);
+          M = fmaxf(M, stat[1][k][col]);
         }
-        o.x = fmaf(r, x.x, o.x);
-        o.y = fmaf(r, x.y, o.y);
-        o.z = fmaf(r, x.z, o.z);
-        o.w = fmaf(r, x.w, o.w);
+#pragma unroll
+      for (int k = 0; k < S::NW; ++k) {
+        r[k] = 0.f;
+        if (k < live) {
+          l += stat[2][k][col] * ptx::ex2(stat[0][k][col] - m);
+          r[k] = ptx::ex2(stat[1][k][col] - M);
+        }
       }
-      const float inv = l > 0.f ? ptx::ex2(M - m - kWeightShift) / l : 0.f;
-      o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-      if (whole) {
-        const int gc = cg * a.width + col;
-        float* out = a.out + (((size_t)b * a.Q + gc / a.G) * a.H + kvh * a.G + gc % a.G) * D + d;
-        *reinterpret_cast<float4*>(out) = o;
-      } else {
-        *reinterpret_cast<float4*>(a.part_o + (slot * a.width + col) * D + d) = o;
-        if (d == 0) a.part_lse[slot * a.width + col] = l > 0.f ? m + log2f(l) : -INFINITY;
+      const float inv = l > 0.f ? __fdividef(ptx::ex2(M - m - kWeightShift), l) : 0.f;
+      const int gc = cg * a.width + col;
+      float* out = whole ? a.out + (((size_t)done.b * a.Q + gc / a.G) * a.H + kvh * a.G + gc % a.G) * D
+                         : a.part_o + ((size_t)slot * a.width + col) * D;
+#pragma unroll
+      for (int d = 4 * lane; d < D; d += 128) {
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < S::NW; ++k)
+          if (k < live) {
+            const float* from = reinterpret_cast<const float*>(smem + k * S::NS * S::STAGE);
+            float4 x = *reinterpret_cast<const float4*>(from + joined<D>(col, d));
+            if constexpr (V == kPair) {      // hi and lo parts
+              const float4 y = *reinterpret_cast<const float4*>(from + joined<D>(col + 4, d));
+              x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+            }
+            o = make_float4(fmaf(r[k], x.x, o.x), fmaf(r[k], x.y, o.y), fmaf(r[k], x.z, o.z),
+                            fmaf(r[k], x.w, o.w));
+          }
+        *reinterpret_cast<float4*>(out + d) =
+            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
       }
+      if (!whole && lane == 0)
+        a.part_lse[(size_t)slot * a.width + col] = l > 0.f ? m + log2f(l) : -INFINITY;
     }
-    if (a.shares == 0) return;
-    at += last - first;
-    __syncthreads();      // the next segment's copies overwrite the merge buffer
+    if (!more) return;
+    __syncthreads();      // the next segment's copies reach stage 0
   }
 }
 
