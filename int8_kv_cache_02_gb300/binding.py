@@ -102,28 +102,35 @@ def _check(status, where):
         raise Int8KVError(status, where)
 
 
+# The current stream's handle of a device, without building a torch.cuda.Stream for every call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
 def _dev(t, dtype, name):
+    """The address of a contiguous CUDA tensor of this dtype (argtypes take the integer)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _shape(t, shape, name):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
 
 
@@ -281,16 +288,19 @@ def kv_pool_set_decode_kernel(pool, kind):
 def _block_rows(pool, t, lead, name):
     """A block-scaled pool's K/V rows have the shape lead + [n_kv_heads][head_dim]."""
     if getattr(pool, "block", False):
-        _shape(t, tuple(lead) + (pool.n_kv_heads, pool.head_dim), name)
+        _shape(t, (*lead, pool.n_kv_heads, pool.head_dim), name)
 
 
 def _block_call(pool, q, seq_lens, page_table, out):
     """Shapes of a decode call on a block-scaled pool."""
     if getattr(pool, "block", False):
-        _shape(q, q.shape[:-1] + (pool.head_dim,), "q")
-        _shape(out, q.shape, "out")
-        _shape(seq_lens, q.shape[:1], "seq_lens")
-        _shape(page_table, (q.shape[0], page_table.shape[-1]), "page_table")
+        shape = q.shape
+        if shape[-1] != pool.head_dim:
+            raise ValueError(f"q must have shape [..., {pool.head_dim}], got {list(shape)}")
+        _shape(out, shape, "out")
+        _shape(seq_lens, shape[:1], "seq_lens")
+        if page_table.shape[:-1] != shape[:1]:
+            raise ValueError(f"page_table must have shape [{shape[0]}, max_pages]")
 
 
 def _host_lens(seq_lens):

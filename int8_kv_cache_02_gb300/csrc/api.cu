@@ -521,6 +521,7 @@ static int decode_entry(const int8kv_pool* pool, int layer, const uint16_t* q,
     const long long most = ((long long)max_pages_per_seq * pool->page_size + 15) / 16 + 64;
     if (units * most > INT32_MAX / 2) d.shares = 0;
     d.scale_log2 = scale * 1.4426950408889634f;
+    d.appended = k_new != nullptr;
     return launch_status(launch_block_decode(d, pool->head_dim, pool->f8, s));
   }
   a.pool = layer_view(pool, layer);

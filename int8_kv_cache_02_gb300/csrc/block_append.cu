@@ -52,8 +52,10 @@ __global__ void __launch_bounds__(NT* GROUPS) block_append_kernel(
   constexpr int PPR = D / 8;     // pieces per row
   static_assert(GROUPS == 1 || NT == 32, "groups of a block are single warps");
   __shared__ float red[NT / 32];
-  ptx::grid_launch_dependents();
+  // Dependents may start once everything before this kernel is complete (not earlier: a
+  // decode of the same call reads what those kernels wrote without waiting again).
   ptx::grid_dependency_wait();
+  ptx::grid_launch_dependents();
   const int tid = threadIdx.x % NT;
   const long long unit = (long long)blockIdx.x * GROUPS + threadIdx.x / NT;
   // unit = ((sequence * nb + block) * Hkv + kv head) * 2 + store

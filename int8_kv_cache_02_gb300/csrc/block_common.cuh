@@ -161,6 +161,9 @@ struct BlockDecodeArgs {
   int n_cg, width;            // column groups per (sequence, kv head), columns of each
   int shares;                 // blocks of the balanced schedule, or 0: one block per unit
   float scale_log2;           // softmax_scale * log2(e)
+  // Whether the kernel launched just before appends position seq_lens[b] - 1 of every
+  // sequence: then only the blocks of those positions are waited for.
+  bool appended;
 };
 
 cudaError_t launch_block_append(const BlockView& p, int head_dim, bool f8, const uint16_t* k_new,

@@ -38,8 +38,13 @@
 // block's next unit are under way while its warps are joined for the last one.  With
 // a.shares = 0 every block takes one whole unit and writes it out.
 //
+// Behind an append of the same call (a.appended) the kernel starts under it: only the
+// blocks that the append writes, the last of every sequence, wait for it.
+//
 // Bound by HBM: 2 D bytes per position and kv head.
 #pragma once
+
+#include <climits>
 
 #include "block_common.cuh"
 #include "decode_common.cuh"
@@ -59,7 +64,7 @@ struct Shape {
   static constexpr int NS = D == 256 ? 3 : 3;         // ring stages per warp
   static constexpr int BLOCKS = 2;                    // per SM
   static constexpr int START = 2 * NW * TPI;          // a unit's start, in tiles
-  static constexpr int LEAST = START + NW * TPI * (NS - 1);   // a share at least: its rings' first fill
+  static constexpr int LEAST = NW * TPI * (NS - 1);   // a share at least: its rings' first fill
   static constexpr int KP = D / 64;                   // 16-byte K pieces per lane and row
   static constexpr int ROWS = kTile * D;              // bytes of a tile's K rows, or V rows
   static constexpr int TILE = 2 * ROWS;               // bytes of a tile in the ring: K, then V
@@ -501,7 +506,7 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
   const BlockView& p = a.pool;
   const int per_seq = p.Hkv * a.n_cg;      // units of a sequence
   ptx::grid_launch_dependents();
-  ptx::grid_dependency_wait();
+  if (!a.appended) ptx::grid_dependency_wait();
 
   Place place;
   Segment seg;
@@ -515,7 +520,10 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
     place.at = place.end = 0;
   } else {
     place = find_share(a, per_seq, S::START, S::LEAST);
-    if (!next_segment(a, place, per_seq, S::START, seg)) return;
+    if (!next_segment(a, place, per_seq, S::START, seg)) {
+      ptx::grid_dependency_wait();    // (the grid is not complete before the append is)
+      return;
+    }
   }
 
   // The warp's stages of a segment: TPI tiles each, from first + TPI * (warp + NW * i).
@@ -523,24 +531,34 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
   int pages = -1;                       // lane TPI * i + j: tile j of stage (issue index & ~(BATCH - 1)) + i
   float ks = 0.f, vs = 0.f;
   int slot_in = 0, slot_out = 0;        // stages' bytes in the ring
-  int mine0, n;
+  int mine0, n, fresh;        // fresh: positions from here on are waited for
   auto issue = [&](int i) {
     const int kvh = seg.u / a.n_cg;
+    const int tile = mine0 + ((i & ~(BATCH - 1)) + lane / TPI) * (S::NW * TPI) + lane % TPI;
+    const int at = (seg.lo / kTile + tile) * kTile;
+    auto block_of = [&](int page) {
+      return (((size_t)page * p.Hkv + kvh) << (p.ps_log2 - p.t_log2)) +
+             ((at & ((1 << p.ps_log2) - 1)) >> p.t_log2);
+    };
     if ((i & (BATCH - 1)) == 0) {
-      const int tile = mine0 + (i + lane / TPI) * (S::NW * TPI) + lane % TPI;
-      pages = -1;
-      if (tile < seg.last) {
-        const int pos = (seg.lo / kTile + tile) * kTile;
-        pages = block_page(a.page_table + (size_t)seg.b * a.max_pages, pos >> p.ps_log2, p);
-        if (pages >= 0) {
-          const size_t blk = (((size_t)pages * p.Hkv + kvh) << (p.ps_log2 - p.t_log2)) +
-                             ((pos & ((1 << p.ps_log2) - 1)) >> p.t_log2);
-          ks = __ldg(p.ks + blk);
-          vs = __ldg(p.vs + blk);
-        }
+      pages = tile < seg.last ? block_page(a.page_table + (size_t)seg.b * a.max_pages,
+                                           at >> p.ps_log2, p)
+                              : -1;
+      if (pages >= 0 && at < fresh) {
+        ks = __ldg(p.ks + block_of(pages));
+        vs = __ldg(p.vs + block_of(pages));
       }
     }
+    bool late = false;
     if (i < n) {
+      late = (seg.lo / kTile + mine0 + i * (S::NW * TPI) + TPI) * kTile > fresh;
+      if (late) {
+        ptx::grid_dependency_wait();
+        if (pages >= 0 && at >= fresh) {      // (written while this kernel may run: not through L1)
+          ks = __ldcg(p.ks + block_of(pages));
+          vs = __ldcg(p.vs + block_of(pages));
+        }
+      }
 #pragma unroll
       for (int j = 0; j < TPI; ++j) {
         const int page = __shfl_sync(0xffffffffu, pages, (i & (BATCH - 1)) * TPI + j);
@@ -557,9 +575,11 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
     }
     commit_copies();
     slot_in = slot_in == (S::NS - 1) * S::STAGE ? 0 : slot_in + S::STAGE;
+    return late;
   };
   auto begin = [&]() {       // the first copies of a segment
     mine0 = seg.first + warp * TPI;
+    fresh = a.appended ? (seg.hi - 1) >> p.t_log2 << p.t_log2 : INT_MAX;
     n = seg.last > mine0 ? (seg.last - mine0 + S::NW * TPI - 1) / (S::NW * TPI) : 0;
 #pragma unroll
     for (int i = 0; i < S::NS - 1; ++i) issue(i);
@@ -592,7 +612,10 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
       }
       wait_copies<S::NS - 2>();
       __syncwarp();     // stage i is there for all lanes, and none still reads the one before
-      issue(i + S::NS - 1);
+      if (issue(i + S::NS - 1) && ((i + S::NS - 1) & (BATCH - 1)) >= S::NS - 1) {
+        fs_now = pages < 0 ? 0.f : ks * a.scale_log2;     // scales that came late, of the same batch
+        ls_now = pages < 0 ? 0.f : log2f(vs);
+      }
       float f[TPI], lv[TPI];
       const uint32_t none =
           __ballot_sync(0xffffffffu, pages_now < 0) >> ((i & (BATCH - 1)) * TPI) & ((1u << TPI) - 1);
@@ -687,9 +710,10 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
       if (!whole && lane == 0)
         a.part_lse[(size_t)slot * a.width + col] = l > 0.f ? m + log2f(l) : -INFINITY;
     }
-    if (!more) return;
+    if (!more) break;
     __syncthreads();      // the next segment's copies reach stage 0
   }
+  ptx::grid_dependency_wait();    // (the grid is not complete before the append is)
 }
 
 template <int D, bool F8, int V>
