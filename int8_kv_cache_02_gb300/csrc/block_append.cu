@@ -24,22 +24,51 @@
 namespace int8kv {
 namespace {
 
-// x / s as the IEEE quotient wherever that decides a code.  y = x * (1 / s) is
-// within 2^-22 of it (two roundings and the quotient's own); only where a rounding boundary of the codes
-// lies that near (or, e4m3, where codes are subnormal) the division is made.
+// Codes of eight values x.  A code is decided by the IEEE quotient x / s; y = x * (1 / s)
+// is within 2^-22 of it (two roundings, and the quotient's own).  Only where a rounding
+// boundary of the codes lies that near to one of the eight are the divisions made:
+//   e4m3: where x (1 / s) (1 - 2^-21) and x (1 / s) (1 + 2^-21), which enclose the
+//         quotient, have different codes;
+//   int8: where y is within 1e-4 of a half-integer (|y| < 128), which 127.5, the one
+//         value that needs saturation, is too.
 template <bool F8>
-__device__ __forceinline__ float quotient(float x, float s, float inv) {
-  float y = x * inv;
-  bool near;
-  if constexpr (F8) {
-    // codes of a binade lie 2^20 fp32 steps apart, so boundaries where the low 20 bits are 0x80000
-    const int d = (int)(__float_as_uint(y) & 0xFFFFFu) - 0x80000;
-    near = (d <= 8 && d >= -8) || fabsf(y) < 0.0157f;
-  } else {
-    near = fabsf((y - floorf(y)) - 0.5f) < 1.0e-4f;
+__device__ __forceinline__ uint2 quantize8(const uint4& x, float s, float inv) {
+  const __half2* h = reinterpret_cast<const __half2*>(&x);
+  float v[8], y[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = __half22float2(h[e]);
+    v[2 * e] = f.x;
+    v[2 * e + 1] = f.y;
   }
-  if (near) y = __fdiv_rn(x, s);
-  return y;
+  uint2 w;
+  bool near = false;
+  if constexpr (F8) {
+    const float below = inv * (1.f - 0x1p-21f), above = inv * (1.f + 0x1p-21f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = v[e] * below;
+    w = round_codes8<F8>(y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = v[e] * above;
+    const uint2 u = round_codes8<F8>(y);
+    near = w.x != u.x || w.y != u.y;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      y[e] = v[e] * inv;
+      near |= fabsf(y[e] - ((y[e] + kRoundToInt) - kRoundToInt)) > 0.5f - 1.0e-4f;
+    }
+    w = round_codes8<F8>(y);
+  }
+  if (near) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      y[e] = __fdiv_rn(v[e], s);
+      if constexpr (!F8) y[e] = fminf(fmaxf(y[e], -127.f), 127.f);
+    }
+    w = round_codes8<F8>(y);
+  }
+  return w;
 }
 
 // NT threads per group; GROUPS groups per thread block; CH 16-byte pieces of new
@@ -82,15 +111,8 @@ __global__ void __launch_bounds__(NT* GROUPS) block_append_kernel(
     if (tid == 0) flag_error(p.err, INT8KV_DEVERR_LENGTH);
     return;
   }
-  const int page = block_page(page_table + b * max_pages, (int)lp, p);
-  if (page < 0) return;
-  const int slot = (int)(first & ((1 << p.ps_log2) - 1));
-  const size_t ph = (size_t)page * p.Hkv + kvh;
-  uint8_t* codes = (is_v ? p.v : p.k) + ((ph << p.ps_log2) + slot) * D;
-  float* scale = (is_v ? p.vs : p.ks) + (ph << (p.ps_log2 - p.t_log2)) + (slot >> p.t_log2);
-  const float s_old = r0 ? *scale : 0.f;
 
-  // the new rows, once
+  // the new rows, once (their loads and the table's are under way together)
   const uint16_t* src = (is_v ? v_new : k_new) + (((size_t)b * n_new + i0) * p.Hkv + kvh) * D;
   uint4 x[CH];
 #pragma unroll
@@ -99,6 +121,14 @@ __global__ void __launch_bounds__(NT* GROUPS) block_append_kernel(
     x[c] = r < rows ? ptx::ldg128(src + (size_t)r * p.Hkv * D + (i % PPR) * 8)
                     : make_uint4(0, 0, 0, 0);
   }
+  const int page = block_page(page_table + b * max_pages, (int)lp, p);
+  if (page < 0) return;
+  const int slot = (int)(first & ((1 << p.ps_log2) - 1));
+  const size_t ph = (size_t)page * p.Hkv + kvh;
+  uint8_t* codes = (is_v ? p.v : p.k) + ((ph << p.ps_log2) + slot) * D;
+  float* scale = (is_v ? p.vs : p.ks) + (ph << (p.ps_log2 - p.t_log2)) + (slot >> p.t_log2);
+  const float s_old = r0 ? *scale : 0.f;
+
   float a = 0.f;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
@@ -139,7 +169,7 @@ __global__ void __launch_bounds__(NT* GROUPS) block_append_kernel(
           code_values<F8>(u[e], y);
 #pragma unroll
           for (int f = 0; f < 4; ++f) y[f] *= shrink;
-          u[e] = round_codes<F8>(y);
+          u[e] = round_codes<F8>(y);      // (|y| <= 64, or e4m3)
         }
         *reinterpret_cast<uint4*>(codes + i * 16) = w;
       }
@@ -152,21 +182,9 @@ __global__ void __launch_bounds__(NT* GROUPS) block_append_kernel(
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int i = tid + c * NT, r = i / PPR;
-    const __half2* h = reinterpret_cast<const __half2*>(&x[c]);
-    uint2 w = make_uint2(0, 0);
-    if (s > 0.f) {
-      float y[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = __half22float2(h[e]);
-        y[2 * (e & 1)] = quotient<F8>(f.x, s, inv);
-        y[2 * (e & 1) + 1] = quotient<F8>(f.y, s, inv);
-        if (e == 1) w.x = round_codes<F8>(y);
-        if (e == 3) w.y = round_codes<F8>(y);
-      }
-    }
     if (r < rows)
-      *reinterpret_cast<uint2*>(codes + (size_t)(r0 + r) * D + (i % PPR) * 8) = w;
+      *reinterpret_cast<uint2*>(codes + (size_t)(r0 + r) * D + (i % PPR) * 8) =
+          s > 0.f ? quantize8<F8>(x[c], s, inv) : make_uint2(0, 0);
   }
 }
 
@@ -208,13 +226,14 @@ cudaError_t dispatch(const AppendCall& c) {
   const int pieces = (c.n_new < T ? c.n_new : T) * (D / 8);   // most new 16-byte pieces of a block
   if (pieces <= 32) return launch<D, F8, 32, 4, 1>(c);
   if (pieces <= 64) return launch<D, F8, 32, 4, 2>(c);
-  if (pieces <= 256) return launch<D, F8, 256, 1, 1>(c);
-  if (pieces <= 512) return launch<D, F8, 256, 1, 2>(c);
-  if (pieces <= 1024) return launch<D, F8, 256, 1, 4>(c);
+  if (pieces <= 128) return launch<D, F8, 32, 4, 4>(c);
+  if (pieces <= 256) return launch<D, F8, 32, 4, 8>(c);
+  if (pieces <= 512) return launch<D, F8, 64, 1, 8>(c);
+  if (pieces <= 1024) return launch<D, F8, 128, 1, 8>(c);
   if constexpr (D >= 128)
     if (pieces > 1024 && pieces <= 2048) return launch<D, F8, 256, 1, 8>(c);
   if constexpr (D >= 256)
-    if (pieces > 2048) return launch<D, F8, 256, 1, 16>(c);
+    if (pieces > 2048) return launch<D, F8, 512, 1, 8>(c);
   return cudaErrorNotSupported;
 }
 

@@ -118,8 +118,10 @@ __device__ __forceinline__ void pair_words(uint32_t a, uint32_t b, uint32_t& fir
   second = ptx::prmt(a, b, F8 ? 0x7362 : 0x7632);
 }
 
-// Four quotients y = x / s, rounded to nearest even and saturated, as four code
-// bytes (y[0] in the lowest).
+constexpr float kRoundToInt = 12582912.f;   // 1.5 * 2^23
+
+// Four values in units of the scale, rounded to nearest even, as four code bytes (y[0]
+// in the lowest).  e4m3 saturates; int8 takes |y| < 127.5.
 template <bool F8>
 __device__ __forceinline__ uint32_t round_codes(const float (&y)[4]) {
   if constexpr (F8) {
@@ -128,12 +130,19 @@ __device__ __forceinline__ uint32_t round_codes(const float (&y)[4]) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y[3]), "f"(y[2]));
     return (uint32_t)lo | ((uint32_t)hi << 16);
   } else {
+    // y + 1.5 * 2^23 is the nearest integer (ties to even) plus that, exactly: its low byte
     uint32_t c[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      c[i] = (uint32_t)max(-127, min(127, __float2int_rn(y[i])));
+      c[i] = __float_as_uint(y[i] + kRoundToInt);
     return ptx::prmt(ptx::prmt(c[0], c[1], 0x0040), ptx::prmt(c[2], c[3], 0x0040), 0x5410);
   }
+}
+
+template <bool F8>
+__device__ __forceinline__ uint2 round_codes8(const float (&y)[8]) {
+  const float a[4] = {y[0], y[1], y[2], y[3]}, b[4] = {y[4], y[5], y[6], y[7]};
+  return make_uint2(round_codes<F8>(a), round_codes<F8>(b));
 }
 
 // Four code bytes as fp32 values in units of the scale.

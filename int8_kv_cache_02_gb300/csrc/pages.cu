@@ -28,59 +28,63 @@ constexpr int kRuns = kBlocks * kThreads;
 
 // ---- copies -----------------------------------------------------------------
 constexpr int kCopyThreads = 256;
-constexpr int kChunk = 16384;     // bytes a block copies at a time
+constexpr int kPieces = 4;                                   // 16-byte pieces a thread has in flight
+constexpr int kChunk = kCopyThreads * kPieces * 16;          // bytes a block copies at a time
 
 struct Regions {
-  char* base[4];             // stores and scales, all layers (null: the pool has none)
-  unsigned bytes[4];         // of one page of one layer
-  int chunks[4];             // per page and layer, summed up to and including this region
+  char* store[2];            // K and V, all layers
+  char* scales[2];           // theirs, or null
+  unsigned bytes[2];         // of a page of one layer
+  unsigned scale_bytes[2];
+  int k_chunks, chunks;      // chunks of a page's K store, and of both stores
   int n_layers, n_pages;
   int32_t* err;
 };
 
-// Pages (src[i], dst[i]) of every layer and region, i < n (or *n_dev).  A negative
-// entry on either side is no copy.
+// Pages (src[i], dst[i]) of every layer, i < n (or *n_dev).  A negative entry on either
+// side is no copy.  One block per chunk of a store (a block per chunk balances better
+// than blocks that stay: 134 MB copied in 43 against 47 us); the first chunk of a store
+// brings its scales.
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const Regions r, const int32_t* src,
                                                                  const int32_t* dst, int n,
                                                                  const int32_t* n_dev) {
   ptx::grid_launch_dependents();
   ptx::grid_dependency_wait();
   if (n_dev) n = *n_dev;
-  const int per = r.chunks[3];                         // chunks of a page and layer
-  const long long total = (long long)n * r.n_layers * per;
+  const long long total = (long long)n * r.n_layers * r.chunks;
   for (long long w = blockIdx.x; w < total; w += gridDim.x) {
-    const int c = (int)(w % per);
-    const long long il = w / per;
+    const int c = (int)(w % r.chunks);
+    const long long il = w / r.chunks;
     const int layer = (int)(il % r.n_layers), i = (int)(il / r.n_layers);
     const int s = src[i], d = dst[i];
     if (s < 0 || d < 0 || s >= r.n_pages || d >= r.n_pages) {
-      if ((s >= r.n_pages || d >= r.n_pages) && threadIdx.x == 0)
-        flag_error(r.err, INT8KV_DEVERR_PAGE_ID);
+      if (threadIdx.x == 0 && s >= 0 && d >= 0) flag_error(r.err, INT8KV_DEVERR_PAGE_ID);
       continue;
     }
     if (s == d) continue;
-    int k = 0;
-    while (c >= r.chunks[k]) ++k;
-    const unsigned bytes = r.bytes[k];
-    const unsigned at = (unsigned)(c - (k ? r.chunks[k - 1] : 0)) * kChunk;
-    const unsigned len = min(bytes - at, (unsigned)kChunk);
-    const char* from = r.base[k] + ((size_t)layer * r.n_pages + s) * bytes + at;
-    char* to = r.base[k] + ((size_t)layer * r.n_pages + d) * bytes + at;
-    if (bytes % 16 == 0) {
-      uint4 x[kChunk / 16 / kCopyThreads];
+    const int k = c >= r.k_chunks;
+    const unsigned at = (unsigned)(k ? c - r.k_chunks : c) * kChunk;
+    const unsigned len = min(r.bytes[k] - at, (unsigned)kChunk);
+    const size_t from = (size_t)layer * r.n_pages + s, to = (size_t)layer * r.n_pages + d;
+    const char* in = r.store[k] + from * r.bytes[k] + at;
+    char* out = r.store[k] + to * r.bytes[k] + at;
+    uint4 x[kPieces];
 #pragma unroll
-      for (int j = 0; j < kChunk / 16 / kCopyThreads; ++j) {
-        const unsigned o = (threadIdx.x + j * kCopyThreads) * 16;
-        if (o < len) x[j] = *reinterpret_cast<const uint4*>(from + o);
-      }
+    for (int j = 0; j < kPieces; ++j) {
+      const unsigned o = (threadIdx.x + j * kCopyThreads) * 16;
+      if (o < len) x[j] = *reinterpret_cast<const uint4*>(in + o);
+    }
+    if (at == 0 && r.scales[k]) {      // a multiple of 4 bytes
+      const unsigned bytes = r.scale_bytes[k];
+      const char* f = r.scales[k] + from * bytes;
+      char* t = r.scales[k] + to * bytes;
+      for (unsigned o = threadIdx.x * 4; o < bytes; o += kCopyThreads * 4)
+        *reinterpret_cast<uint32_t*>(t + o) = *reinterpret_cast<const uint32_t*>(f + o);
+    }
 #pragma unroll
-      for (int j = 0; j < kChunk / 16 / kCopyThreads; ++j) {
-        const unsigned o = (threadIdx.x + j * kCopyThreads) * 16;
-        if (o < len) *reinterpret_cast<uint4*>(to + o) = x[j];
-      }
-    } else {     // scales of a few blocks: a multiple of 4 bytes
-      for (unsigned o = threadIdx.x * 4; o < len; o += kCopyThreads * 4)
-        *reinterpret_cast<uint32_t*>(to + o) = *reinterpret_cast<const uint32_t*>(from + o);
+    for (int j = 0; j < kPieces; ++j) {
+      const unsigned o = (threadIdx.x + j * kCopyThreads) * 16;
+      if (o < len) *reinterpret_cast<uint4*>(out + o) = x[j];
     }
   }
 }
@@ -439,24 +443,31 @@ cudaError_t launch_cluster(void (*kernel)(A...), cudaStream_t stream, A... args)
 cudaError_t launch_copy(const int8kv_pool* p, const int32_t* src, const int32_t* dst, int most,
                         const int32_t* n_dev, cudaStream_t stream) {
   Regions r;
-  void* base[4] = {p->k_store, p->v_store, p->k_scales, p->v_scales};
-  int sum = 0;
-  for (int k = 0; k < 4; ++k) {
-    size_t bytes = 0;
+  const auto bytes = [&](int region, unsigned* out) {
+    size_t b = 0;
     int8kv_pool_region_bytes(1, p->n_kv_heads, p->head_dim, p->group_size, p->page_size, 1,
-                             p->variant, k, &bytes);
-    if (bytes > 0x7fffffff) return cudaErrorNotSupported;
-    r.base[k] = (char*)base[k];
-    r.bytes[k] = (unsigned)bytes;
-    sum += (int)((bytes + kChunk - 1) / kChunk);
-    r.chunks[k] = sum;
-  }
+                             p->variant, region, &b);
+    *out = (unsigned)b;
+    return b <= 0x7fffffff;
+  };
+  if (!bytes(INT8KV_REGION_K_STORE, &r.bytes[0]) || !bytes(INT8KV_REGION_V_STORE, &r.bytes[1]) ||
+      !bytes(INT8KV_REGION_K_SCALES, &r.scale_bytes[0]) ||
+      !bytes(INT8KV_REGION_V_SCALES, &r.scale_bytes[1]))
+    return cudaErrorNotSupported;
+  r.store[0] = (char*)p->k_store;
+  r.store[1] = (char*)p->v_store;
+  r.scales[0] = (char*)p->k_scales;
+  r.scales[1] = (char*)p->v_scales;
+  r.k_chunks = (int)((r.bytes[0] + kChunk - 1) / kChunk);
+  r.chunks = r.k_chunks + (int)((r.bytes[1] + kChunk - 1) / kChunk);
   r.n_layers = p->n_layers;
   r.n_pages = p->n_pages;
   r.err = p->dev_error;
-  const long long total = (long long)most * p->n_layers * sum, full = 8LL * p->num_sms;
+  // a number of pairs known on the device only: at most four blocks a slot, which stride
+  const long long total = (long long)most * p->n_layers * r.chunks;
+  const long long cap = n_dev ? 32LL * p->num_sms : 0x7fffffffLL;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(total < full ? total : full));
+  cfg.gridDim = dim3((unsigned)(total < cap ? total : cap));
   cfg.blockDim = dim3(kCopyThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
