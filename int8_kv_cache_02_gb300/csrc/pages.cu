@@ -8,9 +8,8 @@
 //
 // The bookkeeping of one call runs in one cluster of thread blocks (the calls read
 // a few hundred KB: a grid-wide barrier would cost more than the other SMs bring).
-// A range of entries or pages is cut into one contiguous run per thread; a rank is
-// the prefix sum over the runs before it, exchanged through distributed shared
-// memory.  The bytes of pages move in a second, grid-wide kernel, which reads its
+// A range of entries or pages is cut into one contiguous run per warp; a rank is the
+// prefix sum over the runs before it, exchanged through distributed shared memory.  The bytes of pages move in a second, grid-wide kernel, which reads its
 // list of (source, destination) pairs from device memory.
 #include <cooperative_groups.h>
 
@@ -23,8 +22,8 @@ namespace int8kv {
 namespace {
 
 constexpr int kBlocks = 8;        // blocks of the bookkeeping cluster
-constexpr int kThreads = 512;     // threads of each
-constexpr int kRuns = kBlocks * kThreads;
+constexpr int kThreads = 1024;    // threads of each
+constexpr int kWarps = kBlocks * kThreads / 32;
 
 // ---- copies -----------------------------------------------------------------
 constexpr int kCopyThreads = 256;
@@ -90,29 +89,30 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const Regions 
 }
 
 // ---- bookkeeping ------------------------------------------------------------
+// Each warp of the cluster owns a contiguous run of items, which its lanes read side by
+// side, kAhead loads in flight; ranks within 32 items come from a ballot.
+constexpr int kAhead = 8;
+constexpr unsigned kAll = 0xffffffffu;
+
 struct Ranks {
   int warp[kThreads / 32];
   int block[2];       // this block's sum, double-buffered over calls
 };
 
-// Exclusive prefix sum of v over the cluster's threads, in order; *total its sum.
-// Every thread of the cluster calls it the same number of times.
+// Exclusive prefix sum of v (the same in all lanes) over the cluster's warps, in order;
+// *total its sum.  Every warp of the cluster calls it the same number of times, and the
+// cluster meets at a barrier in it.
 __device__ __forceinline__ int cluster_rank(int v, int& total, Ranks& sh, int& phase) {
   cg::cluster_group cl = cg::this_cluster();
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  int inc = v;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, inc, off);
-    if (lane >= off) inc += o;
-  }
-  if (lane == 31) sh.warp[wid] = inc;
+  if (lane == 0) sh.warp[wid] = v;
   __syncthreads();
-  int before = 0, sum = 0;
+  const int mine = lane < kThreads / 32 ? sh.warp[lane] : 0;
+  int before = lane < wid ? mine : 0, sum = mine;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < wid) before += sh.warp[w];
-    sum += sh.warp[w];
+  for (int off = 16; off > 0; off >>= 1) {
+    before += __shfl_xor_sync(kAll, before, off);
+    sum += __shfl_xor_sync(kAll, sum, off);
   }
   if (threadIdx.x == 0) sh.block[phase] = sum;
   cl.sync();     // (also: sh.warp may be written again)
@@ -124,14 +124,15 @@ __device__ __forceinline__ int cluster_rank(int v, int& total, Ranks& sh, int& p
     total += o;
   }
   phase ^= 1;    // the other slot was read before the last cluster barrier
-  return before + inc - v;
+  return before;
 }
 
-// This thread's run [a, z) of n items.
-__device__ __forceinline__ void run_of(long long n, long long& a, long long& z) {
-  const long long per = (n + kRuns - 1) / kRuns;
-  a = per * (blockIdx.x * kThreads + threadIdx.x);
-  z = a + per < n ? a + per : n;
+// This warp's run [a, z) of n items, whole groups of `group`.
+__device__ __forceinline__ void run_of(int n, int group, int& a, int& z) {
+  const long long per = (((long long)n + group - 1) / group + kWarps - 1) / kWarps * group;
+  const long long at = per * (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5));
+  a = (int)(at < n ? at : n);
+  z = (int)(at + per < n ? at + per : n);
 }
 
 // One reference less.  A page that has none stays at 0 (flagged).
@@ -142,26 +143,45 @@ __device__ __forceinline__ void give_back(int32_t* refs, int page, int32_t* err)
   }
 }
 
-// The `want` first free pages in ascending order -> list; returns how many there are.
+// The `want` first free pages in ascending order -> list; returns how many there are of
+// them (fewer than `want` when the pool runs out).  Pools are searched a span at a time.
 __device__ __forceinline__ int free_pages(const int32_t* refs, int n_pages, int want, int32_t* list,
                                           Ranks& sh, int& phase) {
-  long long a, z;
-  run_of(n_pages, a, z);
-  int mine = 0;
-  for (long long i = a; i < z; ++i) mine += __ldcg(refs + i) == 0;
-  int n;
-  int at = cluster_rank(mine, n, sh, phase);
-  if (mine && at < want)
-    for (long long i = a; i < z && at < want; ++i)
-      if (__ldcg(refs + i) == 0) list[at++] = (int)i;
+  constexpr int SPAN = kWarps * 32 * kAhead;
+  const int lane = threadIdx.x & 31;
+  int got = 0;
+  for (int base = 0; base < n_pages && got < want; base += SPAN) {
+    const int first = base + (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * 32 * kAhead;
+    unsigned free[kAhead];
+    int mine = 0;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = first + 32 * k + lane;
+      free[k] = i < n_pages ? __ldcg(refs + i) : 1;
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      free[k] = __ballot_sync(kAll, free[k] == 0);
+      mine += __popc(free[k]);
+    }
+    int found;
+    int at = got + cluster_rank(mine, found, sh, phase);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int rank = at + __popc(free[k] & ((1u << lane) - 1));
+      if ((free[k] >> lane & 1) && rank < want) list[rank] = first + 32 * k + lane;
+      at += __popc(free[k]);
+    }
+    got += found;
+  }
   cg::this_cluster().sync();
-  return n;
+  return got < want ? got : want;
 }
 
 struct PagesArgs {
   int32_t* refs;
   int32_t* table;          // [n_seqs][max_pages]
-  int n_seqs, max_pages, n_pages, page_size;
+  int n_seqs, max_pages, n_pages, page_size, ps_log2;
   int32_t* err;
   int32_t* list;           // workspace: free pages, [n_pages]
   int32_t* src;            // workspace: pages to copy, [max(n_pages, n_seqs)] each
@@ -170,119 +190,147 @@ struct PagesArgs {
   int32_t* count;          // workspace: pairs to copy
 };
 
-// Pages that `len` positions need, at most what a row holds (more is flagged).
-__device__ __forceinline__ int pages_needed(int len, const PagesArgs& a) {
-  if (len <= 0) return 0;
-  const int n = (len - 1) / a.page_size + 1;
-  if (n > a.max_pages) {
-    flag_error(a.err, INT8KV_DEVERR_LENGTH);
-    return a.max_pages;
-  }
-  return n;
-}
+// The table in pieces of 32 entries of a row: a warp reads its run of them kBatch at a
+// time and only looks for work; the few pieces that have some are read again.  (Kernels
+// like this run their code once: unrolled handling of every piece took longer to fetch
+// than to execute.)
+constexpr int kBatch = 8;
 
 __global__ void __launch_bounds__(kThreads) resize_kernel(const PagesArgs a,
                                                           const int32_t* __restrict__ lens) {
   __shared__ Ranks sh;
   int phase = 0;
+  const int lane = threadIdx.x & 31;
+  const int per_row = (a.max_pages + 31) / 32;      // pieces of a row
   ptx::grid_launch_dependents();
   ptx::grid_dependency_wait();
-  long long lo, hi;
-  run_of((long long)a.n_seqs * a.max_pages, lo, hi);
-  int missing = 0;
-  if (lo < hi) {
-    int row = (int)(lo / a.max_pages), p = (int)(lo % a.max_pages), need = pages_needed(lens[row], a);
-    for (long long i = lo; i < hi; ++i) {
-      const int e = a.table[i];
-      if (e >= a.n_pages) {
-        flag_error(a.err, INT8KV_DEVERR_PAGE_ID);
-        a.table[i] = -1;
-      }
-      const bool has = e >= 0 && e < a.n_pages;
-      if (p < need) {
-        missing += !has;
-      } else if (has) {
-        give_back(a.refs, e, a.err);
-        a.table[i] = -1;
-      }
-      if (++p == a.max_pages && i + 1 < hi) {
-        p = 0;
-        need = pages_needed(lens[++row], a);
+  int lo, hi;
+  run_of(a.n_seqs * per_row, 1, lo, hi);
+  int missing = 0, first_missing = hi, row = lo / per_row, c = lo % per_row;
+  for (int base = lo; base < hi; base += kBatch) {
+    int e[kBatch], len[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int p = c * 32 + lane;
+      const bool in = base + k < hi && p < a.max_pages;
+      len[k] = in ? __ldg(lens + row) : 0;
+      e[k] = in ? a.table[(size_t)row * a.max_pages + p] : -1;
+      len[k] -= p << a.ps_log2;                     // > 0: the entry is needed
+      if (++c == per_row) {
+        c = 0;
+        ++row;
       }
     }
+    unsigned work = 0;      // bit k: this lane's entry of piece k goes back, or is no page
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const bool none = e[k] < 0 || e[k] >= a.n_pages;
+      missing += __popc(__ballot_sync(kAll, len[k] > 0 && none));
+      if (e[k] >= a.n_pages || (len[k] <= 0 && !none)) work |= 1u << k;
+    }
+    if (missing && first_missing == hi) first_missing = base;
+    while (work) {
+      const int k = __ffs(work) - 1, w = base + k;
+      work &= work - 1;
+      int32_t* at = a.table + (size_t)(w / per_row) * a.max_pages + w % per_row * 32 + lane;
+      if (*at >= a.n_pages) flag_error(a.err, INT8KV_DEVERR_PAGE_ID);
+      else give_back(a.refs, *at, a.err);
+      *at = -1;
+    }
   }
+  for (int r = blockIdx.x * kThreads + threadIdx.x; r < a.n_seqs; r += kBlocks * kThreads)
+    if (__ldg(lens + r) > (long long)a.max_pages << a.ps_log2) flag_error(a.err, INT8KV_DEVERR_LENGTH);
   int want;
-  int at = cluster_rank(missing, want, sh, phase);
+  int rank = cluster_rank(missing, want, sh, phase);
   if (want == 0) {            // the same for the whole cluster
     cg::this_cluster().sync();   // the others may still read this block's sum
     return;
   }
   const int n = free_pages(a.refs, a.n_pages, want, a.list, sh, phase);
-  if (missing) {
-    int row = (int)(lo / a.max_pages), p = (int)(lo % a.max_pages), need = pages_needed(lens[row], a);
-    for (long long i = lo; i < hi; ++i) {
-      if (p < need && a.table[i] < 0) {
-        if (at < n) {
-          const int page = __ldcg(a.list + at);
-          a.table[i] = page;
-          a.refs[page] = 1;
-        } else {
-          flag_error(a.err, INT8KV_DEVERR_NO_PAGE);
-        }
-        ++at;
-      }
-      if (++p == a.max_pages && i + 1 < hi) {
-        p = 0;
-        need = pages_needed(lens[++row], a);
+#pragma unroll 1
+  for (int w = first_missing; w < hi && missing > 0; ++w) {
+    const int r = w / per_row, p = w % per_row * 32 + lane;
+    int32_t* at = a.table + (size_t)r * a.max_pages + p;
+    const bool miss = p < a.max_pages && __ldg(lens + r) > p << a.ps_log2 && *at < 0;
+    const unsigned all = __ballot_sync(kAll, miss);
+    const int mine = rank + __popc(all & ((1u << lane) - 1));
+    if (miss) {
+      if (mine < n) {
+        const int page = __ldcg(a.list + mine);
+        *at = page;
+        a.refs[page] = 1;
+      } else {
+        flag_error(a.err, INT8KV_DEVERR_NO_PAGE);
       }
     }
+    rank += __popc(all);
+    missing -= __popc(all);
   }
 }
+
+// Which forks take place.  Up to kRows rows every block keeps its own marks in shared
+// memory; beyond, the cluster shares marks in the workspace.
+constexpr int kRows = 4096;
+struct Marks {
+  int* first;      // lowest fork that names a row as its child
+  int* parent;     // whether a row is some fork's parent
+  bool shared;
+  // one that names no two rows (-1) is left out silently
+  __device__ __forceinline__ bool take(const PagesArgs& a, int i, int p, int c) const {
+    if (p < 0 || c < 0 || p >= a.n_seqs || c >= a.n_seqs) return false;
+    return shared ? first[c] == i && parent[c] == 0
+                  : __ldcg(first + c) == i && __ldcg(parent + c) == 0;
+  }
+};
 
 __global__ void __launch_bounds__(kThreads) fork_kernel(const PagesArgs a, int32_t* lens, int n,
                                                         const int32_t* __restrict__ parents,
                                                         const int32_t* __restrict__ children) {
   __shared__ Ranks sh;
+  __shared__ int marks[2 * kRows];
   int phase = 0;
   cg::cluster_group cl = cg::this_cluster();
-  const int me = blockIdx.x * kThreads + threadIdx.x;
+  const int lane = threadIdx.x & 31;
   ptx::grid_launch_dependents();
   ptx::grid_dependency_wait();
-  int32_t* first = a.map;              // lowest fork that names a row as its child
-  int32_t* parent = a.map + a.n_seqs;  // whether a row is some fork's parent
-  for (int i = me; i < a.n_seqs; i += kRuns) {
-    first[i] = INT32_MAX;
-    parent[i] = 0;
+  Marks m;
+  m.shared = a.n_seqs <= kRows;
+  m.first = m.shared ? marks : a.map;
+  m.parent = m.first + a.n_seqs;
+  const int me = m.shared ? threadIdx.x : blockIdx.x * kThreads + threadIdx.x;
+  const int step = m.shared ? kThreads : kBlocks * kThreads;
+  auto meet = [&]() {
+    if (m.shared) __syncthreads();
+    else cl.sync();
+  };
+  for (int i = me; i < a.n_seqs; i += step) {
+    m.first[i] = INT32_MAX;
+    m.parent[i] = 0;
   }
-  cl.sync();
-  for (int i = me; i < n; i += kRuns) {
+  meet();
+  for (int i = me; i < n; i += step) {
     const int p = parents[i], c = children[i];
     if (p < 0 || c < 0 || p >= a.n_seqs || c >= a.n_seqs) continue;
-    atomicMin(first + c, i);
-    atomicExch(parent + p, 1);
+    atomicMin(m.first + c, i);
+    atomicExch(m.parent + p, 1);
   }
-  cl.sync();
-  // whether fork i takes place; one that names no two rows (-1) is left out silently
-  auto takes = [&](int i, int& p, int& c) {
-    p = parents[i];
-    c = children[i];
-    if (p < 0 || c < 0) return false;
-    return p < a.n_seqs && c < a.n_seqs && __ldcg(first + c) == i && __ldcg(parent + c) == 0;
-  };
+  meet();
+  const long long cap = (long long)a.max_pages * a.page_size;
   // children's rows: what they held goes back, the parent's full pages are shared
   const long long entries = (long long)n * a.max_pages;
-  for (long long w = me; w < entries; w += kRuns) {
+  for (long long w = blockIdx.x * kThreads + threadIdx.x; w < entries; w += kBlocks * kThreads) {
     const int i = (int)(w / a.max_pages), k = (int)(w % a.max_pages);
-    int p, c;
-    if (!takes(i, p, c)) {
+    const int p = parents[i], c = children[i];
+    if (!m.take(a, i, p, c)) {
       if (k == 0 && p >= 0 && c >= 0) flag_error(a.err, INT8KV_DEVERR_FORK);
       continue;
     }
-    const long long cap = (long long)a.max_pages * a.page_size;
-    const int len = (int)min((long long)max(lens[p], 0), cap);
-    if (k == 0 && lens[p] > cap) flag_error(a.err, INT8KV_DEVERR_LENGTH);
+    const int len = lens[p];
+    if (k == 0 && len > cap) flag_error(a.err, INT8KV_DEVERR_LENGTH);
+    int32_t* mine = a.table + (size_t)c * a.max_pages + k;
+    const int was = *mine;
     int e = -1;
-    if (k < len / a.page_size) {
+    if (k < min((long long)max(len, 0), cap) / a.page_size) {
       e = a.table[(size_t)p * a.max_pages + k];
       if (e < 0 || e >= a.n_pages) {
         flag_error(a.err, INT8KV_DEVERR_PAGE_ID);
@@ -291,8 +339,6 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const PagesArgs a, int32
         atomicAdd(a.refs + e, 1);
       }
     }
-    int32_t* mine = a.table + (size_t)c * a.max_pages + k;
-    const int was = *mine;
     if (was >= 0) {
       if (was < a.n_pages) give_back(a.refs, was, a.err);
       else flag_error(a.err, INT8KV_DEVERR_PAGE_ID);
@@ -300,43 +346,53 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const PagesArgs a, int32
     *mine = e;
   }
   // forks whose parent ends inside a page need a page of their own for its copy
-  long long lo, hi;
-  run_of(n, lo, hi);
+  int lo, hi;
+  run_of(n, 32, lo, hi);
   int need = 0;
-  for (long long i = lo; i < hi; ++i) {
-    int p, c, page = -1;
-    if (takes((int)i, p, c)) {
-      const int len = (int)min((long long)max(lens[p], 0), (long long)a.max_pages * a.page_size);
-      if (len % a.page_size) {
-        page = a.table[(size_t)p * a.max_pages + len / a.page_size];
-        if (page < 0 || page >= a.n_pages) {
-          flag_error(a.err, INT8KV_DEVERR_PAGE_ID);
-          page = -1;
+  for (int base = lo; base < hi; base += 32) {
+    const int i = base + lane;
+    int page = -1;
+    if (i < hi) {
+      const int p = parents[i], c = children[i];
+      if (m.take(a, i, p, c)) {
+        const long long len = min((long long)max(lens[p], 0), cap);
+        if (len % a.page_size) {
+          page = a.table[(size_t)p * a.max_pages + len / a.page_size];
+          if (page < 0 || page >= a.n_pages) {
+            flag_error(a.err, INT8KV_DEVERR_PAGE_ID);
+            page = -1;
+          }
         }
       }
+      a.src[i] = page;
     }
-    a.src[i] = page;
-    need += page >= 0;
+    need += __popc(__ballot_sync(kAll, page >= 0));
   }
   int want;
   int at = cluster_rank(need, want, sh, phase);
   int got = 0;
   if (want) got = free_pages(a.refs, a.n_pages, want, a.list, sh, phase);
   else cl.sync();     // the others may still read this block's sum
-  for (long long i = lo; i < hi; ++i) {
-    int p, c, page = -1;
-    if (takes((int)i, p, c)) {
-      int len = (int)min((long long)max(lens[p], 0), (long long)a.max_pages * a.page_size);
-      if (a.src[i] >= 0) {
-        if (at < got) {
-          page = __ldcg(a.list + at);
+  for (int base = lo; base < hi; base += 32) {
+    const int i = base + lane;
+    const bool copies = i < hi && a.src[i] >= 0;
+    const unsigned all = __ballot_sync(kAll, copies);
+    const int rank = at + __popc(all & ((1u << lane) - 1));
+    at += __popc(all);
+    if (i >= hi) continue;
+    const int p = parents[i], c = children[i];
+    int page = -1;
+    if (m.take(a, i, p, c)) {
+      int len = (int)min((long long)max(lens[p], 0), cap);
+      if (copies) {
+        if (rank < got) {
+          page = __ldcg(a.list + rank);
           a.refs[page] = 1;
           a.table[(size_t)c * a.max_pages + len / a.page_size] = page;
         } else {     // no page for the rest: the child ends with the shared ones
           flag_error(a.err, INT8KV_DEVERR_NO_PAGE);
           len -= len % a.page_size;
         }
-        ++at;
       }
       lens[c] = len;
     }
@@ -344,58 +400,77 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const PagesArgs a, int32
   }
 }
 
+// Ids [0, used) are to be the used ones.  Free ids there (holes) are filled, in order, with
+// the used pages from `used` on (movers).  A free id i < used is hole number i - (used
+// pages before i); a used id i >= used is mover number (used pages before i) - (used
+// pages below `used`), and those are `used` less the holes.
 __global__ void __launch_bounds__(kThreads) compact_kernel(const PagesArgs a, int32_t* refs_out,
                                                            int32_t* table_out, int32_t* n_used) {
   __shared__ Ranks sh;
   int phase = 0;
   cg::cluster_group cl = cg::this_cluster();
+  const int lane = threadIdx.x & 31;
+  const unsigned before_me = (1u << lane) - 1;
   ptx::grid_launch_dependents();
   ptx::grid_dependency_wait();
-  long long lo, hi;
-  run_of(a.n_pages, lo, hi);
+  int lo, hi;
+  run_of(a.n_pages, 32, lo, hi);
   int mine = 0;
-  for (long long i = lo; i < hi; ++i) mine += a.refs[i] > 0;
-  int used;
-  const int below = cluster_rank(mine, used, sh, phase);     // used pages before the run
-  // pages [0, used) are to be the used ones: free ids there are filled, in order, with
-  // the used pages from there on.  Used pages before `used` number used - movers.
-  long long cut = used < lo ? lo : used > hi ? hi : used;     // run's first id >= used
-  int holes = 0;
-  for (long long i = lo; i < cut; ++i) holes += a.refs[i] <= 0;
-  int n;
-  int hole = cluster_rank(holes, n, sh, phase);               // n: pages to move
-  // of the run's used pages, those from `cut` on move
-  int low = 0;
-  for (long long i = lo; i < cut; ++i) low += a.refs[i] > 0;
-  int mover = below + low - (used - n);                       // rank of the run's first mover
-  const int first_mover = mover;
-  for (long long i = lo; i < cut; ++i) {
-    const int r = a.refs[i];
-    a.map[i] = r > 0 ? (int)i : -1;
-    if (r > 0) refs_out[i] = r;      // (a hole's count comes with the page that fills it)
-    else a.dst[hole++] = (int)i;
+  for (int base = lo; base < hi; base += 32 * kAhead) {
+    int r[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = base + 32 * k + lane;
+      r[k] = i < hi ? a.refs[i] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) mine += __popc(__ballot_sync(kAll, r[k] > 0));
   }
-  for (long long i = cut; i < hi; ++i)
-    if (a.refs[i] > 0) a.src[mover++] = (int)i;
+  int used;
+  const int before = cluster_rank(mine, used, sh, phase);     // used pages before the run
+  int holes = 0, at = before;
+  for (int base = lo; base < hi && base < used; base += 32) {
+    const int i = base + lane;
+    const int r = i < hi && i < used ? a.refs[i] : 0;
+    const unsigned all = __ballot_sync(kAll, r > 0);
+    if (i < hi && i < used) {
+      a.map[i] = r > 0 ? i : -1;
+      if (r > 0) refs_out[i] = r;      // (a hole's count comes with the page that fills it)
+      else a.dst[i - (at + __popc(all & before_me))] = i;
+      holes += r <= 0;
+    }
+    at += __popc(all);
+  }
+  int n;
+  holes = __reduce_add_sync(kAll, holes);
+  cluster_rank(holes, n, sh, phase);       // n: pages to move (and a.dst is there)
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     *n_used = used;
     *a.count = n;
   }
-  cl.sync();
-  mover = first_mover;
-  for (long long i = cut; i < hi; ++i) {
-    const int r = a.refs[i];
-    int to = -1;
-    if (r > 0) {
-      to = __ldcg(a.dst + mover++);
-      refs_out[to] = r;
+  // the run's pages from `used` on: `at` counts the used ones before them
+  const int from = lo > used ? lo : used;
+  if (lo >= used) at = before;
+  for (int base = from; base < hi; base += 32) {
+    const int i = base + lane;
+    const int r = i < hi ? a.refs[i] : 0;
+    const unsigned all = __ballot_sync(kAll, r > 0);
+    if (i < hi) {
+      int to = -1;
+      if (r > 0) {
+        const int rank = at + __popc(all & before_me) - (used - n);
+        to = __ldcg(a.dst + rank);
+        a.src[rank] = i;
+        refs_out[to] = r;
+      }
+      a.map[i] = to;
+      refs_out[i] = 0;
     }
-    a.map[i] = to;
-    refs_out[i] = 0;
+    at += __popc(all);
   }
   cl.sync();
   const long long entries = (long long)a.n_seqs * a.max_pages;
-  for (long long i = blockIdx.x * kThreads + threadIdx.x; i < entries; i += kRuns) {
+  for (long long i = blockIdx.x * kThreads + threadIdx.x; i < entries; i += kBlocks * kThreads) {
     int e = a.table[i];
     if (e >= 0) {
       e = e < a.n_pages ? __ldcg(a.map + e) : -1;
@@ -483,6 +558,9 @@ int prepare(const int8kv_pool* pool, const int32_t* refs, const int32_t* table, 
             int max_pages, void* ws, size_t ws_bytes, PagesArgs* a) {
   if (!pool) return INT8KV_ERR_NULL_PTR;
   if (n_seqs < 0 || max_pages <= 0) return INT8KV_ERR_INVALID_ARG;
+  if ((long long)n_seqs * (max_pages / 32 + 1) > INT32_MAX / 2 ||
+      (long long)max_pages * pool->page_size > INT32_MAX)     // pieces and positions count in 32 bits
+    return INT8KV_ERR_UNSUPPORTED;
   if (!refs || (n_seqs > 0 && !table)) return INT8KV_ERR_NULL_PTR;
   if (!ws || ws_bytes < workspace(pool, n_seqs, nullptr, nullptr)) return INT8KV_ERR_WORKSPACE;
   if (((uintptr_t)ws & 15) != 0) return INT8KV_ERR_ALIGNMENT;
@@ -492,6 +570,7 @@ int prepare(const int8kv_pool* pool, const int32_t* refs, const int32_t* table, 
   a->max_pages = max_pages;
   a->n_pages = pool->n_pages;
   a->page_size = pool->page_size;
+  for (a->ps_log2 = 0; 1 << a->ps_log2 < pool->page_size;) ++a->ps_log2;
   a->err = pool->dev_error;
   workspace(pool, n_seqs, a, ws);
   return INT8KV_OK;
