@@ -164,6 +164,10 @@ def kv_quant_append(pool, layer, k_new, v_new, seq_pos, page_table, stream=None)
     n_seqs, n_new = k_new.shape[0], k_new.shape[1]
     _block_rows(pool, k_new, (n_seqs, n_new), "k_new")
     _block_rows(pool, v_new, (n_seqs, n_new), "v_new")
+    if getattr(pool, "block", False):
+        _shape(seq_pos, (n_seqs,), "seq_pos")
+        _shape(page_table, (n_seqs, page_table.shape[-1]), "page_table")
+        _here(pool, seq_pos, page_table)
     _check(lib().kv_quant_append(pool.handle, layer, _dev(k_new, torch.float16, "k_new"),
                                  _dev(v_new, torch.float16, "v_new"), n_seqs, n_new,
                                  _dev(seq_pos, torch.int32, "seq_pos"),
@@ -190,7 +194,7 @@ def attn_decode_int8(pool, layer, q, seq_lens, page_table, out, workspace=None, 
     """q fp16 [B][H][D]; seq_lens int32 [B]; page_table int32 [B][max_pages];
     out fp32 [B][H][D]; workspace uint8 tensor (any contents) or None."""
     B, H = q.shape[0], q.shape[1]
-    _block_call(pool, q, seq_lens, page_table, out)
+    _block_call(pool, q, seq_lens, page_table, out, workspace)
     ws = _dev(workspace, torch.uint8, "workspace") if workspace is not None else None
     nbytes = workspace.numel() if workspace is not None else 0
     _check(lib().attn_decode_int8(pool.handle, layer, _dev(q, torch.float16, "q"), B, H,
@@ -221,7 +225,7 @@ def attn_decode_append_int8(pool, layer, q, k_new, v_new, seq_lens, page_table, 
     B, H = q.shape[0], q.shape[1]
     _block_rows(pool, k_new, (B,), "k_new")
     _block_rows(pool, v_new, (B,), "v_new")
-    _block_call(pool, q, seq_lens, page_table, out)
+    _block_call(pool, q, seq_lens, page_table, out, workspace)
     ws = _dev(workspace, torch.uint8, "workspace") if workspace is not None else None
     nbytes = workspace.numel() if workspace is not None else 0
     _check(lib().attn_decode_append_int8(pool.handle, layer, _dev(q, torch.float16, "q"),
@@ -242,7 +246,7 @@ def attn_decode_multi_int8(pool, layer, q, seq_lens, page_table, out, workspace=
     seq_lens[b] - q_len + i.  out: fp32 [B][q_len][H][D].  The workspace is sized
     by attn_decode_workspace_bytes(B * q_len, H, ...)."""
     B, Q, H = q.shape[0], q.shape[1], q.shape[2]
-    _block_call(pool, q, seq_lens, page_table, out)
+    _block_call(pool, q, seq_lens, page_table, out, workspace)
     ws = _dev(workspace, torch.uint8, "workspace") if workspace is not None else None
     nbytes = workspace.numel() if workspace is not None else 0
     _check(lib().attn_decode_multi_int8(pool.handle, layer, _dev(q, torch.float16, "q"), B, Q, H,
@@ -285,14 +289,23 @@ def kv_pool_set_decode_kernel(pool, kind):
     _check(lib().kv_pool_set_decode_kernel(pool.handle, int(kind)), "kv_pool_set_decode_kernel")
 
 
+def _here(pool, *tensors):
+    """Block-scaled pools and the page calls: tensors of the pool's device, which is current."""
+    at = pool.device_index
+    for t in tensors:
+        if t is not None and t.is_cuda and t.get_device() != at:
+            raise ValueError(f"a tensor is on device {t.get_device()}, the pool on {at}")
+
+
 def _block_rows(pool, t, lead, name):
     """A block-scaled pool's K/V rows have the shape lead + [n_kv_heads][head_dim]."""
     if getattr(pool, "block", False):
         _shape(t, (*lead, pool.n_kv_heads, pool.head_dim), name)
+        _here(pool, t)
 
 
-def _block_call(pool, q, seq_lens, page_table, out):
-    """Shapes of a decode call on a block-scaled pool."""
+def _block_call(pool, q, seq_lens, page_table, out, workspace=None):
+    """Shapes and devices of a decode call on a block-scaled pool."""
     if getattr(pool, "block", False):
         shape = q.shape
         if shape[-1] != pool.head_dim:
@@ -301,6 +314,7 @@ def _block_call(pool, q, seq_lens, page_table, out):
         _shape(seq_lens, shape[:1], "seq_lens")
         if page_table.shape[:-1] != shape[:1]:
             raise ValueError(f"page_table must have shape [{shape[0]}, max_pages]")
+        _here(pool, q, seq_lens, page_table, out, workspace)
 
 
 def _host_lens(seq_lens):
@@ -362,6 +376,7 @@ def kv_pages_copy(pool, src, dst, stream=None):
     """Copy page src[i] of every layer, codes and scales, to page dst[i] (int32 [n])."""
     s, d = _dev(src, torch.int32, "src"), _dev(dst, torch.int32, "dst")
     _shape(dst, (src.numel(),), "dst")
+    _here(pool, src, dst)
     _check(lib().kv_pages_copy(pool.handle, src.numel(), s, d, _stream(stream)), "kv_pages_copy")
 
 
@@ -373,6 +388,7 @@ def kv_pages_resize(pool, page_refs, page_table, seq_lens, workspace, stream=Non
     w = _dev(workspace, torch.uint8, "workspace")
     _shape(page_refs, (pool.n_pages,), "page_refs")
     _shape(seq_lens, (page_table.shape[0],), "seq_lens")
+    _here(pool, page_refs, page_table, seq_lens, workspace)
     _check(lib().kv_pages_resize(pool.handle, r, t, page_table.shape[0], page_table.shape[1], n,
                                  w, workspace.numel(), _stream(stream)), "kv_pages_resize")
 
@@ -388,6 +404,7 @@ def kv_pages_fork(pool, page_refs, page_table, seq_lens, parents, children, work
     _shape(page_refs, (pool.n_pages,), "page_refs")
     _shape(seq_lens, (page_table.shape[0],), "seq_lens")
     _shape(children, (parents.numel(),), "children")
+    _here(pool, page_refs, page_table, seq_lens, parents, children, workspace)
     _check(lib().kv_pages_fork(pool.handle, r, t, page_table.shape[0], page_table.shape[1], n,
                                parents.numel(), p, c, w, workspace.numel(), _stream(stream)),
            "kv_pages_fork")
@@ -405,6 +422,8 @@ def kv_pages_compact(pool, page_refs, page_table, page_refs_out, page_table_out,
     _shape(page_refs, (pool.n_pages,), "page_refs")
     _shape(page_refs_out, (pool.n_pages,), "page_refs_out")
     _shape(page_table_out, page_table.shape, "page_table_out")
+    _shape(n_used, (1,), "n_used")
+    _here(pool, page_refs, page_table, page_refs_out, page_table_out, n_used, workspace)
     _check(lib().kv_pages_compact(pool.handle, r, t, page_table.shape[0], page_table.shape[1], ro,
                                   to, u, w, workspace.numel(), _stream(stream)),
            "kv_pages_compact")
@@ -432,6 +451,7 @@ class KVPool:
         if isinstance(variant, str):
             variant = VARIANTS[variant]
         dev = torch.device("cuda", torch.cuda.current_device() if device is None else device)
+        self.device_index = dev.index
         shape = (n_layers, n_pages, n_kv_heads, page_size, head_dim)
         self.block = variant in (K8V8_BLOCK, F8_BLOCK)
         if self.block:

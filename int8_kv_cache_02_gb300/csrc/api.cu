@@ -46,10 +46,6 @@ bool variant_stores(int variant, bool* k8, bool* v8, bool* k4, bool* v4) {
   }
 }
 
-bool block_variant(int variant) {
-  return variant == INT8KV_K8V8_BLOCK || variant == INT8KV_F8_BLOCK;
-}
-
 // group_size of a block-scaled pool: positions that share a scale.
 bool valid_block(int page_size, int gs) {
   return (gs == 16 || gs == 32 || gs == 64 || gs == 128) && gs <= page_size;
@@ -188,12 +184,17 @@ int decode_splits_heuristic(const int8kv_pool* pool, long long units, int max_ct
 }
 
 // Splits of a block-scaled pool's decode call: the balanced schedule runs up to
-// units * (n - 1) + 1 blocks, so n is the least that fills the device.  A context
-// of one tile per warp is left to one block per unit: it needs no combine.
+// units * (n - 1) + 1 blocks, so n is the least that fills the device.  Short contexts
+// are left to one block per unit, which needs no combine.  Measured, in us, one
+// block per unit against equal shares: 2 x 8 units of D 128 at 256 / 512 / 1024 / 2048
+// positions 5.8, 7.8, 11.7, 19.5 against 8.0, 9.9, 10.1, 10.7; 64 x 8 units of D 128 at
+// 512 / 1024 / 2048 14.9, 27.9, 46.9 against 19.9, 30.3, 48.6; 2 units of D 256 at 256 /
+// 512 / 1024 7.5, 11.1, 18.1 against 9.6, 9.9, 9.9; one of D 64 at 1024 / 2048 8.9, 13.6
+// against 9.5, 9.7.
 static int block_splits(const int8kv_pool* pool, long long units, int max_ctx) {
-  if (max_ctx <= kBlockSingle) return 1;
+  if ((long long)max_ctx * pool->head_dim <= kBlockSingle) return 1;
   // (query windows may take 16 columns to a unit: up to twice the splits per unit)
-  const long long n = (pool->head_dim <= 128 ? 2 : 1) * ((pool->block_resident + units - 2) / units) + 1;
+  const long long n = (pool->head_dim <= 128 ? 2 : 1) * ((pool->resident[kBlockKernel] + units - 2) / units) + 1;
   return (int)(n < 2 ? 2 : n > kMaxSplits ? kMaxSplits : n);
 }
 
@@ -206,14 +207,14 @@ static int block_shares(const int8kv_pool* pool, long long units, int width, lon
   long long n = units * (n_splits - 1) + 1;
   const long long fit = rows / width - units + 1;
   if (n > fit) n = fit;
-  if (n > pool->block_resident) n = pool->block_resident;
+  if (n > pool->resident[kBlockKernel]) n = pool->resident[kBlockKernel];
   return (int)(n < 1 ? 1 : n);
 }
 
 int decode_auto_splits(const int8kv_pool* pool, int batch, int q_len, int G, int max_pages,
                        int window, size_t max_workspace) {
   const int n_cg = (q_len * G + 7) / 8;   // blocks per (sequence, kv head) sharing the columns
-  if (pool->block) {
+  if (is_block(pool)) {
     const long long cap = (long long)max_pages * pool->page_size;
     int n = block_splits(pool, (long long)batch * n_cg * pool->n_kv_heads,
                          (int)(window > 0 && window < cap ? window : cap < INT32_MAX ? cap : INT32_MAX));
@@ -320,10 +321,7 @@ int kv_pool_create(int8kv_pool** out, int n_layers, int n_kv_heads, int head_dim
   p->n_kv_heads = n_kv_heads;
   p->head_dim = head_dim;
   p->group_size = group_size;
-  p->block = block_variant(variant);
-  p->f8 = variant == INT8KV_F8_BLOCK;
-  p->block_resident = 0;
-  p->n_groups = p->block ? 1 : head_dim / group_size;
+  p->n_groups = block_variant(variant) ? 1 : head_dim / group_size;
   p->page_size = page_size;
   p->n_pages = n_pages;
   p->variant = variant;
@@ -342,9 +340,9 @@ int kv_pool_create(int8kv_pool** out, int n_layers, int n_kv_heads, int head_dim
   p->decode_kernel = INT8KV_DECODE_AUTO;
   for (int k = 0; k < 4; ++k) p->resident[k] = 0;
   p->expire_polls = 0;
-  if (p->block) {
-    p->block_resident = block_decode_resident(head_dim, p->f8);
-    if (p->block_resident <= 0) {
+  if (is_block(p)) {
+    p->resident[kBlockKernel] = block_decode_resident(head_dim, is_f8(p));
+    if (p->resident[kBlockKernel] <= 0) {
       delete p;
       return INT8KV_ERR_CUDA;
     }
@@ -378,9 +376,12 @@ int kv_quant_append(const int8kv_pool* pool, int layer, const uint16_t* k_new,
   if ((long long)n_seqs * n_new == 0) return INT8KV_OK;
   if (!k_new || !v_new || !seq_pos || !page_table) return INT8KV_ERR_NULL_PTR;
   if (!aligned16(k_new) || !aligned16(v_new)) return INT8KV_ERR_ALIGNMENT;
-  if (pool->block) return launch_status(launch_block_append(
-      block_view(pool, layer), pool->head_dim, pool->f8, k_new, v_new, n_seqs, n_new, seq_pos, 0,
-      page_table, max_pages_per_seq, (cudaStream_t)stream));
+  if (is_block(pool)) {
+    if (!on_current_device(pool)) return INT8KV_ERR_INVALID_ARG;
+    return launch_status(launch_block_append(
+        block_view(pool, layer), pool->head_dim, is_f8(pool), k_new, v_new, n_seqs, n_new, seq_pos, 0,
+        page_table, max_pages_per_seq, (cudaStream_t)stream));
+  }
   const cudaError_t e = launch_quant_append(layer_view(pool, layer), k_new, v_new, n_seqs, n_new,
                                             seq_pos, page_table, max_pages_per_seq, pool->k_int8,
                                             pool->v_int8, (cudaStream_t)stream);
@@ -391,7 +392,7 @@ int kv_pool_set_decode_kernel(int8kv_pool* pool, int kind) {
   if (!pool) return INT8KV_ERR_NULL_PTR;
   if (kind != INT8KV_DECODE_AUTO && kind != INT8KV_DECODE_WARP_MMA && kind != INT8KV_DECODE_SIMT)
     return INT8KV_ERR_INVALID_ARG;
-  if (pool->block)     // one kernel serves these pools
+  if (is_block(pool))     // one kernel serves these pools
     return kind == INT8KV_DECODE_AUTO ? INT8KV_OK : INT8KV_ERR_UNSUPPORTED;
   const PoolView v = layer_view(pool, 0);
   if (kind == INT8KV_DECODE_WARP_MMA && !(pool->has_tmaps && decode_mma_supported(v, 1)))
@@ -403,7 +404,7 @@ int kv_pool_set_decode_kernel(int8kv_pool* pool, int kind) {
 int attn_decode_n_splits(const int8kv_pool* pool, int batch, int max_ctx) {
   if (!pool) return INT8KV_ERR_NULL_PTR;
   if (batch <= 0 || max_ctx < 0) return INT8KV_ERR_INVALID_ARG;
-  if (pool->block) return block_splits(pool, (long long)batch * pool->n_kv_heads, max_ctx);
+  if (is_block(pool)) return block_splits(pool, (long long)batch * pool->n_kv_heads, max_ctx);
   return decode_splits_heuristic(pool, (long long)batch * pool->n_kv_heads, max_ctx, kMaxSplits);
 }
 
@@ -469,7 +470,7 @@ static int decode_entry(const int8kv_pool* pool, int layer, const uint16_t* q,
   const int G = n_heads / pool->n_kv_heads;
   if (G > 8) return INT8KV_ERR_UNSUPPORTED;
   // a query window runs on the warp-level tensor-core kernel only
-  if (q_len > 1 && !pool->block && decode_kernel_for(pool, G) != INT8KV_DECODE_WARP_MMA)
+  if (q_len > 1 && !is_block(pool) && decode_kernel_for(pool, G) != INT8KV_DECODE_WARP_MMA)
     return INT8KV_ERR_UNSUPPORTED;
   if (batch == 0) return INT8KV_OK;
   if (!q || !seq_lens || !page_table || !out) return INT8KV_ERR_NULL_PTR;
@@ -487,10 +488,13 @@ static int decode_entry(const int8kv_pool* pool, int layer, const uint16_t* q,
     if (!aligned16(workspace)) return INT8KV_ERR_ALIGNMENT;
   }
   const float scale = softmax_scale != 0.f ? softmax_scale : 1.0f / std::sqrt((float)pool->head_dim);
-  if (pool->block) {
+  if (is_block(pool)) {
+    if (!on_current_device(pool)) return INT8KV_ERR_INVALID_ARG;
+    if ((long long)max_pages_per_seq * pool->page_size > kBlockMostPositions)
+      return INT8KV_ERR_UNSUPPORTED;
     cudaStream_t s = (cudaStream_t)stream;
     if (k_new) {
-      const cudaError_t e = launch_block_append(block_view(pool, layer), pool->head_dim, pool->f8,
+      const cudaError_t e = launch_block_append(block_view(pool, layer), pool->head_dim, is_f8(pool),
                                                 k_new, v_new, batch, 1, seq_lens, -1, page_table,
                                                 max_pages_per_seq, s);
       if (e != cudaSuccess) return launch_status(e);
@@ -522,7 +526,7 @@ static int decode_entry(const int8kv_pool* pool, int layer, const uint16_t* q,
     if (units * most > INT32_MAX / 2) d.shares = 0;
     d.scale_log2 = scale * 1.4426950408889634f;
     d.appended = k_new != nullptr;
-    return launch_status(launch_block_decode(d, pool->head_dim, pool->f8, s));
+    return launch_status(launch_block_decode(d, pool->head_dim, is_f8(pool), s));
   }
   a.pool = layer_view(pool, layer);
   a.q = q;
@@ -549,7 +553,7 @@ int attn_prefill_n_splits(const int8kv_pool* pool, int n_new, int n_heads, int s
   if (n_new <= 0 || n_heads <= 0 || start_pos < 0 || n_heads % pool->n_kv_heads != 0)
     return INT8KV_ERR_INVALID_ARG;
   const int G = n_heads / pool->n_kv_heads;
-  if (G > 8 || pool->block) return INT8KV_ERR_UNSUPPORTED;
+  if (G > 8 || is_block(pool)) return INT8KV_ERR_UNSUPPORTED;
   // One block per SM at a time: (query tiles of 128 rows) x kv heads x splits
   // blocks run in ceil(blocks / SMs) waves of ceil(pages / splits) pages each.
   // Take the split count with the shortest such chain, counting two pages of
@@ -624,7 +628,7 @@ int attn_prefill_chunk_int8(const int8kv_pool* pool, int layer, const uint16_t* 
 
 int kv_pool_test_expire_waits(int8kv_pool* pool, uint32_t max_polls) {
   if (!pool) return INT8KV_ERR_NULL_PTR;
-  if (max_polls != 0 && pool->block) return INT8KV_ERR_UNSUPPORTED;
+  if (max_polls != 0 && is_block(pool)) return INT8KV_ERR_UNSUPPORTED;
   if (max_polls != 0 && decode_kernel_for(pool, 1) != INT8KV_DECODE_WARP_MMA)
     return INT8KV_ERR_UNSUPPORTED;
   pool->expire_polls = max_polls;

@@ -15,6 +15,24 @@
 
 namespace int8kv {
 
+// ---- host side: what a pool's variant says, and limits ----------------------
+inline bool block_variant(int variant) {
+  return variant == INT8KV_K8V8_BLOCK || variant == INT8KV_F8_BLOCK;
+}
+inline bool is_block(const int8kv_pool* p) { return block_variant(p->variant); }
+inline bool is_f8(const int8kv_pool* p) { return p->variant == INT8KV_F8_BLOCK; }
+
+constexpr int kBlockKernel = 2;       // index of its decode kernel in int8kv_pool::resident
+constexpr int kBlockSingle = 65536;   // values (positions x head_dim) of a context decoded in one
+                                      // block per unit
+constexpr int kBlockMostPositions = 1 << 30;   // of a page-table row (positions count in 32 bits)
+
+// Whether the pool's device is the current one, on which the launches go.
+inline bool on_current_device(const int8kv_pool* p) {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess && dev == p->device;
+}
+
 // The layer of a block-scaled pool that a kernel works on.
 struct BlockView {
   uint8_t* k;        // codes [n_pages][Hkv][ps][D], one byte each

@@ -105,11 +105,12 @@ __device__ __forceinline__ int unit_tiles(int lo, int hi) {
   return hi > lo ? (hi - 1) / kTile - lo / kTile + 1 : 0;
 }
 
-// Length of sequence b's units in the line.
-__device__ __forceinline__ int line_length(const BlockDecodeArgs& a, int b, int per_seq, int start) {
-  int lo, hi;
-  unit_range(a, b, lo, hi);
-  const int nt = unit_tiles(lo, hi);
+// Length in the line of the units of a sequence of length `len`.
+__device__ __forceinline__ int line_length(const BlockDecodeArgs& a, int len, int per_seq,
+                                           int start) {
+  const int cap = a.max_pages << a.pool.ps_log2;
+  const int hi = len < cap ? len : cap;
+  const int nt = unit_tiles(a.window > 0 && hi > a.window ? hi - a.window : 0, hi);
   return nt ? (nt + start) * per_seq : 0;
 }
 
@@ -123,8 +124,14 @@ __device__ __forceinline__ Place find_share(const BlockDecodeArgs& a, int per_se
                                             int least) {
   const int lane = threadIdx.x & 31, run = (a.B + 31) / 32;
   int sum = 0;
-  for (int i = 0; i < run; ++i)
-    if (lane * run + i < a.B) sum += line_length(a, lane * run + i, per_seq, start);
+  for (int i = 0; i < run; i += 8) {      // (eight lengths under way)
+    int len[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      len[k] = i + k < run && lane * run + i + k < a.B ? __ldg(a.seq_lens + lane * run + i + k) : 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum += line_length(a, len[k], per_seq, start);
+  }
   int inc = sum;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -149,7 +156,7 @@ __device__ __forceinline__ Place find_share(const BlockDecodeArgs& a, int per_se
   const bool mine = p.at >= base && p.at < inc;
   if (mine && run > 1)
     for (;;) {
-      const int n = line_length(a, b, per_seq, start);
+      const int n = line_length(a, __ldg(a.seq_lens + b), per_seq, start);
       if (p.at < base + n) break;
       base += n;
       ++b;

@@ -13,9 +13,6 @@
 struct int8kv_pool {
   int n_layers, n_kv_heads, head_dim, group_size, n_groups, page_size, n_pages, variant;
   bool k_int8, v_int8;
-  bool block;        // one fp32 scale per (group_size positions, kv head), 8-bit codes
-  bool f8;           // ... and the codes are e4m3 (else int8)
-  int block_resident;   // ... and blocks of its decode kernel resident at once
   bool k_q4, v_q4;   // K / V rotated (FWHT) and stored as Q4_0 (4-bit codes, fp16 per 32)
   void* k_store;
   void* v_store;

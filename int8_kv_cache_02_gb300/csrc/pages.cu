@@ -13,6 +13,7 @@
 // list of (source, destination) pairs from device memory.
 #include <cooperative_groups.h>
 
+#include "block_common.cuh"
 #include "common.cuh"
 #include "ptx.cuh"
 
@@ -564,6 +565,7 @@ int prepare(const int8kv_pool* pool, const int32_t* refs, const int32_t* table, 
   if (!refs || (n_seqs > 0 && !table)) return INT8KV_ERR_NULL_PTR;
   if (!ws || ws_bytes < workspace(pool, n_seqs, nullptr, nullptr)) return INT8KV_ERR_WORKSPACE;
   if (((uintptr_t)ws & 15) != 0) return INT8KV_ERR_ALIGNMENT;
+  if (!on_current_device(pool)) return INT8KV_ERR_INVALID_ARG;
   a->refs = const_cast<int32_t*>(refs);
   a->table = const_cast<int32_t*>(table);
   a->n_seqs = n_seqs;
@@ -601,6 +603,7 @@ int kv_pages_copy(const int8kv_pool* pool, int n, const int32_t* src, const int3
   if (n < 0) return INT8KV_ERR_INVALID_ARG;
   if (n == 0) return INT8KV_OK;
   if (!src || !dst) return INT8KV_ERR_NULL_PTR;
+  if (!on_current_device(pool)) return INT8KV_ERR_INVALID_ARG;
   return status(launch_copy(pool, src, dst, n, nullptr, (cudaStream_t)stream));
 }
 

@@ -29,6 +29,7 @@
 
 #include <cuda_runtime.h>
 
+#include "block_common.cuh"
 #include "common.cuh"
 #include "internal.h"
 
@@ -196,7 +197,7 @@ int kv_pool_image_bytes(const int8kv_pool* pool, int n_seqs, const int32_t* seq_
                         size_t* out_bytes) {
   if (!pool || !out_bytes || (n_seqs > 0 && !seq_lens)) return INT8KV_ERR_NULL_PTR;
   if (n_seqs < 0) return INT8KV_ERR_INVALID_ARG;
-  if (pool->block) return INT8KV_ERR_UNSUPPORTED;   // format 3 has scales per position
+  if (is_block(pool)) return INT8KV_ERR_UNSUPPORTED;   // format 3 has scales per position
   for (int b = 0; b < n_seqs; ++b)
     if (seq_lens[b] < 0) return INT8KV_ERR_INVALID_ARG;
   *out_bytes = head_bytes(n_seqs) + payload_bytes(shape_of(pool), n_seqs, seq_lens);
@@ -253,7 +254,7 @@ int kv_pool_load(const int8kv_pool* pool, const void* image, size_t image_bytes,
   if (!pool || !image || !staging || (n_seqs > 0 && (!page_table || !seq_lens)))
     return INT8KV_ERR_NULL_PTR;
   if (n_seqs < 0 || max_pages_per_seq <= 0) return INT8KV_ERR_INVALID_ARG;
-  if (pool->block) return INT8KV_ERR_UNSUPPORTED;
+  if (is_block(pool)) return INT8KV_ERR_UNSUPPORTED;
   if (!aligned16(staging)) return INT8KV_ERR_ALIGNMENT;
   const unsigned char* h = (const unsigned char*)image;
   const size_t hb = head_bytes(n_seqs);
