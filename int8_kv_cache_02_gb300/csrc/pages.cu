@@ -214,9 +214,8 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const PagesArgs a,
     for (int k = 0; k < kBatch; ++k) {
       const int p = c * 32 + lane;
       const bool in = base + k < hi && p < a.max_pages;
-      len[k] = in ? __ldg(lens + row) : 0;
+      len[k] = in ? __ldg(lens + row) - (p << a.ps_log2) : 0;      // > 0: the entry is needed
       e[k] = in ? a.table[(size_t)row * a.max_pages + p] : -1;
-      len[k] -= p << a.ps_log2;                     // > 0: the entry is needed
       if (++c == per_row) {
         c = 0;
         ++row;

@@ -80,6 +80,7 @@ def decode(dev, layer, q, lens, pt, window=0, n_splits=0, scale=0.0):
     from int8_kv_cache_02_gb300 import binding
     B, Q, H, D = q.shape
     ws = dev.decode_workspace(B * Q, H, n_splits or 256)
+    ws.fill_(0xFF)          # any contents will do
     out = torch.full((B, Q, H, D), float("nan"), dtype=torch.float32, device="cuda")
     lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
     if Q == 1:

@@ -157,7 +157,8 @@ def test_decode_windows(kind, window):
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("D,Hkv,G,Q", [(64, 2, 4, 2), (128, 2, 3, 3), (128, 1, 8, 5),
-                                       (256, 2, 8, 2), (64, 1, 1, 64), (256, 1, 5, 7)])
+                                       (256, 2, 8, 2), (64, 1, 1, 64), (256, 1, 5, 7),
+                                       (128, 2, 1, 3), (128, 1, 8, 64)])
 def test_query_windows(kind, D, Hkv, G, Q):
     lens = [0, 1, Q, 70, 403]        # queries at negative positions get zero rows
     q, pt, dev, orc = _filled(kind, D + Q, lens, Hkv, G, D, 16, 32, Q)
@@ -165,6 +166,72 @@ def test_query_windows(kind, D, Hkv, G, Q):
     for n_splits in (0, 1, 2, 9):
         bu.assert_close(bu.decode(dev, 0, q, lens, pt, n_splits=n_splits), ref,
                         what=f"splits {n_splits}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_layers_and_pages_behind_four_gigabytes(kind):
+    """Two layers, the second one's pages at byte offsets past 2^32 in each store."""
+    from int8_kv_cache_02_gb300 import binding as b
+    Hkv, D, ps, n_pages, lens = 8, 128, 64, 40000, [130, 65]
+    dev = b.KVPool(2, Hkv, D, 32, ps, n_pages, bu.KINDS[kind])
+    assert dev.k_store.numel() > 2 ** 32
+    pt = torch.tensor([[39999, 5, 39900], [39998, 39000, -1]], dtype=torch.int32)
+    small = torch.tensor([[0, 1, 2], [3, 4, -1]], dtype=torch.int32)
+    orc = bu.oblock.BlockPool(2, Hkv, D, 32, ps, 5, kind)
+    g = torch.Generator().manual_seed(3)
+    q = torch.randn((2, 1, 2 * Hkv, D), generator=g).half()
+    for layer in (0, 1):
+        for i, n in enumerate(lens):
+            k, v = _rows(g, 1, n, Hkv, D)
+            bu.append(dev, None, layer, k, v, [0], pt[i:i + 1])
+            orc.append(layer, k.numpy(), v.numpy(), [0], small[i:i + 1].numpy())
+    for layer in (0, 1):
+        for n_splits in (1, 6):
+            out = bu.decode(dev, layer, q, lens, pt, n_splits=n_splits)
+            bu.assert_close(out, bu.reference(orc, layer, q, lens, small), what=f"layer {layer}")
+    b.kv_pages_copy(dev, torch.tensor([39999, 39998], dtype=torch.int32, device="cuda"),
+                    torch.tensor([7, 39997], dtype=torch.int32, device="cuda"))
+    for x, y in ((39999, 7), (39998, 39997)):
+        for t in (dev.k_store, dev.v_store):
+            t = t.view(torch.uint8)
+            assert t[1, x].any() and torch.equal(t[:, x], t[:, y])
+    assert b.kv_pool_read_device_error(dev) == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_many_sequences(kind):
+    """More sequences than the lanes that look for a share's place take in one step."""
+    lens = [(7 * i) % 90 for i in range(700)]
+    lens[300], lens[699] = 5000, 3001
+    q, pt, dev, orc = _filled(kind, 21, lens, 1, 4, 64, 16, 16)
+    ref = bu.reference(orc, 0, q, lens, pt)
+    for n_splits in (0, 2, 4):
+        bu.assert_close(bu.decode(dev, 0, q, lens, pt, n_splits=n_splits), ref)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_fused_append_behind_long_contexts(kind):
+    """The decode kernel starts under its append: the last block of each sequence lies in the
+    first, a middle and a late batch of a warp's tiles, and grows."""
+    from int8_kv_cache_02_gb300 import binding as b
+    for D, gs in ((64, 128), (128, 16), (256, 64)):
+        lens = [1, 129, 3000, 9001]
+        q, pt, dev, orc = _filled(kind, D, lens, 1, 4, D, gs, 128)
+        g = torch.Generator().manual_seed(2)
+        for n_splits in (1, 3, 40):
+            k, v = _rows(g, 4, 1, 1, D)
+            k = (4 * n_splits * k).half()
+            pos = [n - 1 for n in lens]
+            orc.append(0, k.numpy(), v.numpy(), pos, pt.numpy())
+            out = torch.full((4, 4, D), float("nan"), device="cuda")
+            ws = dev.decode_workspace(4, 4, n_splits)
+            b.attn_decode_append_int8(dev, 0, q[:, 0].contiguous().cuda(),
+                                      k[:, 0].contiguous().cuda(), v[:, 0].contiguous().cuda(),
+                                      torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                      pt.cuda(), out, ws, n_splits=n_splits)
+            ref = bu.reference(orc, 0, q, lens, pt)[:, 0]
+            bu.assert_close(out.cpu().numpy(), ref, z_max=600, what=f"{D} {n_splits}")
+            bu.assert_same(dev, orc)
 
 
 @pytest.mark.parametrize("kind", KINDS)
