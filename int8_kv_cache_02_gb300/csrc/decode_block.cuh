@@ -59,10 +59,13 @@ constexpr float kWeightShift = 6.f;   // W is scaled by 2^6: at most 2^14 in fp1
 
 template <int D>
 struct Shape {
-  static constexpr int NW = 4;                        // warps per block
+  // Warps per block, eight to an SM.  D 256: one block of eight halves the partials
+  // (128K 31.6 -> 29.8 us; an 8K step 11.3 -> 12.0 us); below, two blocks of four
+  // keep more units apart (64 sequences at D 128: 314 us against 318).
+  static constexpr int NW = D == 256 ? 8 : 4;
   static constexpr int TPI = 256 / D;                 // tiles a warp takes at a time
-  static constexpr int NS = D == 256 ? 3 : 3;         // ring stages per warp
-  static constexpr int BLOCKS = 2;                    // per SM
+  static constexpr int NS = 3;                        // ring stages per warp
+  static constexpr int BLOCKS = 8 / NW;               // per SM
   static constexpr int START = 2 * NW * TPI;          // a unit's start, in tiles
   static constexpr int LEAST = NW * TPI * (NS - 1);   // a share at least: its rings' first fill
   static constexpr int KP = D / 64;                   // 16-byte K pieces per lane and row
