@@ -275,6 +275,12 @@ def attn_prefill_chunk_int8(pool, layer, q, start_pos, page_table, out, workspac
                             softmax_scale=0.0, n_splits=0, stream=None):
     """q fp16 [n_new][H][D]; page_table int32 [max_pages] (one sequence); out fp32 [n_new][H][D]."""
     n_new, H = q.shape[0], q.shape[1]
+    if getattr(pool, "block", False):
+        _shape(q, (n_new, H, pool.head_dim), "q")
+        _shape(out, q.shape, "out")
+        if page_table.numel() != page_table.shape[-1]:
+            raise ValueError("page_table must be one sequence's row")
+        _here(pool, q, page_table, out, workspace)
     ws = _dev(workspace, torch.uint8, "workspace") if workspace is not None else None
     nbytes = workspace.numel() if workspace is not None else 0
     _check(lib().attn_prefill_chunk_int8(pool.handle, layer, _dev(q, torch.float16, "q"), n_new,

@@ -3,6 +3,7 @@
 // Nothing here allocates device memory or synchronises (except
 // kv_pool_read_device_error, which is documented to).
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -239,6 +240,45 @@ int decode_auto_splits(const int8kv_pool* pool, int batch, int q_len, int G, int
 static int launch_status(cudaError_t e) {
   if (e == cudaErrorNotSupported) return INT8KV_ERR_UNSUPPORTED;
   return e == cudaSuccess ? INT8KV_OK : INT8KV_ERR_CUDA;
+}
+
+// The decode kernel of a block-scaled pool over batch x q_len queries (seq_lens null: the
+// one sequence has `length` positions).
+static int block_attention(const int8kv_pool* pool, int layer, const uint16_t* q, int batch,
+                           int q_len, int n_heads, const int32_t* seq_lens, int length,
+                           const int32_t* page_table, int max_pages, int window, float scale,
+                           int n_splits, float* out, const DecodeWorkspace& ws, bool appended,
+                           cudaStream_t stream) {
+  const int G = n_heads / pool->n_kv_heads;
+  BlockDecodeArgs d;
+  d.pool = block_view(pool, layer);
+  d.q = q;
+  d.seq_lens = seq_lens;
+  d.length = length;
+  d.page_table = page_table;
+  d.out = out;
+  d.part_o = ws.part_o;
+  d.part_lse = (float*)ws.part_ml;
+  // (the region holds two floats a row; the units' words follow the first of them)
+  const size_t rows = (size_t)batch * q_len * n_heads * n_splits;
+  d.part_units = (int2*)((char*)ws.part_ml + (rows * sizeof(float) + 7) / 8 * 8);
+  d.B = batch;
+  d.H = n_heads;
+  d.G = G;
+  d.Q = q_len;
+  d.max_pages = max_pages;
+  d.window = window;
+  const int cols = q_len * G, per = pool->head_dim <= 128 && cols > 8 ? 16 : 8;
+  d.n_cg = (cols + per - 1) / per;
+  d.width = (cols + d.n_cg - 1) / d.n_cg;
+  const long long units = (long long)batch * pool->n_kv_heads * d.n_cg;
+  d.shares = block_shares(pool, units, d.width, (long long)rows, n_splits);
+  // the kernels count the line of tiles in 32 bits; one block per unit needs no line
+  const long long most = ((long long)max_pages * pool->page_size + 15) / 16 + 64;
+  if (units * most > INT32_MAX / 2) d.shares = 0;
+  d.scale_log2 = scale * 1.4426950408889634f;
+  d.appended = appended;
+  return launch_status(launch_block_decode(d, pool->head_dim, is_f8(pool), stream));
 }
 
 }  // namespace int8kv
@@ -499,34 +539,8 @@ static int decode_entry(const int8kv_pool* pool, int layer, const uint16_t* q,
                                                 max_pages_per_seq, s);
       if (e != cudaSuccess) return launch_status(e);
     }
-    BlockDecodeArgs d;
-    d.pool = block_view(pool, layer);
-    d.q = q;
-    d.seq_lens = seq_lens;
-    d.page_table = page_table;
-    d.out = out;
-    d.part_o = a.ws.part_o;
-    d.part_lse = (float*)a.ws.part_ml;
-    // (the region holds two floats a row; the units' words follow the first of them)
-    const size_t rows = (size_t)batch * q_len * n_heads * n_splits;
-    d.part_units = (int2*)((char*)a.ws.part_ml + (rows * sizeof(float) + 7) / 8 * 8);
-    d.B = batch;
-    d.H = n_heads;
-    d.G = G;
-    d.Q = q_len;
-    d.max_pages = max_pages_per_seq;
-    d.window = window;
-    const int cols = q_len * G, per = pool->head_dim <= 128 && cols > 8 ? 16 : 8;
-    d.n_cg = (cols + per - 1) / per;
-    d.width = (cols + d.n_cg - 1) / d.n_cg;
-    const long long units = (long long)batch * pool->n_kv_heads * d.n_cg;
-    d.shares = block_shares(pool, units, d.width, (long long)rows, n_splits);
-    // the kernels count the line of tiles in 32 bits; one block per unit needs no line
-    const long long most = ((long long)max_pages_per_seq * pool->page_size + 15) / 16 + 64;
-    if (units * most > INT32_MAX / 2) d.shares = 0;
-    d.scale_log2 = scale * 1.4426950408889634f;
-    d.appended = k_new != nullptr;
-    return launch_status(launch_block_decode(d, pool->head_dim, is_f8(pool), s));
+    return block_attention(pool, layer, q, batch, q_len, n_heads, seq_lens, 0, page_table,
+                           max_pages_per_seq, window, scale, n_splits, out, a.ws, k_new != nullptr, s);
   }
   a.pool = layer_view(pool, layer);
   a.q = q;
@@ -553,7 +567,10 @@ int attn_prefill_n_splits(const int8kv_pool* pool, int n_new, int n_heads, int s
   if (n_new <= 0 || n_heads <= 0 || start_pos < 0 || n_heads % pool->n_kv_heads != 0)
     return INT8KV_ERR_INVALID_ARG;
   const int G = n_heads / pool->n_kv_heads;
-  if (G > 8 || is_block(pool)) return INT8KV_ERR_UNSUPPORTED;
+  if (G > 8) return INT8KV_ERR_UNSUPPORTED;
+  if (is_block(pool))
+    return block_splits(pool, ((long long)n_new * G + 7) / 8 * pool->n_kv_heads,
+                        (int)std::min((long long)start_pos + n_new, (long long)INT32_MAX));
   // One block per SM at a time: (query tiles of 128 rows) x kv heads x splits
   // blocks run in ceil(blocks / SMs) waves of ceil(pages / splits) pages each.
   // Take the split count with the shortest such chain, counting two pages of
@@ -591,7 +608,9 @@ int attn_prefill_chunk_int8(const int8kv_pool* pool, int layer, const uint16_t* 
       !std::isfinite(softmax_scale) || n_heads % pool->n_kv_heads != 0)
     return INT8KV_ERR_INVALID_ARG;
   const int G = n_heads / pool->n_kv_heads;
-  if (!prefill_supported(pool, G)) return INT8KV_ERR_UNSUPPORTED;
+  if (is_block(pool) ? G > 8 || (long long)n_new * G > kBlockMostPositions
+                     : !prefill_supported(pool, G))
+    return INT8KV_ERR_UNSUPPORTED;
   if (n_new == 0) return INT8KV_OK;
   if ((long long)start_pos + n_new > (long long)max_pages_per_seq * pool->page_size)
     return INT8KV_ERR_CAPACITY;
@@ -607,6 +626,17 @@ int attn_prefill_chunk_int8(const int8kv_pool* pool, int layer, const uint16_t* 
   if (need > 0) {
     if (!workspace || workspace_bytes < need) return INT8KV_ERR_WORKSPACE;
     if (!aligned16(workspace)) return INT8KV_ERR_ALIGNMENT;
+  }
+  if (is_block(pool)) {
+    // the chunk is one long query window; its kernel is bound by the warp-level products
+    if (!on_current_device(pool)) return INT8KV_ERR_INVALID_ARG;
+    if ((long long)max_pages_per_seq * pool->page_size > kBlockMostPositions)
+      return INT8KV_ERR_UNSUPPORTED;
+    return block_attention(pool, layer, q, 1, n_new, n_heads, nullptr, start_pos + n_new, page_table,
+                           max_pages_per_seq, 0,
+                           softmax_scale != 0.f ? softmax_scale
+                                                : 1.0f / std::sqrt((float)pool->head_dim),
+                           n_splits, out, a.ws, false, (cudaStream_t)stream);
   }
   a.pool = layer_view(pool, layer);
   a.q = q;

@@ -178,7 +178,8 @@ __device__ __forceinline__ void code_values(uint32_t w, float (&y)[4]) {
 struct BlockDecodeArgs {
   BlockView pool;
   const uint16_t* q;          // [B][Q][H][D] fp16
-  const int32_t* seq_lens;    // [B]
+  const int32_t* seq_lens;    // [B], or null: `length` for the one sequence (a prefill chunk)
+  int length;
   const int32_t* page_table;  // [B][max_pages]
   float* out;                 // [B][Q][H][D]
   float* part_o;              // [slots][width][D] normalised partial outputs

@@ -200,7 +200,7 @@ int block_decode_resident(int head_dim, bool f8) {
 cudaError_t launch_block_decode(const BlockDecodeArgs& a, int head_dim, bool f8,
                                 cudaStream_t stream) {
   const long long rows = (long long)a.B * a.Q * a.H;
-  if (rows > 0x7fffffffLL) return cudaErrorNotSupported;
+  if (rows > 0x3fffffffLL) return cudaErrorNotSupported;
   cudaError_t e;
   switch (head_dim) {
     case 64:

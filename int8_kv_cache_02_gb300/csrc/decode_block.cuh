@@ -99,9 +99,13 @@ __device__ __forceinline__ void wait_copies() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+__device__ __forceinline__ int length_of(const BlockDecodeArgs& a, int b) {
+  return a.seq_lens ? __ldg(a.seq_lens + b) : a.length;
+}
+
 // The positions of sequence b that some query of it attends: [lo, hi).
 __device__ __forceinline__ void unit_range(const BlockDecodeArgs& a, int b, int& lo, int& hi) {
-  hi = block_length(__ldg(a.seq_lens + b), a.max_pages, a.pool);
+  hi = block_length(length_of(a, b), a.max_pages, a.pool);
   lo = a.window > 0 && hi > a.window ? hi - a.window : 0;
 }
 __device__ __forceinline__ int unit_tiles(int lo, int hi) {
@@ -131,7 +135,7 @@ __device__ __forceinline__ Place find_share(const BlockDecodeArgs& a, int per_se
     int len[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      len[k] = i + k < run && lane * run + i + k < a.B ? __ldg(a.seq_lens + lane * run + i + k) : 0;
+      len[k] = i + k < run && lane * run + i + k < a.B ? length_of(a, lane * run + i + k) : 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) sum += line_length(a, len[k], per_seq, start);
   }
@@ -159,7 +163,7 @@ __device__ __forceinline__ Place find_share(const BlockDecodeArgs& a, int per_se
   const bool mine = p.at >= base && p.at < inc;
   if (mine && run > 1)
     for (;;) {
-      const int n = line_length(a, __ldg(a.seq_lens + b), per_seq, start);
+      const int n = line_length(a, length_of(a, b), per_seq, start);
       if (p.at < base + n) break;
       base += n;
       ++b;

@@ -350,6 +350,29 @@ def test_long_ragged_batches_against_fp64_on_the_device():
         bu.assert_close(out.numpy(), ref.numpy(), z_max=64, what=kind)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,Hkv,G,start,n_new,ps", [
+    (64, 2, 3, 0, 1, 16), (128, 2, 4, 0, 77, 64), (128, 1, 8, 1000, 130, 32), (256, 2, 8, 37, 20, 64),
+    (256, 1, 1, 500, 65, 128), (64, 1, 5, 3, 300, 64)])
+def test_prefill_chunk(kind, D, Hkv, G, start, n_new, ps):
+    from int8_kv_cache_02_gb300 import binding as b
+    n = start + n_new
+    _, pt, dev, orc = _filled(kind, D + n_new, [n], Hkv, G, D, 16, ps)
+    g = torch.Generator().manual_seed(n)
+    q = torch.randn((n_new, Hkv * G, D), generator=g).half()
+    kh, vh = orc.gather(0, pt[0].numpy(), n)
+    ref = bu.oatt.prefill_chunk(q.numpy(), kh, vh, start)
+    auto = b.attn_prefill_n_splits(dev, n_new, Hkv * G, start)
+    for n_splits in (auto, 1, 2, 11):
+        ws = torch.full((max(16, b.attn_prefill_workspace_bytes(n_new, Hkv * G, Hkv, D, n_splits)),),
+                        255, dtype=torch.uint8, device="cuda")
+        out = torch.full((n_new, Hkv * G, D), float("nan"), device="cuda")
+        b.attn_prefill_chunk_int8(dev, 0, q.cuda(), start, pt[0].cuda(), out, ws,
+                                  n_splits=0 if n_splits == auto else n_splits)
+        bu.assert_close(out.cpu().numpy(), ref, what=f"splits {n_splits}")
+    assert b.kv_pool_read_device_error(dev) == 0
+
+
 # ---- calls together --------------------------------------------------------
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -437,10 +460,12 @@ def test_noalloc_decode_and_refusals():
     with status("-6"):
         b.kv_pool_set_decode_kernel(dev, b.DECODE_WARP_MMA)
     b.kv_pool_set_decode_kernel(dev, b.DECODE_AUTO)
-    with status("-6"):
-        b.attn_prefill_chunk_int8(dev, 0, qd, 0, ptd[0], out)
-    with status("-6"):
-        b.attn_prefill_n_splits(dev, 2, 8, 0)
+    with status("-5"):
+        b.attn_prefill_chunk_int8(dev, 0, qd, 64 * pt.shape[1] - 1, ptd[0], out, n_splits=1)
+    with status("-8"):
+        b.attn_prefill_chunk_int8(dev, 0, qd, 900, ptd[0], out, n_splits=2)
+    with pytest.raises(ValueError, match="one sequence"):
+        b.attn_prefill_chunk_int8(dev, 0, qd, 0, ptd, out, n_splits=1)
     with status("-6"):
         b.kv_pool_save(dev, lens, ptd)
     with status("-6"):
