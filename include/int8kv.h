@@ -68,10 +68,19 @@
  *     new codes: round_half_even(fp32(x / s)) saturated to +-qmax, 0 where s = 0
  * so a code is off by at most half a step of its block's scale, or one step in a
  * block that grew.  A position that is written again (after a sequence was cut
- * back) keeps the block's scale.  Decode, query windows and the fused append
- * serve them at every head_dim, page size and group size; prefill chunks and
- * saved images return UNSUPPORTED.  Blocks behind a sequence's end are neither
- * read nor written.
+ * back) keeps the block's scale.  Appending reads the scale of the block that the
+ * first new position lies in (unless it is the block's first) and may rewrite
+ * that block's earlier codes; no other sequence may hold its page.  Values have to
+ * be finite.  Every append and attention call serves these pools at every
+ * head_dim, page size and group size, with any n_heads / n_kv_heads up to 8; saved
+ * images return UNSUPPORTED.  Nothing behind a sequence's end is read or written.
+ * Calls on them want the pool's device to be the current one (INVALID_ARG) and
+ * page-table rows of at most 2^30 positions (UNSUPPORTED).  n_splits means for
+ * them: 1, one thread block per unit (a unit: a kv head of a sequence with its
+ * query heads, per 8 or 16 (query, head) pairs); n >= 2, up to units * (n - 1) + 1
+ * blocks, at most what the device holds at once, each of which takes an equal share
+ * of the tiles of all units, whatever the sequences' lengths, and a combine
+ * kernel.  The workspace is the same as for the other pools.
  *
  * Pages: with reference counts in device memory, sequences share pages, and the
  * kv_pages_* calls give pages out, take them back, fork sequences and compact
@@ -220,7 +229,7 @@ int kv_quant_append(const int8kv_pool* pool, int layer, const uint16_t* k_new,
  * split-K scheme both follow is genie-ai-runtime v1.3.0, "split-K decode
  * attention" (a partial per split, combined per head).
  * Errors: NULL_PTR, INVALID_ARG (unknown kind), UNSUPPORTED (the kernel does not
- * serve the pool's shape). */
+ * serve the pool's shape, or the pool is block-scaled and kind not AUTO). */
 int kv_pool_set_decode_kernel(int8kv_pool* pool, int kind);
 
 /* Splits the library picks when attn_decode_int8 gets n_splits = 0, for a
@@ -232,7 +241,8 @@ int kv_pool_set_decode_kernel(int8kv_pool* pool, int kind);
  * keeps resident on the pool's device (queried once per pool and kernel); the
  * count with the shortest chain of waves x (pages per block + 1), plus 2 when
  * the splits need combining, is returned (the smallest on a tie): at least 1,
- * at most the pages of max_ctx and 256.
+ * at most the pages of max_ctx and 256.  For a block-scaled pool: 1 where max_ctx *
+ * head_dim <= 65536, else the least count that fills the device (2 to 256).
  * Returns >= 1, or a negative status (NULL_PTR, INVALID_ARG). */
 int attn_decode_n_splits(const int8kv_pool* pool, int batch, int max_ctx);
 
@@ -310,7 +320,8 @@ int attn_decode_append_int8(const int8kv_pool* pool, int layer, const uint16_t* 
  * products, eight per block: q_len * G <= 8 reads each page once per split,
  * more reads it once per group of eight pairs.  Served by the warp-level
  * tensor-core kernel only (page_size 64, head_dim 128/256, group_size >= 64, a
- * multiple of 64); other pools return UNSUPPORTED.  No sliding window.
+ * multiple of 64) and on block-scaled pools (up to 16 pairs per block at
+ * head_dim 64 and 128); other pools return UNSUPPORTED.  No sliding window.
  * Errors: NULL_PTR, INVALID_ARG, UNSUPPORTED, WORKSPACE, ALIGNMENT, CUDA. */
 int attn_decode_multi_int8(const int8kv_pool* pool, int layer, const uint16_t* q, int batch,
                            int q_len, int n_heads, const int32_t* seq_lens,
@@ -344,7 +355,8 @@ int attn_prefill_workspace_bytes(int n_new, int n_heads, int n_kv_heads, int hea
  *   out         device fp32 [n_new][n_heads][head_dim]
  *   workspace   device, >= attn_prefill_workspace_bytes (any contents)
  * Built for page_size 64, head_dim 128/256, group_size >= 64 and
- * n_heads / n_kv_heads in {1, 2, 4, 8}; other shapes return UNSUPPORTED.
+ * n_heads / n_kv_heads in {1, 2, 4, 8}, and for every block-scaled pool (as one long
+ * query window); other shapes return UNSUPPORTED.
  * Errors: NULL_PTR, INVALID_ARG, UNSUPPORTED, CAPACITY (start_pos + n_new beyond
  * the page-table row), WORKSPACE, ALIGNMENT, CUDA. */
 int attn_prefill_chunk_int8(const int8kv_pool* pool, int layer, const uint16_t* q, int n_new,

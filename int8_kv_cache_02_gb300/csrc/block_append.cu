@@ -86,14 +86,14 @@ __global__ void __launch_bounds__(NT* GROUPS) block_append_kernel(
   ptx::grid_dependency_wait();
   ptx::grid_launch_dependents();
   const int tid = threadIdx.x % NT;
-  const long long unit = (long long)blockIdx.x * GROUPS + threadIdx.x / NT;
+  const unsigned unit = blockIdx.x * GROUPS + threadIdx.x / NT;     // (fewer than 2^31)
   // unit = ((sequence * nb + block) * Hkv + kv head) * 2 + store
   const bool is_v = unit & 1;
-  const int kvh = (int)((unit >> 1) % p.Hkv);
-  const long long sb = (unit >> 1) / p.Hkv;
-  const int j = (int)(sb % nb);
-  const long long b = sb / nb;
-  if (b >= n_seqs) return;
+  const int kvh = (unit >> 1) % (unsigned)p.Hkv;
+  const unsigned sb = (unit >> 1) / (unsigned)p.Hkv;
+  const int j = sb % (unsigned)nb;
+  const size_t b = sb / (unsigned)nb;
+  if (b >= (size_t)n_seqs) return;
   const int T = 1 << p.t_log2;
   long long pos = (long long)__ldg(seq_pos + b) + pos_offset, skip = 0;
   if (pos < 0) {     // tokens at negative positions have no place
@@ -205,7 +205,7 @@ cudaError_t launch(const AppendCall& c) {
   const int nb = (c.n_new + T - 2) / T + 1;   // blocks that n_new tokens may touch
   const long long units = (long long)c.n_seqs * nb * c.p.Hkv * 2;
   const long long grid = (units + GROUPS - 1) / GROUPS;
-  if (grid > 0x7fffffffLL) return cudaErrorNotSupported;
+  if (units > 0x7fffff00LL) return cudaErrorNotSupported;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(NT * GROUPS);

@@ -51,11 +51,11 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const Regions 
   ptx::grid_launch_dependents();
   ptx::grid_dependency_wait();
   if (n_dev) n = *n_dev;
-  const long long total = (long long)n * r.n_layers * r.chunks;
-  for (long long w = blockIdx.x; w < total; w += gridDim.x) {
-    const int c = (int)(w % r.chunks);
-    const long long il = w / r.chunks;
-    const int layer = (int)(il % r.n_layers), i = (int)(il / r.n_layers);
+  const unsigned total = (unsigned)n * r.n_layers * r.chunks;      // (fewer than 2^31)
+  for (unsigned w = blockIdx.x; w < total; w += gridDim.x) {
+    const int c = w % (unsigned)r.chunks;
+    const unsigned il = w / (unsigned)r.chunks;
+    const int layer = il % (unsigned)r.n_layers, i = il / (unsigned)r.n_layers;
     const int s = src[i], d = dst[i];
     if (s < 0 || d < 0 || s >= r.n_pages || d >= r.n_pages) {
       if (threadIdx.x == 0 && s >= 0 && d >= 0) flag_error(r.err, INT8KV_DEVERR_PAGE_ID);
@@ -540,6 +540,7 @@ cudaError_t launch_copy(const int8kv_pool* p, const int32_t* src, const int32_t*
   r.err = p->dev_error;
   // a number of pairs known on the device only: at most four blocks a slot, which stride
   const long long total = (long long)most * p->n_layers * r.chunks;
+  if (total > 0x7fffffffLL) return cudaErrorNotSupported;
   const long long cap = n_dev ? 32LL * p->num_sms : 0x7fffffffLL;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(total < cap ? total : cap));
