@@ -292,13 +292,22 @@ __device__ __forceinline__ void v_words(uint32_t tile, const Lane<D>& ln, int h,
   }
 }
 
+// D = A * B, as ptx::mma_f16 with no sum to add to.
+__device__ __forceinline__ void mma_from_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // S^T of one tile: z[n][2r + c] is row g + 8r, column 2t + c of group n.
 template <int D, bool F8, int V>
 __device__ __forceinline__ void score_tile(const Warp<D, V>& w, uint32_t tile, const Lane<D>& ln,
                                            float (&z)[Cols<V>::NC][4]) {
   using S = Shape<D>;
   constexpr int NC = Cols<V>::NC;
-  float s[2][NC][4] = {};
+  float s[2][NC][4];
 #pragma unroll
   for (int c = 0; c < S::KP; ++c) {
     // piece 4c + t of rows g and g + 8
@@ -312,7 +321,10 @@ __device__ __forceinline__ void score_tile(const Warp<D, V>& w, uint32_t tile, c
                              codes_behind_to_h2<F8>(xw[u]), codes_behind_to_h2<F8>(yw[u])};
 #pragma unroll
       for (int n = 0; n < NC; ++n)
-        ptx::mma_f16(s[u & 1][n], a, w.q[n][8 * c + 2 * u], w.q[n][8 * c + 2 * u + 1]);
+        if (c == 0 && u < 2)
+          mma_from_zero(s[u][n], a, w.q[n][2 * u], w.q[n][2 * u + 1]);
+        else
+          ptx::mma_f16(s[u & 1][n], a, w.q[n][8 * c + 2 * u], w.q[n][8 * c + 2 * u + 1]);
     }
   }
 #pragma unroll
@@ -430,24 +442,35 @@ __device__ __forceinline__ void take_stage(Warp<D, V>& w, uint32_t stage, int po
           pair_words<F8>(a[2 * kh][x], a[2 * kh + 1][x], pa[kh][0], pa[kh][1]);
           pair_words<F8>(b[2 * kh][x], b[2 * kh + 1][x], pb[kh][0], pb[kh][1]);
         }
-        uint32_t fr[4][4];
+        // E rows' fragments at a time: as many as the registers hold beside the sums
+        constexpr int E = V == kSixteen || (D == 256 && V == kEight) ? 2 : 4;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e0 = 0; e0 < 4; e0 += E) {
+          uint32_t fr[E][4];
 #pragma unroll
-          for (int kh = 0; kh < 2; ++kh) {
-            const uint32_t wa = pa[kh][e >> 1], wb = pb[kh][e >> 1];
-            fr[e][2 * kh] = e & 1 ? codes_behind_to_h2<F8>(wa) : codes_to_h2<F8>(wa);
-            fr[e][2 * kh + 1] = e & 1 ? codes_behind_to_h2<F8>(wb) : codes_to_h2<F8>(wb);
+          for (int e = 0; e < E; ++e)
+#pragma unroll
+            for (int kh = 0; kh < 2; ++kh) {
+              const uint32_t wa = pa[kh][(e0 + e) >> 1], wb = pb[kh][(e0 + e) >> 1];
+              fr[e][2 * kh] = e & 1 ? codes_behind_to_h2<F8>(wa) : codes_to_h2<F8>(wa);
+              fr[e][2 * kh + 1] = e & 1 ? codes_behind_to_h2<F8>(wb) : codes_to_h2<F8>(wb);
+            }
+#pragma unroll
+          for (int n = 0; n < NC; ++n) {
+            // The products' own sum drops the bits below its last place instead of rounding:
+            // over a long chain that is a drift (512 tiles: 2e-5 of the result).  So a tile's
+            // products start from zero and are added, rounded, to the lane's sums.
+            float part[E][4];
+#pragma unroll
+            for (int e = 0; e < E; ++e) mma_from_zero(part[e], fr[e], hi[n][0], hi[n][1]);
+            if constexpr (V != kPair)
+#pragma unroll
+              for (int e = 0; e < E; ++e) ptx::mma_f16(part[e], fr[e], lw[n][0], lw[n][1]);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) w.acc[n][(h * N + x) * 4 + e0 + e][k] += part[e][k];
           }
-#pragma unroll
-        for (int n = 0; n < NC; ++n) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            ptx::mma_f16(w.acc[n][(h * N + x) * 4 + e], fr[e], hi[n][0], hi[n][1]);
-          if constexpr (V != kPair)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              ptx::mma_f16(w.acc[n][(h * N + x) * 4 + e], fr[e], lw[n][0], lw[n][1]);
         }
       }
     }

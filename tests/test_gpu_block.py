@@ -373,6 +373,30 @@ def test_prefill_chunk(kind, D, Hkv, G, start, n_new, ps):
     assert b.kv_pool_read_device_error(dev) == 0
 
 
+def test_long_chains_do_not_drift():
+    """One block takes 32,768 positions alone: 512 tiles a warp.  The products' sums drop bits
+    instead of rounding, so their error would grow with the chain (to 2e-5); sums rounded tile by
+    tile keep the bound of assert_close."""
+    from int8_kv_cache_02_gb300 import binding as b
+    n, D = 32768, 128
+    for kind, G in (("e4m3", 8), ("int8", 3)):
+        dev, _ = bu.make_pools(kind, 1, D, 64, 64, n // 64)
+        g = torch.Generator(device="cuda").manual_seed(1)
+        pt = torch.arange(n // 64, dtype=torch.int32, device="cuda")[None]
+        k, v = (torch.randn((1, n, 1, D), generator=g, device="cuda").half() for _ in range(2))
+        b.kv_quant_append(dev, 0, k, v, torch.zeros(1, dtype=torch.int32, device="cuda"), pt)
+        q = torch.randn((1, G, D), generator=g, device="cuda").half()
+        x = [(t.float().double() * s.repeat_interleave(64, 3).double()[..., None]).reshape(n, D)
+             for t, s in ((dev.k_store, dev.k_scales), (dev.v_store, dev.v_scales))]
+        ref = torch.softmax(q[0].double() @ x[0].T / D ** 0.5, -1) @ x[1]
+        lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+        for n_splits in (1, 2):
+            out = torch.empty((1, G, D), device="cuda")
+            b.attn_decode_int8(dev, 0, q, lens, pt, out, dev.decode_workspace(1, G, 2),
+                               n_splits=n_splits)
+            bu.assert_close(out[0].cpu().numpy(), ref.cpu().numpy(), what=f"{kind} {n_splits}")
+
+
 # ---- calls together --------------------------------------------------------
 
 @pytest.mark.parametrize("kind", KINDS)
