@@ -195,7 +195,7 @@ int decode_splits_heuristic(const int8kv_pool* pool, long long units, int max_ct
 static int block_splits(const int8kv_pool* pool, long long units, int max_ctx) {
   if ((long long)max_ctx * pool->head_dim <= kBlockSingle) return 1;
   // (query windows may take 16 columns to a unit: up to twice the splits per unit)
-  const long long n = (pool->head_dim <= 128 ? 2 : 1) * ((pool->resident[kBlockKernel] + units - 2) / units) + 1;
+  const long long n = 2 * ((pool->resident[kBlockKernel] + units - 2) / units) + 1;
   return (int)(n < 2 ? 2 : n > kMaxSplits ? kMaxSplits : n);
 }
 
@@ -268,7 +268,7 @@ static int block_attention(const int8kv_pool* pool, int layer, const uint16_t* q
   d.Q = q_len;
   d.max_pages = max_pages;
   d.window = window;
-  const int cols = q_len * G, per = pool->head_dim <= 128 && cols > 8 ? 16 : 8;
+  const int cols = q_len * G, per = cols > 8 ? 16 : 8;
   d.n_cg = (cols + per - 1) / per;
   d.width = (cols + d.n_cg - 1) / d.n_cg;
   const long long units = (long long)batch * pool->n_kv_heads * d.n_cg;

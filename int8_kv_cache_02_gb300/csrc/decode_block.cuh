@@ -27,8 +27,9 @@
 // A column is a (query, head) pair of the kv head.  With at most four of them
 // (kPair) columns 4 - 7 hold the same queries again: there W is the lo part, and one
 // product brings both (the halves are added at the end).  More than eight take two
-// groups of columns per pass where the registers hold them (NC = 2, D <= 128), so
-// that a page is read and converted once for 16 columns.
+// groups of columns per pass (NC = 2), so that a page is read and converted once for
+// 16 columns; at D 256 their queries' fragments lie in shared memory, the sums alone
+// taking 128 registers.
 //
 // Schedule: all (sequence, kv head, column group) units in one line, each as long as
 // its tiles plus a start of kStart (what a block spends on a unit besides its tiles:
@@ -44,6 +45,7 @@
 // Bound by HBM: 2 D bytes per position and kv head.
 #pragma once
 
+#include <algorithm>
 #include <climits>
 
 #include "block_common.cuh"
@@ -82,6 +84,12 @@ struct Cols {
   static constexpr int NC = V == kSixteen ? 2 : 1;
   static constexpr int N = 8 * NC;                    // columns of the products
 };
+
+// Whether the queries' fragments lie in shared memory, behind the rings, and its size.
+template <int D, int V>
+constexpr bool kSharedQ = D == 256 && V == kSixteen;
+template <int D, int V>
+constexpr int kSmem = Shape<D>::RING + (kSharedQ<D, V> ? 16 * D * 2 : 0);
 
 template <bool FULL>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool valid) {
@@ -210,7 +218,7 @@ struct Warp {
   static constexpr int NC = Cols<V>::NC;
   float acc[NC][D / 16][4];    // O^T: rows in out_dim's order, columns 2t, 2t + 1
   float m[NC][2], M[NC][2], l[NC][2];
-  uint32_t q[NC][D / 8];       // q^T fragments
+  uint32_t q[NC][kSharedQ<D, V> ? 1 : D / 8];       // q^T fragments
 
   __device__ __forceinline__ void reset() {
 #pragma unroll
@@ -304,7 +312,7 @@ __device__ __forceinline__ void mma_from_zero(float (&d)[4], const uint32_t (&a)
 // S^T of one tile: z[n][2r + c] is row g + 8r, column 2t + c of group n.
 template <int D, bool F8, int V>
 __device__ __forceinline__ void score_tile(const Warp<D, V>& w, uint32_t tile, const Lane<D>& ln,
-                                           float (&z)[Cols<V>::NC][4]) {
+                                           uint32_t shared_q, float (&z)[Cols<V>::NC][4]) {
   using S = Shape<D>;
   constexpr int NC = Cols<V>::NC;
   float s[2][NC][4];
@@ -320,11 +328,17 @@ __device__ __forceinline__ void score_tile(const Warp<D, V>& w, uint32_t tile, c
       const uint32_t a[4] = {codes_to_h2<F8>(xw[u]), codes_to_h2<F8>(yw[u]),
                              codes_behind_to_h2<F8>(xw[u]), codes_behind_to_h2<F8>(yw[u])};
 #pragma unroll
-      for (int n = 0; n < NC; ++n)
-        if (c == 0 && u < 2)
-          mma_from_zero(s[u][n], a, w.q[n][2 * u], w.q[n][2 * u + 1]);
+      for (int n = 0; n < NC; ++n) {
+        uint2 q;
+        if constexpr (kSharedQ<D, V>)
+          q = ptx::lds64(shared_q + (n * (D / 16) + 4 * c + u) * 256);
         else
-          ptx::mma_f16(s[u & 1][n], a, w.q[n][8 * c + 2 * u], w.q[n][8 * c + 2 * u + 1]);
+          q = make_uint2(w.q[n][8 * c + 2 * u], w.q[n][8 * c + 2 * u + 1]);
+        if (c == 0 && u < 2)
+          mma_from_zero(s[u][n], a, q.x, q.y);
+        else
+          ptx::mma_f16(s[u & 1][n], a, q.x, q.y);
+      }
     }
   }
 #pragma unroll
@@ -341,14 +355,14 @@ __device__ __forceinline__ void take_stage(Warp<D, V>& w, uint32_t stage, int po
                                            const float (&f)[Shape<D>::TPI],
                                            const float (&lv)[Shape<D>::TPI], bool masked,
                                            uint32_t none, int lo, const int (&lim)[Cols<V>::NC][2],
-                                           const Lane<D>& ln, int g, int t) {
+                                           const Lane<D>& ln, uint32_t shared_q, int g, int t) {
   using S = Shape<D>;
   constexpr int NC = Cols<V>::NC, TPI = S::TPI;
   float z[TPI][NC][4];
   float top[NC][2], topM[NC][2];
 #pragma unroll
   for (int i = 0; i < TPI; ++i) {
-    score_tile<D, F8, V>(w, stage + i * S::TILE, ln, z[i]);
+    score_tile<D, F8, V>(w, stage + i * S::TILE, ln, shared_q, z[i]);
 #pragma unroll
     for (int n = 0; n < NC; ++n)
 #pragma unroll
@@ -522,6 +536,26 @@ __device__ __forceinline__ void order_queries(Warp<D, V>& w, int cols, int g) {
   }
 }
 
+// The fragments of a unit's queries in shared memory (kSharedQ), a block's threads
+// together: lane's two words of group n and 16 values ks at ((n * D / 16 + ks) * 32 + lane) * 8.
+template <int D, bool F8, int V>
+__device__ __forceinline__ void share_queries(unsigned char* shared, const BlockDecodeArgs& a,
+                                              const Segment& s) {
+  const int kvh = s.u / a.n_cg, cg = s.u % a.n_cg, cols = min(a.width, a.G * a.Q - cg * a.width);
+  for (int i = threadIdx.x; i < Cols<V>::NC * (D / 16) * 32; i += Shape<D>::NW * 32) {
+    const int lane = i & 31, ks = i / 32 % (D / 16), n = i / 32 / (D / 16);
+    const int mine = 8 * n + (lane >> 2), t = lane & 3;
+    uint2 x = make_uint2(0, 0);
+    if (mine < cols) {
+      const int col = cg * a.width + mine;
+      const uint16_t* q = a.q + (((size_t)s.b * a.Q + col / a.G) * a.H + kvh * a.G + col % a.G) * D;
+      const uint2 v = *reinterpret_cast<const uint2*>(q + 64 * (ks / 4) + 16 * t + 4 * (ks % 4));
+      x = F8 ? v : make_uint2(ptx::prmt(v.x, v.y, 0x5410), ptx::prmt(v.x, v.y, 0x7632));
+    }
+    *reinterpret_cast<uint2*>(shared + i * 8) = x;
+  }
+}
+
 // Joining the warps: where a warp's output (column, d) lies in its region of D * N floats.
 // The xor spreads the four columns and the pieces of 16 that a warp writes at once.
 template <int D>
@@ -534,7 +568,8 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
     decode_block_kernel(const BlockDecodeArgs a) {
   using S = Shape<D>;
   constexpr int NC = Cols<V>::NC, N = Cols<V>::N, TPI = S::TPI;
-  static_assert(N * D * 4 <= S::STAGE, "a warp's output fits one stage of its ring");
+  constexpr bool EARLY = N * D * 4 <= S::STAGE;
+  static_assert(N * D * 4 <= S::NS * S::STAGE, "a warp's output fits its ring");
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float stat[3][S::NW][N];     // m, M, l of each warp and column
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -623,12 +658,17 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
   };
 
   Warp<D, V> w;
-  load_queries(w, a, seg, g, t);
+  const uint32_t shared_q = ptx::smem_u32(smem) + S::RING + 8 * lane;
+  if constexpr (!kSharedQ<D, V>) load_queries(w, a, seg, g, t);
   begin();
+  if constexpr (kSharedQ<D, V>) {
+    share_queries<D, F8, V>(smem + S::RING, a, seg);
+    __syncthreads();
+  }
   for (;;) {
     const int kvh = seg.u / a.n_cg, cg = seg.u % a.n_cg;
     const int cols = min(a.width, a.G * a.Q - cg * a.width);
-    order_queries<D, F8, V>(w, cols, g);
+    if constexpr (!kSharedQ<D, V>) order_queries<D, F8, V>(w, cols, g);
     w.reset();
     int lim[NC][2];           // columns 2t, 2t + 1 of the fragments
 #pragma unroll
@@ -663,18 +703,19 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
       }
       const int pos = (seg.lo / kTile + mine0 + i * (S::NW * TPI)) * kTile;
       const bool masked = none || pos < seg.lo || pos + TPI * kTile - 1 > least;
-      take_stage<D, F8, V>(w, ring + slot_out, pos, f, lv, masked, none, seg.lo, lim, ln, g, t);
+      take_stage<D, F8, V>(w, ring + slot_out, pos, f, lv, masked, none, seg.lo, lim, ln, shared_q, g, t);
       slot_out = slot_out == (S::NS - 1) * S::STAGE ? 0 : slot_out + S::STAGE;
     }
     __syncwarp();
 
-    // the next segment's first copies, into stages 1 and on: stage 0 joins the warps
+    // the next segment's first copies, into stages 1 and on: stage 0 joins the warps (where it
+    // holds their outputs; else the copies wait)
     const Segment done = seg;
     const bool more = next_segment(a, place, per_seq, S::START, seg);
     slot_in = slot_out = S::STAGE;
     if (more) {
-      load_queries(w, a, seg, g, t);
-      begin();
+      if constexpr (!kSharedQ<D, V>) load_queries(w, a, seg, g, t);
+      if constexpr (EARLY) begin();
     }
 
     const int live = min(S::NW, (done.last - done.first + TPI - 1) / TPI);     // warps that had tiles
@@ -702,6 +743,8 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
         }
       }
     __syncthreads();
+    if constexpr (kSharedQ<D, V>)      // (no warp needs the last ones any more)
+      if (more) share_queries<D, F8, V>(smem + S::RING, a, seg);
     const bool whole = done.first == 0 && done.last == done.nt;
     const int unit = done.b * per_seq + done.u, slot = unit + blockIdx.x;
     if (a.shares && done.first == 0 && threadIdx.x == 0)     // for the combine
@@ -749,6 +792,7 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
     }
     if (!more) break;
     __syncthreads();      // the next segment's copies reach stage 0
+    if constexpr (!EARLY) begin();
   }
   ptx::grid_dependency_wait();    // (the grid is not complete before the append is)
 }
@@ -761,7 +805,7 @@ cudaError_t launch_variant(const BlockDecodeArgs& a, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(Shape<D>::NW * 32);
-  cfg.dynamicSmemBytes = Shape<D>::RING;
+  cfg.dynamicSmemBytes = kSmem<D, V>;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -776,9 +820,9 @@ template <int D, bool F8, int V>
 int variant_blocks() {
   int per_sm = 0;
   if (cudaFuncSetAttribute(decode_block_kernel<D, F8, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Shape<D>::RING) != cudaSuccess ||
+                           kSmem<D, V>) != cudaSuccess ||
       cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, decode_block_kernel<D, F8, V>,
-                                                    Shape<D>::NW * 32, Shape<D>::RING) != cudaSuccess)
+                                                    Shape<D>::NW * 32, kSmem<D, V>) != cudaSuccess)
     return -1;
   return per_sm;
 }
@@ -787,19 +831,13 @@ template <int D, bool F8>
 cudaError_t launch_codes(const BlockDecodeArgs& a, cudaStream_t stream) {
   if (a.width <= 4) return launch_variant<D, F8, kPair>(a, stream);
   if (a.width <= 8) return launch_variant<D, F8, kEight>(a, stream);
-  if constexpr (D <= 128) return launch_variant<D, F8, kSixteen>(a, stream);
-  return cudaErrorNotSupported;
+  return launch_variant<D, F8, kSixteen>(a, stream);
 }
 
 template <int D, bool F8>
 int codes_blocks() {
-  int n = variant_blocks<D, F8, kPair>(), x = variant_blocks<D, F8, kEight>();
-  if (x < n) n = x;
-  if constexpr (D <= 128) {
-    x = variant_blocks<D, F8, kSixteen>();
-    if (x < n) n = x;
-  }
-  return n;
+  return std::min({variant_blocks<D, F8, kPair>(), variant_blocks<D, F8, kEight>(),
+                   variant_blocks<D, F8, kSixteen>()});
 }
 
 }  // namespace block
