@@ -242,7 +242,8 @@ int kv_pool_set_decode_kernel(int8kv_pool* pool, int kind);
  * count with the shortest chain of waves x (pages per block + 1), plus 2 when
  * the splits need combining, is returned (the smallest on a tie): at least 1,
  * at most the pages of max_ctx and 256.  For a block-scaled pool: 1 where max_ctx *
- * head_dim <= 65536, else the least count that fills the device (2 to 256).
+ * head_dim <= 65536 (32768 where one wave of clusters of eight blocks holds a cluster
+ * for each sequence and kv head), else the least count that fills the device (2 to 256).
  * Returns >= 1, or a negative status (NULL_PTR, INVALID_ARG). */
 int attn_decode_n_splits(const int8kv_pool* pool, int batch, int max_ctx);
 

@@ -102,14 +102,16 @@ def _check(status, where):
         raise Int8KVError(status, where)
 
 
-# The current stream's handle of a device, without building a torch.cuda.Stream for every call.
+# The current stream's handle of a device, without building a torch.cuda.Stream for every call,
+# and the current device, without the lazy initialisation (a call's tensors are on a device).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream):
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -299,7 +301,7 @@ def _here(pool, *tensors):
     """Block-scaled pools and the page calls: tensors of the pool's device, which is current."""
     at = pool.device_index
     for t in tensors:
-        if t is not None and t.is_cuda and t.get_device() != at:
+        if t is not None and t.get_device() != at and t.is_cuda:
             raise ValueError(f"a tensor is on device {t.get_device()}, the pool on {at}")
 
 

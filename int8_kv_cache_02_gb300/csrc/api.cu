@@ -193,7 +193,8 @@ int decode_splits_heuristic(const int8kv_pool* pool, long long units, int max_ct
 // 512 / 1024 7.5, 11.1, 18.1 against 9.6, 9.9, 9.9; one of D 64 at 1024 / 2048 8.9, 13.6
 // against 9.5, 9.7.
 static int block_splits(const int8kv_pool* pool, long long units, int max_ctx) {
-  if ((long long)max_ctx * pool->head_dim <= kBlockSingle) return 1;
+  const int single = units <= pool->resident[kBlockClusters] ? kBlockSingle / 2 : kBlockSingle;
+  if ((long long)max_ctx * pool->head_dim <= single) return 1;
   // (query windows may take 16 columns to a unit: up to twice the splits per unit)
   const long long n = 2 * ((pool->resident[kBlockKernel] + units - 2) / units) + 1;
   return (int)(n < 2 ? 2 : n > kMaxSplits ? kMaxSplits : n);
@@ -210,6 +211,22 @@ static int block_shares(const int8kv_pool* pool, long long units, int width, lon
   if (n > fit) n = fit;
   if (n > pool->resident[kBlockKernel]) n = pool->resident[kBlockKernel];
   return (int)(n < 1 ? 1 : n);
+}
+
+// Contexts of middling length, and units for one wave of clusters: the blocks of a cluster
+// share a unit and join it through shared memory, without partials and a combine kernel.
+// Measured, in us, at 256 / 512 / 1024 / 2048 / 4096 / 8192 positions: 8 units of D 128 5.8, 5.9,
+// 6.2, 6.9, 8.8, 12.0, one block per unit 5.3, 6.9, 10.1, 16.2, 29.2, 54.7, equal shares 7.4,
+// 9.2, 9.4, 9.4, 10.0, 10.1; 32 of them 7.0, 7.1, 7.4, 9.0, 12.6, 19.7, shares 8.7, 11.0, 11.2,
+// 11.4, 15.8, 21.3; 2 of D 256 7.5, 7.6, 8.1, 9.6, 12.8, 18.8, shares 9.5, 11.4, 11.3, 11.6,
+// 11.4, 11.7.  In two waves (16 of D 256) clusters lose to the shares: 14.4 against 11.0 at
+// 1024.  Clusters of 16 win at 2 x 4096 of D 256 alone (10.3) and need an opt-in.
+static int block_cluster(const int8kv_pool* pool, long long units, int width, long long max_ctx,
+                         int n_splits) {
+  return width <= 8 && n_splits >= kBlockCluster && units <= pool->resident[kBlockClusters] &&
+                 max_ctx * pool->head_dim <= kBlockJoined
+             ? kBlockCluster
+             : 1;
 }
 
 int decode_auto_splits(const int8kv_pool* pool, int batch, int q_len, int G, int max_pages,
@@ -276,6 +293,9 @@ static int block_attention(const int8kv_pool* pool, int layer, const uint16_t* q
   // the kernels count the line of tiles in 32 bits; one block per unit needs no line
   const long long most = ((long long)max_pages * pool->page_size + 15) / 16 + 64;
   if (units * most > INT32_MAX / 2) d.shares = 0;
+  const long long cap = (long long)max_pages * pool->page_size;
+  d.cluster = block_cluster(pool, units, d.width, window > 0 && window < cap ? window : cap, n_splits);
+  if (d.cluster > 1) d.shares = 0;
   d.scale_log2 = scale * 1.4426950408889634f;
   d.appended = appended;
   return launch_status(launch_block_decode(d, pool->head_dim, is_f8(pool), stream));
@@ -383,6 +403,11 @@ int kv_pool_create(int8kv_pool** out, int n_layers, int n_kv_heads, int head_dim
   if (is_block(p)) {
     p->resident[kBlockKernel] = block_decode_resident(head_dim, is_f8(p));
     if (p->resident[kBlockKernel] <= 0) {
+      delete p;
+      return INT8KV_ERR_CUDA;
+    }
+    p->resident[kBlockClusters] = block_decode_clusters(head_dim, is_f8(p));
+    if (p->resident[kBlockClusters] < 0) {
       delete p;
       return INT8KV_ERR_CUDA;
     }

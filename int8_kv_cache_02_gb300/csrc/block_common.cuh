@@ -22,9 +22,12 @@ inline bool block_variant(int variant) {
 inline bool is_block(const int8kv_pool* p) { return block_variant(p->variant); }
 inline bool is_f8(const int8kv_pool* p) { return p->variant == INT8KV_F8_BLOCK; }
 
-constexpr int kBlockKernel = 2;       // index of its decode kernel in int8kv_pool::resident
+constexpr int kBlockKernel = 2;       // index of its decode kernel in int8kv_pool::resident,
+constexpr int kBlockClusters = 0;     // and of how many clusters of its blocks run at once
+constexpr int kBlockCluster = 8;      // blocks of a cluster that share a unit
 constexpr int kBlockSingle = 65536;   // values (positions x head_dim) of a context decoded in one
-                                      // block per unit
+                                      // block per unit: at most these, or half of them where
+constexpr int kBlockJoined = 1 << 19; // clusters may take the unit, up to these
 constexpr int kBlockMostPositions = 1 << 30;   // of a page-table row (positions count in 32 bits)
 
 // Whether the pool's device is the current one, on which the launches go.
@@ -187,7 +190,8 @@ struct BlockDecodeArgs {
   int2* part_units;           // [units] first partial and number of them (1: none, it is in out)
   int B, H, G, Q, max_pages, window;
   int n_cg, width;            // column groups per (sequence, kv head), columns of each
-  int shares;                 // blocks of the balanced schedule, or 0: one block per unit
+  int shares;                 // blocks of the balanced schedule, or 0: `cluster` blocks per unit
+  int cluster;                // 1 or kBlockCluster
   float scale_log2;           // softmax_scale * log2(e)
   // Whether the kernel launched just before appends position seq_lens[b] - 1 of every
   // sequence: then only the blocks of those positions are waited for.
@@ -203,5 +207,7 @@ cudaError_t launch_block_decode(const BlockDecodeArgs& a, int head_dim, bool f8,
 // Blocks of the decode kernel resident at once on the current device (and the
 // kernel's shared-memory attribute set there); <= 0 on a CUDA error.
 int block_decode_resident(int head_dim, bool f8);
+// Clusters of kBlockCluster of its blocks that run at once; 0 where none does.
+int block_decode_clusters(int head_dim, bool f8);
 
 }  // namespace int8kv

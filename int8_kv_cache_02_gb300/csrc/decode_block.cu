@@ -197,6 +197,15 @@ int block_decode_resident(int head_dim, bool f8) {
   }
 }
 
+int block_decode_clusters(int head_dim, bool f8) {
+  switch (head_dim) {
+    case 64: return block_decode_clusters_64(f8);
+    case 128: return block_decode_clusters_128(f8);
+    case 256: return block_decode_clusters_256(f8);
+    default: return 0;
+  }
+}
+
 cudaError_t launch_block_decode(const BlockDecodeArgs& a, int head_dim, bool f8,
                                 cudaStream_t stream) {
   const long long rows = (long long)a.B * a.Q * a.H;

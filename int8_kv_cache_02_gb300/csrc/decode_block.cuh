@@ -37,7 +37,9 @@
 // resident block (a.shares).  A unit that a share boundary cuts leaves partials,
 // numbered unit + share, which the combine kernel joins.  The first copies of a
 // block's next unit are under way while its warps are joined for the last one.  With
-// a.shares = 0 every block takes one whole unit and writes it out.
+// a.shares = 0 every block takes one whole unit and writes it out, or, for few units of
+// middling length, the blocks of a cluster share a unit's tiles and join their outputs
+// through distributed shared memory: no partials, no combine kernel.
 //
 // Behind an append of the same call (a.appended) the kernel starts under it: only the
 // blocks that the append writes, the last of every sequence, wait for it.
@@ -47,6 +49,8 @@
 
 #include <algorithm>
 #include <climits>
+
+#include <cooperative_groups.h>
 
 #include "block_common.cuh"
 #include "decode_common.cuh"
@@ -572,6 +576,7 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
   static_assert(N * D * 4 <= S::NS * S::STAGE, "a warp's output fits its ring");
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float stat[3][S::NW][N];     // m, M, l of each warp and column
+  __shared__ float block_lse[N];          // of a cluster's block, whose outputs are in warp 0's stage 1
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const uint32_t ring = ptx::smem_u32(smem) + warp * S::NS * S::STAGE;
   const Lane<D> ln(lane);
@@ -583,11 +588,14 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
   Place place;
   Segment seg;
   if (a.shares == 0) {
-    seg.b = blockIdx.x / per_seq;
-    seg.u = blockIdx.x % per_seq;
+    const int unit = blockIdx.x / a.cluster;
+    seg.b = unit / per_seq;
+    seg.u = unit % per_seq;
     unit_range(a, seg.b, seg.lo, seg.hi);
-    seg.nt = seg.last = unit_tiles(seg.lo, seg.hi);    // (none: zero rows)
-    seg.first = 0;
+    seg.nt = unit_tiles(seg.lo, seg.hi);               // (none: zero rows)
+    const int per = (seg.nt + a.cluster - 1) / a.cluster;
+    seg.first = min(seg.nt, blockIdx.x % a.cluster * per);
+    seg.last = min(seg.nt, seg.first + per);
     seg.pieces = 1;
     place.at = place.end = 0;
   } else {
@@ -745,7 +753,8 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
     __syncthreads();
     if constexpr (kSharedQ<D, V>)      // (no warp needs the last ones any more)
       if (more) share_queries<D, F8, V>(smem + S::RING, a, seg);
-    const bool whole = done.first == 0 && done.last == done.nt;
+    const bool joins = V != kSixteen && a.cluster > 1;     // with the cluster's other blocks
+    const bool whole = !joins && done.first == 0 && done.last == done.nt;
     const int unit = done.b * per_seq + done.u, slot = unit + blockIdx.x;
     if (a.shares && done.first == 0 && threadIdx.x == 0)     // for the combine
       a.part_units[unit] = make_int2(slot, done.pieces);
@@ -767,8 +776,9 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
       }
       const float inv = l > 0.f ? __fdividef(ptx::ex2(M - m - kWeightShift), l) : 0.f;
       const int gc = cg * a.width + col;
-      float* out = whole ? a.out + (((size_t)done.b * a.Q + gc / a.G) * a.H + kvh * a.G + gc % a.G) * D
-                         : a.part_o + ((size_t)slot * a.width + col) * D;
+      float* out = a.out + (((size_t)done.b * a.Q + gc / a.G) * a.H + kvh * a.G + gc % a.G) * D;
+      if (joins) out = reinterpret_cast<float*>(smem + S::STAGE) + col * D;
+      else if (!whole) out = a.part_o + ((size_t)slot * a.width + col) * D;
 #pragma unroll
       for (int d = 4 * lane; d < D; d += 128) {
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -787,8 +797,44 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
         *reinterpret_cast<float4*>(out + d) =
             make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
       }
-      if (!whole && lane == 0)
-        a.part_lse[(size_t)slot * a.width + col] = l > 0.f ? m + log2f(l) : -INFINITY;
+      if (!whole && lane == 0) {
+        const float lse = l > 0.f ? m + log2f(l) : -INFINITY;
+        if (joins) block_lse[col] = lse;
+        else a.part_lse[(size_t)slot * a.width + col] = lse;
+      }
+    }
+    if constexpr (V != kSixteen) {
+      if (joins) {        // (the last segment: no copies are under way)
+        static_assert(EARLY && N * D * 4 <= (S::NS - 1) * S::STAGE, "outputs behind stage 0");
+        const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+        cluster.sync();
+        float* part = reinterpret_cast<float*>(smem + S::STAGE);
+        for (int i = blockIdx.x % kBlockCluster * S::NW * 32 + threadIdx.x; i < cols * (D / 4);
+             i += kBlockCluster * S::NW * 32) {
+          const int col = i / (D / 4), d = i % (D / 4) * 4;
+          float lse[kBlockCluster], m = kUnset, l = 0.f;
+          float4 x[kBlockCluster], o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int r = 0; r < kBlockCluster; ++r) {
+            lse[r] = *cluster.map_shared_rank(block_lse + col, r);
+            x[r] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(part + col * D + d, r));
+            m = fmaxf(m, lse[r]);
+          }
+#pragma unroll
+          for (int r = 0; r < kBlockCluster; ++r) {
+            const float wt = ptx::ex2(lse[r] - m);
+            l += wt;
+            o = make_float4(fmaf(wt, x[r].x, o.x), fmaf(wt, x[r].y, o.y), fmaf(wt, x[r].z, o.z),
+                            fmaf(wt, x[r].w, o.w));
+          }
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+          const int gc = cg * a.width + col;
+          *reinterpret_cast<float4*>(
+              a.out + (((size_t)done.b * a.Q + gc / a.G) * a.H + kvh * a.G + gc % a.G) * D + d) =
+              make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        }
+        cluster.sync();      // others may still read this block's outputs
+      }
     }
     if (!more) break;
     __syncthreads();      // the next segment's copies reach stage 0
@@ -800,18 +846,21 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
 template <int D, bool F8, int V>
 cudaError_t launch_variant(const BlockDecodeArgs& a, cudaStream_t stream) {
   const long long units = (long long)a.B * a.pool.Hkv * a.n_cg;
-  const long long grid = a.shares ? a.shares : units;
+  const long long grid = a.shares ? a.shares : units * a.cluster;
   if (grid > 0x7fffffffLL) return cudaErrorNotSupported;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(Shape<D>::NW * 32);
   cfg.dynamicSmemBytes = kSmem<D, V>;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kBlockCluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = a.cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, decode_block_kernel<D, F8, V>, a);
 }
 
@@ -827,6 +876,23 @@ int variant_blocks() {
   return per_sm;
 }
 
+// Clusters of one variant that run at once, after variant_blocks.
+template <int D, bool F8, int V>
+int variant_clusters() {
+  int n = 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kBlockCluster);
+  cfg.blockDim = dim3(Shape<D>::NW * 32);
+  cfg.dynamicSmemBytes = kSmem<D, V>;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kBlockCluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaOccupancyMaxActiveClusters(&n, decode_block_kernel<D, F8, V>, &cfg) == cudaSuccess ? n : -1;
+}
+
 template <int D, bool F8>
 cudaError_t launch_codes(const BlockDecodeArgs& a, cudaStream_t stream) {
   if (a.width <= 4) return launch_variant<D, F8, kPair>(a, stream);
@@ -840,6 +906,11 @@ int codes_blocks() {
                    variant_blocks<D, F8, kSixteen>()});
 }
 
+template <int D, bool F8>
+int codes_clusters() {
+  return std::min(variant_clusters<D, F8, kPair>(), variant_clusters<D, F8, kEight>());
+}
+
 }  // namespace block
 
 // One head_dim's kernels, each in a translation unit of its own.
@@ -849,6 +920,9 @@ int codes_blocks() {
   }                                                                                              \
   int block_decode_blocks_##D(bool f8) {                                                         \
     return f8 ? block::codes_blocks<D, true>() : block::codes_blocks<D, false>();                \
+  }                                                                                              \
+  int block_decode_clusters_##D(bool f8) {                                                       \
+    return f8 ? block::codes_clusters<D, true>() : block::codes_clusters<D, false>();            \
   }
 
 cudaError_t launch_block_decode_64(const BlockDecodeArgs& a, bool f8, cudaStream_t stream);
@@ -857,5 +931,8 @@ cudaError_t launch_block_decode_256(const BlockDecodeArgs& a, bool f8, cudaStrea
 int block_decode_blocks_64(bool f8);
 int block_decode_blocks_128(bool f8);
 int block_decode_blocks_256(bool f8);
+int block_decode_clusters_64(bool f8);
+int block_decode_clusters_128(bool f8);
+int block_decode_clusters_256(bool f8);
 
 }  // namespace int8kv

@@ -169,6 +169,22 @@ def test_query_windows(kind, D, Hkv, G, Q):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,Hkv,G,Q,window", [(64, 1, 8, 1, 0), (64, 2, 2, 3, 0), (128, 2, 4, 1, 300),
+                                              (128, 1, 4, 2, 0), (256, 1, 8, 1, 0),
+                                              (256, 2, 3, 1, 700)])
+def test_contexts_of_middling_length(kind, D, Hkv, G, Q, window):
+    """A unit's tiles divided among a cluster's blocks (8 splits and more), some of which
+    then have none, against fp64; fewer splits take the shares."""
+    lens = [0, 1, 127, 129, 1300, 1999]
+    q, pt, dev, orc = _filled(kind, D + window, lens, Hkv, G, D, 32, 64, Q)
+    ref = bu.reference(orc, 0, q, lens, pt, window)
+    outs = [bu.decode(dev, 0, q, lens, pt, window, n) for n in (0, 8, 64, 7, 1)]
+    for out in outs:
+        bu.assert_close(out, ref)
+    assert np.array_equal(outs[0], outs[1]) and np.array_equal(outs[1], outs[2])
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_layers_and_pages_behind_four_gigabytes(kind):
     """Two layers, the second one's pages at byte offsets past 2^32 in each store."""
     from int8_kv_cache_02_gb300 import binding as b
