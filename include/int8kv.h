@@ -334,7 +334,9 @@ int attn_decode_multi_int8(const int8kv_pool* pool, int layer, const uint16_t* q
  * kernel runs one block per SM at a time, so tiles x kv heads x splits blocks
  * take ceil(blocks / SMs) waves of ceil(pages / splits) pages; the count with
  * the shortest such chain (two pages of per-block overhead added per wave) is
- * returned: at least 1, at most the pages of the context and 256.  Returns
+ * returned: at least 1, at most the pages of the context and 256.  Block-scaled
+ * pools: the same over tiles of 64 positions, with six tiles of overhead and the
+ * cost of joining; a chunk of few rows takes attn_decode_n_splits' counts.  Returns
  * >= 1, or NULL_PTR, INVALID_ARG, UNSUPPORTED. */
 int attn_prefill_n_splits(const int8kv_pool* pool, int n_new, int n_heads, int start_pos);
 

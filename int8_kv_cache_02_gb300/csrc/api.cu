@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 
 #include "block_common.cuh"
+#include "block_prefill.h"
 #include "decode_common.cuh"
 #include "internal.h"
 
@@ -227,6 +228,36 @@ static int block_cluster(const int8kv_pool* pool, long long units, int width, lo
                  max_ctx * pool->head_dim <= kBlockJoined
              ? kBlockCluster
              : 1;
+}
+
+// Whether a prefill chunk has rows enough for the tcgen05 kernel's tiles of 128, or is one long
+// query window of the decode kernel.  Measured, in us, tiles against windows, at 1024 / 8192 /
+// 32768 positions: D 256, 2 kv heads, 64 rows a head 21, 34, 42 against 19, 25, 46, 128 rows 26,
+// 36, 47 against 22, 35, 76; D 128, 8 heads, 64 rows 17, 24, 49 against 20, 33, 76; D 64, one
+// head, 128 rows 15, 32, 35 against 17, 20, 26, 512 rows 15, 23, 33 against 20, 27, 51.
+static bool block_tiled(const int8kv_pool* pool, long long n_new, int G) {
+  return n_new * G >= (pool->head_dim == 64 ? 512 : 128);
+}
+
+// Splits of a chunk there: tiles of 64 positions divided among the blocks of a unit (128 rows of
+// a kv head), one block an SM.  A block costs its tiles and six more (its start and its end, 9 us
+// against 1.5 a tile), joining splits the traffic of their rows, 6 MB a tile's time.
+static int block_prefill_splits(const int8kv_pool* pool, int n_new, int n_heads, int G, int start) {
+  const long long units = ((long long)n_new * G + 127) / 128 * pool->n_kv_heads;
+  const long long tiles = ((long long)start + n_new + 63) / 64;
+  const long long sms = pool->num_sms > 0 ? pool->num_sms : 1;
+  const double row_bytes = 8.0 * n_new * n_heads * pool->head_dim;      // written and read
+  double best = -1;
+  int n = 1;
+  for (int s = 1; s <= kMaxSplits && s <= tiles; ++s) {
+    const double cost = (double)((units * s + sms - 1) / sms) * ((tiles + s - 1) / s + 6) +
+                        (s > 1 ? 3 + row_bytes * s / 6e6 : 0);
+    if (best < 0 || cost < best) {
+      best = cost;
+      n = s;
+    }
+  }
+  return n;
 }
 
 int decode_auto_splits(const int8kv_pool* pool, int batch, int q_len, int G, int max_pages,
@@ -593,9 +624,10 @@ int attn_prefill_n_splits(const int8kv_pool* pool, int n_new, int n_heads, int s
     return INT8KV_ERR_INVALID_ARG;
   const int G = n_heads / pool->n_kv_heads;
   if (G > 8) return INT8KV_ERR_UNSUPPORTED;
-  if (is_block(pool))
+  if (is_block(pool) && !block_tiled(pool, n_new, G))
     return block_splits(pool, ((long long)n_new * G + 7) / 8 * pool->n_kv_heads,
                         (int)std::min((long long)start_pos + n_new, (long long)INT32_MAX));
+  if (is_block(pool)) return block_prefill_splits(pool, n_new, n_heads, G, start_pos);
   // One block per SM at a time: (query tiles of 128 rows) x kv heads x splits
   // blocks run in ceil(blocks / SMs) waves of ceil(pages / splits) pages each.
   // Take the split count with the shortest such chain, counting two pages of
@@ -653,15 +685,15 @@ int attn_prefill_chunk_int8(const int8kv_pool* pool, int layer, const uint16_t* 
     if (!aligned16(workspace)) return INT8KV_ERR_ALIGNMENT;
   }
   if (is_block(pool)) {
-    // the chunk is one long query window; its kernel is bound by the warp-level products
     if (!on_current_device(pool)) return INT8KV_ERR_INVALID_ARG;
     if ((long long)max_pages_per_seq * pool->page_size > kBlockMostPositions)
       return INT8KV_ERR_UNSUPPORTED;
-    return block_attention(pool, layer, q, 1, n_new, n_heads, nullptr, start_pos + n_new, page_table,
-                           max_pages_per_seq, 0,
-                           softmax_scale != 0.f ? softmax_scale
-                                                : 1.0f / std::sqrt((float)pool->head_dim),
-                           n_splits, out, a.ws, false, (cudaStream_t)stream);
+    if (!block_tiled(pool, n_new, G))
+      return block_attention(pool, layer, q, 1, n_new, n_heads, nullptr, start_pos + n_new,
+                             page_table, max_pages_per_seq, 0,
+                             softmax_scale != 0.f ? softmax_scale
+                                                  : 1.0f / std::sqrt((float)pool->head_dim),
+                             n_splits, out, a.ws, false, (cudaStream_t)stream);
   }
   a.pool = layer_view(pool, layer);
   a.q = q;
@@ -676,6 +708,9 @@ int attn_prefill_chunk_int8(const int8kv_pool* pool, int layer, const uint16_t* 
   const float scale =
       softmax_scale != 0.f ? softmax_scale : 1.0f / std::sqrt((float)pool->head_dim);
   a.scale_log2 = scale * 1.4426950408889634f;
+  if (is_block(pool))
+    return launch_status(launch_block_prefill(block_view(pool, layer), a, pool->head_dim, is_f8(pool),
+                                              (cudaStream_t)stream));
   const cudaError_t e = launch_prefill(pool, layer, a, (cudaStream_t)stream);
   if (e == cudaErrorNotSupported) return INT8KV_ERR_UNSUPPORTED;
   return e == cudaSuccess ? INT8KV_OK : INT8KV_ERR_CUDA;

@@ -1,0 +1,12 @@
+// The prefill kernel of block-scaled pools: its launcher.
+#pragma once
+
+#include "block_common.cuh"
+
+namespace int8kv {
+
+// Attention of a prefill chunk, and the joining of a.n_splits splits (a.pool is not used).
+cudaError_t launch_block_prefill(const BlockView& pool, const PrefillArgs& a, int head_dim, bool f8,
+                                 cudaStream_t stream);
+
+}  // namespace int8kv

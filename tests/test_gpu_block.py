@@ -389,6 +389,153 @@ def test_prefill_chunk(kind, D, Hkv, G, start, n_new, ps):
     assert b.kv_pool_read_device_error(dev) == 0
 
 
+def _prefill(dev, q, start, pt, n_splits=0, scale=0.0):
+    """q [n_new][H][D] on the host -> fp32 of the same shape."""
+    from int8_kv_cache_02_gb300 import binding as b
+    n_new, H, D = q.shape
+    ns = n_splits or b.attn_prefill_n_splits(dev, n_new, H, start)
+    ws = torch.full((max(16, b.attn_prefill_workspace_bytes(n_new, H, dev.n_kv_heads, D, ns)),), 255,
+                    dtype=torch.uint8, device="cuda")
+    out = torch.full((n_new, H, D), float("nan"), device="cuda")
+    b.attn_prefill_chunk_int8(dev, 0, q.cuda(), start, pt.cuda(), out, ws, softmax_scale=scale,
+                              n_splits=n_splits)
+    torch.cuda.synchronize()
+    return out.cpu().numpy()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,Hkv,G,start,n_new,ps,gs,scale", [
+    (64, 2, 8, 0, 64, 16, 16, 0.0),         # one whole tile of rows, positions in part
+    (64, 1, 7, 130, 75, 32, 32, -0.1),      # rows of a query in two tiles, a negative scale
+    (128, 2, 3, 63, 43, 16, 16, 0.0),       # a last tile of one row
+    (128, 1, 1, 500, 128, 128, 128, 0.0),
+    (256, 2, 5, 1, 26, 64, 32, 0.0),
+    (256, 1, 8, 321, 17, 32, 16, -0.05)])
+def test_prefill_in_tiles_of_rows(kind, D, Hkv, G, start, n_new, ps, gs, scale):
+    """Rows, positions and splits that do not fill their tiles; NaN codes, NaN and infinite scales
+    behind the chunk."""
+    from int8_kv_cache_02_gb300 import binding as b
+    n = start + n_new
+    _, pt, dev, orc = _filled(kind, D + n_new, [n], Hkv, G, D, gs, ps)
+    q = torch.randn((n_new, Hkv * G, D), generator=torch.Generator().manual_seed(n)).half()
+    kh, vh = orc.gather(0, pt[0].numpy(), n)
+    ref = bu.oatt.prefill_chunk(q.numpy(), kh, vh, start, scale or None)
+    last = int(pt[0, (n - 1) // ps])
+    for t in (dev.k_store, dev.v_store):
+        t.view(torch.uint8)[0, last, :, (n - 1) % ps + 1:] = 0x7F
+    for t, x in ((dev.k_scales, float("nan")), (dev.v_scales, float("inf"))):
+        t[0, last, :, -(-((n - 1) % ps + 1) // gs):] = x
+    for n_splits in (0, 1, 3, 40):          # (40: most blocks have no tile)
+        bu.assert_close(_prefill(dev, q, start, pt[0], n_splits, scale), ref, z_max=16,
+                        what=f"splits {n_splits}")
+    assert b.kv_pool_read_device_error(dev) == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rising", [True, False])
+def test_prefill_v_scales_of_any_range(kind, rising):
+    """V magnitudes over 2^24 and zeros along the sequence; rows that attend the small ones."""
+    D, ps, n, G = 128, 16, 16 * 26, 4
+    g = torch.Generator().manual_seed(8)
+    k, v = _rows(g, 1, n, 1, D)
+    size = 2.0 ** -torch.arange(26).repeat_interleave(16).float()
+    size[-16:] = 0
+    size = size.flip(0) if rising else size
+    v = (v.float() * 64 * size[None, :, None, None]).half()
+    k[:, :, 0, 0] = torch.where(size < 2.0 ** -12, 9.0, -9.0).half()[None]
+    pt, n_pages = inputs.page_table([n], ps, seed=8)
+    dev, orc = bu.make_pools(kind, 1, D, 16, ps, n_pages)
+    bu.append(dev, orc, 0, k, v, [0], pt)
+    q = torch.randn((40, G, D), generator=g).half()
+    q[..., 0] = 24.0
+    kh, vh = orc.gather(0, pt[0].numpy(), n)
+    ref = bu.oatt.prefill_chunk(q.numpy(), kh, vh, n - 40)
+    for n_splits in (0, 1, 3):
+        bu.assert_close(_prefill(dev, q, n - 40, pt[0], n_splits), ref, z_max=64)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("ps", [16, 64])
+def test_prefill_flags_bad_pages_and_leaves_them_out(kind, ps):
+    from int8_kv_cache_02_gb300 import binding as b
+    n, n_new, G, D = 256, 32, 4, 128
+    _, pt, dev, orc = _filled(kind, 3, [n], 1, G, D, 16, ps)
+    q = torch.randn((n_new, G, D), generator=torch.Generator().manual_seed(1)).half()
+    kh, vh = orc.gather(0, pt[0].numpy(), n)
+    for lp, entry in ((0, -1), (64 // ps, 10 ** 6), (128 // ps, -(2 ** 31))):
+        bad = pt.clone()
+        bad[0, lp] = entry
+        seen = np.arange(n) // ps != lp
+        ref = bu.oatt.prefill_chunk(q.numpy(), kh[seen], vh[seen], n - n_new - ps)
+        for n_splits in (1, 4):
+            bu.assert_close(_prefill(dev, q, n - n_new, bad[0], n_splits), ref, what=f"{lp}")
+            assert b.kv_pool_read_device_error(dev) == b.DEVERR_PAGE_ID
+    gone = torch.full_like(pt, -1)          # no page at all: rows of zeros
+    for n_splits in (1, 4):
+        assert not _prefill(dev, q, n - n_new, gone[0], n_splits).any()
+        assert b.kv_pool_read_device_error(dev) == b.DEVERR_PAGE_ID
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_captured_prefill_chunks_with_one_workspace(kind):
+    """Two captured chunks that share a workspace, replayed in turn with new queries; and a run
+    on another stream gives the same bits."""
+    from int8_kv_cache_02_gb300 import binding as b
+    n, n_new, G, D = 700, 64, 4, 128
+    _, pt, dev, orc = _filled(kind, 4, [n], 2, G, D, 64, 64)
+    kh, vh = orc.gather(0, pt[0].numpy(), n)
+    ptd = pt[0].cuda()
+    q = [torch.zeros((n_new, 2 * G, D), dtype=torch.float16, device="cuda") for _ in range(2)]
+    out = [torch.empty((n_new, 2 * G, D), device="cuda") for _ in range(2)]
+    ws = torch.empty(b.attn_prefill_workspace_bytes(n_new, 2 * G, 2, D, 5), dtype=torch.uint8,
+                     device="cuda")
+    starts, graphs = (n - n_new, 100), []
+    for i in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            b.attn_prefill_chunk_int8(dev, 0, q[i], starts[i], ptd, out[i], ws, n_splits=5)
+    g = torch.Generator().manual_seed(5)
+    for _ in range(3):
+        for i in range(2):
+            q[i].copy_(torch.randn(q[i].shape, generator=g).half())
+            graphs[i].replay()
+        for i in range(2):
+            ref = bu.oatt.prefill_chunk(q[i].cpu().numpy(), kh, vh, starts[i])
+            bu.assert_close(out[i].cpu().numpy(), ref)
+    other = torch.cuda.Stream()
+    with torch.cuda.stream(other):
+        again = _prefill(dev, q[0], starts[0], pt[0], 5)
+    assert np.array_equal(again, out[0].cpu().numpy())
+
+
+def test_prefill_over_long_contexts():
+    """The sums in tensor memory drop bits below their last place: an output takes n / 8 sums of
+    products in a block (two parts of the weights for every 16 of its n positions), each of
+    which loses at most 2^-23 of it."""
+    n, n_new, D = 16384, 64, 128
+    for kind, G in (("e4m3", 8), ("int8", 2)):
+        dev, _ = bu.make_pools(kind, 1, D, 64, 64, n // 64)
+        g = torch.Generator(device="cuda").manual_seed(1)
+        pt = torch.randperm(n // 64, generator=g, device="cuda").int()[None]
+        k, v = (torch.randn((1, n, 1, D), generator=g, device="cuda").half() for _ in range(2))
+        from int8_kv_cache_02_gb300 import binding as b
+        b.kv_quant_append(dev, 0, k, v, torch.zeros(1, dtype=torch.int32, device="cuda"), pt)
+        q = torch.randn((n_new, G, D), generator=g, device="cuda").half()
+        x = [(t.float().double() * s.double()[..., None]).reshape(-1, 64, D)[pt[0].long()].reshape(n, D)
+             for t, s in ((dev.k_store, dev.k_scales.repeat_interleave(64, 3)),
+                          (dev.v_store, dev.v_scales.repeat_interleave(64, 3)))]
+        z = q.double() @ x[0].T / D ** 0.5                      # [n_new][G][n]
+        at = torch.arange(n, device="cuda")
+        z.masked_fill_((at > (n - n_new + torch.arange(n_new, device="cuda"))[:, None])[:, None],
+                       float("-inf"))
+        ref = torch.softmax(z, -1) @ x[1]
+        for n_splits in (0, 1, 8):
+            got = torch.from_numpy(_prefill(dev, q, n - n_new, pt[0], n_splits)).cuda()
+            rel = ((got - ref).norm(dim=-1) / ref.norm(dim=-1)).max().item()
+            block = n / (n_splits or b.attn_prefill_n_splits(dev, n_new, G, n - n_new))
+            assert rel <= 2 * (6.6e-7 * 8 + 3 * 2.0 ** -21) + block / 8 * 2.0 ** -23, (kind, n_splits, rel)
+
+
 def test_long_chains_do_not_drift():
     """One block takes 32,768 positions alone: 512 tiles a warp.  The products' sums drop bits
     instead of rounding, so their error would grow with the chain (to 2e-5); sums rounded tile by
