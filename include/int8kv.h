@@ -539,6 +539,14 @@ int kv_pages_compact(const int8kv_pool* pool, const int32_t* page_refs, const in
  * (the pool's decode calls do not run on the warp-level kernel). */
 int kv_pool_test_expire_waits(int8kv_pool* pool, uint32_t max_polls);
 
+/* The same for the prefill chunks of a block-scaled pool that run on the tensor-memory
+ * kernel.  With max_us > 0 a thread block's products wait for a tile of V that is never
+ * handed over and give up after max_us microseconds (at most 1000000): the call completes,
+ * INT8KV_DEVERR_TIMEOUT is set, and the block's rows are zeros (of several splits: they
+ * count for nothing).  0 restores normal operation.  Errors: NULL_PTR, INVALID_ARG,
+ * UNSUPPORTED (the pool is not block-scaled). */
+int kv_pool_test_expire_prefill_waits(int8kv_pool* pool, uint32_t max_us);
+
 /* Copy the pool's device error word into *out (host) and clear it.  Blocks
  * until `stream` has finished.  Errors: NULL_PTR (no word given), CUDA. */
 int kv_pool_read_device_error(const int8kv_pool* pool, int32_t* out, void* stream);

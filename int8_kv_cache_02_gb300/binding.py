@@ -53,6 +53,7 @@ _SIGS = {
     "kv_pool_set_decode_kernel": (_c_int, [_vp, _c_int]),
     "kv_pool_image_bytes": (_c_int, [_vp, _c_int, _vp, ctypes.POINTER(_c_size)]),
     "kv_pool_test_expire_waits": (_c_int, [_vp, ctypes.c_uint32]),
+    "kv_pool_test_expire_prefill_waits": (_c_int, [_vp, ctypes.c_uint32]),
     "kv_pool_save": (_c_int, [_vp, _c_int, _vp, _vp, _c_int, _vp, _c_size, _vp, _c_size, _vp]),
     "kv_pages_workspace_bytes": (_c_int, [_vp, _c_int, ctypes.POINTER(_c_size)]),
     "kv_pages_copy": (_c_int, [_vp, _c_int, _vp, _vp, _vp]),
@@ -449,6 +450,14 @@ def kv_pool_read_device_error(pool, stream=None):
     _check(lib().kv_pool_read_device_error(pool.handle, ctypes.byref(v), _stream(stream)),
            "kv_pool_read_device_error")
     return v.value
+
+
+def kv_pool_test_expire_prefill_waits(pool, max_us):
+    """Diagnostic: later prefill chunks of a block-scaled pool (on the tensor-memory kernel) let a
+    wait of every thread block run out after max_us microseconds and report
+    INT8KV_DEVERR_TIMEOUT (0 switches it off)."""
+    _check(lib().kv_pool_test_expire_prefill_waits(pool.handle, int(max_us)),
+           "kv_pool_test_expire_prefill_waits")
 
 
 class KVPool:

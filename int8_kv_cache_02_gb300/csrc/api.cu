@@ -710,7 +710,7 @@ int attn_prefill_chunk_int8(const int8kv_pool* pool, int layer, const uint16_t* 
   a.scale_log2 = scale * 1.4426950408889634f;
   if (is_block(pool))
     return launch_status(launch_block_prefill(block_view(pool, layer), a, pool->head_dim, is_f8(pool),
-                                              (cudaStream_t)stream));
+                                              pool->expire_polls, (cudaStream_t)stream));
   const cudaError_t e = launch_prefill(pool, layer, a, (cudaStream_t)stream);
   if (e == cudaErrorNotSupported) return INT8KV_ERR_UNSUPPORTED;
   return e == cudaSuccess ? INT8KV_OK : INT8KV_ERR_CUDA;
@@ -722,6 +722,14 @@ int kv_pool_test_expire_waits(int8kv_pool* pool, uint32_t max_polls) {
   if (max_polls != 0 && decode_kernel_for(pool, 1) != INT8KV_DECODE_WARP_MMA)
     return INT8KV_ERR_UNSUPPORTED;
   pool->expire_polls = max_polls;
+  return INT8KV_OK;
+}
+
+int kv_pool_test_expire_prefill_waits(int8kv_pool* pool, uint32_t max_us) {
+  if (!pool) return INT8KV_ERR_NULL_PTR;
+  if (max_us > 1000000) return INT8KV_ERR_INVALID_ARG;
+  if (max_us != 0 && !is_block(pool)) return INT8KV_ERR_UNSUPPORTED;
+  if (is_block(pool)) pool->expire_polls = max_us;
   return INT8KV_OK;
 }
 

@@ -81,10 +81,12 @@ struct PrefillBlockArgs {
   float2* part_ml;            // [n_new][H][splits] m, l
   int n_new, H, G, start, splits, n_cg;
   float scale_log2;
+  uint64_t patience;          // ns after which a wait has run out
+  int expire;                 // 1: diagnostic, V's barriers wait for a warp that never comes
 };
 
 struct Shared {
-  uint64_t k_full[2], v_full[2], s_done[2], w_full[2], o_done[2], t_full[4], q_full, drain;
+  uint64_t k_full[2], v_full[2], s_done[2], w_full[2], o_done[2], t_full[4], q_full, drain, stopped;
   uint32_t tmem;
   int failed;
   float k_scale[4][4], v_log2[4][4];       // of a tile's 16-position pieces; four tiles
@@ -100,9 +102,12 @@ __device__ __forceinline__ uint64_t now_ns() {
   return t;
 }
 
-// Bounded wait; false once any wait of the block has run out (failed: null for the last
-// one, which the products in flight end).
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* failed) {
+// Bounded wait: true once the barrier's phase is complete, false where it has run out or
+// another wait of the block has (failed: null for the last one, which the products in flight
+// end).  A complete phase says nothing about the block's other waits.  But every wait is one
+// that the products need, and they complete `drain` only when none was left out.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* failed,
+                                     uint64_t patience) {
   uint64_t from = 0;
   for (;;) {
     for (int i = 0; i < 64; ++i)
@@ -110,7 +115,7 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* failed
     if (failed && *(volatile int*)failed) return false;
     const uint64_t now = now_ns();
     if (from == 0) from = now;
-    if (now - from > kPatience) break;
+    if (now - from > patience) break;
   }
   if (failed) *(volatile int*)failed = 1;
   return false;
@@ -179,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&s.k_full[i], kConvert / 32);
-      ptx::mbar_init(&s.v_full[i], kConvert / 32);
+      ptx::mbar_init(&s.v_full[i], kConvert / 32 + a.expire);
       ptx::mbar_init(&s.s_done[i], 1);
       ptx::mbar_init(&s.w_full[i], kSoftmax / 32);
       ptx::mbar_init(&s.o_done[i], 1);
@@ -187,6 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
     for (int i = 0; i < 4; ++i) ptx::mbar_init(&s.t_full[i], 1);
     ptx::mbar_init(&s.q_full, kSoftmax / 32);
     ptx::mbar_init(&s.drain, 1);
+    ptx::mbar_init(&s.stopped, 1);
     ptx::fence_mbar_init();
     s.failed = 0;
   }
@@ -230,10 +236,11 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&s.q_full);
     float m = kUnset, M = kUnset, l = 0.f;
+    bool ok = true;      // (once it is false the warp only keeps the barrier's count)
     for (int i = 0; i < n; ++i) {
       const int pos = (t0 + i) * kKeys + half * 32, tab = i & 3;
-      bool ok = wait(&s.t_full[tab], (i >> 2) & 1, &s.failed);
-      ok = ok && wait(&s.s_done[i & 1], (i >> 1) & 1, &s.failed);
+      ok = ok && wait(&s.t_full[tab], (i >> 2) & 1, &s.failed, a.patience);
+      ok = ok && wait(&s.s_done[i & 1], (i >> 1) & 1, &s.failed, a.patience);
       ok = __all_sync(0xffffffffu, ok);
       const uint32_t sc = lanes + (i % 3) * kKeys + half * 32;
       uint32_t v[2][16];
@@ -286,8 +293,9 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
         M = topM;
       }
       if (i > 0 && __any_sync(0xffffffffu, r != 1.f)) {
-        if (!__all_sync(0xffffffffu, wait(&s.o_done[(i - 1) & 1], ((i - 1) >> 1) & 1, &s.failed)))
-          continue;
+        ok = wait(&s.o_done[(i - 1) & 1], ((i - 1) >> 1) & 1, &s.failed, a.patience);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) continue;
         tc::fence_after();
         tmem_scale(lanes + L::O + half * (D / 2), D / 2, r);
       }
@@ -325,13 +333,11 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
     s.top[n & 1][half][R] = make_float2(l, 0.f);      // (the last tile's may still be read)
     ptx::named_barrier_sync(1, kSoftmax);
     l += s.top[n & 1][half ^ 1][R].x;
-    bool ok = wait(&s.drain, 0, &s.failed);
-    ok = __all_sync(0xffffffffu, ok);
+    ok = __all_sync(0xffffffffu, wait(&s.drain, 0, &s.failed, a.patience));
     tc::fence_after();
-    if (!ok) {
-      if (tid == 0) flag_error(p.err, INT8KV_DEVERR_TIMEOUT);
-    } else {
-      const bool live = n > 0 && l > 0.f;
+    if (!ok && tid == 0) flag_error(p.err, INT8KV_DEVERR_TIMEOUT);
+    {
+      const bool live = ok && n > 0 && l > 0.f;      // (a block that failed counts for nothing)
       float f = live ? ptx::ex2(M - m - kWeightShift) : 0.f;
       const size_t h = (size_t)(gc / a.G) * a.H + kvh * a.G + gc % a.G;
       float* out = a.out + h * D;
@@ -455,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
     for (int i = 0; i < n; ++i) {
       const int b = i & 1, before = ((i - 2) >> 1) & 1;
       // K's place is free once the scores of tile i - 2 are done, V's once its output is
-      bool ok = i < 2 || wait(&s.s_done[b], before, &s.failed);
+      bool ok = i < 2 || wait(&s.s_done[b], before, &s.failed, a.patience);
       if (!__all_sync(0xffffffffu, ok)) break;
       if (tables) {      // (scores i - 2 were issued behind the output of tile i - 4: its entry is free)
         if (lane < 4) {
@@ -478,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
         load_scale(i + 1);
         find(i + 2);
       }
-      ok = i < 2 || wait(&s.o_done[b], before, &s.failed);
+      ok = i < 2 || wait(&s.o_done[b], before, &s.failed, a.patience);
       if (!__all_sync(0xffffffffu, ok)) break;
       store(smem + L::V + b * L::TILE, v);
       ptx::fence_proxy_async();
@@ -494,8 +500,8 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
     const uint64_t dk = tc::sdesc(ptx::smem_u32(smem + L::K), 16, 1024);
     const uint64_t dv = tc::sdesc(ptx::smem_u32(smem + L::V), kBox, 1024);
     auto scores = [&](int i) {
-      bool ok = i < 3 || wait(&s.o_done[(i - 3) & 1], ((i - 3) >> 1) & 1, &s.failed);
-      ok = ok && wait(&s.k_full[i & 1], (i >> 1) & 1, &s.failed);
+      bool ok = i < 3 || wait(&s.o_done[(i - 3) & 1], ((i - 3) >> 1) & 1, &s.failed, a.patience);
+      ok = ok && wait(&s.k_full[i & 1], (i >> 1) & 1, &s.failed, a.patience);
       if (!__all_sync(0xffffffffu, ok)) return false;
       tc::fence_after();
       if (ptx::elect_one()) {
@@ -508,11 +514,12 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
       __syncwarp();
       return true;
     };
-    bool ok = __all_sync(0xffffffffu, wait(&s.q_full, 0, &s.failed)) && (n == 0 || scores(0));
-    for (int i = 0; ok && i < n; ++i) {
+    bool ok = __all_sync(0xffffffffu, wait(&s.q_full, 0, &s.failed, a.patience)) && (n == 0 || scores(0));
+    int i = 0;
+    for (; ok && i < n; ++i) {
       if (i + 1 < n && !scores(i + 1)) break;
-      ok = wait(&s.w_full[i & 1], (i >> 1) & 1, &s.failed) &&
-           wait(&s.v_full[i & 1], (i >> 1) & 1, &s.failed);
+      ok = wait(&s.w_full[i & 1], (i >> 1) & 1, &s.failed, a.patience) &&
+           wait(&s.v_full[i & 1], (i >> 1) & 1, &s.failed, a.patience);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc::fence_after();
       if (ptx::elect_one()) {
@@ -527,9 +534,11 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
       }
       __syncwarp();
     }
-    if (ptx::elect_one()) tc::mma_commit(&s.drain);      // all products, whatever failed
+    // all products: complete, or the ones issued before a wait ran out
+    uint64_t* end = ok && i == n ? &s.drain : &s.stopped;
+    if (ptx::elect_one()) tc::mma_commit(end);
     __syncwarp();
-    wait(&s.drain, 0, nullptr);
+    wait(end, 0, nullptr, kPatience);
   }
   tc::fence_before();
   __syncthreads();
@@ -639,7 +648,7 @@ cudaError_t launch_codes(const PrefillBlockArgs& a, bool f8, cudaStream_t stream
 }  // namespace
 
 cudaError_t launch_block_prefill(const BlockView& pool, const PrefillArgs& a, int head_dim, bool f8,
-                                 cudaStream_t stream) {
+                                 uint32_t expire_us, cudaStream_t stream) {
   PrefillBlockArgs b;
   b.pool = pool;
   b.q = a.q;
@@ -654,6 +663,8 @@ cudaError_t launch_block_prefill(const BlockView& pool, const PrefillArgs& a, in
   b.splits = a.n_splits;
   b.n_cg = (int)(((long long)a.n_new * a.G + kRows - 1) / kRows);
   b.scale_log2 = a.scale_log2;
+  b.patience = expire_us ? expire_us * 1000ull : kPatience;
+  b.expire = expire_us != 0;
   switch (head_dim) {
     case 64: return launch_codes<64>(b, f8, stream);
     case 128: return launch_codes<128>(b, f8, stream);

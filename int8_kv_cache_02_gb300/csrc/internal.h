@@ -24,7 +24,8 @@ struct int8kv_pool {
   bool has_tmaps;    // TMA descriptors below are valid (shapes the tensor-core decode serves)
   int decode_kernel; // INT8KV_DECODE_*: the kernel its decode calls use (AUTO = the library's choice)
   int resident[4];   // per INT8KV_DECODE_* kernel: blocks resident at once (0 = not yet queried)
-  uint32_t expire_polls;   // diagnostic wait expiry of the decode calls (0: off)
+  uint32_t expire_polls;   // diagnostic wait expiry of the decode calls (0: off); of a block-scaled
+                           // pool's prefill chunks, in microseconds
   CUtensorMap tmap_k;              // K store as [rows][head_dim], 64-row x 128-byte swizzled boxes
   CUtensorMap tmap_v;              // V store, same
 };

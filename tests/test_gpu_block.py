@@ -508,6 +508,39 @@ def test_captured_prefill_chunks_with_one_workspace(kind):
     assert np.array_equal(again, out[0].cpu().numpy())
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,G,n_new", [(64, 8, 100), (128, 4, 64), (256, 8, 32)])
+def test_an_expired_prefill_wait_is_reported_and_its_rows_count_for_nothing(kind, D, G, n_new):
+    """The diagnostic withholds V: the wait for it gives up when weights and their sums are there
+    already.  The error word tells, the rows are zeros, and the same pool gives the same bits as
+    before once it is off."""
+    from int8_kv_cache_02_gb300 import binding as b
+    n = 500
+    _, pt, dev, orc = _filled(kind, D, [n], 2, G, D, 32, 64)
+    q = torch.randn((n_new, 2 * G, D), generator=torch.Generator().manual_seed(2)).half()
+    for n_splits in (1, 3):
+        want = _prefill(dev, q, n - n_new, pt[0], n_splits)
+        assert b.kv_pool_read_device_error(dev) == 0 and want.any()
+        b.kv_pool_test_expire_prefill_waits(dev, 1000)
+        got = _prefill(dev, q, n - n_new, pt[0], n_splits)
+        assert b.kv_pool_read_device_error(dev) == b.DEVERR_TIMEOUT
+        assert not got.any(), n_splits
+        b.kv_pool_test_expire_prefill_waits(dev, 0)
+        assert np.array_equal(_prefill(dev, q, n - n_new, pt[0], n_splits), want)
+        assert b.kv_pool_read_device_error(dev) == 0
+
+
+def test_the_prefill_diagnostic_wants_a_block_scaled_pool_and_a_short_limit():
+    from int8_kv_cache_02_gb300 import binding as b
+    dev, _ = bu.make_pools("int8", 1, 64, 16, 16, 2)
+    rows = b.KVPool(1, 1, 64, 64, 16, 2, "k8v8")
+    for pool, us, status in ((rows, 10, "-6"), (dev, 1000001, "-1")):
+        with pytest.raises(b.Int8KVError, match=status):
+            b.kv_pool_test_expire_prefill_waits(pool, us)
+    b.kv_pool_test_expire_prefill_waits(rows, 0)
+    assert b.lib().kv_pool_test_expire_prefill_waits(None, 1) == -2
+
+
 def test_prefill_over_long_contexts():
     """The sums in tensor memory drop bits below their last place: an output takes n / 8 sums of
     products in a block (two parts of the weights for every 16 of its n positions), each of
