@@ -9,7 +9,7 @@
 // Tiles of 16 positions (T and the page size are multiples of 16, so a tile has
 // one page and one scale of each store).  A warp owns its tiles alone:
 //   S^T[16 x 8] = K[16 x D] q^T[D x 8]            mma.sync m16n8k16, heads on N
-//   O^T[D x 8] += V^T[D x 16] W^T[16 x 8]         W = 2^(z - M) sv, as fp16 hi + lo
+//   O^T[D x 8] += V^T[D x 16] W^T[16 x 8]         W = 2^(z - m - e) sv, as fp16 hi + lo
 // A tile's rows are contiguous in the pool; the warp copies them with cp.async, whole
 // 128-byte lines at a time, into a ring of its own (no barrier but the warp's), with
 // zeros in place of rows outside the context.  (Lanes that fetched just the 64 bytes of
@@ -19,10 +19,13 @@
 // swizzled, so that an operand is a 16-byte shared-memory load without bank conflicts
 // (D = 64: V two-way).
 //
-// Two references per head: m for the softmax sum and M for the weights times their
+// Two references per head: m for the softmax sum and m + e for the weights times their
 // V scales, both the running maximum of what they scale (moved only when exceeded by
 // 2^8), so the fp16 pair of W keeps ~22 bits of the largest weight whatever
-// the scales' range.
+// the scales' range.  A score meets nothing but m, in a difference of near numbers that is
+// exact; e and the V scales' logarithms are small.  (One reference of the scores' own size
+// for the weights would round each tile's exponents to its last place: 2^-9 off
+// at scores of 4e4, and past fp16's range at 4e7.)
 //
 // A column is a (query, head) pair of the kv head.  With at most four of them
 // (kPair) columns 4 - 7 hold the same queries again: there W is the lo part, and one
@@ -221,7 +224,7 @@ template <int D, int V>
 struct Warp {
   static constexpr int NC = Cols<V>::NC;
   float acc[NC][D / 16][4];    // O^T: rows in out_dim's order, columns 2t, 2t + 1
-  float m[NC][2], M[NC][2], l[NC][2];
+  float m[NC][2], e[NC][2], l[NC][2];
   uint32_t q[NC][kSharedQ<D, V> ? 1 : D / 8];       // q^T fragments
 
   __device__ __forceinline__ void reset() {
@@ -230,7 +233,7 @@ struct Warp {
 #pragma unroll
       for (int j = 0; j < D / 16; ++j)
         acc[n][j][0] = acc[n][j][1] = acc[n][j][2] = acc[n][j][3] = 0.f;
-      m[n][0] = m[n][1] = M[n][0] = M[n][1] = kUnset;
+      m[n][0] = m[n][1] = e[n][0] = e[n][1] = kUnset;
       l[n][0] = l[n][1] = 0.f;
     }
   }
@@ -363,7 +366,7 @@ __device__ __forceinline__ void take_stage(Warp<D, V>& w, uint32_t stage, int po
   using S = Shape<D>;
   constexpr int NC = Cols<V>::NC, TPI = S::TPI;
   float z[TPI][NC][4];
-  float top[NC][2], topM[NC][2];
+  float top[NC][2];
 #pragma unroll
   for (int i = 0; i < TPI; ++i) {
     score_tile<D, F8, V>(w, stage + i * S::TILE, ln, shared_q, z[i]);
@@ -392,9 +395,9 @@ __device__ __forceinline__ void take_stage(Warp<D, V>& w, uint32_t stage, int po
       for (int i = 0; i < TPI; ++i) {
         const float x = fmaxf(z[i][n][c], z[i][n][2 + c]);
         top[n][c] = i ? fmaxf(top[n][c], x) : x;
-        topM[n][c] = i ? fmaxf(topM[n][c], x + lv[i]) : x + lv[i];
+        over |= (x - w.m[n][c]) + lv[i] > w.e[n][c] + kLazy;
       }
-      over |= top[n][c] > w.m[n][c] + kLazy || topM[n][c] > w.M[n][c] + kLazy;
+      over |= top[n][c] > w.m[n][c] + kLazy;
     }
   if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
@@ -402,17 +405,22 @@ __device__ __forceinline__ void take_stage(Warp<D, V>& w, uint32_t stage, int po
       float r[2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float x = top[n][c], y = topM[n][c];
+        float nm = fmaxf(w.m[n][c], top[n][c]);
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
-        }
-        const float nm = fmaxf(w.m[n][c], x), nM = fmaxf(w.M[n][c], y);
+        for (int off = 4; off < 32; off <<= 1)
+          nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, off));
+        const float e = w.e[n][c] + (w.m[n][c] - nm);      // (the same reference, from the new m)
+        float ne = e;
+#pragma unroll
+        for (int i = 0; i < TPI; ++i)
+          ne = fmaxf(ne, (fmaxf(z[i][n][c], z[i][n][2 + c]) - nm) + lv[i]);
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1)
+          ne = fmaxf(ne, __shfl_xor_sync(0xffffffffu, ne, off));
         w.l[n][c] *= ptx::ex2(w.m[n][c] - nm);
-        r[c] = ptx::ex2(w.M[n][c] - nM);
+        r[c] = ptx::ex2(e - ne);
         w.m[n][c] = nm;
-        w.M[n][c] = nM;
+        w.e[n][c] = ne;
       }
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {
@@ -431,8 +439,9 @@ __device__ __forceinline__ void take_stage(Warp<D, V>& w, uint32_t stage, int po
       float wt[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        w.l[n][k & 1] += ptx::ex2(z[i][n][k] - w.m[n][k & 1]);
-        wt[k] = ptx::ex2(z[i][n][k] + (lv[i] + kWeightShift - w.M[n][k & 1]));
+        const float d = z[i][n][k] - w.m[n][k & 1];
+        w.l[n][k & 1] += ptx::ex2(d);
+        wt[k] = ptx::ex2(d + (lv[i] + kWeightShift - w.e[n][k & 1]));
       }
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -575,7 +584,7 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
   constexpr bool EARLY = N * D * 4 <= S::STAGE;
   static_assert(N * D * 4 <= S::NS * S::STAGE, "a warp's output fits its ring");
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ float stat[3][S::NW][N];     // m, M, l of each warp and column
+  __shared__ float stat[3][S::NW][N];     // m, e, l of each warp and column
   __shared__ float block_lse[N];          // of a cluster's block, whose outputs are in warp 0's stage 1
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const uint32_t ring = ptx::smem_u32(smem) + warp * S::NS * S::STAGE;
@@ -746,7 +755,7 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
         for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
         if (g == 0) {
           stat[0][warp][col] = w.m[k][c];
-          stat[1][warp][col] = w.M[k][c];
+          stat[1][warp][col] = w.e[k][c];
           stat[2][warp][col] = l;
         }
       }
@@ -759,22 +768,23 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
     if (a.shares && done.first == 0 && threadIdx.x == 0)     // for the combine
       a.part_units[unit] = make_int2(slot, done.pieces);
     for (int col = warp; col < cols; col += S::NW) {
-      float m = kUnset, M = kUnset, l = 0.f, r[S::NW];
+      float m = kUnset, e = -INFINITY, l = 0.f, r[S::NW];
 #pragma unroll
       for (int k = 0; k < S::NW; ++k)
-        if (k < live) {
-          m = fmaxf(m, stat[0][k][col]);
-          M = fmaxf(M, stat[1][k][col]);
-        }
+        if (k < live) m = fmaxf(m, stat[0][k][col]);
 #pragma unroll
       for (int k = 0; k < S::NW; ++k) {
-        r[k] = 0.f;
+        r[k] = -INFINITY;
         if (k < live) {
-          l += stat[2][k][col] * ptx::ex2(stat[0][k][col] - m);
-          r[k] = ptx::ex2(stat[1][k][col] - M);
+          const float d = stat[0][k][col] - m;
+          l += stat[2][k][col] * ptx::ex2(d);
+          r[k] = stat[1][k][col] + d;
+          e = fmaxf(e, r[k]);
         }
       }
-      const float inv = l > 0.f ? __fdividef(ptx::ex2(M - m - kWeightShift), l) : 0.f;
+#pragma unroll
+      for (int k = 0; k < S::NW; ++k) r[k] = k < live ? ptx::ex2(r[k] - e) : 0.f;
+      const float inv = l > 0.f ? __fdividef(ptx::ex2(e - kWeightShift), l) : 0.f;
       const int gc = cg * a.width + col;
       float* out = a.out + (((size_t)done.b * a.Q + gc / a.G) * a.H + kvh * a.G + gc % a.G) * D;
       if (joins) out = reinterpret_cast<float*>(smem + S::STAGE) + col * D;

@@ -389,6 +389,37 @@ def test_prefill_chunk(kind, D, Hkv, G, start, n_new, ps):
     assert b.kv_pool_read_device_error(dev) == 0
 
 
+def _one_winner(kind, D, Hkv, size, lens, ps, seed):
+    """Pools whose sequences' position n // 3 beats the others by half its score: K rows there of
+    +-size, and zeros or half as large elsewhere, beside queries of the same signs."""
+    g = torch.Generator().manual_seed(seed)
+    pt, n_pages = inputs.page_table(lens, ps, seed=seed)
+    dev, orc = bu.make_pools(kind, Hkv, D, 16, ps, n_pages)
+    sign = torch.where(torch.rand((Hkv, D), generator=g) < 0.5, -1.0, 1.0)
+    for b, n in enumerate(lens):
+        k, v = _rows(g, 1, n, Hkv, D)
+        k = sign * size * 0.5 * (torch.arange(n) % 2).view(1, n, 1, 1)
+        k[:, n // 3] = sign * size
+        bu.append(dev, orc, 0, k.half(), v, [0], pt[b:b + 1])
+    return sign, pt, dev, orc
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("size", [60.0, 2000.0])
+@pytest.mark.parametrize("D,Hkv,G,Q", [(64, 2, 4, 1), (128, 1, 8, 1), (128, 2, 8, 2), (256, 2, 3, 1),
+                                       (256, 1, 8, 3)])
+def test_decode_of_large_scores(kind, size, D, Hkv, G, Q):
+    """One position wins by far, with a score of 4e4 to 9e7 in base 2: the output is its V row.
+    What is rounded are exponents relative to the winner's, so the bound is that of small
+    scores; rounded at the scores' own size they would be off by 2^-9 and more."""
+    lens = [1, 40, 700, 2500]
+    sign, pt, dev, orc = _one_winner(kind, D, Hkv, size, lens, 64, D + G)
+    q = (size * sign).repeat_interleave(G, 0).half().expand(len(lens), Q, Hkv * G, D).contiguous()
+    ref = bu.reference(orc, 0, q, lens, pt)
+    for n_splits in (0, 1, 3, 8):
+        bu.assert_close(bu.decode(dev, 0, q, lens, pt, n_splits=n_splits), ref, what=f"{n_splits}")
+
+
 def _prefill(dev, q, start, pt, n_splits=0, scale=0.0):
     """q [n_new][H][D] on the host -> fp32 of the same shape."""
     from int8_kv_cache_02_gb300 import binding as b
