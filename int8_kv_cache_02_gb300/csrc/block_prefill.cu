@@ -16,10 +16,12 @@
 //     from tensor memory), the next tile's scores ahead of this tile's weights: three S
 //     buffers, so that scores never wait for the product that reads the last weights.
 //   - warps 0 - 7 turn scores into weights, two threads a row with 32 positions each.  As in
-//     the decode kernel a row has two references, m for the sum and M for weights
+//     the decode kernel a row has two references, m for the sum and m + e for weights
 //     times their V scales, moved only when exceeded by 2^8, and then O in tensor memory is
-//     rescaled.  w = 2^(z + c), c = log2 sv - M + 6, and the sum takes 2^(-c - m) times the
-//     sum of a piece's 16 weights: one exponential and one multiply-add a score.
+//     rescaled.  w = 2^(z - m + c), c = log2 sv - e + 6, and the sum takes 2^-c times the
+//     sum of a piece's 16 weights: one exponential and one multiply-add a score, which has
+//     c - m as one summand.  That rounds the exponents to the last place of m, so where |m| > 64
+//     (2^-18) the score meets m alone first.
 //
 // Bound by the warps that convert and weigh, then by the tensor pipe (a tile costs 3 * 128 *
 // 64 * D multiply-adds, W being in two parts): a tile takes 1.5 us at D 256 and 1.3 at 128,
@@ -59,6 +61,7 @@ constexpr uint64_t kPatience = 2000000000;      // ns after which a wait has run
 constexpr float kUnset = -1e30f;
 constexpr float kLazy = 8.f;
 constexpr float kWeightShift = 6.f;        // w <= 2^14 in fp16
+constexpr float kNear = 64.f;              // |m| up to here: c - m is one summand
 
 template <int D>
 struct Layout {
@@ -91,7 +94,7 @@ struct Shared {
   int failed;
   float k_scale[4][4], v_log2[4][4];       // of a tile's 16-position pieces; four tiles
   int none[4][4];                          // piece without a page
-  float2 top[2][2][kRows];                 // a thread's largest z and z + log2 sv, by tile and half
+  float2 top[2][2][kRows];                 // largest z of a thread's two pieces, by tile and half
 };
 
 __device__ __forceinline__ int swizzled(int row, int c) { return row * 128 + ((c ^ (row & 7)) << 4); }
@@ -235,7 +238,8 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
     ptx::fence_proxy_async();
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&s.q_full);
-    float m = kUnset, M = kUnset, l = 0.f;
+    float m = kUnset, e = kUnset, l = 0.f;
+    bool far = false;    // whether a row of the warp has |m| > kNear
     bool ok = true;      // (once it is false the warp only keeps the barrier's count)
     for (int i = 0; i < n; ++i) {
       const int pos = (t0 + i) * kKeys + half * 32, tab = i & 3;
@@ -244,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
       ok = __all_sync(0xffffffffu, ok);
       const uint32_t sc = lanes + (i % 3) * kKeys + half * 32;
       uint32_t v[2][16];
-      float f[2], lv[2], top = -INFINITY, topM = -INFINITY;
+      float f[2], lv[2], lo[2], most[2] = {-INFINITY, -INFINITY};
       if (ok) {
         tc::fence_after();
         tc::ld16(sc, v[0]);
@@ -254,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
         for (int j = 0; j < 2; ++j) {
           f[j] = s.k_scale[tab][2 * half + j];
           lv[j] = s.v_log2[tab][2 * half + j];
+          lo[j] = s.v_log2[tab][2 * (half ^ 1) + j];      // (the other thread's)
           none[j] = s.none[tab][2 * half + j];
         }
         tc::wait_ld();
@@ -272,39 +277,62 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
           for (int k = 0; k < 4; ++k)
             x[k] = fmaxf(fmaxf(__uint_as_float(v[j][k]), __uint_as_float(v[j][k + 4])),
                          fmaxf(__uint_as_float(v[j][k + 8]), __uint_as_float(v[j][k + 12])));
-          const float most = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * f[j];
-          top = fmaxf(top, most);
-          topM = fmaxf(topM, most + lv[j]);
+          most[j] = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * f[j];
         }
       }
-      s.top[i & 1][half][R] = make_float2(top, topM);
+      s.top[i & 1][half][R] = make_float2(most[0], most[1]);
       ptx::named_barrier_sync(1, kSoftmax);      // (also once a wait has failed)
       if (!ok) continue;
       const float2 other = s.top[i & 1][half ^ 1][R];
-      top = fmaxf(top, other.x);
-      topM = fmaxf(topM, other.y);
-      if (top > m + kLazy) {
-        l *= ptx::ex2(m - top);
-        m = top;
+      const float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(other.x, other.y));
+      const auto above_m = [&]() {      // the tile's largest z - m + log2 sv
+        return fmaxf(fmaxf(most[0] - m + lv[0], most[1] - m + lv[1]),
+                     fmaxf(other.x - m + lo[0], other.y - m + lo[1]));
+      };
+      if (__any_sync(0xffffffffu, top > m + kLazy || above_m() > e + kLazy)) {
+        if (top > m + kLazy) {
+          l *= ptx::ex2(m - top);
+          e += m - top;      // (the same reference, from the new m)
+          m = top;
+        }
+        const float topE = above_m();
+        float r = 1.f;
+        if (topE > e + kLazy) {
+          r = ptx::ex2(e - topE);
+          e = topE;
+        }
+        far = __any_sync(0xffffffffu, fabsf(m) > kNear && m != kUnset);
+        if (i > 0 && __any_sync(0xffffffffu, r != 1.f)) {
+          ok = wait(&s.o_done[(i - 1) & 1], ((i - 1) >> 1) & 1, &s.failed, a.patience);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) continue;
+          tc::fence_after();
+          tmem_scale(lanes + L::O + half * (D / 2), D / 2, r);
+        }
       }
-      float r = 1.f;
-      if (topM > M + kLazy) {
-        r = ptx::ex2(M - topM);
-        M = topM;
-      }
-      if (i > 0 && __any_sync(0xffffffffu, r != 1.f)) {
-        ok = wait(&s.o_done[(i - 1) & 1], ((i - 1) >> 1) & 1, &s.failed, a.patience);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) continue;
-        tc::fence_after();
-        tmem_scale(lanes + L::O + half * (D / 2), D / 2, r);
+      float to = m;
+      if (far) {      // scores less m, rounded once
+        const uint64_t less = pack2(-m, -m);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint64_t f2 = pack2(f[j], f[j]);
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {
+            float z0, z1;
+            unpack2(fma2(pack2(__uint_as_float(v[j][k]), __uint_as_float(v[j][k + 1])), f2, less), z0, z1);
+            v[j][k] = __float_as_uint(z0);
+            v[j][k + 1] = __float_as_uint(z1);
+          }
+          f[j] = 1.f;
+        }
+        to = 0.f;
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        // w = 2^(z + c) and its share of the sum, w 2^(-c - m).  A scale below 2^-60 of the
+        // w = 2^(z - m + c) and its share of the sum, w 2^-c.  A scale below 2^-60 of the
         // row's reference, or zero, counts as that: its weights only carry the sum.
-        const float c = fmaxf(lv[j] - M + kWeightShift, -60.f - m);
-        const uint64_t f2 = pack2(f[j], f[j]), c2 = pack2(c, c), minus = pack2(-1.f, -1.f);
+        const float c = fmaxf(lv[j] - e + kWeightShift, -60.f), cm = c - to;
+        const uint64_t f2 = pack2(f[j], f[j]), c2 = pack2(cm, cm), minus = pack2(-1.f, -1.f);
         uint64_t sum = pack2(0.f, 0.f);
         uint32_t w[16];
 #pragma unroll
@@ -323,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
         tc::st16(sc + 16 * j, w);
         float s0, s1;
         unpack2(sum, s0, s1);
-        l = fmaf(s0 + s1, ptx::ex2(-c - m), l);
+        l = fmaf(s0 + s1, ptx::ex2(-to - cm), l);
       }
       tc::wait_st();
       tc::fence_before();
@@ -338,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
     if (!ok && tid == 0) flag_error(p.err, INT8KV_DEVERR_TIMEOUT);
     {
       const bool live = ok && n > 0 && l > 0.f;      // (a block that failed counts for nothing)
-      float f = live ? ptx::ex2(M - m - kWeightShift) : 0.f;
+      float f = live ? ptx::ex2(e - kWeightShift) : 0.f;
       const size_t h = (size_t)(gc / a.G) * a.H + kvh * a.G + gc % a.G;
       float* out = a.out + h * D;
       if (a.splits > 1) {

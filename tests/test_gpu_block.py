@@ -572,6 +572,21 @@ def test_the_prefill_diagnostic_wants_a_block_scaled_pool_and_a_short_limit():
     assert b.lib().kv_pool_test_expire_prefill_waits(None, 1) == -2
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("size", [60.0, 2000.0])
+@pytest.mark.parametrize("D,Hkv,G,n_new", [(64, 1, 8, 64), (128, 2, 4, 40), (256, 1, 8, 20),
+                                           (256, 2, 2, 10)])
+def test_prefill_of_large_scores(kind, size, D, Hkv, G, n_new):
+    """As for decode: one position before the chunk wins every row."""
+    n = 700
+    sign, pt, dev, orc = _one_winner(kind, D, Hkv, size, [n], 64, D + G)
+    q = (size * sign).repeat_interleave(G, 0).half().expand(n_new, Hkv * G, D).contiguous()
+    kh, vh = orc.gather(0, pt[0].numpy(), n)
+    ref = bu.oatt.prefill_chunk(q.numpy(), kh, vh, n - n_new)
+    for n_splits in (0, 1, 3):
+        bu.assert_close(_prefill(dev, q, n - n_new, pt[0], n_splits), ref, what=f"{n_splits}")
+
+
 def test_prefill_over_long_contexts():
     """The sums in tensor memory drop bits below their last place: an output takes n / 8 sums of
     products in a block (two parts of the weights for every 16 of its n positions), each of
