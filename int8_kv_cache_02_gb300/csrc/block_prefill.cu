@@ -26,20 +26,23 @@
 // Bound by the warps that convert and weigh, then by the tensor pipe (a tile costs 3 * 128 *
 // 64 * D multiply-adds, W being in two parts): a tile takes 1.5 us at D 256 and 1.3 at 128,
 // 0.8 and 0.4 at the tensor rate.  256 queries over 33,024 positions: 16 / 2 heads of D 256
-// 201 us (int8, 687 TFLOP/s of the formula's operations) and 189 (e4m3), 32 / 8 of D 128 321
-// and 300; the decode kernel's windows took 912, 784, 908 and 758.  What brought it there
+// 199 us (int8, 695 TFLOP/s of the formula's operations) and 186 (e4m3), 32 / 8 of D 128 323
+// and 299; the decode kernel's windows took 912, 784, 908 and 758.  What brought it there
 // (D 256, int8): the products' first form 469 us; O in one product of N = D and one warp a
 // row to join the splits 371; codes' addresses from one page entry a tile 253; packed fp32
 // pairs in the weights, the queries loaded under the first codes, and splits that
-// count a block's start and end 201.
+// count a block's start and end 201 (199 as it is now).
 // Slower: 16 converting warps with registers moved to the others (setmaxnreg; -2 % to +5 %), four
 // threads a row for the scores (+20 %), K converted a tile ahead of V (+8 %), whichever
 // product has its operands issued first (+5 %).
 //
 // The sums in tensor memory drop the bits below their last place instead of rounding: over
-// a block's n positions O loses up to n / 8 * 2^-23 of itself (measured: 2e-5 at 8192
-// positions in one block, 4e-6 as split by default at 32K).  The decode kernel, whose sums are
-// in registers, avoids that.
+// n positions O loses up to n / 8 * 2^-23 of itself (measured: 2e-5 at 8192 positions).  So
+// every kChain tiles the scoring threads add O to their rows' sums in global memory (where the
+// output, or the split's partial, will be) and the next product starts from zero: at most
+// 5120 / 8 * 2^-23 = 8e-5 is lost whatever the context.  131,072 positions in one block:
+// 1.3e-5 off, 3.5e-4 as one chain; 1.5 us a chain of 109 us (D 128) or 129 (D 256).  The decode
+// kernel, whose sums are in registers, has no such loss.
 #include <cuda_fp16.h>
 
 #include "block_prefill.h"
@@ -61,6 +64,7 @@ constexpr uint64_t kPatience = 2000000000;      // ns after which a wait has run
 constexpr float kUnset = -1e30f;
 constexpr float kLazy = 8.f;
 constexpr float kWeightShift = 6.f;        // w <= 2^14 in fp16
+constexpr int kChain = 80;                 // tiles that one sum in tensor memory takes
 constexpr float kNear = 64.f;              // |m| up to here: c - m is one summand
 
 template <int D>
@@ -156,6 +160,83 @@ __device__ __forceinline__ void tmem_scale(uint32_t ta, int n, float f) {
   tc::wait_st();
 }
 
+// The sums of a scoring warp's rows over their earlier chains, D / 2 values of each, which lie
+// where the rows' output will be (own: the lane's).  A whole warp keeps them in pieces of 512
+// bytes, four values of every lane, D / 8 lanes to a row: a lane's own row would be 32
+// lines at a time.  In a warp whose rows are not all there each lane that has one uses it.
+template <int D>
+struct Sums {
+  float* own;
+  bool whole, there;
+  __device__ __forceinline__ float* at(int q) const {      // the lane's values 4q ..
+    constexpr int LANES = D / 8;
+    const int lane = threadIdx.x & 31;
+    const uint64_t other = __shfl_sync(0xffffffffu, (uint64_t)own, q * (32 / LANES) + lane / LANES);
+    return whole ? (float*)other + lane % LANES * 4 : own + 4 * q;
+  }
+  // O (in tensor memory at `from`) times `by` is put there, or added: by reductions in L2, which
+  // nothing waits for.  (Loads, adds and stores took 6.9 us a chain at D 256 instead of 1.5.)
+  // Nobody else adds to them, so the order is the program's.
+  __device__ __forceinline__ void take(uint32_t from, float by, bool first) const {
+#pragma unroll 1
+    for (int c = 0; c < D / 2; c += 16) {
+      uint32_t o[16];
+      tc::ld16(from + c, o);
+      tc::wait_ld();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float* to = at(c / 4 + k);
+        const float4 x = make_float4(
+            __uint_as_float(o[4 * k]) * by, __uint_as_float(o[4 * k + 1]) * by,
+            __uint_as_float(o[4 * k + 2]) * by, __uint_as_float(o[4 * k + 3]) * by);
+        if (there) {
+          if (first)
+            *reinterpret_cast<float4*>(to) = x;
+          else
+            asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(to),
+                         "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w)
+                         : "memory");
+        }
+      }
+    }
+  }
+  // the sums times `by`
+  __device__ __forceinline__ void scale(float by) const {
+#pragma unroll 1
+    for (int q = 0; q < D / 8; ++q) {
+      float4* to = reinterpret_cast<float4*>(at(q));
+      if (there) {
+        const float4 x = __ldcg(to);
+        *to = make_float4(x.x * by, x.y * by, x.z * by, x.w * by);
+      }
+    }
+  }
+  // O gets them added, times `by`
+  __device__ __forceinline__ void give(uint32_t to, float by) const {
+#pragma unroll 1
+    for (int c = 0; c < D / 2; c += 16) {
+      float4 x[4];
+      uint32_t o[16];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4* from = reinterpret_cast<const float4*>(at(c / 4 + k));
+        x[k] = there ? __ldcg(from) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      tc::ld16(to + c, o);
+      tc::wait_ld();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        o[4 * k] = __float_as_uint(fmaf(x[k].x, by, __uint_as_float(o[4 * k])));
+        o[4 * k + 1] = __float_as_uint(fmaf(x[k].y, by, __uint_as_float(o[4 * k + 1])));
+        o[4 * k + 2] = __float_as_uint(fmaf(x[k].z, by, __uint_as_float(o[4 * k + 2])));
+        o[4 * k + 3] = __float_as_uint(fmaf(x[k].w, by, __uint_as_float(o[4 * k + 3])));
+      }
+      tc::st16(to + c, o);
+    }
+    tc::wait_st();
+  }
+};
+
 // Sixteen codes as fp16 in the order codes_to_h2 gives (int8: dims 0 2 1 3 of every four).
 template <bool F8>
 __device__ __forceinline__ void halves_of(const uint4 w, uint4& lo, uint4& hi) {
@@ -238,125 +319,157 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
     ptx::fence_proxy_async();
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&s.q_full);
-    float m = kUnset, e = kUnset, l = 0.f;
+    // where the row's output goes, or its split's partial: until then the sum of earlier chains
+    const auto row_h = [&](int g) { return (size_t)(g / a.G) * a.H + kvh * a.G + g % a.G; };
+    const auto row_out = [&](int g) {
+      return a.splits > 1 ? a.part_o + (row_h(g) * a.splits + split) * D : a.out + row_h(g) * D;
+    };
+    const auto sums = [&]() {
+      int g = gc;
+      asm volatile("" : "+r"(g));      // (computed where it is used, not kept over the loops)
+      return Sums<D>{row_out(g) + half * (D / 2), (g | 31) < rows, g < rows};
+    };
+    const uint32_t my_o = lanes + L::O + half * (D / 2);
+    float m = kUnset, e = kUnset, l = 0.f, e_sum = kUnset;      // (e_sum: e of that sum)
     bool far = false;    // whether a row of the warp has |m| > kNear
     bool ok = true;      // (once it is false the warp only keeps the barrier's count)
-    for (int i = 0; i < n; ++i) {
-      const int pos = (t0 + i) * kKeys + half * 32, tab = i & 3;
-      ok = ok && wait(&s.t_full[tab], (i >> 2) & 1, &s.failed, a.patience);
-      ok = ok && wait(&s.s_done[i & 1], (i >> 1) & 1, &s.failed, a.patience);
-      ok = __all_sync(0xffffffffu, ok);
-      const uint32_t sc = lanes + (i % 3) * kKeys + half * 32;
-      uint32_t v[2][16];
-      float f[2], lv[2], lo[2], most[2] = {-INFINITY, -INFINITY};
-      if (ok) {
-        tc::fence_after();
-        tc::ld16(sc, v[0]);
-        tc::ld16(sc + 16, v[1]);
-        bool none[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          f[j] = s.k_scale[tab][2 * half + j];
-          lv[j] = s.v_log2[tab][2 * half + j];
-          lo[j] = s.v_log2[tab][2 * (half ^ 1) + j];      // (the other thread's)
-          none[j] = s.none[tab][2 * half + j];
+    for (int from = 0; from < n; from += kChain) {
+      if (from > 0) {      // the sum in tensor memory starts anew with the next product
+        ok = ok && wait(&s.o_done[(from - 1) & 1], ((from - 1) >> 1) & 1, &s.failed, a.patience);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+          tc::fence_after();
+          const Sums<D> sum = sums();
+          if (from == kChain) {
+            e_sum = e;
+          } else if (__any_sync(0xffffffffu, e - e_sum > 64.f)) {      // (else O grows to it)
+            sum.scale(ptx::ex2(e_sum - e));
+            e_sum = e;
+          }
+          sum.take(my_o, ptx::ex2(e - e_sum), from == kChain);
         }
-        tc::wait_ld();
-        const bool masked = pos + 31 > least || none[0] || none[1];
+      }
+      const int behind = min(n, from + kChain);
+      for (int i = from; i < behind; ++i) {
+        const int pos = (t0 + i) * kKeys + half * 32, tab = i & 3;
+        ok = ok && wait(&s.t_full[tab], (i >> 2) & 1, &s.failed, a.patience);
+        ok = ok && wait(&s.s_done[i & 1], (i >> 1) & 1, &s.failed, a.patience);
+        ok = __all_sync(0xffffffffu, ok);
+        const uint32_t sc = lanes + (i % 3) * kKeys + half * 32;
+        uint32_t v[2][16];
+        float f[2], lv[2], lo[2], most[2] = {-INFINITY, -INFINITY};
+        if (ok) {
+          tc::fence_after();
+          tc::ld16(sc, v[0]);
+          tc::ld16(sc + 16, v[1]);
+          bool none[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (masked) {
-            const int to = none[j] ? -1 : last - pos - 16 * j;
+          for (int j = 0; j < 2; ++j) {
+            f[j] = s.k_scale[tab][2 * half + j];
+            lv[j] = s.v_log2[tab][2 * half + j];
+            lo[j] = s.v_log2[tab][2 * (half ^ 1) + j];      // (the other thread's)
+            none[j] = s.none[tab][2 * half + j];
+          }
+          tc::wait_ld();
+          const bool masked = pos + 31 > least || none[0] || none[1];
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              v[j][k] = __float_as_uint(k > to ? -INFINITY : __uint_as_float(v[j][k]) * f[j]);
+          for (int j = 0; j < 2; ++j) {
+            if (masked) {
+              const int to = none[j] ? -1 : last - pos - 16 * j;
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                v[j][k] = __float_as_uint(k > to ? -INFINITY : __uint_as_float(v[j][k]) * f[j]);
+              f[j] = 1.f;
+            }
+            float x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              x[k] = fmaxf(fmaxf(__uint_as_float(v[j][k]), __uint_as_float(v[j][k + 4])),
+                           fmaxf(__uint_as_float(v[j][k + 8]), __uint_as_float(v[j][k + 12])));
+            most[j] = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * f[j];
+          }
+        }
+        s.top[i & 1][half][R] = make_float2(most[0], most[1]);
+        ptx::named_barrier_sync(1, kSoftmax);      // (also once a wait has failed)
+        if (!ok) continue;
+        const float2 other = s.top[i & 1][half ^ 1][R];
+        const float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(other.x, other.y));
+        const auto above_m = [&]() {      // the tile's largest z - m + log2 sv
+          return fmaxf(fmaxf(most[0] - m + lv[0], most[1] - m + lv[1]),
+                       fmaxf(other.x - m + lo[0], other.y - m + lo[1]));
+        };
+        if (__any_sync(0xffffffffu, top > m + kLazy || above_m() > e + kLazy)) {
+          if (top > m + kLazy) {
+            l *= ptx::ex2(m - top);
+            e += m - top;      // (the same references, from the new m)
+            e_sum += m - top;
+            m = top;
+          }
+          const float topE = above_m();
+          float r = 1.f;
+          if (topE > e + kLazy) {
+            r = ptx::ex2(e - topE);
+            e = topE;
+          }
+          far = __any_sync(0xffffffffu, fabsf(m) > kNear && m != kUnset);
+          if (i > 0 && __any_sync(0xffffffffu, r != 1.f)) {
+            ok = wait(&s.o_done[(i - 1) & 1], ((i - 1) >> 1) & 1, &s.failed, a.patience);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) continue;
+            tc::fence_after();
+            tmem_scale(lanes + L::O + half * (D / 2), D / 2, r);
+          }
+        }
+        float to = m;
+        if (far) {      // scores less m, rounded once
+          const uint64_t less = pack2(-m, -m);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint64_t f2 = pack2(f[j], f[j]);
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              float z0, z1;
+              unpack2(fma2(pack2(__uint_as_float(v[j][k]), __uint_as_float(v[j][k + 1])), f2, less),
+                      z0, z1);
+              v[j][k] = __float_as_uint(z0);
+              v[j][k + 1] = __float_as_uint(z1);
+            }
             f[j] = 1.f;
           }
-          float x[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            x[k] = fmaxf(fmaxf(__uint_as_float(v[j][k]), __uint_as_float(v[j][k + 4])),
-                         fmaxf(__uint_as_float(v[j][k + 8]), __uint_as_float(v[j][k + 12])));
-          most[j] = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * f[j];
+          to = 0.f;
         }
-      }
-      s.top[i & 1][half][R] = make_float2(most[0], most[1]);
-      ptx::named_barrier_sync(1, kSoftmax);      // (also once a wait has failed)
-      if (!ok) continue;
-      const float2 other = s.top[i & 1][half ^ 1][R];
-      const float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(other.x, other.y));
-      const auto above_m = [&]() {      // the tile's largest z - m + log2 sv
-        return fmaxf(fmaxf(most[0] - m + lv[0], most[1] - m + lv[1]),
-                     fmaxf(other.x - m + lo[0], other.y - m + lo[1]));
-      };
-      if (__any_sync(0xffffffffu, top > m + kLazy || above_m() > e + kLazy)) {
-        if (top > m + kLazy) {
-          l *= ptx::ex2(m - top);
-          e += m - top;      // (the same reference, from the new m)
-          m = top;
-        }
-        const float topE = above_m();
-        float r = 1.f;
-        if (topE > e + kLazy) {
-          r = ptx::ex2(e - topE);
-          e = topE;
-        }
-        far = __any_sync(0xffffffffu, fabsf(m) > kNear && m != kUnset);
-        if (i > 0 && __any_sync(0xffffffffu, r != 1.f)) {
-          ok = wait(&s.o_done[(i - 1) & 1], ((i - 1) >> 1) & 1, &s.failed, a.patience);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) continue;
-          tc::fence_after();
-          tmem_scale(lanes + L::O + half * (D / 2), D / 2, r);
-        }
-      }
-      float to = m;
-      if (far) {      // scores less m, rounded once
-        const uint64_t less = pack2(-m, -m);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const uint64_t f2 = pack2(f[j], f[j]);
+          // w = 2^(z - m + c) and its share of the sum, w 2^-c.  A scale below 2^-60 of the
+          // row's reference, or zero, counts as that: its weights only carry the sum.
+          const float c = fmaxf(lv[j] - e + kWeightShift, -60.f), cm = c - to;
+          const uint64_t f2 = pack2(f[j], f[j]), c2 = pack2(cm, cm), minus = pack2(-1.f, -1.f);
+          uint64_t sum = pack2(0.f, 0.f);
+          uint32_t w[16];
 #pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            float z0, z1;
-            unpack2(fma2(pack2(__uint_as_float(v[j][k]), __uint_as_float(v[j][k + 1])), f2, less), z0, z1);
-            v[j][k] = __float_as_uint(z0);
-            v[j][k + 1] = __float_as_uint(z1);
+          for (int k = 0; k < 8; ++k) {
+            float w0, w1, s0, s1;
+            unpack2(fma2(pack2(__uint_as_float(v[j][2 * k]), __uint_as_float(v[j][2 * k + 1])), f2,
+                         c2),
+                    w0, w1);
+            const uint64_t w2 = pack2(ptx::ex2(w0), ptx::ex2(w1));
+            sum = add2(sum, w2);
+            unpack2(w2, w0, w1);
+            w[k] = ptx::pack_f16x2(w0, w1);
+            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+            unpack2(fma2(pack2(x.x, x.y), minus, w2), s0, s1);
+            w[8 + k] = ptx::pack_f16x2(s0, s1);
           }
-          f[j] = 1.f;
+          tc::st16(sc + 16 * j, w);
+          float s0, s1;
+          unpack2(sum, s0, s1);
+          l = fmaf(s0 + s1, ptx::ex2(-to - cm), l);
         }
-        to = 0.f;
+        tc::wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&s.w_full[i & 1]);
       }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        // w = 2^(z - m + c) and its share of the sum, w 2^-c.  A scale below 2^-60 of the
-        // row's reference, or zero, counts as that: its weights only carry the sum.
-        const float c = fmaxf(lv[j] - e + kWeightShift, -60.f), cm = c - to;
-        const uint64_t f2 = pack2(f[j], f[j]), c2 = pack2(cm, cm), minus = pack2(-1.f, -1.f);
-        uint64_t sum = pack2(0.f, 0.f);
-        uint32_t w[16];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          float w0, w1, s0, s1;
-          unpack2(fma2(pack2(__uint_as_float(v[j][2 * k]), __uint_as_float(v[j][2 * k + 1])), f2, c2),
-                  w0, w1);
-          const uint64_t w2 = pack2(ptx::ex2(w0), ptx::ex2(w1));
-          sum = add2(sum, w2);
-          unpack2(w2, w0, w1);
-          w[k] = ptx::pack_f16x2(w0, w1);
-          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-          unpack2(fma2(pack2(x.x, x.y), minus, w2), s0, s1);
-          w[8 + k] = ptx::pack_f16x2(s0, s1);
-        }
-        tc::st16(sc + 16 * j, w);
-        float s0, s1;
-        unpack2(sum, s0, s1);
-        l = fmaf(s0 + s1, ptx::ex2(-to - cm), l);
-      }
-      tc::wait_st();
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&s.w_full[i & 1]);
     }
     s.top[n & 1][half][R] = make_float2(l, 0.f);      // (the last tile's may still be read)
     ptx::named_barrier_sync(1, kSoftmax);
@@ -367,15 +480,18 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
     {
       const bool live = ok && n > 0 && l > 0.f;      // (a block that failed counts for nothing)
       float f = live ? ptx::ex2(e - kWeightShift) : 0.f;
-      const size_t h = (size_t)(gc / a.G) * a.H + kvh * a.G + gc % a.G;
-      float* out = a.out + h * D;
+      float* const out = row_out(gc);
+      if (n > kChain) {
+        sums().give(my_o, ptx::ex2(e_sum - e));
+        __syncwarp();      // (other lanes' sums lay where this lane's row goes)
+      }
       if (a.splits > 1) {
-        out = a.part_o + (h * a.splits + split) * D;
         if (gc < rows && half == 0)
-          a.part_ml[h * a.splits + split] = make_float2(live ? m : -INFINITY, live ? l : 0.f);
+          a.part_ml[row_h(gc) * a.splits + split] = make_float2(live ? m : -INFINITY, live ? l : 0.f);
       } else if (live) {
         f /= l;
       }
+#pragma unroll 1
       for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
         uint32_t v[16];
         tc::ld16(lanes + L::O + c, v);
@@ -555,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
         for (int j = 0; j < kKeys / 16; ++j) {
           const uint64_t d = dv + (((i & 1) * L::TILE + j * 2048) >> 4);
           const uint32_t w = tmem + i % 3 * kKeys + j * 16;
-          tc::mma_ts(tmem + L::O, w, d, id_o, i > 0 || j > 0);
+          tc::mma_ts(tmem + L::O, w, d, id_o, i % kChain > 0 || j > 0);
           tc::mma_ts(tmem + L::O, w + 8, d, id_o, true);
         }
         tc::mma_commit(&s.o_done[i & 1]);

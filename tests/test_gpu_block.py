@@ -615,6 +615,65 @@ def test_prefill_over_long_contexts():
             assert rel <= 2 * (6.6e-7 * 8 + 3 * 2.0 ** -21) + block / 8 * 2.0 ** -23, (kind, n_splits, rel)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,Hkv,G,n_new", [(64, 4, 8, 608), (128, 8, 4, 608), (256, 2, 8, 1216)])
+def test_prefill_error_does_not_grow_with_the_context(kind, D, Hkv, G, n_new):
+    """131,072 positions before a chunk whose blocks fill the device without splits, and the
+    whole context in one block.  A sum in tensor memory is read out every 5120 positions, in which
+    it takes 5120 / 8 sums of products that lose at most 2^-23 of it each."""
+    from int8_kv_cache_02_gb300 import binding as b
+    start = 131072
+    n = start + n_new
+    n_pages = -(-n // 64)
+    dev, _ = bu.make_pools(kind, Hkv, D, 64, 64, n_pages)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    pt = torch.randperm(n_pages, generator=g, device="cuda").int()[None]
+    k, v = (torch.randn((1, n, Hkv, D), generator=g, device="cuda").half() for _ in range(2))
+    b.kv_quant_append(dev, 0, k, v, torch.zeros(1, dtype=torch.int32, device="cuda"), pt)
+    q = torch.randn((n_new, Hkv * G, D), generator=g, device="cuda").half()
+    rows = torch.tensor([0, 1, n_new // 2, n_new - 2, n_new - 1], device="cuda")
+    hide = torch.arange(n, device="cuda") > (start + rows)[:, None]
+    ref = torch.empty((len(rows), Hkv, G, D), dtype=torch.float64, device="cuda")
+    for h in range(Hkv):
+        kh, vh = (t[0, :, h].float().double().mul_(s[0, :, h].double().repeat_interleave(64, 1)[..., None])
+                  [pt[0].long()].reshape(-1, D)[:n]
+                  for t, s in ((dev.k_store, dev.k_scales), (dev.v_store, dev.v_scales)))
+        z = q[rows].double().view(-1, Hkv, G, D)[:, h] @ kh.T / D ** 0.5
+        z.masked_fill_(hide[:, None], float("-inf"))
+        ref[:, h] = torch.softmax(z, -1) @ vh
+    ref = ref.reshape(len(rows), -1, D)
+    for n_splits in (0, 1, 3):
+        got = torch.from_numpy(_prefill(dev, q, start, pt[0], n_splits)).cuda()[rows]
+        rel = ((got - ref).norm(dim=-1) / ref.norm(dim=-1)).max().item()
+        assert rel <= 2 * (6.6e-7 * 8 + 3 * 2.0 ** -21) + 5120 / 8 * 2.0 ** -23, (n_splits, rel)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("levels", [(0, 4, 2), (3, 0, 5), (0, 66, 70), (0, 130, 300), (300, 80, 0)])
+def test_prefill_sums_over_chains_whose_scores_move(kind, levels):
+    """Three thirds of 5,440 positions whose scores differ by powers of two, with the V rows as far
+    apart the other way: the sums that were read out are worth more, as much and nothing
+    beside the next ones.  Rows in parts of a warp, of one block and of several splits."""
+    n_new, G, D, third = 45, 3, 128, 5440
+    n = 3 * third
+    g = torch.Generator().manual_seed(sum(levels))
+    k, v = _rows(g, 1, n, 1, D)
+    level = torch.tensor(levels).repeat_interleave(third).float()
+    k[:, :, 0, 0] = level * (D ** 0.5 / 24 / 1.4426950)
+    v = (v.float() * torch.exp2(-level.clamp(max=8))[None, :, None, None]).half()
+    pt, n_pages = inputs.page_table([n], 64, seed=8)
+    dev, orc = bu.make_pools(kind, 1, D, 16, 64, n_pages)
+    bu.append(dev, orc, 0, k, v, [0], pt)
+    q = torch.randn((n_new, G, D), generator=g).half()
+    q[..., 0] = 24.0
+    kh, vh = orc.gather(0, pt[0].numpy(), n)
+    ref = bu.oatt.prefill_chunk(q.numpy(), kh, vh, n - n_new)
+    for n_splits in (1, 2, 3):
+        out = _prefill(dev, q, n - n_new, pt[0], n_splits)
+        bu.assert_close(out, ref, z_max=max(levels) + 8 + 5120 / 8 * 2.0 ** -23 / (2 * 6.6e-7),
+                        what=f"{n_splits}")
+
+
 def test_long_chains_do_not_drift():
     """One block takes 32,768 positions alone: 512 tiles a warp.  The products' sums drop bits
     instead of rounding, so their error would grow with the chain (to 2e-5); sums rounded tile by
