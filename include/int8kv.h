@@ -462,7 +462,12 @@ int kv_pool_load(const int8kv_pool* pool, const void* image, size_t image_bytes,
  * one that would take a page's count below 0, is flagged
  * (INT8KV_DEVERR_PAGE_ID) and dropped; so is a length beyond the row
  * (INT8KV_DEVERR_LENGTH), which counts as the row's whole.  Calls whose
- * tables, counts or workspaces are the same must not overlap on the device. */
+ * tables, counts or workspaces are the same must not overlap on the device.
+ * UNSUPPORTED, before anything is changed: a table of more than 2^30 pieces of 32 entries of a
+ * row, rows of 2^31 positions and more, pages of 2^31 bytes and more in a store, or page copies
+ * (of a fork: n_forks, of a compaction: half of the pool) times layers times 16 KB pieces of a
+ * page, K and V counted apart, from 2^31 on.  INVALID_ARG: the pool's device is not the current
+ * one. */
 
 /* Bytes of the workspace of kv_pages_resize, kv_pages_fork and
  * kv_pages_compact for a table of n_seqs rows.  Errors: NULL_PTR, INVALID_ARG. */
@@ -473,7 +478,7 @@ int kv_pages_workspace_bytes(const int8kv_pool* pool, int n_seqs, size_t* out_by
  *              twice, is no copy; one with an entry beyond the pool is flagged and
  *              left out
  * The destinations must differ from each other and from all sources.
- * Errors: NULL_PTR, INVALID_ARG, CUDA. */
+ * Errors: NULL_PTR, INVALID_ARG, UNSUPPORTED, CUDA. */
 int kv_pages_copy(const int8kv_pool* pool, int n, const int32_t* src, const int32_t* dst,
                   void* stream);
 
@@ -489,7 +494,7 @@ int kv_pages_copy(const int8kv_pool* pool, int n, const int32_t* src, const int3
  * Entries for which no page is left stay -1 (INT8KV_DEVERR_NO_PAGE).  A page that
  * is still shared is not copied: cut a sequence back into a shared page only with
  * a fork or copy of it.  Contents of pages are not touched.
- * Errors: NULL_PTR, INVALID_ARG, WORKSPACE, ALIGNMENT, CUDA. */
+ * Errors: NULL_PTR, INVALID_ARG, UNSUPPORTED, WORKSPACE, ALIGNMENT, CUDA. */
 int kv_pages_resize(const int8kv_pool* pool, int32_t* page_refs, int32_t* page_table, int n_seqs,
                     int max_pages_per_seq, const int32_t* seq_lens, void* workspace,
                     size_t workspace_bytes, void* stream);
@@ -507,7 +512,7 @@ int kv_pages_resize(const int8kv_pool* pool, int32_t* page_refs, int32_t* page_t
  * whose child is a parent, and one with a row outside the table are flagged
  * (INT8KV_DEVERR_FORK) and left out.  Where no page is left for the copy
  * (INT8KV_DEVERR_NO_PAGE) the child ends behind the shared pages.
- * Errors: NULL_PTR, INVALID_ARG, WORKSPACE, ALIGNMENT, CUDA. */
+ * Errors: NULL_PTR, INVALID_ARG, UNSUPPORTED, WORKSPACE, ALIGNMENT, CUDA. */
 int kv_pages_fork(const int8kv_pool* pool, int32_t* page_refs, int32_t* page_table, int n_seqs,
                   int max_pages_per_seq, int32_t* seq_lens, int n_forks, const int32_t* parents,
                   const int32_t* children, void* workspace, size_t workspace_bytes, void* stream);
@@ -521,7 +526,7 @@ int kv_pages_fork(const int8kv_pool* pool, int32_t* page_refs, int32_t* page_tab
  * The moved pages keep their old contents too, so work that still reads through
  * the old table may overlap the call while nothing is appended or given out.  An
  * entry that names a free page is flagged and becomes -1.
- * Errors: NULL_PTR, INVALID_ARG, WORKSPACE, ALIGNMENT, CUDA. */
+ * Errors: NULL_PTR, INVALID_ARG, UNSUPPORTED, WORKSPACE, ALIGNMENT, CUDA. */
 int kv_pages_compact(const int8kv_pool* pool, const int32_t* page_refs, const int32_t* page_table,
                      int n_seqs, int max_pages_per_seq, int32_t* page_refs_out,
                      int32_t* page_table_out, int32_t* n_used, void* workspace,

@@ -514,10 +514,18 @@ cudaError_t launch_cluster(void (*kernel)(A...), cudaStream_t stream, A... args)
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// most: pairs at most (the grid); n_dev: their number on the device, or null.
-cudaError_t launch_copy(const int8kv_pool* p, const int32_t* src, const int32_t* dst, int most,
-                        const int32_t* n_dev, cudaStream_t stream) {
+// A copy of at most `most` pairs: what its kernel gets, and its blocks' number.  n_dev: the number
+// of pairs on the device, or null.  Made before a call launches anything, so that one that
+// cannot copy changes nothing.
+struct Copy {
   Regions r;
+  unsigned grid;
+  int most;
+  const int32_t* n_dev;
+};
+
+cudaError_t plan_copy(const int8kv_pool* p, int most, const int32_t* n_dev, Copy* c) {
+  Regions& r = c->r;
   const auto bytes = [&](int region, unsigned* out) {
     size_t b = 0;
     int8kv_pool_region_bytes(1, p->n_kv_heads, p->head_dim, p->group_size, p->page_size, 1,
@@ -538,12 +546,19 @@ cudaError_t launch_copy(const int8kv_pool* p, const int32_t* src, const int32_t*
   r.n_layers = p->n_layers;
   r.n_pages = p->n_pages;
   r.err = p->dev_error;
-  // a number of pairs known on the device only: at most four blocks a slot, which stride
   const long long total = (long long)most * p->n_layers * r.chunks;
   if (total > 0x7fffffffLL) return cudaErrorNotSupported;
+  // a number of pairs known on the device only: at most four blocks a slot, which stride
   const long long cap = n_dev ? 32LL * p->num_sms : 0x7fffffffLL;
+  c->grid = (unsigned)(total < cap ? total : cap);
+  c->most = most;
+  c->n_dev = n_dev;
+  return cudaSuccess;
+}
+
+cudaError_t launch_copy(const Copy& c, const int32_t* src, const int32_t* dst, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(total < cap ? total : cap));
+  cfg.gridDim = dim3(c.grid);
   cfg.blockDim = dim3(kCopyThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -551,7 +566,7 @@ cudaError_t launch_copy(const int8kv_pool* p, const int32_t* src, const int32_t*
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, copy_pages_kernel, r, src, dst, most, n_dev);
+  return cudaLaunchKernelEx(&cfg, copy_pages_kernel, c.r, src, dst, c.most, c.n_dev);
 }
 
 // The checks that the bookkeeping calls share, and their kernels' arguments.
@@ -604,7 +619,9 @@ int kv_pages_copy(const int8kv_pool* pool, int n, const int32_t* src, const int3
   if (n == 0) return INT8KV_OK;
   if (!src || !dst) return INT8KV_ERR_NULL_PTR;
   if (!on_current_device(pool)) return INT8KV_ERR_INVALID_ARG;
-  return status(launch_copy(pool, src, dst, n, nullptr, (cudaStream_t)stream));
+  Copy c;
+  const cudaError_t e = plan_copy(pool, n, nullptr, &c);
+  return status(e != cudaSuccess ? e : launch_copy(c, src, dst, (cudaStream_t)stream));
 }
 
 int kv_pages_resize(const int8kv_pool* pool, int32_t* page_refs, int32_t* page_table, int n_seqs,
@@ -630,10 +647,11 @@ int kv_pages_fork(const int8kv_pool* pool, int32_t* page_refs, int32_t* page_tab
   if (n_forks == 0) return INT8KV_OK;
   if (!seq_lens || !parents || !children) return INT8KV_ERR_NULL_PTR;
   const cudaStream_t s = (cudaStream_t)stream;
-  const cudaError_t e = launch_cluster(fork_kernel, s, (const PagesArgs)a, seq_lens, n_forks,
-                                       parents, children);
-  if (e != cudaSuccess) return status(e);
-  return status(launch_copy(pool, a.src, a.dst, n_forks, nullptr, s));
+  Copy c;
+  cudaError_t e = plan_copy(pool, n_forks, nullptr, &c);
+  if (e == cudaSuccess)
+    e = launch_cluster(fork_kernel, s, (const PagesArgs)a, seq_lens, n_forks, parents, children);
+  return status(e != cudaSuccess ? e : launch_copy(c, a.src, a.dst, s));
 }
 
 int kv_pages_compact(const int8kv_pool* pool, const int32_t* page_refs, const int32_t* page_table,
@@ -646,10 +664,11 @@ int kv_pages_compact(const int8kv_pool* pool, const int32_t* page_refs, const in
   if (st != INT8KV_OK) return st;
   if (!page_refs_out || (n_seqs > 0 && !page_table_out) || !n_used) return INT8KV_ERR_NULL_PTR;
   const cudaStream_t s = (cudaStream_t)stream;
-  const cudaError_t e = launch_cluster(compact_kernel, s, (const PagesArgs)a, page_refs_out,
-                                       page_table_out, n_used);
-  if (e != cudaSuccess) return status(e);
-  return status(launch_copy(pool, a.src, a.dst, pool->n_pages / 2 + 1, a.count, s));
+  Copy c;
+  cudaError_t e = plan_copy(pool, pool->n_pages / 2 + 1, a.count, &c);
+  if (e == cudaSuccess)
+    e = launch_cluster(compact_kernel, s, (const PagesArgs)a, page_refs_out, page_table_out, n_used);
+  return status(e != cudaSuccess ? e : launch_copy(c, a.src, a.dst, s));
 }
 
 }  // extern "C"

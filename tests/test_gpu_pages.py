@@ -190,6 +190,25 @@ def test_large_tables():
         assert u.item() == used and not err
 
 
+def test_a_fork_that_cannot_copy_changes_nothing():
+    """More page copies than a launch counts: refused before the table and the counts change."""
+    from int8_kv_cache_02_gb300 import binding as b
+    layers, forks = 4096, 2 ** 18              # times two chunks a layer's page: 2^31
+    p = b.KVPool(layers, 1, 64, 16, 16, 2, "k8v8_block")
+    refs, lens = _dev([1, 0]), torch.zeros(forks, dtype=torch.int32, device="cuda")
+    table = torch.full((forks, 1), -1, dtype=torch.int32, device="cuda")
+    par, ch = (torch.full((forks,), -1, dtype=torch.int32, device="cuda") for _ in range(2))
+    table[0], lens[0], par[0], ch[0] = 0, 5, 0, 1
+    was = [t.clone() for t in (refs, table, lens)]
+    ws = p.pages_workspace(forks)
+    with pytest.raises(b.Int8KVError, match="-6"):
+        b.kv_pages_fork(p, refs, table, lens, par, ch, ws)
+    for t, x in zip((refs, table, lens), was):
+        assert torch.equal(t, x)
+    b.kv_pages_fork(p, refs, table, lens, par[:-1].contiguous(), ch[:-1].contiguous(), ws)
+    assert refs.tolist() == [1, 1] and table[:3, 0].tolist() == [0, 1, -1] and lens[1] == 5
+
+
 def test_refusals():
     from int8_kv_cache_02_gb300 import binding as b
     s = _State(POOLS[3], 6, 3, 3)
