@@ -209,12 +209,13 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const PagesArgs a,
   run_of(a.n_seqs * per_row, 1, lo, hi);
   int missing = 0, first_missing = hi, row = lo / per_row, c = lo % per_row;
   for (int base = lo; base < hi; base += kBatch) {
-    int e[kBatch], len[kBatch];
+    int e[kBatch];
+    bool need[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int p = c * 32 + lane;
       const bool in = base + k < hi && p < a.max_pages;
-      len[k] = in ? __ldg(lens + row) - (p << a.ps_log2) : 0;      // > 0: the entry is needed
+      need[k] = in && __ldg(lens + row) > p << a.ps_log2;
       e[k] = in ? a.table[(size_t)row * a.max_pages + p] : -1;
       if (++c == per_row) {
         c = 0;
@@ -225,8 +226,8 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const PagesArgs a,
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const bool none = e[k] < 0 || e[k] >= a.n_pages;
-      missing += __popc(__ballot_sync(kAll, len[k] > 0 && none));
-      if (e[k] >= a.n_pages || (len[k] <= 0 && !none)) work |= 1u << k;
+      missing += __popc(__ballot_sync(kAll, need[k] && none));
+      if (e[k] >= a.n_pages || (!need[k] && !none)) work |= 1u << k;
     }
     if (missing && first_missing == hi) first_missing = base;
     while (work) {

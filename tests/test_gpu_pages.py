@@ -209,6 +209,22 @@ def test_a_fork_that_cannot_copy_changes_nothing():
     assert refs.tolist() == [1, 1] and table[:3, 0].tolist() == [0, 1, -1] and lens[1] == 5
 
 
+def test_lengths_far_below_zero_are_empty_rows():
+    """The lowest lengths int32 has: their rows' pages go back, and the others get the lowest
+    free ones."""
+    from int8_kv_cache_02_gb300 import binding as b
+    s = _State(POOLS[3], 12, 4, 4)
+    s.refs[:5] = [1] * 5
+    s.table = [[0, 1, 2, -1], [3, -1, -1, -1], [4, -1, -1, -1], [-1] * 4]
+    s.lens = [-2 ** 31, 40, -2 ** 31 + 20, 64]
+    s.push()
+    before = _snapshot(s.p)
+    moves, err = opages.resize(s.refs, s.table, s.lens, 16)
+    b.kv_pages_resize(s.p, s.d["refs"], s.d["table"], s.d["lens"], s.ws)
+    s.check(moves, err, before, "resize")
+    assert s.table[1] == [3, 0, 1, -1] and not err
+
+
 def test_refusals():
     from int8_kv_cache_02_gb300 import binding as b
     s = _State(POOLS[3], 6, 3, 3)
