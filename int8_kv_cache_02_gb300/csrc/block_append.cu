@@ -82,7 +82,8 @@ __global__ void __launch_bounds__(NT* GROUPS) block_append_kernel(
   static_assert(GROUPS == 1 || NT == 32, "groups of a block are single warps");
   __shared__ float red[NT / 32];
   // Dependents may start once everything before this kernel is complete (not earlier: a
-  // decode of the same call reads what those kernels wrote without waiting again).
+  // decode of the same call reads what those kernels wrote without waiting again, which rests
+  // on these two lines' order).
   ptx::grid_dependency_wait();
   ptx::grid_launch_dependents();
   const int tid = threadIdx.x % NT;

@@ -45,7 +45,15 @@
 // through distributed shared memory: no partials, no combine kernel.
 //
 // Behind an append of the same call (a.appended) the kernel starts under it: only the
-// blocks that the append writes, the last of every sequence, wait for it.
+// blocks that the append writes, the last of every sequence, wait for it.  Lengths, page
+// table, queries and the other blocks are read without a wait of this kernel's own.  What that
+// rests on is an order: every block of the append has waited, so that all kernels before it
+// are complete and their results in global memory, before it lets this one start, and nothing
+// writes them while this one runs.  That a kernel two launches on sees such results without
+// waiting is documented nowhere; steps back to back with forks of their rows, with nothing
+// between them but these launches, bear it out (test_forks_and_fused_steps_back_to_back).
+// Reading them past L1, the one place where older copies could be, cost 3 % of a fused step
+// (8K 11.8 -> 12.1 us) and 1 to 4 % of the calls without an append.
 //
 // Bound by HBM: 2 D bytes per position and kv head.
 #pragma once

@@ -766,6 +766,108 @@ def test_results_do_not_depend_on_the_run_or_the_stream(kind):
     assert np.array_equal(one, two)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n_splits", [1, 3, 8])
+def test_steps_read_what_the_kernels_just_before_them_wrote(kind, n_splits):
+    """A captured step: lengths, tables and queries are written by the launches right before the
+    fused call, whose decode starts under its append, and differ from replay to replay.  A row
+    is on one set of pages in one replay and on the other, with other contents, in the next."""
+    from int8_kv_cache_02_gb300 import binding as b
+    lens = [700, 40, 1900, 129]
+    q0, pt, dev, orc = _filled(kind, 31, [n + 8 for n in lens] * 2, 2, 4, 128, 16, 64)
+    B, H, steps = len(lens), 8, 6
+    g = torch.Generator().manual_seed(3)
+    tables = torch.stack([pt[:B], pt[B:]])                       # [2][B][max_pages]
+    qs = torch.randn((steps, B, 1, H, 128), generator=g).half()
+    at = torch.tensor([[n + s // 2 + 1 for n in lens] for s in range(steps)], dtype=torch.int32)
+    k, v = _rows(g, steps * B, 1, 2, 128)
+    k, v = k.view(steps, B, 2, 128), v.view(steps, B, 2, 128)
+    all_t, all_q, all_n, all_k, all_v = (x.cuda() for x in (tables, qs[:, :, 0].contiguous(), at, k, v))
+    step = torch.zeros(1, dtype=torch.int64, device="cuda")
+    table, q = torch.zeros_like(all_t[0]), torch.zeros_like(all_q[0])
+    n, k1, v1 = torch.zeros_like(all_n[0]), torch.zeros_like(all_k[0]), torch.zeros_like(all_v[0])
+    out, ws = torch.empty((B, H, 128), device="cuda"), dev.decode_workspace(B, H, n_splits)
+
+    def run():
+        for to, src, i in ((k1, all_k, step), (v1, all_v, step), (table, all_t, step % 2),
+                           (n, all_n, step), (q, all_q, step)):
+            torch.index_select(src, 0, i, out=to[None])
+        b.attn_decode_append_int8(dev, 0, q, k1, v1, n, table, out, ws, n_splits=n_splits)
+        step.add_(1)
+
+    torch.index_select(all_q, 0, step, out=q[None])              # (loads its kernels)
+    step % 2, step.add_(0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    outs = []
+    for s in range(steps):
+        graph.replay()
+        outs.append(out.clone())
+    for s in range(steps):
+        pos = (at[s] - 1).tolist()
+        orc.append(0, k[s][:, None].numpy(), v[s][:, None].numpy(), pos, tables[s % 2].numpy())
+        ref = bu.reference(orc, 0, qs[s], at[s].tolist(), tables[s % 2])
+        bu.assert_close(outs[s].cpu().numpy(), ref[:, 0], what=f"step {s}")
+    assert b.kv_pool_read_device_error(dev) == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n_splits,graph", [(1, False), (1, True), (3, True), (8, True)])
+def test_forks_and_fused_steps_back_to_back(kind, n_splits, graph):
+    """Nothing but the library's own launches, each of which may start under the one before it:
+    row 2 becomes a fork of row 0, a step of all rows, a fork of row 1, a step, and so on. Each
+    step's decode starts under its append and must see the table and lengths that the fork before
+    that append wrote, not what the decode before them read."""
+    from int8_kv_cache_02_gb300 import binding as b
+    Hkv, G, D, ps, width, rows = 2, 4, 128, 64, 40, 3
+    lens0 = [700, 2000]
+    dev, orc = bu.make_pools(kind, Hkv, D, 32, ps, 120)
+    refs = torch.zeros(120, dtype=torch.int32, device="cuda")
+    table = torch.full((rows, width), -1, dtype=torch.int32, device="cuda")
+    lens = torch.tensor(lens0 + [0], dtype=torch.int32, device="cuda")
+    ws, dws = dev.pages_workspace(rows), dev.decode_workspace(rows, Hkv * G, n_splits)
+    b.kv_pages_resize(dev, refs, table, lens, ws)
+    g = torch.Generator().manual_seed(7)
+    own = np.arange(rows * width).reshape(rows, width)
+    for i, n in enumerate(lens0):
+        k, v = _rows(g, 1, n, Hkv, D)
+        bu.append(dev, None, 0, k, v, [0], table[i:i + 1].cpu())
+        orc.append(0, k.numpy(), v.numpy(), [0], own[i:i + 1])
+    steps = 10
+    q = torch.randn((steps, rows, 1, Hkv * G, D), generator=g).half()
+    k, v = (torch.randn((steps, rows, Hkv, D), generator=g).half() for _ in range(2))
+    qd, kd, vd = q[:, :, 0].contiguous().cuda(), k.cuda(), v.cuda()
+    out = torch.empty((steps, rows, Hkv * G, D), device="cuda")
+    par = [torch.tensor([s % 2], dtype=torch.int32, device="cuda") for s in range(steps)]
+    child = torch.tensor([2], dtype=torch.int32, device="cuda")
+
+    def run():
+        for s in range(steps):          # (a row's newest position is written again in each step)
+            b.kv_pages_fork(dev, refs, table, lens, par[s], child, ws)
+            b.attn_decode_append_int8(dev, 0, qd[s], kd[s], vd[s], lens, table, out[s], dws,
+                                      n_splits=n_splits)
+
+    if graph:
+        cg = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(cg):
+            run()
+        cg.replay()
+    else:
+        run()
+    torch.cuda.synchronize()
+    n = list(lens0)
+    for s in range(steps):
+        p = s % 2
+        for t in (orc.k_store, orc.v_store, orc.k_scales, orc.v_scales):
+            t[0, own[2]] = t[0, own[p]]
+        now = n + [n[p]]
+        orc.append(0, k[s][:, None].numpy(), v[s][:, None].numpy(), [x - 1 for x in now], own)
+        ref = bu.reference(orc, 0, q[s], now, torch.from_numpy(own))
+        bu.assert_close(out[s].cpu().numpy(), ref[:, 0], what=f"step {s}")
+    assert b.kv_pool_read_device_error(dev) == 0
+
+
 def test_noalloc_decode_and_refusals():
     import ctypes
 
