@@ -674,6 +674,36 @@ def test_prefill_sums_over_chains_whose_scores_move(kind, levels):
                         what=f"{n_splits}")
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_prefill_of_more_units_than_the_device_has_places(kind):
+    """2500 queries of 8/4 heads behind 70,000 positions: 40 tiles of rows for each of four kv
+    heads, 160 blocks, so that some start when others end; pages of 16; and two splits."""
+    from int8_kv_cache_02_gb300 import binding as b
+    Hkv, G, D, n_new, start = 4, 2, 64, 2500, 70000
+    n = start + n_new
+    dev, _ = bu.make_pools(kind, Hkv, D, 16, 16, -(-n // 16))
+    g = torch.Generator(device="cuda").manual_seed(1)
+    pt = torch.randperm(-(-n // 16), generator=g, device="cuda").int()[None]
+    k, v = (torch.randn((1, n, Hkv, D), generator=g, device="cuda").half() for _ in range(2))
+    b.kv_quant_append(dev, 0, k, v, torch.zeros(1, dtype=torch.int32, device="cuda"), pt)
+    q = torch.randn((n_new, Hkv * G, D), generator=g, device="cuda").half()
+    rows = torch.tensor([0, 63, 64, 1250, 2495, 2499], device="cuda")
+    hide = torch.arange(n, device="cuda") > (start + rows)[:, None]
+    ref = torch.empty((len(rows), Hkv, G, D), dtype=torch.float64, device="cuda")
+    for h in range(Hkv):
+        kh, vh = ((t[0, :, h].float().double() * s[0, :, h].double().repeat_interleave(16, 1)[..., None])
+                  [pt[0].long()].reshape(-1, D)[:n]
+                  for t, s in ((dev.k_store, dev.k_scales), (dev.v_store, dev.v_scales)))
+        z = q[rows].double().view(-1, Hkv, G, D)[:, h] @ kh.T / D ** 0.5
+        z.masked_fill_(hide[:, None], float("-inf"))
+        ref[:, h] = torch.softmax(z, -1) @ vh
+    ref = ref.reshape(len(rows), -1, D)
+    for n_splits in (0, 2):
+        got = torch.from_numpy(_prefill(dev, q, start, pt[0], n_splits)).cuda()[rows]
+        rel = ((got - ref).norm(dim=-1) / ref.norm(dim=-1)).max().item()
+        assert rel <= 2 * (6.6e-7 * 8 + 3 * 2.0 ** -21) + 5120 / 8 * 2.0 ** -23, (n_splits, rel)
+
+
 def test_long_chains_do_not_drift():
     """One block takes 32,768 positions alone: 512 tiles a warp.  The products' sums drop bits
     instead of rounding, so their error would grow with the chain (to 2e-5); sums rounded tile by

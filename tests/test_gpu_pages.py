@@ -225,6 +225,73 @@ def test_lengths_far_below_zero_are_empty_rows():
     assert s.table[1] == [3, 0, 1, -1] and not err
 
 
+@pytest.mark.parametrize("rows", [4096, 4097, 9000])
+def test_forks_in_tables_of_many_rows(rows):
+    """Up to 4096 rows every block keeps its own marks; beyond, the cluster shares them in the
+    workspace. Repeated children, children that are parents, rows outside the table, padding."""
+    from int8_kv_cache_02_gb300 import binding as b
+    ps, width = 16, 3
+    rng = random.Random(rows)
+    s = _State(("k8v8_block", 1, 1, 64, 16, 16), rows * 2, rows, width)
+    s.lens = [rng.randint(0, width * ps) if rng.random() < 0.6 else 0 for _ in range(rows)]
+    s.d["lens"].copy_(_dev(s.lens))
+    before = _snapshot(s.p)
+    moves, err = opages.resize(s.refs, s.table, s.lens, ps)
+    b.kv_pages_resize(s.p, s.d["refs"], s.d["table"], s.d["lens"], s.ws)
+    s.check(moves, err, before, "resize")
+    for step in range(2):
+        n = rng.randint(rows // 2, rows)
+        par = [rng.randint(-1, rows) for _ in range(n)]
+        ch = [rng.choice([rng.randint(-1, rows), rng.randint(rows - 40, rows - 1)]) for _ in range(n)]
+        if step:                # few parents: most forks take place
+            par = [rng.randrange(30) if p >= 0 else p for p in par]
+        before = _snapshot(s.p)
+        moves, err = opages.fork(s.refs, s.table, s.lens, par, ch, ps)
+        assert moves and "fork" in err
+        b.kv_pages_fork(s.p, s.d["refs"], s.d["table"], s.d["lens"], _dev(par), _dev(ch), s.ws)
+        s.check(moves, err, before, f"fork {step}")
+
+
+def test_free_pages_behind_the_first_span():
+    """A pool of more than twice the 65,536 pages that are searched at a time: pages from the
+    second and the third span, from all of them at once, and none left."""
+    from int8_kv_cache_02_gb300 import binding as b
+    rows, width, ps, n_pages = 76, 2000, 16, 132500
+    s = _State(("k8v8_block", 1, 1, 64, 16, 16), n_pages, rows, width)
+    full = width * ps
+    before = _snapshot(s.p)
+
+    def resize(what):
+        s.d["lens"].copy_(_dev(s.lens))
+        moves, err = opages.resize(s.refs, s.table, s.lens, ps)
+        b.kv_pages_resize(s.p, s.d["refs"], s.d["table"], s.d["lens"], s.ws)
+        s.check(moves, err, before, what)
+        return err
+
+    s.lens = [full] * 32 + [0] * 44                      # 64,000 pages
+    resize("first")
+    s.lens[32:36] = [full] * 3 + [55]                    # over the border to the second span
+    resize("second")
+    s.lens[:32] = [full - 16 * (i % 2) for i in range(32)]      # holes in the first
+    s.lens[40:71] = [full - 7] * 31                      # all of the second, some of the third
+    assert not resize("third")
+    moves, err = opages.fork(s.refs, s.table, s.lens, [40, 41, 35], [71, 72, 73], ps)
+    b.kv_pages_fork(s.p, s.d["refs"], s.d["table"], s.d["lens"], _dev([40, 41, 35]),
+                    _dev([71, 72, 73]), s.ws)
+    assert min(d for _, d in moves) >= 2 * 65536 and not err
+    s.check(moves, err, before, "fork")
+    before = _snapshot(s.p)
+    s.lens[74] = full
+    assert resize("none left") == {"no_page"}
+    s.lens[:20] = [0] * 20
+    resize("back")
+    moves, err, used = opages.compact(s.refs, s.table)
+    u = _dev([0])
+    b.kv_pages_compact(s.p, s.d["refs"], s.d["table"], s.d["refs"], s.d["table"], u, s.ws)
+    assert u.item() == used and not err
+    s.check(moves, err, before, "compact")
+
+
 def test_refusals():
     from int8_kv_cache_02_gb300 import binding as b
     s = _State(POOLS[3], 6, 3, 3)
