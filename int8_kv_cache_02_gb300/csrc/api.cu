@@ -203,12 +203,13 @@ static int block_splits(const int8kv_pool* pool, long long units, int max_ctx) {
 
 // Blocks of the balanced schedule: one share each.  Unit u's piece in share c is
 // partial u + c, so units + shares - 1 partials of `width` rows must fit the
-// workspace's batch * q_len * n_heads * n_splits rows.
+// workspace's batch * q_len * n_heads * n_splits rows, with the units' records (two words)
+// behind the last one's values.
 static int block_shares(const int8kv_pool* pool, long long units, int width, long long rows,
                         int n_splits) {
   if (n_splits == 1) return 0;
   long long n = units * (n_splits - 1) + 1;
-  const long long fit = rows / width - units + 1;
+  const long long D = pool->head_dim, fit = (rows * D - 2 * units) / (width * D) - units + 1;
   if (n > fit) n = fit;
   if (n > pool->resident[kBlockKernel]) n = pool->resident[kBlockKernel];
   return (int)(n < 1 ? 1 : n);
@@ -306,10 +307,7 @@ static int block_attention(const int8kv_pool* pool, int layer, const uint16_t* q
   d.page_table = page_table;
   d.out = out;
   d.part_o = ws.part_o;
-  d.part_lse = (float*)ws.part_ml;
-  // (the region holds two floats a row; the units' words follow the first of them)
-  const size_t rows = (size_t)batch * q_len * n_heads * n_splits;
-  d.part_units = (int2*)((char*)ws.part_ml + (rows * sizeof(float) + 7) / 8 * 8);
+  d.part_ml = ws.part_ml;
   d.B = batch;
   d.H = n_heads;
   d.G = G;
@@ -320,13 +318,15 @@ static int block_attention(const int8kv_pool* pool, int layer, const uint16_t* q
   d.n_cg = (cols + per - 1) / per;
   d.width = (cols + d.n_cg - 1) / d.n_cg;
   const long long units = (long long)batch * pool->n_kv_heads * d.n_cg;
-  d.shares = block_shares(pool, units, d.width, (long long)rows, n_splits);
+  d.shares = block_shares(pool, units, d.width, (long long)batch * q_len * n_heads * n_splits, n_splits);
   // the kernels count the line of tiles in 32 bits; one block per unit needs no line
   const long long most = ((long long)max_pages * pool->page_size + 15) / 16 + 64;
   if (units * most > INT32_MAX / 2) d.shares = 0;
   const long long cap = (long long)max_pages * pool->page_size;
   d.cluster = block_cluster(pool, units, d.width, window > 0 && window < cap ? window : cap, n_splits);
   if (d.cluster > 1) d.shares = 0;
+  d.part_units =
+      d.shares ? (int2*)(ws.part_o + (size_t)(units + d.shares - 1) * d.width * pool->head_dim) : nullptr;
   d.scale_log2 = scale * 1.4426950408889634f;
   d.appended = appended;
   return launch_status(launch_block_decode(d, pool->head_dim, is_f8(pool), stream));

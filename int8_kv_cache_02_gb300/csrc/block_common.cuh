@@ -186,7 +186,8 @@ struct BlockDecodeArgs {
   const int32_t* page_table;  // [B][max_pages]
   float* out;                 // [B][Q][H][D]
   float* part_o;              // [slots][width][D] normalised partial outputs
-  float* part_lse;            // [slots][width] their log2-sum-exp
+  float2* part_ml;            // [slots][width] their softmax reference m and sum l, apart: in one
+                              // float m + log2 l, a large m would round l away
   int2* part_units;           // [units] first partial and number of them (1: none, it is in out)
   int B, H, G, Q, max_pages, window;
   int n_cg, width;            // column groups per (sequence, kv head), columns of each

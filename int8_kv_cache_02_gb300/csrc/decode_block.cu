@@ -7,7 +7,7 @@ namespace {
 using namespace block;
 
 // Join the partials of units that a share boundary cut; zero rows of empty units:
-//   out = sum_i o_i 2^(lse_i - M) / sum_i 2^(lse_i - M).
+//   out = sum_i o_i l_i 2^(m_i - M) / sum_i l_i 2^(m_i - M).
 // One block per (sequence, query, head) and 128 values of it; a warp takes every 16th
 // partial, a lane four values (D = 64: two).  The decode blocks left each unit's first
 // partial and their number.  The first kAhead rows of each warp are requested before
@@ -34,7 +34,7 @@ template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) decode_block_combine_kernel(
     const BlockDecodeArgs a) {
   constexpr int NT = kJoinWarps * 32, DIMS = D < 128 ? D : 128, PER = DIMS / 32;
-  extern __shared__ float weight[];         // [partials of the unit]
+  extern __shared__ float2 ml[];            // [partials of the unit]
   __shared__ float red[kJoinWarps];
   __shared__ float sums[kJoinWarps][DIMS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -66,9 +66,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_block_combine_kernel(
   }
   float M = -INFINITY;
   for (int i = threadIdx.x; i < n; i += NT) {
-    const float v = a.part_lse[first + (size_t)i * a.width];
-    weight[i] = v;
-    M = fmaxf(M, v);
+    const float2 v = a.part_ml[first + (size_t)i * a.width];
+    ml[i] = v;
+    M = fmaxf(M, v.x);
   }
   M = warp_max(M);
   if (lane == 0) red[warp] = M;
@@ -77,14 +77,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_block_combine_kernel(
   for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, red[w]);
   if (M == -INFINITY) M = 0.f;      // nothing attended: all weights are 0
   float l = 0.f;
-  for (int i = lane; i < n; i += 32) l += ptx::ex2(weight[i] - M);
+  for (int i = lane; i < n; i += 32) l += ml[i].y * ptx::ex2(ml[i].x - M);
   l = warp_sum(l);       // every warp the same sum
   float acc[PER] = {};
 #pragma unroll
   for (int k = 0; k < kAhead; ++k) {
     const int i = warp + k * kJoinWarps;
     if (i < n) {
-      const float r = ptx::ex2(weight[i] - M);
+      const float r = ml[i].y * ptx::ex2(ml[i].x - M);
 #pragma unroll
       for (int e = 0; e < PER; ++e) acc[e] = fmaf(r, x[k][e], acc[e]);
     }
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_block_combine_kernel(
   for (int i = warp + kAhead * kJoinWarps; i < n; i += kJoinWarps) {
     float y[PER];
     load_row<PER>(o + i * stride, y);
-    const float r = ptx::ex2(weight[i] - M);
+    const float r = ml[i].y * ptx::ex2(ml[i].x - M);
 #pragma unroll
     for (int e = 0; e < PER; ++e) acc[e] = fmaf(r, y[e], acc[e]);
   }
@@ -131,15 +131,16 @@ __global__ void __launch_bounds__(kFewWarps * 32) decode_block_combine_few_kerne
   const size_t first = (size_t)unit.x * a.width + col, stride = (size_t)a.width * D;
   float M = kUnset, l = 0.f, acc[PER] = {};
   for (int i0 = 0; i0 < n; i0 += K) {
-    float v[K], x[K][PER], top = M;
+    float2 v[K];
+    float x[K][PER], top = M;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const bool in = i0 + k < n;
-      v[k] = in ? a.part_lse[first + (size_t)(i0 + k) * a.width] : -INFINITY;
+      v[k] = in ? a.part_ml[first + (size_t)(i0 + k) * a.width] : make_float2(-INFINITY, 0.f);
       load_row<PER>(in ? a.part_o + first * D + (i0 + k) * stride + d : nullptr, x[k]);
     }
 #pragma unroll
-    for (int k = 0; k < K; ++k) top = fmaxf(top, v[k]);
+    for (int k = 0; k < K; ++k) top = fmaxf(top, v[k].x);
     const float r = ptx::ex2(M - top);
     M = top;
     l *= r;
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) decode_block_combine_few_kerne
     for (int e = 0; e < PER; ++e) acc[e] *= r;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const float f = ptx::ex2(v[k] - M);
+      const float f = v[k].y * ptx::ex2(v[k].x - M);
       l += f;
 #pragma unroll
       for (int e = 0; e < PER; ++e) acc[e] = fmaf(f, x[k][e], acc[e]);
@@ -178,7 +179,7 @@ cudaError_t launch_combine(const BlockDecodeArgs& a, cudaStream_t stream) {
   }
   cfg.gridDim = dim3(rows, chunks);
   cfg.blockDim = dim3(kJoinWarps * 32);
-  cfg.dynamicSmemBytes = a.shares * sizeof(float);     // a unit has at most a piece in every share
+  cfg.dynamicSmemBytes = a.shares * sizeof(float2);    // a unit has at most a piece in every share
   return cudaLaunchKernelEx(&cfg, decode_block_combine_kernel<D>, a);
 }
 

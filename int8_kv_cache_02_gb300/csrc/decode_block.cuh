@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
   static_assert(N * D * 4 <= S::NS * S::STAGE, "a warp's output fits its ring");
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float stat[3][S::NW][N];     // m, e, l of each warp and column
-  __shared__ float block_lse[N];          // of a cluster's block, whose outputs are in warp 0's stage 1
+  __shared__ float2 block_ml[N];          // of a cluster's block, whose outputs are in warp 0's stage 1
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const uint32_t ring = ptx::smem_u32(smem) + warp * S::NS * S::STAGE;
   const Lane<D> ln(lane);
@@ -816,9 +816,9 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
             make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
       }
       if (!whole && lane == 0) {
-        const float lse = l > 0.f ? m + log2f(l) : -INFINITY;
-        if (joins) block_lse[col] = lse;
-        else a.part_lse[(size_t)slot * a.width + col] = lse;
+        const float2 ml = make_float2(l > 0.f ? m : -INFINITY, l);
+        if (joins) block_ml[col] = ml;
+        else a.part_ml[(size_t)slot * a.width + col] = ml;
       }
     }
     if constexpr (V != kSixteen) {
@@ -830,17 +830,18 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
         for (int i = blockIdx.x % kBlockCluster * S::NW * 32 + threadIdx.x; i < cols * (D / 4);
              i += kBlockCluster * S::NW * 32) {
           const int col = i / (D / 4), d = i % (D / 4) * 4;
-          float lse[kBlockCluster], m = kUnset, l = 0.f;
+          float2 ml[kBlockCluster];
+          float m = kUnset, l = 0.f;
           float4 x[kBlockCluster], o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int r = 0; r < kBlockCluster; ++r) {
-            lse[r] = *cluster.map_shared_rank(block_lse + col, r);
+            ml[r] = *cluster.map_shared_rank(block_ml + col, r);
             x[r] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(part + col * D + d, r));
-            m = fmaxf(m, lse[r]);
+            m = fmaxf(m, ml[r].x);
           }
 #pragma unroll
           for (int r = 0; r < kBlockCluster; ++r) {
-            const float wt = ptx::ex2(lse[r] - m);
+            const float wt = ml[r].y * ptx::ex2(ml[r].x - m);
             l += wt;
             o = make_float4(fmaf(wt, x[r].x, o.x), fmaf(wt, x[r].y, o.y), fmaf(wt, x[r].z, o.z),
                             fmaf(wt, x[r].w, o.w));

@@ -587,6 +587,26 @@ def test_prefill_of_large_scores(kind, size, D, Hkv, G, n_new):
         bu.assert_close(_prefill(dev, q, n - n_new, pt[0], n_splits), ref, what=f"{n_splits}")
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("size", [60.0, 2000.0])
+@pytest.mark.parametrize("D,Hkv,G,Q", [(64, 2, 4, 1), (128, 1, 8, 1), (128, 2, 8, 2), (256, 2, 3, 1)])
+def test_decode_of_large_equal_scores(kind, size, D, Hkv, G, Q):
+    """All K rows alike: every score is the same, 4e4 to 9e7 in base 2, and the output the mean of
+    the V rows, however many of them each partial has."""
+    lens = [1, 40, 700, 2500]
+    g = torch.Generator().manual_seed(D)
+    pt, n_pages = inputs.page_table(lens, 64, seed=D)
+    dev, orc = bu.make_pools(kind, Hkv, D, 16, 64, n_pages)
+    sign = torch.where(torch.rand((Hkv, D), generator=g) < 0.5, -1.0, 1.0)
+    for b, n in enumerate(lens):
+        k = (size * sign).half().expand(1, n, Hkv, D).contiguous()
+        bu.append(dev, orc, 0, k, 1 + _rows(g, 1, n, Hkv, D)[1], [0], pt[b:b + 1])
+    q = (size * sign).repeat_interleave(G, 0).half().expand(len(lens), Q, Hkv * G, D).contiguous()
+    ref = bu.reference(orc, 0, q, lens, pt)
+    for n_splits in (0, 1, 3, 8, 40):
+        bu.assert_close(bu.decode(dev, 0, q, lens, pt, n_splits=n_splits), ref, what=f"{n_splits}")
+
+
 def test_prefill_over_long_contexts():
     """The sums in tensor memory drop bits below their last place: an output takes n / 8 sums of
     products in a block (two parts of the weights for every 16 of its n positions), each of
