@@ -421,19 +421,12 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
           }
         }
         float to = m;
-        if (far) {      // scores less m, rounded once
-          const uint64_t less = pack2(-m, -m);
+        if (far) {      // scores, rounded like m, less m, which is exact
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const uint64_t f2 = pack2(f[j], f[j]);
 #pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              float z0, z1;
-              unpack2(fma2(pack2(__uint_as_float(v[j][k]), __uint_as_float(v[j][k + 1])), f2, less),
-                      z0, z1);
-              v[j][k] = __float_as_uint(z0);
-              v[j][k + 1] = __float_as_uint(z1);
-            }
+            for (int k = 0; k < 16; ++k)
+              v[j][k] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(v[j][k]), f[j]), m));
             f[j] = 1.f;
           }
           to = 0.f;

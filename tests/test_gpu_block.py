@@ -607,6 +607,23 @@ def test_decode_of_large_equal_scores(kind, size, D, Hkv, G, Q):
         bu.assert_close(bu.decode(dev, 0, q, lens, pt, n_splits=n_splits), ref, what=f"{n_splits}")
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("size", [60.0, 2000.0])
+def test_prefill_of_large_equal_scores(kind, size):
+    n, n_new, Hkv, G, D = 900, 70, 2, 3, 128
+    g = torch.Generator().manual_seed(D)
+    pt, n_pages = inputs.page_table([n], 64, seed=D)
+    dev, orc = bu.make_pools(kind, Hkv, D, 16, 64, n_pages)
+    sign = torch.where(torch.rand((Hkv, D), generator=g) < 0.5, -1.0, 1.0)
+    k = (size * sign).half().expand(1, n, Hkv, D).contiguous()
+    bu.append(dev, orc, 0, k, 1 + _rows(g, 1, n, Hkv, D)[1], [0], pt)
+    q = (size * sign).repeat_interleave(G, 0).half().expand(n_new, Hkv * G, D).contiguous()
+    kh, vh = orc.gather(0, pt[0].numpy(), n)
+    ref = bu.oatt.prefill_chunk(q.numpy(), kh, vh, n - n_new)
+    for n_splits in (0, 1, 2, 5):
+        bu.assert_close(_prefill(dev, q, n - n_new, pt[0], n_splits), ref, what=f"{n_splits}")
+
+
 def test_prefill_over_long_contexts():
     """The sums in tensor memory drop bits below their last place: an output takes n / 8 sums of
     products in a block (two parts of the weights for every 16 of its n positions), each of
