@@ -78,9 +78,14 @@
  * page-table rows of at most 2^30 positions (UNSUPPORTED).  n_splits means for
  * them: 1, one thread block per unit (a unit: a kv head of a sequence with its
  * query heads, per 8 or 16 (query, head) pairs); n >= 2, up to units * (n - 1) + 1
- * blocks, at most what the device holds at once, each of which takes an equal share
- * of the tiles of all units, whatever the sequences' lengths, and a combine
- * kernel.  The workspace is the same as for the other pools.
+ * blocks, at most what the device holds at once and the workspace's partials allow,
+ * each of which takes an equal share of the tiles of all units, whatever the
+ * sequences' lengths, and a combine kernel.  n >= 8 also permits a cluster of eight
+ * blocks for each unit and no combine kernel; it is taken where a unit has at most
+ * eight (query, head) pairs, one wave of clusters holds all units, and what a
+ * page-table row holds (or the window, if that is less) times head_dim is at most 2^19:
+ * by the row's capacity, not the lengths.  There every n >= 8 is the same.  The
+ * workspace is the same as for the other pools.
  *
  * Pages: with reference counts in device memory, sequences share pages, and the
  * kv_pages_* calls give pages out, take them back, fork sequences and compact
@@ -321,8 +326,8 @@ int attn_decode_append_int8(const int8kv_pool* pool, int layer, const uint16_t* 
  * products, eight per block: q_len * G <= 8 reads each page once per split,
  * more reads it once per group of eight pairs.  Served by the warp-level
  * tensor-core kernel only (page_size 64, head_dim 128/256, group_size >= 64, a
- * multiple of 64) and on block-scaled pools (up to 16 pairs per block at
- * head_dim 64 and 128); other pools return UNSUPPORTED.  No sliding window.
+ * multiple of 64) and on block-scaled pools (up to 16 pairs per block); other pools
+ * return UNSUPPORTED.  No sliding window.
  * Errors: NULL_PTR, INVALID_ARG, UNSUPPORTED, WORKSPACE, ALIGNMENT, CUDA. */
 int attn_decode_multi_int8(const int8kv_pool* pool, int layer, const uint16_t* q, int batch,
                            int q_len, int n_heads, const int32_t* seq_lens,
@@ -358,8 +363,9 @@ int attn_prefill_workspace_bytes(int n_new, int n_heads, int n_kv_heads, int hea
  *   out         device fp32 [n_new][n_heads][head_dim]
  *   workspace   device, >= attn_prefill_workspace_bytes (any contents)
  * Built for page_size 64, head_dim 128/256, group_size >= 64 and
- * n_heads / n_kv_heads in {1, 2, 4, 8}, and for every block-scaled pool (as one long
- * query window); other shapes return UNSUPPORTED.
+ * n_heads / n_kv_heads in {1, 2, 4, 8}, and for every block-scaled pool: on a kernel of
+ * its own from 128 rows (queries x heads of a kv head) on, 512 at head_dim 64, else as one
+ * long query window; other shapes return UNSUPPORTED.
  * Errors: NULL_PTR, INVALID_ARG, UNSUPPORTED, CAPACITY (start_pos + n_new beyond
  * the page-table row), WORKSPACE, ALIGNMENT, CUDA. */
 int attn_prefill_chunk_int8(const int8kv_pool* pool, int layer, const uint16_t* q, int n_new,

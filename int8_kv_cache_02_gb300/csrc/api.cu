@@ -231,11 +231,13 @@ static int block_cluster(const int8kv_pool* pool, long long units, int width, lo
              : 1;
 }
 
-// Whether a prefill chunk has rows enough for the tcgen05 kernel's tiles of 128, or is one long
-// query window of the decode kernel.  Measured, in us, tiles against windows, at 1024 / 8192 /
-// 32768 positions: D 256, 2 kv heads, 64 rows a head 21, 34, 42 against 19, 25, 46, 128 rows 26,
-// 36, 47 against 22, 35, 76; D 128, 8 heads, 64 rows 17, 24, 49 against 20, 33, 76; D 64, one
-// head, 128 rows 15, 32, 35 against 17, 20, 26, 512 rows 15, 23, 33 against 20, 27, 51.
+// Whether a prefill chunk has rows enough to fill one of the tcgen05 kernel's tiles of 128 (four at
+// D 64), or is one long query window of the decode kernel.  Measured, in us, tiles against
+// windows, at 1024 / 8192 / 32768 positions: D 256, 2 kv heads, 64 rows a head 21, 34, 42 against
+// 19, 25, 46, 128 rows 26, 36, 47 against 22, 35, 76; D 128, 8 heads, 64 rows 17, 24, 49 against
+// 20, 33, 76; D 64, one head, 128 rows 15, 32, 35 against 17, 20, 26, 512 rows 15, 23, 33 against
+// 20, 27, 51.  So the count of rows alone is a rough rule: half-filled tiles would win at D 128, and
+// at D 256 windows win by 1 to 4 us behind few positions.
 static bool block_tiled(const int8kv_pool* pool, long long n_new, int G) {
   return n_new * G >= (pool->head_dim == 64 ? 512 : 128);
 }

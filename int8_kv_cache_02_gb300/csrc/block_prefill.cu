@@ -26,12 +26,12 @@
 // Bound by the warps that convert and weigh, then by the tensor pipe (a tile costs 3 * 128 *
 // 64 * D multiply-adds, W being in two parts): a tile takes 1.5 us at D 256 and 1.3 at 128,
 // 0.8 and 0.4 at the tensor rate.  256 queries over 33,024 positions: 16 / 2 heads of D 256
-// 199 us (int8, 695 TFLOP/s of the formula's operations) and 186 (e4m3), 32 / 8 of D 128 323
-// and 299; the decode kernel's windows took 912, 784, 908 and 758.  What brought it there
+// 200 us (int8, 690 TFLOP/s of the formula's operations) and 186 (e4m3), 32 / 8 of D 128 326
+// and 301; the decode kernel's windows took 912, 784, 908 and 758.  What brought it there
 // (D 256, int8): the products' first form 469 us; O in one product of N = D and one warp a
 // row to join the splits 371; codes' addresses from one page entry a tile 253; packed fp32
 // pairs in the weights, the queries loaded under the first codes, and splits that
-// count a block's start and end 201 (199 as it is now).
+// count a block's start and end 201 (200 as it is now).
 // Slower: 16 converting warps with registers moved to the others (setmaxnreg; -2 % to +5 %), four
 // threads a row for the scores (+20 %), K converted a tile ahead of V (+8 %), whichever
 // product has its operands issued first (+5 %).

@@ -77,7 +77,8 @@ constexpr float kWeightShift = 6.f;   // W is scaled by 2^6: at most 2^14 in fp1
 template <int D>
 struct Shape {
   // Warps per block, eight to an SM.  D 256: one block of eight halves the partials
-  // (128K 31.6 -> 29.8 us; an 8K step 11.3 -> 12.0 us); below, two blocks of four
+  // (128K 31.6 -> 29.8 us; an 8K step 11.3 -> 12.0 us; with sums rounded tile by tile, as they
+  // are now, 31.1 and 12.5, and e4m3 30.0 and 11.6); below, two blocks of four
   // keep more units apart (64 sequences at D 128: 314 us against 318).
   static constexpr int NW = D == 256 ? 8 : 4;
   static constexpr int TPI = 256 / D;                 // tiles a warp takes at a time
