@@ -540,13 +540,13 @@ def test_captured_prefill_chunks_with_one_workspace(kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("D,G,n_new", [(64, 8, 100), (128, 4, 64), (256, 8, 32)])
-def test_an_expired_prefill_wait_is_reported_and_its_rows_count_for_nothing(kind, D, G, n_new):
+@pytest.mark.parametrize("D,G,n_new,n", [(64, 8, 100, 500), (128, 4, 64, 500), (256, 8, 32, 500),
+                                         (128, 4, 64, 6000)])
+def test_an_expired_prefill_wait_is_reported_and_its_rows_count_for_nothing(kind, D, G, n_new, n):
     """The diagnostic withholds V: the wait for it gives up when weights and their sums are there
     already.  The error word tells, the rows are zeros, and the same pool gives the same bits as
     before once it is off."""
     from int8_kv_cache_02_gb300 import binding as b
-    n = 500
     _, pt, dev, orc = _filled(kind, D, [n], 2, G, D, 32, 64)
     q = torch.randn((n_new, 2 * G, D), generator=torch.Generator().manual_seed(2)).half()
     for n_splits in (1, 3):
@@ -707,6 +707,7 @@ def test_prefill_sums_over_chains_whose_scores_move(kind, levels):
     ref = bu.oatt.prefill_chunk(q.numpy(), kh, vh, n - n_new)
     for n_splits in (1, 2, 3):
         out = _prefill(dev, q, n - n_new, pt[0], n_splits)
+        assert np.array_equal(out, _prefill(dev, q, n - n_new, pt[0], n_splits))
         bu.assert_close(out, ref, z_max=max(levels) + 8 + 5120 / 8 * 2.0 ** -23 / (2 * 6.6e-7),
                         what=f"{n_splits}")
 
@@ -933,6 +934,35 @@ def test_forks_and_fused_steps_back_to_back(kind, n_splits, graph):
         ref = bu.reference(orc, 0, q[s], now, torch.from_numpy(own))
         bu.assert_close(out[s].cpu().numpy(), ref[:, 0], what=f"step {s}")
     assert b.kv_pool_read_device_error(dev) == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("window,gs,scale", [(1, 16, 0.0), (5, 64, -0.07), (16, 32, 0.0), (100, 128, 0.2),
+                                             (3000, 16, -0.05)])
+def test_fused_append_with_windows_and_scales(kind, window, gs, scale):
+    """Windows that begin inside the block that the call appends to, and before it; negative
+    softmax scales; rows of length 0 and 1."""
+    from int8_kv_cache_02_gb300 import binding as b
+    lens = [0, 1, 17, 128, 2000]
+    q, pt, dev, orc = _filled(kind, window, lens, 2, 4, 128, gs, 128)
+    g = torch.Generator().manual_seed(4)
+    for n_splits in (1, 3, 8):
+        k, v = _rows(g, 5, 1, 2, 128)
+        pos = [n - 1 for n in lens]
+        orc.append(0, k.numpy(), v.numpy(), pos, pt.numpy())
+        out = torch.full((5, 8, 128), float("nan"), device="cuda")
+        b.attn_decode_append_int8(dev, 0, q[:, 0].contiguous().cuda(), k[:, 0].contiguous().cuda(),
+                                  v[:, 0].contiguous().cuda(),
+                                  torch.tensor(lens, dtype=torch.int32, device="cuda"), pt.cuda(),
+                                  out, dev.decode_workspace(5, 8, n_splits), window=window,
+                                  softmax_scale=scale, n_splits=n_splits)
+        ref = np.zeros(q.shape[:1] + q.shape[2:])
+        for i, n in enumerate(lens):
+            if n:
+                kh, vh = orc.gather(0, pt[i].numpy(), n)
+                ref[i] = bu.oatt.decode(q[i, 0].numpy(), kh, vh, n, window, scale or None)
+        bu.assert_close(out.cpu().numpy(), ref, z_max=16, what=f"{n_splits}")
+        bu.assert_same(dev, orc)
 
 
 def test_noalloc_decode_and_refusals():
