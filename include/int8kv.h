@@ -219,6 +219,47 @@ int kv_quant_append(const int8kv_pool* pool, int layer, const uint16_t* k_new,
                     const uint16_t* v_new, int n_seqs, int n_new, const int32_t* seq_pos,
                     const int32_t* page_table, int max_pages_per_seq, void* stream);
 
+/* Pairs of values that kv_rope_append turns together, of the first rope_dim of a row. */
+#define INT8KV_ROPE_HALVES      0  /* pair i: values i and i + rope_dim / 2 */
+#define INT8KV_ROPE_PAIRS       1  /* pair i: values 2i and 2i + 1 */
+
+/* Rotate the queries and keys of new tokens by their positions, and append keys and values as
+ * kv_quant_append does, in one kernel; every variant.  Pair i, values (a, b), becomes
+ *     a' = fl(fl(a c) - fl(b s)),  b' = fl(fl(b c) + fl(a s))        (fp32, every operation rounded)
+ * with c and s the table's cosine and sine of the position that the pair goes by.  Queries are
+ * rounded to fp16; keys are quantized from the fp32 values, without a rounding between.
+ *   q             device fp16, token t = b * n_new + i at q + t * q_stride: [n_heads][head_dim]; or
+ *                 NULL: keys and values alone (n_heads, q_stride and q_out are not looked at)
+ *   k_new, v_new  device fp16, token t at + t * k_stride and v_stride: [n_kv_heads][head_dim]
+ *                 (so the three may be parts of one projection's rows)
+ *   *_stride      values from a token to the next: at least one token's, multiples of 8
+ *   seq_pos       device int32 [n_seqs]: position in the cache of each sequence's first new token
+ *   new_lens      device int32 [n_seqs], or NULL: sequence b brings its first new_lens[b] of the
+ *                 n_new tokens (fewer than 0 count as 0); the others are not read, and their
+ *                 rows of q_out are left as they are
+ *   rope_table    device fp32 [n_table][rope_dim], 16-byte aligned: cosines of the rope_dim / 2
+ *                 pairs, then their sines
+ *   rope_dim      16, 32, ... head_dim: values of a row that are turned; the others are kept
+ *   rope_style    INT8KV_ROPE_HALVES or INT8KV_ROPE_PAIRS
+ *   positions     device int32 [n_axes][n_seqs][n_new]: rows of the table (images and video: one for
+ *                 each axis), or NULL: seq_pos[b] + i; with several axes it is required
+ *   n_axes        1 .. 4
+ *   pair_axis     HOST uint8 [rope_dim / 2]: the axis that each pair goes by, read before the call
+ *                 returns; NULL for one axis
+ *   q_out         device fp16 [n_seqs][n_new][n_heads][head_dim]; may be q itself where q_stride is
+ *                 n_heads * head_dim, but overlaps nothing else
+ * A position outside the table is flagged (INT8KV_DEVERR_LENGTH) and its pairs are not turned; so is
+ * a new_lens[b] beyond n_new, which counts as n_new.  Tokens without a place in the cache are flagged
+ * and left out as by kv_quant_append; their queries are turned all the same.
+ * Errors: NULL_PTR, INVALID_ARG (also: the pool's device is not the current one), ALIGNMENT,
+ * UNSUPPORTED (n_seqs * n_new * n_heads * head_dim of 2^35 and more), CUDA. */
+int kv_rope_append(const int8kv_pool* pool, int layer, const uint16_t* q, const uint16_t* k_new,
+                   const uint16_t* v_new, long long q_stride, long long k_stride,
+                   long long v_stride, int n_seqs, int n_new, int n_heads, const int32_t* seq_pos,
+                   const int32_t* new_lens, const float* rope_table, int n_table, int rope_dim,
+                   int rope_style, const int32_t* positions, int n_axes, const uint8_t* pair_axis,
+                   uint16_t* q_out, const int32_t* page_table, int max_pages_per_seq, void* stream);
+
 /* Decode kernels, for kv_pool_set_decode_kernel. */
 #define INT8KV_DECODE_AUTO      0  /* the library's choice (the default) */
 #define INT8KV_DECODE_WARP_MMA  1  /* warp-level tensor-core kernel (mma.sync): fused append,
@@ -402,6 +443,40 @@ int attn_decode_int8_noalloc(const int8kv_pool* pool, int layer, const uint16_t*
                              int n_heads, const int32_t* seq_lens, const int32_t* page_table,
                              int max_pages_per_seq, int window, float softmax_scale,
                              int n_splits, float* out, void* stream);
+
+/* Verification of drafted tokens (speculative decoding): behind a verify window's attention
+ * (attn_decode_multi_int8) and the model's head, how many of a sequence's drafts the target's
+ * probabilities accept, and the token behind them, from given random numbers:
+ *     draft i is taken while accept_u[b][i] * q_i(x_i) < p_i(x_i)               (exactly)
+ *     r: the first draft that is not; weights max(p_r - q_r, 0), or p_r where they are all 0
+ *     all n taken: r = n, weights p_n
+ *     the token is the lowest v whose weights 0 .. v sum to more than sample_u[b] * all weights
+ * so that tokens come out as the target alone would draw them.  Sums are exact (in units of 2^-60): a
+ * result does not depend on the shape of the call.
+ *   target_probs  device fp32, row i of sequence b at + (b * (n_draft + 1) + i) * target_stride
+ *   draft_probs   device fp32, row i of sequence b at + (b * n_draft + i) * draft_stride; or NULL:
+ *                 drafts without probabilities (q_i is 1 at x_i)
+ *   *_stride      values from a row to the next, at least vocab
+ *   draft_tokens  device int32 [batch][n_draft]; one outside [0, vocab) is not taken
+ *   n_drafts      device int32 [batch], or NULL (n_draft each): sequence b has its first n_drafts[b]
+ *                 drafts (more than n_draft count as n_draft) and its probabilities are rows
+ *                 0 .. n_drafts[b]; a negative one: the sequence takes no part (tokens -1,
+ *                 n_accepted 0, its length as it is)
+ *   accept_u      device fp32 [batch][n_draft], sample_u device fp32 [batch]: in [0, 1)
+ *   tokens        device int32 [batch][n_draft + 1]: the drafts that are taken, the token behind
+ *                 them, then -1.  That token is -1 where the target's row has no positive value.
+ *   n_accepted    device int32 [batch]: drafts taken
+ *   seq_lens, seq_lens_out  device int32 [batch], both or neither: seq_lens_out[b] = seq_lens[b] less
+ *                 the drafts that were not taken, for a cache that holds the whole window (it may be
+ *                 seq_lens; kv_pages_resize takes the pages back).
+ * Probabilities outside [0, 1] count as the nearest of the two, NaN as 0; below 2^-37 they are cut
+ * to multiples of 2^-60.  n_draft may be 0: plain sampling.
+ * Errors: NULL_PTR, INVALID_ARG (vocab beyond 2^30, too), UNSUPPORTED (a batch of 2^28 and more), CUDA. */
+int kv_verify_drafts(int batch, int n_draft, int vocab, const float* target_probs,
+                     long long target_stride, const float* draft_probs, long long draft_stride,
+                     const int32_t* draft_tokens, const int32_t* n_drafts, const float* accept_u,
+                     const float* sample_u, int32_t* tokens, int32_t* n_accepted,
+                     const int32_t* seq_lens, int32_t* seq_lens_out, void* stream);
 
 /* ---- saved pool images ------------------------------------------------
  * The used positions 0 .. L_b - 1 of each sequence, every layer, with the int8

@@ -16,4 +16,5 @@ from .binding import (F8_BLOCK, K8V8, K8V8_BLOCK, K8V16, K16V8, VARIANTS,  # noq
                       int8kv_pool_region_bytes, int8kv_status_string, kv_pages_compact,
                       kv_pages_copy, kv_pages_fork, kv_pages_resize, kv_pages_workspace_bytes,
                       kv_pool_create,
-                      kv_pool_destroy, kv_pool_read_device_error, kv_quant_append, lib)
+                      kv_pool_destroy, kv_pool_read_device_error, kv_quant_append, kv_rope_append,
+                      kv_verify_drafts, lib)

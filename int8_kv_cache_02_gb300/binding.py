@@ -26,14 +26,21 @@ DEVERR_PAGE_ID, DEVERR_LENGTH, DEVERR_TIMEOUT = 1, 2, 4
 DEVERR_NO_PAGE, DEVERR_FORK = 8, 16
 ERR_FORMAT = -9
 DECODE_AUTO, DECODE_WARP_MMA, DECODE_SIMT = 0, 1, 3
+ROPE_STYLES = {"halves": 0, "pairs": 1}
 
 _c_int, _c_size, _vp, _c_float = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float
+_c_ll = ctypes.c_longlong
 _SIGS = {
     "int8kv_status_string": (ctypes.c_char_p, [_c_int]),
     "int8kv_pool_region_bytes": (_c_int, [_c_int] * 8 + [ctypes.POINTER(_c_size)]),
     "kv_pool_create": (_c_int, [ctypes.POINTER(_vp)] + [_c_int] * 7 + [_vp] * 5),
     "kv_pool_destroy": (None, [_vp]),
     "kv_quant_append": (_c_int, [_vp, _c_int, _vp, _vp, _c_int, _c_int, _vp, _vp, _c_int, _vp]),
+    "kv_rope_append": (_c_int, [_vp, _c_int, _vp, _vp, _vp, _c_ll, _c_ll, _c_ll, _c_int, _c_int,
+                                _c_int, _vp, _vp, _vp, _c_int, _c_int, _c_int, _vp, _c_int, _vp,
+                                _vp, _vp, _c_int, _vp]),
+    "kv_verify_drafts": (_c_int, [_c_int, _c_int, _c_int, _vp, _c_ll, _vp, _c_ll, _vp, _vp, _vp,
+                                  _vp, _vp, _vp, _vp, _vp, _vp]),
     "attn_decode_n_splits": (_c_int, [_vp, _c_int, _c_int]),
     "attn_decode_workspace_bytes": (_c_int, [_c_int] * 5 + [ctypes.POINTER(_c_size)]),
     "attn_decode_int8": (_c_int, [_vp, _c_int, _vp, _c_int, _c_int, _vp, _vp, _c_int, _c_int,
@@ -176,6 +183,140 @@ def kv_quant_append(pool, layer, k_new, v_new, seq_pos, page_table, stream=None)
                                  _dev(seq_pos, torch.int32, "seq_pos"),
                                  _dev(page_table, torch.int32, "page_table"),
                                  page_table.shape[1], _stream(stream)), "kv_quant_append")
+
+
+def _token_rows(t, n_heads, head_dim, name):
+    """Address and token stride of fp16 rows [n_seqs][n_new][n_heads][head_dim], evenly spaced (a part
+    of a wider projection's rows will do)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dtype != torch.float16:
+        raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
+    _shape(t, (*t.shape[:2], n_heads, head_dim), name)
+    seqs, n_new = t.shape[:2]
+    if t.numel() == 0:
+        return t.data_ptr(), n_heads * head_dim
+    s0, s1, s2, s3 = t.stride()
+    if n_new <= 1:
+        s1 = s0 if seqs > 1 else n_heads * head_dim
+    if s3 != 1 or (n_heads > 1 and s2 != head_dim) or (seqs > 1 and s0 != n_new * s1):
+        raise ValueError(f"{name}'s tokens must lie evenly apart, each token's heads together")
+    return t.data_ptr(), s1
+
+
+def kv_rope_append(pool, layer, k_new, v_new, seq_pos, page_table, rope_table, q=None, q_out=None,
+                   positions=None, pair_axis=None, rope_dim=None, style="halves", new_lens=None,
+                   stream=None):
+    """Rotate q (fp16 [n_seqs][n_new][H][D], may be None) into q_out (the same shape, contiguous) and
+    k_new (fp16 [n_seqs][n_new][Hkv][D]) by their positions, and append k_new and v_new behind
+    seq_pos (int32 [n_seqs]).
+
+    rope_table: fp32 [n_table][rope_dim], cosines then sines.  positions: int32
+    [n_axes][n_seqs][n_new] or [n_seqs][n_new]; None: seq_pos[b] + i.  pair_axis: uint8
+    [rope_dim / 2] on the HOST, the axis of each pair.  new_lens: int32 [n_seqs], tokens that each
+    sequence brings.  q, k_new and v_new may be parts of one projection's rows."""
+    if k_new.dim() != 4 or v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must have shape [n_seqs][n_new][n_kv_heads][head_dim]")
+    n_seqs, n_new = k_new.shape[:2]
+    k, ks = _token_rows(k_new, pool.n_kv_heads, pool.head_dim, "k_new")
+    v, vs = _token_rows(v_new, pool.n_kv_heads, pool.head_dim, "v_new")
+    qp = qo = axis = at = lens = None
+    n_heads = qs = 0
+    if q is not None:
+        if q.dim() != 4 or q.shape[:2] != k_new.shape[:2]:
+            raise ValueError("q must have shape [n_seqs][n_new][n_heads][head_dim]")
+        n_heads = q.shape[2]
+        qp, qs = _token_rows(q, n_heads, pool.head_dim, "q")
+        qo = _dev(q_out, torch.float16, "q_out")
+        _shape(q_out, q.shape, "q_out")
+    table = _dev(rope_table, torch.float32, "rope_table")
+    if rope_table.dim() != 2 or (rope_dim is not None and rope_dim != rope_table.shape[1]):
+        raise ValueError("rope_table must have shape [n_table][rope_dim]")
+    n_table, rope_dim = rope_table.shape
+    n_axes = 1
+    if positions is not None:
+        at = _dev(positions, torch.int32, "positions")
+        n_axes = positions.shape[0] if positions.dim() == 3 else 1
+        if positions.shape[-2:] != k_new.shape[:2] or positions.dim() not in (2, 3):
+            raise ValueError(f"positions must have shape [n_axes][{n_seqs}][{n_new}]")
+    if pair_axis is not None:
+        if pair_axis.is_cuda or pair_axis.dtype != torch.uint8 or not pair_axis.is_contiguous():
+            raise TypeError("pair_axis must be a contiguous uint8 tensor on the host")
+        _shape(pair_axis, (rope_dim // 2,), "pair_axis")
+        axis = pair_axis.data_ptr()
+    if new_lens is not None:
+        lens = _dev(new_lens, torch.int32, "new_lens")
+        _shape(new_lens, (n_seqs,), "new_lens")
+    pos, pages = _dev(seq_pos, torch.int32, "seq_pos"), _dev(page_table, torch.int32, "page_table")
+    _shape(seq_pos, (n_seqs,), "seq_pos")
+    _shape(page_table, (n_seqs, page_table.shape[-1]), "page_table")
+    _here(pool, k_new, v_new, q, q_out, rope_table, positions, new_lens, seq_pos, page_table)
+    _check(lib().kv_rope_append(pool.handle, layer, qp, k, v, qs, ks, vs, n_seqs, n_new, n_heads,
+                                pos, lens, table, n_table, rope_dim, ROPE_STYLES[style], at, n_axes,
+                                axis, qo, pages, page_table.shape[1], _stream(stream)),
+           "kv_rope_append")
+
+
+def _prob_rows(t, shape, name):
+    """Address and row stride of fp32 probabilities [batch][rows][vocab], rows evenly spaced."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be {torch.float32}, got {t.dtype}")
+    _shape(t, shape, name)
+    batch, rows, vocab = shape
+    if t.numel() == 0:
+        return t.data_ptr(), vocab
+    s0, s1, s2 = t.stride()
+    if rows <= 1:
+        s1 = s0 if batch > 1 else vocab
+    if (vocab > 1 and s2 != 1) or (batch > 1 and s0 != rows * s1):
+        raise ValueError(f"{name}'s rows must lie evenly apart")
+    return t.data_ptr(), s1
+
+
+def kv_verify_drafts(target_probs, draft_tokens, accept_u, sample_u, tokens, n_accepted,
+                     draft_probs=None, n_drafts=None, seq_lens=None, seq_lens_out=None,
+                     stream=None):
+    """Accept drafted tokens (int32 [batch][n_draft]) by the target's probabilities (fp32
+    [batch][n_draft + 1][vocab]) and draw the token behind them.
+
+    draft_probs: fp32 [batch][n_draft][vocab], None for drafts without probabilities; accept_u fp32
+    [batch][n_draft], sample_u fp32 [batch]; n_drafts int32 [batch], drafts of each sequence.
+    Writes tokens (int32 [batch][n_draft + 1]) and n_accepted (int32 [batch]), and seq_lens less the
+    refused drafts to seq_lens_out (int32 [batch] each).  Vocabularies may be padded: a slice of
+    wider rows will do."""
+    x, u = _dev(draft_tokens, torch.int32, "draft_tokens"), _dev(accept_u, torch.float32, "accept_u")
+    if draft_tokens.dim() != 2 or target_probs.dim() != 3:
+        raise ValueError("draft_tokens must have shape [batch][n_draft], target_probs "
+                         "[batch][n_draft + 1][vocab]")
+    batch, n = draft_tokens.shape
+    vocab = target_probs.shape[2]
+    p, ps = _prob_rows(target_probs, (batch, n + 1, vocab), "target_probs")
+    q, qs = _prob_rows(draft_probs, (batch, n, vocab), "draft_probs") if draft_probs is not None \
+        else (None, 0)
+    _shape(accept_u, (batch, n), "accept_u")
+    s, t = _dev(sample_u, torch.float32, "sample_u"), _dev(tokens, torch.int32, "tokens")
+    acc = _dev(n_accepted, torch.int32, "n_accepted")
+    _shape(sample_u, (batch,), "sample_u")
+    _shape(tokens, (batch, n + 1), "tokens")
+    _shape(n_accepted, (batch,), "n_accepted")
+    optional = []
+    for name, v in (("n_drafts", n_drafts), ("seq_lens", seq_lens), ("seq_lens_out", seq_lens_out)):
+        optional.append(_dev(v, torch.int32, name) if v is not None else None)
+        if v is not None:
+            _shape(v, (batch,), name)
+    at = _device()
+    for v in (target_probs, draft_tokens, accept_u, sample_u, tokens, n_accepted, draft_probs,
+              n_drafts, seq_lens, seq_lens_out):
+        if v is not None and v.get_device() != at:
+            raise ValueError(f"a tensor is on device {v.get_device()}, the current one is {at}")
+    _check(lib().kv_verify_drafts(batch, n, vocab, p, ps, q, qs, x, optional[0], u, s, t, acc,
+                                  optional[1], optional[2], _stream(stream)), "kv_verify_drafts")
 
 
 def attn_decode_n_splits(pool, batch, max_ctx):

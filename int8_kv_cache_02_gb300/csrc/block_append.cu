@@ -24,51 +24,18 @@
 namespace int8kv {
 namespace {
 
-// Codes of eight values x.  A code is decided by the IEEE quotient x / s; y = x * (1 / s)
-// is within 2^-22 of it (two roundings, and the quotient's own).  Only where a rounding
-// boundary of the codes lies that near to one of the eight are the divisions made:
-//   e4m3: where x (1 / s) (1 - 2^-21) and x (1 / s) (1 + 2^-21), which enclose the
-//         quotient, have different codes;
-//   int8: where y is within 1e-4 of a half-integer (|y| < 128), which 127.5, the one
-//         value that needs saturation, is too.
+// Codes of eight fp16 values.
 template <bool F8>
-__device__ __forceinline__ uint2 quantize8(const uint4& x, float s, float inv) {
+__device__ __forceinline__ uint2 quantize_halves8(const uint4& x, float s, float inv) {
   const __half2* h = reinterpret_cast<const __half2*>(&x);
-  float v[8], y[8];
+  float v[8];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float2 f = __half22float2(h[e]);
     v[2 * e] = f.x;
     v[2 * e + 1] = f.y;
   }
-  uint2 w;
-  bool near = false;
-  if constexpr (F8) {
-    const float below = inv * (1.f - 0x1p-21f), above = inv * (1.f + 0x1p-21f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = v[e] * below;
-    w = round_codes8<F8>(y);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = v[e] * above;
-    const uint2 u = round_codes8<F8>(y);
-    near = w.x != u.x || w.y != u.y;
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      y[e] = v[e] * inv;
-      near |= fabsf(y[e] - ((y[e] + kRoundToInt) - kRoundToInt)) > 0.5f - 1.0e-4f;
-    }
-    w = round_codes8<F8>(y);
-  }
-  if (near) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      y[e] = __fdiv_rn(v[e], s);
-      if constexpr (!F8) y[e] = fminf(fmaxf(y[e], -127.f), 127.f);
-    }
-    w = round_codes8<F8>(y);
-  }
-  return w;
+  return quantize8<F8>(v, s, inv, false);
 }
 
 // NT threads per group; GROUPS groups per thread block; CH 16-byte pieces of new
@@ -152,29 +119,9 @@ __global__ void __launch_bounds__(NT* GROUPS) block_append_kernel(
 
   float s;
   if (s_old > 0.f) {
-    s = s_old;
-    float lim = Codes<F8>::kFits * s_old;
-    float shrink = 1.f;
-    for (int k = 0; k < 256 && a > lim; ++k) {   // a <= 65504: at most 48 doublings of any scale
-      lim *= 2.f;
-      s *= 2.f;
-      shrink *= 0.5f;
-    }
-    if (shrink != 1.f) {
-      for (int i = tid; i < r0 * (D / 16); i += NT) {
-        uint4 w = *reinterpret_cast<const uint4*>(codes + i * 16);
-        uint32_t* u = reinterpret_cast<uint32_t*>(&w);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float y[4];
-          code_values<F8>(u[e], y);
-#pragma unroll
-          for (int f = 0; f < 4; ++f) y[f] *= shrink;
-          u[e] = round_codes<F8>(y);      // (|y| <= 64, or e4m3)
-        }
-        *reinterpret_cast<uint4*>(codes + i * 16) = w;
-      }
-    }
+    float shrink;
+    s = grown_scale<F8>(s_old, a, shrink);
+    if (shrink != 1.f) shrink_codes<F8>(codes, r0 * D, shrink, tid, NT);
   } else {
     s = __fdiv_rn(a, Codes<F8>::kMax);
   }
@@ -185,7 +132,7 @@ __global__ void __launch_bounds__(NT* GROUPS) block_append_kernel(
     const int i = tid + c * NT, r = i / PPR;
     if (r < rows)
       *reinterpret_cast<uint2*>(codes + (size_t)(r0 + r) * D + (i % PPR) * 8) =
-          s > 0.f ? quantize8<F8>(x[c], s, inv) : make_uint2(0, 0);
+          s > 0.f ? quantize_halves8<F8>(x[c], s, inv) : make_uint2(0, 0);
   }
 }
 

@@ -1,0 +1,119 @@
+"""Refusals of rotated appends and draft verification that need no GPU."""
+
+import ctypes
+
+import pytest
+import torch
+
+from int8_kv_cache_02_gb300 import binding as b
+
+
+@pytest.fixture(scope="module")
+def L():
+    from int8_kv_cache_02_gb300 import build
+    build.build()
+    return b.lib()
+
+
+P, ODD = 0x10000, 0x10008
+
+
+def test_rope_append_rejects_a_null_pool(L):
+    assert L.kv_rope_append(None, 0, None, None, None, 0, 0, 0, 1, 1, 1, None, None, None, 1, 64, 0,
+                            None, 1, None, None, None, 1, None) == -2
+
+
+class _Fake(ctypes.Structure):
+    """The head of a pool's descriptor, which the refusals below look at before any CUDA call."""
+    _fields_ = [(n, ctypes.c_int) for n in ("n_layers", "n_kv_heads", "head_dim", "group_size",
+                                            "n_groups", "page_size", "n_pages", "variant")] + \
+               [("rest", ctypes.c_ubyte * 1024)]
+
+
+def _rope(L, **kw):
+    a = dict(layer=0, q=P, k=P, v=P, qs=1024, ks=256, vs=256, n_seqs=2, n_new=3, n_heads=8, pos=P,
+             lens=None, table=P, n_table=10, dim=64, style=0, positions=None, n_axes=1, axis=None,
+             out=P, pages=P, max_pages=4)
+    a.update(kw)
+    f = _Fake(1, 2, 128, 128, 1, 64, 4, 0)
+    return L.kv_rope_append(ctypes.byref(f), *a.values(), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(layer=1), -1), (dict(layer=-1), -1), (dict(n_seqs=-1), -1), (dict(n_new=-1), -1),
+    (dict(max_pages=0), -1), (dict(n_table=0), -1), (dict(dim=0), -1), (dict(dim=24), -1),
+    (dict(dim=144), -1), (dict(style=2), -1), (dict(n_axes=0), -1), (dict(n_axes=5), -1),
+    (dict(n_heads=0), -1), (dict(qs=1023), -1), (dict(ks=255), -1), (dict(vs=0), -1),
+    (dict(n_axes=2), -2), (dict(n_axes=2, axis=(ctypes.c_uint8 * 32)(*[2] * 32), positions=P), -1),
+    (dict(n_axes=2, axis=(ctypes.c_uint8 * 32)(*[1] * 32)), -2),
+    (dict(axis=(ctypes.c_uint8 * 32)(1)), -1),
+    (dict(k=None), -2), (dict(v=None), -2), (dict(pos=None), -2), (dict(table=None), -2),
+    (dict(pages=None), -2), (dict(out=None), -2),
+    (dict(q=ODD), -3), (dict(k=ODD), -3), (dict(v=ODD), -3), (dict(out=ODD), -3),
+    (dict(table=ODD), -3), (dict(qs=1028), -3), (dict(ks=260), -3), (dict(vs=260), -3),
+    (dict(n_seqs=0), 0), (dict(n_new=0, k=None, v=None), 0),
+])
+def test_rope_append_refusals(L, kw, status):
+    assert _rope(L, **kw) == status
+
+
+def _verify(L, **kw):
+    a = dict(batch=2, n_draft=3, vocab=100, target=P, ts=100, draft=P, ds=100, x=P, n=None, u=P, s=P,
+             tokens=P, acc=P, lens=None, out=None)
+    a.update(kw)
+    return L.kv_verify_drafts(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(batch=-1), -1), (dict(n_draft=-1), -1), (dict(vocab=0), -1), (dict(ts=99), -1),
+    (dict(ds=99), -1), (dict(vocab=(1 << 30) + 1, ts=1 << 31, ds=1 << 31), -1),
+    (dict(target=None), -2), (dict(x=None), -2), (dict(u=None), -2), (dict(s=None), -2),
+    (dict(tokens=None), -2), (dict(acc=None), -2), (dict(lens=P), -2), (dict(out=P), -2),
+    (dict(batch=1 << 28), -6), (dict(batch=0, target=None), 0),
+])
+def test_verify_refusals(L, kw, status):
+    assert _verify(L, **kw) == status
+
+
+class _Pool:
+    handle = None
+    block, n_kv_heads, head_dim, n_pages, device_index = True, 2, 64, 4, 0
+
+
+def test_the_binding_refuses(L):
+    i, f = torch.zeros(4, dtype=torch.int32), torch.zeros(4)
+    k = torch.zeros((1, 4, 2, 64), dtype=torch.float16)
+    with pytest.raises(ValueError, match="k_new and v_new must have shape"):
+        b.kv_rope_append(_Pool(), 0, k, k[:, :2], i[:1], i.view(1, 4), f)
+    with pytest.raises(ValueError, match="CUDA"):
+        b.kv_rope_append(_Pool(), 0, k, k, i[:1], i.view(1, 4), f)
+    with pytest.raises(ValueError, match="CUDA"):
+        b.kv_verify_drafts(f.view(1, 2, 2), i[:1].view(1, 1), f[:1].view(1, 1), f[:1],
+                           i[:2].view(1, 2), i[:1])
+
+
+def test_token_and_row_strides(monkeypatch):
+    """What counts as evenly apart (addresses are not looked at here)."""
+    real = torch.Tensor.is_cuda
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True))
+    try:
+        wide = torch.zeros((3, 5, 12, 64), dtype=torch.float16)
+        assert b._token_rows(wide[:, :, 2:4], 2, 64, "k")[1] == 12 * 64
+        assert b._token_rows(wide[:, :1, :2], 2, 64, "k")[1] == 5 * 12 * 64
+        assert b._token_rows(wide[:1, 1:4, :2], 2, 64, "k")[1] == 12 * 64
+        assert b._token_rows(wide[:1, :1, :2], 2, 64, "k")[1] == 128
+        with pytest.raises(ValueError, match="evenly"):
+            b._token_rows(wide[:, :3, :2], 2, 64, "k")
+        with pytest.raises(ValueError, match="evenly"):
+            b._token_rows(wide.transpose(0, 1)[:, :, :2], 2, 64, "k")
+        with pytest.raises(ValueError, match="evenly"):
+            b._token_rows(wide[:, :, ::2][:, :, :2], 2, 64, "k")
+        with pytest.raises(ValueError, match="shape"):
+            b._token_rows(wide, 2, 64, "k")
+        p = torch.zeros((2, 4, 40))
+        assert b._prob_rows(p[..., :33], (2, 4, 33), "p")[1] == 40
+        assert b._prob_rows(p[:, :1, :33], (2, 1, 33), "p")[1] == 160
+        with pytest.raises(ValueError, match="evenly"):
+            b._prob_rows(p[:, :3], (2, 3, 40), "p")
+    finally:
+        monkeypatch.setattr(torch.Tensor, "is_cuda", real)
