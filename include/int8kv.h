@@ -376,6 +376,35 @@ int attn_decode_multi_int8(const int8kv_pool* pool, int layer, const uint16_t* q
                            int n_splits, float* out, void* workspace, size_t workspace_bytes,
                            void* stream);
 
+/* Decode of one query or a window of queries per sequence with shaped scores, over a block-scaled
+ * pool.  Query i of sequence b sits at position P = seq_lens[b] - q_len + i, as in
+ * attn_decode_multi_int8.  Its score with position p, s = softmax_scale * (q . k), becomes
+ *     s <- softcap * tanh(s / softcap)                    where softcap is not 0
+ *     s <- s + slopes[h] * (p - P)                        where slopes are given
+ * and it attends the positions p below seq_lens[b] that are in the prefix, p < prefix_lens[b], or
+ * neither behind it nor out of its window: p <= P and, with window > 0, p > P - window.  (A slope
+ * of 2^(-8 (h + 1) / n_heads) is the usual bias by distance; positions of the prefix that are ahead
+ * of the query get a bias above 0.  A prefix of a few positions keeps a long stream's first ones in
+ * sight of its window.)
+ *   q, out        device fp16, fp32 [batch][q_len][n_heads][head_dim]; a query at a negative position
+ *                 gets a zero row
+ *   q_len         1 .. 64
+ *   softcap       0, or 2^-64 .. 2^64
+ *   slopes        device fp32 [n_heads], or NULL
+ *   prefix_lens   device int32 [batch], or NULL; below 0 counts as 0, beyond seq_lens[b] as all of it
+ * The other arguments are attn_decode_multi_int8's, and so are the workspace and n_splits (0: with
+ * prefix_lens the context counts as what a page-table row holds, else as the window).  Pages that
+ * hold neither a position of the prefix nor one of the window are not looked at: their entries may
+ * be negative.
+ * Errors: NULL_PTR, INVALID_ARG, UNSUPPORTED (a pool that is not block-scaled), WORKSPACE, ALIGNMENT,
+ * CUDA. */
+int attn_decode_scored_int8(const int8kv_pool* pool, int layer, const uint16_t* q, int batch,
+                            int q_len, int n_heads, const int32_t* seq_lens,
+                            const int32_t* page_table, int max_pages_per_seq, int window,
+                            float softmax_scale, float softcap, const float* slopes,
+                            const int32_t* prefix_lens, int n_splits, float* out, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
 /* Blocks of the prefill-chunk kernel per (128-row query tile, kv head).  The
  * kernel runs one block per SM at a time, so tiles x kv heads x splits blocks
  * take ceil(blocks / SMs) waves of ceil(pages / splits) pages; the count with
@@ -413,6 +442,19 @@ int attn_prefill_chunk_int8(const int8kv_pool* pool, int layer, const uint16_t* 
                             int n_heads, int start_pos, const int32_t* page_table,
                             int max_pages_per_seq, float softmax_scale, int n_splits,
                             float* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* attn_prefill_chunk_int8 with scores shaped as by attn_decode_scored_int8, over a block-scaled pool:
+ * query i sits at P = start_pos + i; prefix_len (the host's, 0: none) positions from 0 on are seen by
+ * every query, those of the chunk itself among them (an image's tokens that see each other).  With a
+ * window, n_splits' count is that of attn_prefill_n_splits for a start_pos of at most
+ * window + prefix_len.  Pages that no query sees may be missing from the table.
+ * Errors: those of attn_prefill_chunk_int8. */
+int attn_prefill_chunk_scored_int8(const int8kv_pool* pool, int layer, const uint16_t* q, int n_new,
+                                   int n_heads, int start_pos, const int32_t* page_table,
+                                   int max_pages_per_seq, int window, float softmax_scale,
+                                   float softcap, const float* slopes, int prefix_len, int n_splits,
+                                   float* out, void* workspace, size_t workspace_bytes,
+                                   void* stream);
 
 /* attn_decode_int8 for callers that cannot allocate device memory where they
  * decode (inside a graph-capture region of a framework that forbids

@@ -9,10 +9,10 @@ raises if it has not been built (``int8_kv_cache_02_gb300.build.build()``).
 from .binding import (F8_BLOCK, K8V8, K8V8_BLOCK, K8V16, K16V8, VARIANTS,  # noqa: F401
                       Int8KVError, KVPool,
                       attn_decode_append_int8, attn_decode_int8, attn_decode_int8_noalloc,
-                      attn_decode_multi_int8,
+                      attn_decode_multi_int8, attn_decode_scored_int8,
                       attn_decode_n_splits,
                       attn_decode_workspace_bytes, attn_prefill_chunk_int8, attn_prefill_n_splits,
-                      attn_prefill_workspace_bytes,
+                      attn_prefill_chunk_scored_int8, attn_prefill_workspace_bytes,
                       int8kv_pool_region_bytes, int8kv_status_string, kv_pages_compact,
                       kv_pages_copy, kv_pages_fork, kv_pages_resize, kv_pages_workspace_bytes,
                       kv_pool_create,

@@ -41,6 +41,12 @@ _SIGS = {
                                 _vp, _vp, _c_int, _vp]),
     "kv_verify_drafts": (_c_int, [_c_int, _c_int, _c_int, _vp, _c_ll, _vp, _c_ll, _vp, _vp, _vp,
                                   _vp, _vp, _vp, _vp, _vp, _vp]),
+    "attn_decode_scored_int8": (_c_int, [_vp, _c_int, _vp, _c_int, _c_int, _c_int, _vp, _vp, _c_int,
+                                         _c_int, _c_float, _c_float, _vp, _vp, _c_int, _vp, _vp,
+                                         _c_size, _vp]),
+    "attn_prefill_chunk_scored_int8": (_c_int, [_vp, _c_int, _vp, _c_int, _c_int, _c_int, _vp, _c_int,
+                                                _c_int, _c_float, _c_float, _vp, _c_int, _c_int, _vp,
+                                                _vp, _c_size, _vp]),
     "attn_decode_n_splits": (_c_int, [_vp, _c_int, _c_int]),
     "attn_decode_workspace_bytes": (_c_int, [_c_int] * 5 + [ctypes.POINTER(_c_size)]),
     "attn_decode_int8": (_c_int, [_vp, _c_int, _vp, _c_int, _c_int, _vp, _vp, _c_int, _c_int,
@@ -401,6 +407,47 @@ def attn_decode_multi_int8(pool, layer, q, seq_lens, page_table, out, workspace=
                                         _stream(stream)), "attn_decode_multi_int8")
 
 
+def _scored_call(pool, q, slopes, n_heads):
+    """Address of a call's slopes (fp32 [n_heads], or None)."""
+    if not pool.block:
+        raise ValueError("shaped scores want a block-scaled pool")
+    if slopes is None:
+        return None
+    s = _dev(slopes, torch.float32, "slopes")
+    _shape(slopes, (n_heads,), "slopes")
+    _here(pool, slopes)
+    return s
+
+
+def attn_decode_scored_int8(pool, layer, q, seq_lens, page_table, out, workspace=None, window=0,
+                            softcap=0.0, slopes=None, prefix_lens=None, softmax_scale=0.0,
+                            n_splits=0, stream=None):
+    """Decode with scores capped at softcap by a tanh, biased by slopes[h] * (key - query) (fp32 [H]),
+    and a prefix that every query sees (prefix_lens int32 [B]) beside its window.
+
+    q: fp16 [B][H][D], or a window of queries [B][q_len][H][D], the last of them at seq_lens[b] - 1;
+    out: fp32, the same shape; block-scaled pools."""
+    B, H = q.shape[0], q.shape[-2]
+    Q = q.shape[1] if q.dim() == 4 else 1
+    if q.dim() not in (3, 4):
+        raise ValueError("q must have shape [B][H][D] or [B][q_len][H][D]")
+    s = _scored_call(pool, q, slopes, H)
+    _block_call(pool, q, seq_lens, page_table, out, workspace)
+    p = None
+    if prefix_lens is not None:
+        p = _dev(prefix_lens, torch.int32, "prefix_lens")
+        _shape(prefix_lens, (B,), "prefix_lens")
+        _here(pool, prefix_lens)
+    ws = _dev(workspace, torch.uint8, "workspace") if workspace is not None else None
+    nbytes = workspace.numel() if workspace is not None else 0
+    _check(lib().attn_decode_scored_int8(pool.handle, layer, _dev(q, torch.float16, "q"), B, Q, H,
+                                         _dev(seq_lens, torch.int32, "seq_lens"),
+                                         _dev(page_table, torch.int32, "page_table"),
+                                         page_table.shape[1], window, softmax_scale, softcap, s, p,
+                                         n_splits, _dev(out, torch.float32, "out"), ws, nbytes,
+                                         _stream(stream)), "attn_decode_scored_int8")
+
+
 def attn_prefill_n_splits(pool, n_new, n_heads, start_pos):
     n = lib().attn_prefill_n_splits(pool.handle, n_new, n_heads, start_pos)
     if n < 0:
@@ -432,6 +479,29 @@ def attn_prefill_chunk_int8(pool, layer, q, start_pos, page_table, out, workspac
                                          page_table.shape[-1], float(softmax_scale), n_splits,
                                          _dev(out, torch.float32, "out"), ws, nbytes,
                                          _stream(stream)), "attn_prefill_chunk_int8")
+
+
+def attn_prefill_chunk_scored_int8(pool, layer, q, start_pos, page_table, out, workspace=None,
+                                   window=0, softcap=0.0, slopes=None, prefix_len=0,
+                                   softmax_scale=0.0, n_splits=0, stream=None):
+    """attn_prefill_chunk_int8 with scores shaped as by attn_decode_scored_int8: q fp16 [n_new][H][D],
+    query i at start_pos + i; positions below prefix_len are seen by all; block-scaled pools."""
+    n_new, H = q.shape[0], q.shape[1]
+    s = _scored_call(pool, q, slopes, H)
+    _shape(q, (n_new, H, pool.head_dim), "q")
+    _shape(out, q.shape, "out")
+    if page_table.numel() != page_table.shape[-1]:
+        raise ValueError("page_table must be one sequence's row")
+    _here(pool, q, page_table, out, workspace)
+    ws = _dev(workspace, torch.uint8, "workspace") if workspace is not None else None
+    nbytes = workspace.numel() if workspace is not None else 0
+    _check(lib().attn_prefill_chunk_scored_int8(pool.handle, layer, _dev(q, torch.float16, "q"), n_new,
+                                                H, start_pos,
+                                                _dev(page_table, torch.int32, "page_table"),
+                                                page_table.shape[-1], window, softmax_scale, softcap,
+                                                s, prefix_len, n_splits,
+                                                _dev(out, torch.float32, "out"), ws, nbytes,
+                                                _stream(stream)), "attn_prefill_chunk_scored_int8")
 
 
 def kv_pool_set_decode_kernel(pool, kind):

@@ -293,15 +293,34 @@ static int launch_status(cudaError_t e) {
   return e == cudaSuccess ? INT8KV_OK : INT8KV_ERR_CUDA;
 }
 
+// What attn_decode_scored_int8 and attn_prefill_chunk_scored_int8 add to a call.
+struct ScoredCall {
+  float softcap;
+  const float* slopes;
+  const int32_t* prefix_lens;      // device, of a decode call; or null: `prefix` for every sequence
+  int prefix;
+};
+
+// A cap is 0 or one whose reciprocal, in base-2 exponents, has an fp32 value.
+static bool valid_cap(float c) { return c == 0.f || (c >= 0x1p-64f && c <= 0x1p64f); }
+
+static Shaping shaping(const ScoredCall& c) {
+  Shaping s;
+  s.cap = c.softcap * 1.4426950408889634f;
+  s.over_cap = c.softcap != 0.f ? 1.f / s.cap : 0.f;
+  s.slopes = c.slopes;
+  return s;
+}
+
 // The decode kernel of a block-scaled pool over batch x q_len queries (seq_lens null: the
-// one sequence has `length` positions).
+// one sequence has `length` positions; scored null: plain scores).
 static int block_attention(const int8kv_pool* pool, int layer, const uint16_t* q, int batch,
                            int q_len, int n_heads, const int32_t* seq_lens, int length,
                            const int32_t* page_table, int max_pages, int window, float scale,
                            int n_splits, float* out, const DecodeWorkspace& ws, bool appended,
-                           cudaStream_t stream) {
+                           const ScoredCall* scored, cudaStream_t stream) {
   const int G = n_heads / pool->n_kv_heads;
-  BlockDecodeArgs d;
+  BlockScoredArgs d;
   d.pool = block_view(pool, layer);
   d.q = q;
   d.seq_lens = seq_lens;
@@ -325,13 +344,21 @@ static int block_attention(const int8kv_pool* pool, int layer, const uint16_t* q
   const long long most = ((long long)max_pages * pool->page_size + 15) / 16 + 64;
   if (units * most > INT32_MAX / 2) d.shares = 0;
   const long long cap = (long long)max_pages * pool->page_size;
-  d.cluster = block_cluster(pool, units, d.width, window > 0 && window < cap ? window : cap, n_splits);
+  // (a window's prefixes on the device count as the whole row: shares go by the lengths themselves)
+  long long seen = window > 0 ? window : cap;
+  if (scored) seen = scored->prefix_lens ? cap : seen + scored->prefix + q_len - 1;
+  d.cluster = block_cluster(pool, units, d.width, seen < cap ? seen : cap, n_splits);
   if (d.cluster > 1) d.shares = 0;
   d.part_units =
       d.shares ? (int2*)(ws.part_o + (size_t)(units + d.shares - 1) * d.width * pool->head_dim) : nullptr;
   d.scale_log2 = scale * 1.4426950408889634f;
   d.appended = appended;
-  return launch_status(launch_block_decode(d, pool->head_dim, is_f8(pool), stream));
+  if (!scored) return launch_status(launch_block_decode(d, pool->head_dim, is_f8(pool), stream));
+  d.window = window < kBlockMostPositions ? window : kBlockMostPositions;
+  d.shape = shaping(*scored);
+  d.prefix_lens = scored->prefix_lens;
+  d.prefix = scored->prefix;
+  return launch_status(launch_block_decode_scored(d, pool->head_dim, is_f8(pool), stream));
 }
 
 }  // namespace int8kv
@@ -521,7 +548,8 @@ static int decode_entry(const int8kv_pool* pool, int layer, const uint16_t* q,
                         const uint16_t* k_new, const uint16_t* v_new, int batch, int q_len,
                         int n_heads, const int32_t* seq_lens, const int32_t* page_table,
                         int max_pages_per_seq, int window, float softmax_scale, int n_splits,
-                        float* out, void* workspace, size_t workspace_bytes, void* stream);
+                        float* out, void* workspace, size_t workspace_bytes, void* stream,
+                        const ScoredCall* scored = nullptr);
 
 int attn_decode_int8(const int8kv_pool* pool, int layer, const uint16_t* q, int batch,
                      int n_heads, const int32_t* seq_lens, const int32_t* page_table,
@@ -542,6 +570,19 @@ int attn_decode_multi_int8(const int8kv_pool* pool, int layer, const uint16_t* q
                       workspace_bytes, stream);
 }
 
+int attn_decode_scored_int8(const int8kv_pool* pool, int layer, const uint16_t* q, int batch,
+                            int q_len, int n_heads, const int32_t* seq_lens,
+                            const int32_t* page_table, int max_pages_per_seq, int window,
+                            float softmax_scale, float softcap, const float* slopes,
+                            const int32_t* prefix_lens, int n_splits, float* out, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  if (!valid_cap(softcap)) return INT8KV_ERR_INVALID_ARG;
+  const ScoredCall c{softcap, slopes, prefix_lens, 0};
+  return decode_entry(pool, layer, q, nullptr, nullptr, batch, q_len, n_heads, seq_lens,
+                      page_table, max_pages_per_seq, window, softmax_scale, n_splits, out,
+                      workspace, workspace_bytes, stream, &c);
+}
+
 int attn_decode_append_int8(const int8kv_pool* pool, int layer, const uint16_t* q,
                             const uint16_t* k_new, const uint16_t* v_new, int batch, int n_heads,
                             const int32_t* seq_lens, const int32_t* page_table,
@@ -558,7 +599,8 @@ static int decode_entry(const int8kv_pool* pool, int layer, const uint16_t* q,
                         const uint16_t* k_new, const uint16_t* v_new, int batch, int q_len,
                         int n_heads, const int32_t* seq_lens, const int32_t* page_table,
                         int max_pages_per_seq, int window, float softmax_scale, int n_splits,
-                        float* out, void* workspace, size_t workspace_bytes, void* stream) {
+                        float* out, void* workspace, size_t workspace_bytes, void* stream,
+                        const ScoredCall* scored) {
   if (!pool) return INT8KV_ERR_NULL_PTR;
   if (layer < 0 || layer >= pool->n_layers || batch < 0 || n_heads <= 0 ||
       max_pages_per_seq <= 0 || window < 0 || n_splits < 0 || n_splits > kMaxSplits ||
@@ -566,7 +608,7 @@ static int decode_entry(const int8kv_pool* pool, int layer, const uint16_t* q,
     return INT8KV_ERR_INVALID_ARG;
   if (n_heads % pool->n_kv_heads != 0) return INT8KV_ERR_INVALID_ARG;
   const int G = n_heads / pool->n_kv_heads;
-  if (G > 8) return INT8KV_ERR_UNSUPPORTED;
+  if (G > 8 || (scored && !is_block(pool))) return INT8KV_ERR_UNSUPPORTED;
   // a query window runs on the warp-level tensor-core kernel only
   if (q_len > 1 && !is_block(pool) && decode_kernel_for(pool, G) != INT8KV_DECODE_WARP_MMA)
     return INT8KV_ERR_UNSUPPORTED;
@@ -575,7 +617,8 @@ static int decode_entry(const int8kv_pool* pool, int layer, const uint16_t* q,
   if (!aligned16(q) || !aligned16(out)) return INT8KV_ERR_ALIGNMENT;
   const int n_cg = (q_len * G + 7) / 8;   // blocks per (sequence, kv head) sharing the columns
   if (n_splits == 0)
-    n_splits = decode_auto_splits(pool, batch, q_len, G, max_pages_per_seq, window, 0);
+    n_splits = decode_auto_splits(pool, batch, q_len, G, max_pages_per_seq,
+                                  scored && scored->prefix_lens ? 0 : window, 0);
   DecodeArgs a;
   a.q_len = q_len;
   a.n_cg = n_cg;
@@ -598,7 +641,8 @@ static int decode_entry(const int8kv_pool* pool, int layer, const uint16_t* q,
       if (e != cudaSuccess) return launch_status(e);
     }
     return block_attention(pool, layer, q, batch, q_len, n_heads, seq_lens, 0, page_table,
-                           max_pages_per_seq, window, scale, n_splits, out, a.ws, k_new != nullptr, s);
+                           max_pages_per_seq, window, scale, n_splits, out, a.ws, k_new != nullptr,
+                           scored, s);
   }
   a.pool = layer_view(pool, layer);
   a.q = q;
@@ -657,16 +701,18 @@ int attn_prefill_workspace_bytes(int n_new, int n_heads, int n_kv_heads, int hea
   return attn_decode_workspace_bytes(n_new, n_heads, n_kv_heads, head_dim, n_splits, out_bytes);
 }
 
-int attn_prefill_chunk_int8(const int8kv_pool* pool, int layer, const uint16_t* q, int n_new,
-                            int n_heads, int start_pos, const int32_t* page_table,
-                            int max_pages_per_seq, float softmax_scale, int n_splits, float* out,
-                            void* workspace, size_t workspace_bytes, void* stream) {
+static int prefill_entry(const int8kv_pool* pool, int layer, const uint16_t* q, int n_new,
+                         int n_heads, int start_pos, const int32_t* page_table,
+                         int max_pages_per_seq, int window, float softmax_scale, int n_splits,
+                         float* out, void* workspace, size_t workspace_bytes, void* stream,
+                         const ScoredCall* scored) {
   if (!pool) return INT8KV_ERR_NULL_PTR;
   if (layer < 0 || layer >= pool->n_layers || n_new < 0 || n_heads <= 0 || start_pos < 0 ||
       max_pages_per_seq <= 0 || n_splits < 0 || n_splits > kMaxSplits ||
       !std::isfinite(softmax_scale) || n_heads % pool->n_kv_heads != 0)
     return INT8KV_ERR_INVALID_ARG;
   const int G = n_heads / pool->n_kv_heads;
+  if (scored && !is_block(pool)) return INT8KV_ERR_UNSUPPORTED;
   if (is_block(pool) ? G > 8 || (long long)n_new * G > kBlockMostPositions
                      : !prefill_supported(pool, G))
     return INT8KV_ERR_UNSUPPORTED;
@@ -676,7 +722,8 @@ int attn_prefill_chunk_int8(const int8kv_pool* pool, int layer, const uint16_t* 
   if (!q || !page_table || !out) return INT8KV_ERR_NULL_PTR;
   if (!aligned16(q) || !aligned16(out)) return INT8KV_ERR_ALIGNMENT;
   if (n_splits == 0) {
-    n_splits = attn_prefill_n_splits(pool, n_new, n_heads, start_pos);
+    const long long seen = window > 0 ? (long long)window + scored->prefix : start_pos;
+    n_splits = attn_prefill_n_splits(pool, n_new, n_heads, (int)(seen < start_pos ? seen : start_pos));
     if (n_splits < 0) return n_splits;
   }
   PrefillArgs a;
@@ -692,10 +739,10 @@ int attn_prefill_chunk_int8(const int8kv_pool* pool, int layer, const uint16_t* 
       return INT8KV_ERR_UNSUPPORTED;
     if (!block_tiled(pool, n_new, G))
       return block_attention(pool, layer, q, 1, n_new, n_heads, nullptr, start_pos + n_new,
-                             page_table, max_pages_per_seq, 0,
+                             page_table, max_pages_per_seq, window,
                              softmax_scale != 0.f ? softmax_scale
                                                   : 1.0f / std::sqrt((float)pool->head_dim),
-                             n_splits, out, a.ws, false, (cudaStream_t)stream);
+                             n_splits, out, a.ws, false, scored, (cudaStream_t)stream);
   }
   a.pool = layer_view(pool, layer);
   a.q = q;
@@ -710,12 +757,38 @@ int attn_prefill_chunk_int8(const int8kv_pool* pool, int layer, const uint16_t* 
   const float scale =
       softmax_scale != 0.f ? softmax_scale : 1.0f / std::sqrt((float)pool->head_dim);
   a.scale_log2 = scale * 1.4426950408889634f;
-  if (is_block(pool))
+  if (is_block(pool)) {
+    PrefillShape shape;
+    if (scored)
+      shape = PrefillShape{shaping(*scored), window < kBlockMostPositions ? window : kBlockMostPositions,
+                           scored->prefix};
     return launch_status(launch_block_prefill(block_view(pool, layer), a, pool->head_dim, is_f8(pool),
-                                              pool->expire_polls, (cudaStream_t)stream));
+                                              pool->expire_polls, scored ? &shape : nullptr,
+                                              (cudaStream_t)stream));
+  }
   const cudaError_t e = launch_prefill(pool, layer, a, (cudaStream_t)stream);
   if (e == cudaErrorNotSupported) return INT8KV_ERR_UNSUPPORTED;
   return e == cudaSuccess ? INT8KV_OK : INT8KV_ERR_CUDA;
+}
+
+int attn_prefill_chunk_int8(const int8kv_pool* pool, int layer, const uint16_t* q, int n_new,
+                            int n_heads, int start_pos, const int32_t* page_table,
+                            int max_pages_per_seq, float softmax_scale, int n_splits, float* out,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  return prefill_entry(pool, layer, q, n_new, n_heads, start_pos, page_table, max_pages_per_seq, 0,
+                       softmax_scale, n_splits, out, workspace, workspace_bytes, stream, nullptr);
+}
+
+int attn_prefill_chunk_scored_int8(const int8kv_pool* pool, int layer, const uint16_t* q, int n_new,
+                                   int n_heads, int start_pos, const int32_t* page_table,
+                                   int max_pages_per_seq, int window, float softmax_scale,
+                                   float softcap, const float* slopes, int prefix_len, int n_splits,
+                                   float* out, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+  if (!valid_cap(softcap) || window < 0 || prefix_len < 0) return INT8KV_ERR_INVALID_ARG;
+  const ScoredCall c{softcap, slopes, nullptr, prefix_len};
+  return prefill_entry(pool, layer, q, n_new, n_heads, start_pos, page_table, max_pages_per_seq,
+                       window, softmax_scale, n_splits, out, workspace, workspace_bytes, stream, &c);
 }
 
 int kv_pool_test_expire_waits(int8kv_pool* pool, uint32_t max_polls) {

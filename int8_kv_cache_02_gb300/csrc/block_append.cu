@@ -19,7 +19,7 @@
 // and D out per row and store.
 #include <cmath>
 
-#include "block_common.cuh"
+#include "block_quant.cuh"
 
 namespace int8kv {
 namespace {

@@ -90,6 +90,8 @@ struct PrefillBlockArgs {
   float scale_log2;
   uint64_t patience;          // ns after which a wait has run out
   int expire;                 // 1: diagnostic, V's barriers wait for a warp that never comes
+  Shaping shape;              // shaped scores (the kernels' SHAPED): cap and slopes,
+  int window, prefix;         // and what a query sees besides: its last positions, and the first
 };
 
 struct Shared {
@@ -237,6 +239,19 @@ struct Sums {
   }
 };
 
+// Sixteen scores in units of 1 / f, capped and biased; ahead: how far the first one's position is
+// ahead of the query's.
+__device__ __forceinline__ void shape_piece(uint32_t (&v)[16], float f, const Shaping& shape,
+                                            float slope, int ahead) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    float z = __uint_as_float(v[k]) * f;
+    if (shape.cap != 0.f) z = capped(z, shape.cap, shape.over_cap);
+    if (shape.slopes) z = fmaf(slope, (float)(ahead + k), z);
+    v[k] = __float_as_uint(z);
+  }
+}
+
 // Sixteen codes as fp16 in the order codes_to_h2 gives (int8: dims 0 2 1 3 of every four).
 template <bool F8>
 __device__ __forceinline__ void halves_of(const uint4 w, uint4& lo, uint4& hi) {
@@ -246,7 +261,7 @@ __device__ __forceinline__ void halves_of(const uint4 w, uint4& lo, uint4& hi) {
                   codes_behind_to_h2<F8>(w.w));
 }
 
-template <int D, bool F8>
+template <int D, bool F8, bool SHAPED>
 __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const PrefillBlockArgs a) {
   using L = Layout<D>;
   constexpr int CH = L::CH, CPR = D / 16;
@@ -260,8 +275,20 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
   const int split = blockIdx.x % a.splits, unit = blockIdx.x / a.splits;
   const int kvh = unit % p.Hkv, cg = a.n_cg - 1 - unit / p.Hkv;
   const int rows = a.n_new * a.G, row0 = cg * kRows;      // columns (query, head of the group)
-  const int hi = a.start + (min(row0 + kRows, rows) - 1) / a.G + 1;      // positions [0, hi)
-  const int tiles = (hi + kKeys - 1) / kKeys;
+  int hi = a.start + (min(row0 + kRows, rows) - 1) / a.G + 1;      // positions [0, hi)
+  // Shaped scores: of them [0, pre) and [lo, hi); from tile gap_at on, `gap` tiles are left out.
+  int pre = 0, lo = 0, gap_at = 0, gap = 0;
+  if constexpr (SHAPED) {
+    pre = min(a.prefix, a.start + a.n_new);
+    hi = max(hi, pre);
+    lo = a.window > 0 ? max(0, a.start + row0 / a.G + 1 - a.window) : 0;      // (of the first row)
+    gap_at = (pre + kKeys - 1) / kKeys;
+    gap = max(0, lo / kKeys - gap_at);
+  }
+  const auto position = [&](int tile) {
+    return (SHAPED && tile >= gap_at ? tile + gap : tile) * kKeys;
+  };
+  const int tiles = (hi + kKeys - 1) / kKeys - gap;
   const int t0 = (int)((long long)tiles * split / a.splits);
   const int n = (int)((long long)tiles * (split + 1) / a.splits) - t0;
 
@@ -292,6 +319,11 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const int last = gc < rows ? a.start + gc / a.G : -1;      // the row's last position
     const int least = a.start + row0 / a.G;                    // of the block's first row
+    [[maybe_unused]] const int most_last = a.start + (min(row0 + kRows, rows) - 1) / a.G;
+    float slope = 0.f;
+    if constexpr (SHAPED)
+      if (a.shape.slopes && gc < rows)
+        slope = __ldg(a.shape.slopes + kvh * a.G + gc % a.G) * 1.4426950408889634f;
     // the queries, while the first codes come
     constexpr int PIECES = kRows * (D / 8) / kSoftmax, BATCH = PIECES < 8 ? PIECES : 8;
     for (int x0 = 0; x0 < PIECES; x0 += BATCH) {
@@ -351,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
       }
       const int behind = min(n, from + kChain);
       for (int i = from; i < behind; ++i) {
-        const int pos = (t0 + i) * kKeys + half * 32, tab = i & 3;
+        const int pos = position(t0 + i) + half * 32, tab = i & 3;
         ok = ok && wait(&s.t_full[tab], (i >> 2) & 1, &s.failed, a.patience);
         ok = ok && wait(&s.s_done[i & 1], (i >> 1) & 1, &s.failed, a.patience);
         ok = __all_sync(0xffffffffu, ok);
@@ -371,10 +403,24 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
             none[j] = s.none[tab][2 * half + j];
           }
           tc::wait_ld();
-          const bool masked = pos + 31 > least || none[0] || none[1];
+          bool masked = pos + 31 > least || none[0] || none[1];
+          if constexpr (SHAPED) {
+            masked |= a.window > 0 && pos <= most_last - a.window;
+            masked &= pos + 32 > pre || none[0] || none[1];
+          }
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            if (masked) {
+            if constexpr (SHAPED) {      // (f is in the score then)
+              shape_piece(v[j], f[j], a.shape, slope, pos + 16 * j - last);
+              f[j] = 1.f;
+              if (masked) {
+                const int to = last - pos - 16 * j, from = a.window > 0 ? to - a.window : -1;
+                const int seen = last < 0 ? 0 : pre - pos - 16 * j;
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                  if (none[j] || ((k > to || k <= from) && k >= seen)) v[j][k] = 0xff800000u;
+              }
+            } else if (masked) {
               const int to = none[j] ? -1 : last - pos - 16 * j;
 #pragma unroll
               for (int k = 0; k < 16; ++k)
@@ -519,17 +565,23 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
     int table_page = 0, none = 0;
     float scale = 0.f;
     bool bad = false;
-    auto entry = [&](int pos) { return pos < hi ? __ldg(a.page_table + (pos >> p.ps_log2)) : -1; };
+    // A position that some row sees, or one of its 16 does: pages that none sees need not be there.
+    auto needed = [&](int pos) {
+      if constexpr (SHAPED) return pos < hi && ((pos & ~15) < pre || (pos | 15) >= lo);
+      return pos < hi;
+    };
+    auto entry = [&](int pos) { return needed(pos) ? __ldg(a.page_table + (pos >> p.ps_log2)) : -1; };
     auto find = [&](int tile) {
-      const int pos = (t0 + tile) * kKeys + row;
-      page[0] = entry(one_page ? pos - row : pos);
+      const int pos = position(t0 + tile) + row;
+      // (a tile in one page: a position of its end that is there, or its first)
+      page[0] = !one_page ? entry(pos) : pos - row < hi ? __ldg(a.page_table + ((pos - row) >> p.ps_log2)) : -1;
       if (!one_page)
 #pragma unroll
         for (int x = 1; x < CH; ++x) page[x] = entry(pos + STEP * x);
-      if (tables) table_page = entry((t0 + tile) * kKeys + (lane & 3) * 16);
+      if (tables) table_page = entry(position(t0 + tile) + (lane & 3) * 16);
     };
     auto locate = [&](int tile) {      // (the page ids have come by then)
-      const int pos = (t0 + tile) * kKeys + row;
+      const int pos = position(t0 + tile) + row;
       have = 0;
       if (one_page) {
         const bool there = (unsigned)page[0] < (unsigned)p.n_pages;
@@ -549,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
         for (int x = 0; x < CH; ++x) {
           const int at_pos = pos + STEP * x;
           const bool there = (unsigned)page[x] < (unsigned)p.n_pages;
-          bad |= !there && at_pos < hi;
+          bad |= !there && needed(at_pos);
           from[x] = base + (size_t)page[x] * page_bytes + (size_t)(at_pos & in_page) * D;
           have |= there << x;
         }
@@ -569,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
     };
     auto load_scale = [&](int tile) {
       if (!tables) return;
-      const int pos = (t0 + tile) * kKeys + (lane & 3) * 16;
+      const int pos = position(t0 + tile) + (lane & 3) * 16;
       none = (unsigned)table_page >= (unsigned)p.n_pages;
       scale = 0.f;
       if (!none)
@@ -758,9 +810,9 @@ cudaError_t launch_join(const PrefillBlockArgs& a, cudaStream_t stream) {
                             (const float2*)a.part_ml, a.out, rows, a.splits);
 }
 
-template <int D, bool F8>
+template <int D, bool F8, bool SHAPED>
 cudaError_t launch_typed(const PrefillBlockArgs& a, cudaStream_t stream) {
-  auto kernel = block_prefill_kernel<D, F8>;
+  auto kernel = block_prefill_kernel<D, F8, SHAPED>;
   static bool configured[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -778,14 +830,16 @@ cudaError_t launch_typed(const PrefillBlockArgs& a, cudaStream_t stream) {
 }
 
 template <int D>
-cudaError_t launch_codes(const PrefillBlockArgs& a, bool f8, cudaStream_t stream) {
-  return f8 ? launch_typed<D, true>(a, stream) : launch_typed<D, false>(a, stream);
+cudaError_t launch_codes(const PrefillBlockArgs& a, bool f8, bool shaped, cudaStream_t stream) {
+  if (shaped)
+    return f8 ? launch_typed<D, true, true>(a, stream) : launch_typed<D, false, true>(a, stream);
+  return f8 ? launch_typed<D, true, false>(a, stream) : launch_typed<D, false, false>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_block_prefill(const BlockView& pool, const PrefillArgs& a, int head_dim, bool f8,
-                                 uint32_t expire_us, cudaStream_t stream) {
+                                 uint32_t expire_us, const PrefillShape* shape, cudaStream_t stream) {
   PrefillBlockArgs b;
   b.pool = pool;
   b.q = a.q;
@@ -802,10 +856,13 @@ cudaError_t launch_block_prefill(const BlockView& pool, const PrefillArgs& a, in
   b.scale_log2 = a.scale_log2;
   b.patience = expire_us ? expire_us * 1000ull : kPatience;
   b.expire = expire_us != 0;
+  b.shape = shape ? shape->scores : Shaping{};
+  b.window = shape ? shape->window : 0;
+  b.prefix = shape ? shape->prefix : 0;
   switch (head_dim) {
-    case 64: return launch_codes<64>(b, f8, stream);
-    case 128: return launch_codes<128>(b, f8, stream);
-    default: return launch_codes<256>(b, f8, stream);
+    case 64: return launch_codes<64>(b, f8, shape != nullptr, stream);
+    case 128: return launch_codes<128>(b, f8, shape != nullptr, stream);
+    default: return launch_codes<256>(b, f8, shape != nullptr, stream);
   }
 }
 

@@ -1,4 +1,5 @@
-// Block-scaled decode: the dispatch over head_dim, and the combine of partials.
+// Block-scaled decode: the dispatch over head_dim, and the combine of partials (shaped scores
+// included: an empty unit is one of length 0 there, too).
 #include "decode_block.cuh"
 
 namespace int8kv {
@@ -46,9 +47,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_block_combine_kernel(
   float* out = a.out + (size_t)row * D + d;
   ptx::grid_dependency_wait();
   const int2 unit = a.part_units[b * per_seq + u];      // (of no meaning where the unit is empty)
-  int lo, hi;
-  unit_range(a, b, lo, hi);
-  if (unit_tiles(lo, hi) == 0) {
+  Seen seen;
+  if (unit_range(a, b, seen) == 0) {
     if (warp == 0)
 #pragma unroll
       for (int k = 0; k < PER; ++k) out[k] = 0.f;
@@ -123,9 +123,8 @@ __global__ void __launch_bounds__(kFewWarps * 32) decode_block_combine_few_kerne
   ptx::grid_dependency_wait();
   if (row >= rows) return;
   const int2 unit = a.part_units[(b * a.pool.Hkv + kvh) * a.n_cg + cg];
-  int lo, hi;
-  unit_range(a, b, lo, hi);
-  const bool empty = unit_tiles(lo, hi) == 0;
+  Seen seen;
+  const bool empty = unit_range(a, b, seen) == 0;
   const int n = empty ? 0 : unit.y;
   if (n == 1) return;      // one block had the whole unit and wrote it
   const size_t first = (size_t)unit.x * a.width + col, stride = (size_t)a.width * D;
@@ -185,43 +184,53 @@ cudaError_t launch_combine(const BlockDecodeArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
+// (Both kinds are compiled for as many blocks an SM; the least, should one not be.)
 int block_decode_resident(int head_dim, bool f8) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return -1;
   switch (head_dim) {
-    case 64: return sms * block_decode_blocks_64(f8);
-    case 128: return sms * block_decode_blocks_128(f8);
-    case 256: return sms * block_decode_blocks_256(f8);
+    case 64: return sms * std::min(block_decode_blocks_64(f8), block_scored_blocks_64(f8));
+    case 128: return sms * std::min(block_decode_blocks_128(f8), block_scored_blocks_128(f8));
+    case 256: return sms * std::min(block_decode_blocks_256(f8), block_scored_blocks_256(f8));
     default: return -1;
   }
 }
 
 int block_decode_clusters(int head_dim, bool f8) {
   switch (head_dim) {
-    case 64: return block_decode_clusters_64(f8);
-    case 128: return block_decode_clusters_128(f8);
-    case 256: return block_decode_clusters_256(f8);
+    case 64: return std::min(block_decode_clusters_64(f8), block_scored_clusters_64(f8));
+    case 128: return std::min(block_decode_clusters_128(f8), block_scored_clusters_128(f8));
+    case 256: return std::min(block_decode_clusters_256(f8), block_scored_clusters_256(f8));
     default: return 0;
   }
 }
 
+template <int D, class A>
+static cudaError_t launch_joined(cudaError_t (*launch)(const A&, bool, cudaStream_t), const A& a,
+                                 bool f8, cudaStream_t stream) {
+  if ((long long)a.B * a.Q * a.H > 0x3fffffffLL) return cudaErrorNotSupported;
+  const cudaError_t e = launch(a, f8, stream);
+  return e != cudaSuccess || a.shares == 0 ? e : launch_combine<D>(a, stream);
+}
+
 cudaError_t launch_block_decode(const BlockDecodeArgs& a, int head_dim, bool f8,
                                 cudaStream_t stream) {
-  const long long rows = (long long)a.B * a.Q * a.H;
-  if (rows > 0x3fffffffLL) return cudaErrorNotSupported;
-  cudaError_t e;
   switch (head_dim) {
-    case 64:
-      e = launch_block_decode_64(a, f8, stream);
-      return e != cudaSuccess || a.shares == 0 ? e : launch_combine<64>(a, stream);
-    case 128:
-      e = launch_block_decode_128(a, f8, stream);
-      return e != cudaSuccess || a.shares == 0 ? e : launch_combine<128>(a, stream);
-    case 256:
-      e = launch_block_decode_256(a, f8, stream);
-      return e != cudaSuccess || a.shares == 0 ? e : launch_combine<256>(a, stream);
+    case 64: return launch_joined<64>(launch_block_decode_64, a, f8, stream);
+    case 128: return launch_joined<128>(launch_block_decode_128, a, f8, stream);
+    case 256: return launch_joined<256>(launch_block_decode_256, a, f8, stream);
+    default: return cudaErrorNotSupported;
+  }
+}
+
+cudaError_t launch_block_decode_scored(const BlockScoredArgs& a, int head_dim, bool f8,
+                                       cudaStream_t stream) {
+  switch (head_dim) {
+    case 64: return launch_joined<64>(launch_block_scored_64, a, f8, stream);
+    case 128: return launch_joined<128>(launch_block_scored_128, a, f8, stream);
+    case 256: return launch_joined<256>(launch_block_scored_256, a, f8, stream);
     default: return cudaErrorNotSupported;
   }
 }

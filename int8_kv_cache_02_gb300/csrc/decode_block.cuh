@@ -55,15 +55,22 @@
 // Reading them past L1, the one place where older copies could be, cost 3 % of a fused step
 // (8K 11.8 -> 12.1 us) and 1 to 4 % of the calls without an append.
 //
+// Shaped scores (A = BlockScoredArgs; the plain kernels have none of it): a score is capped and
+// biased before it meets the references.  What a unit sees are two runs of positions, [0,
+// pre) and [lo, hi), the second moving with the window: its tiles are those of both, without
+// the gap between.
+//
 // Bound by HBM: 2 D bytes per position and kv head.
 #pragma once
 
 #include <algorithm>
 #include <climits>
 
+#include <type_traits>
+
 #include <cooperative_groups.h>
 
-#include "block_common.cuh"
+#include "block_scored.cuh"
 #include "decode_common.cuh"
 
 namespace int8kv {
@@ -127,21 +134,58 @@ __device__ __forceinline__ int length_of(const BlockDecodeArgs& a, int b) {
   return a.seq_lens ? __ldg(a.seq_lens + b) : a.length;
 }
 
-// The positions of sequence b that some query of it attends: [lo, hi).
-__device__ __forceinline__ void unit_range(const BlockDecodeArgs& a, int b, int& lo, int& hi) {
-  hi = block_length(length_of(a, b), a.max_pages, a.pool);
-  lo = a.window > 0 && hi > a.window ? hi - a.window : 0;
-}
+template <class A>
+constexpr bool kScored = std::is_same_v<A, BlockScoredArgs>;
+
 __device__ __forceinline__ int unit_tiles(int lo, int hi) {
   return hi > lo ? (hi - 1) / kTile - lo / kTile + 1 : 0;
 }
 
-// Length in the line of the units of a sequence of length `len`.
-__device__ __forceinline__ int line_length(const BlockDecodeArgs& a, int len, int per_seq,
-                                           int start) {
+// The positions of a sequence that some query of it attends: [lo, hi), and with shaped scores
+// [0, pre) too.  Its tiles in the order in which they are taken: from tile `gap_at` on, `gap`
+// tiles are left out.
+struct Seen {
+  int lo, hi;
+  int pre, gap_at, gap;
+  template <class A>
+  __device__ __forceinline__ int tile_at(int t) const {
+    if constexpr (kScored<A>) return t + (t >= gap_at ? gap : 0);
+    return lo / kTile + t;
+  }
+};
+
+__device__ __forceinline__ int prefix_of(const BlockScoredArgs& a, int b) {
+  return a.prefix_lens ? __ldg(a.prefix_lens + b) : a.prefix;
+}
+
+// From the length of a sequence (at most what its row holds) -> its number of tiles.
+template <class A>
+__device__ __forceinline__ int seen_tiles(const A& a, int b, int hi, Seen& s) {
+  s.hi = hi;
+  if constexpr (kScored<A>) {
+    s.pre = hi > 0 ? max(0, min(prefix_of(a, b), hi)) : 0;
+    s.lo = a.window > 0 ? max(0, hi - a.Q + 1 - a.window) : 0;      // (of the first query)
+    s.gap_at = (s.pre + kTile - 1) / kTile;
+    s.gap = s.lo / kTile - s.gap_at;
+    if (s.gap <= 0) s.lo = s.gap = 0;
+    return unit_tiles(0, hi) - s.gap;
+  } else {
+    s.lo = a.window > 0 && hi > a.window ? hi - a.window : 0;
+    return unit_tiles(s.lo, hi);
+  }
+}
+// The same for sequence b; a length beyond its row is flagged.
+template <class A>
+__device__ __forceinline__ int unit_range(const A& a, int b, Seen& s) {
+  return seen_tiles(a, b, block_length(length_of(a, b), a.max_pages, a.pool), s);
+}
+
+// Length in the line of the units of sequence b of length `len`.
+template <class A>
+__device__ __forceinline__ int line_length(const A& a, int b, int len, int per_seq, int start) {
   const int cap = a.max_pages << a.pool.ps_log2;
-  const int hi = len < cap ? len : cap;
-  const int nt = unit_tiles(a.window > 0 && hi > a.window ? hi - a.window : 0, hi);
+  Seen s;
+  const int nt = seen_tiles(a, b, max(0, len < cap ? len : cap), s);
   return nt ? (nt + start) * per_seq : 0;
 }
 
@@ -151,8 +195,8 @@ __device__ __forceinline__ int line_length(const BlockDecodeArgs& a, int len, in
 struct Place {
   int at, end, b, base, per;
 };
-__device__ __forceinline__ Place find_share(const BlockDecodeArgs& a, int per_seq, int start,
-                                            int least) {
+template <class A>
+__device__ __forceinline__ Place find_share(const A& a, int per_seq, int start, int least) {
   const int lane = threadIdx.x & 31, run = (a.B + 31) / 32;
   int sum = 0;
   for (int i = 0; i < run; i += 8) {      // (eight lengths under way)
@@ -161,7 +205,7 @@ __device__ __forceinline__ Place find_share(const BlockDecodeArgs& a, int per_se
     for (int k = 0; k < 8; ++k)
       len[k] = i + k < run && lane * run + i + k < a.B ? length_of(a, lane * run + i + k) : 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum += line_length(a, len[k], per_seq, start);
+    for (int k = 0; k < 8; ++k) sum += line_length(a, lane * run + i + k, len[k], per_seq, start);
   }
   int inc = sum;
 #pragma unroll
@@ -187,7 +231,7 @@ __device__ __forceinline__ Place find_share(const BlockDecodeArgs& a, int per_se
   const bool mine = p.at >= base && p.at < inc;
   if (mine && run > 1)
     for (;;) {
-      const int n = line_length(a, length_of(a, b), per_seq, start);
+      const int n = line_length(a, b, length_of(a, b), per_seq, start);
       if (p.at < base + n) break;
       base += n;
       ++b;
@@ -200,16 +244,16 @@ __device__ __forceinline__ Place find_share(const BlockDecodeArgs& a, int per_se
 
 // The part of a unit that one block takes: tiles [first, last) of unit u of sequence b.
 // pieces: how many shares the unit lies in, from this one on.
-struct Segment {
-  int b, u, lo, hi, nt, first, last, pieces;
+struct Segment : Seen {
+  int b, u, nt, first, last, pieces;
 };
 
 // The segment at p.at, and p behind it; false at the share's end.
-__device__ __forceinline__ bool next_segment(const BlockDecodeArgs& a, Place& p, int per_seq,
-                                             int start, Segment& s) {
+template <class A>
+__device__ __forceinline__ bool next_segment(const A& a, Place& p, int per_seq, int start,
+                                             Segment& s) {
   while (p.at < p.end) {
-    unit_range(a, p.b, s.lo, s.hi);
-    s.nt = unit_tiles(s.lo, s.hi);
+    s.nt = unit_range(a, p.b, s);
     const int len = s.nt + start;
     s.u = s.nt ? (int)((unsigned)(p.at - p.base) / (unsigned)len) : per_seq;
     if (s.u >= per_seq) {     // past this sequence's units
@@ -363,15 +407,34 @@ __device__ __forceinline__ void score_tile(const Warp<D, V>& w, uint32_t tile, c
     for (int i = 0; i < 4; ++i) z[n][i] = s[0][n][i] + s[1][n][i];
 }
 
-// The TPI tiles of one stage.  f: K scale * softmax scale * log2(e) of each tile; lv: log2 of
-// its V scale; lim: last position that each column attends; masked: whether lim, lo
-// or a tile that is not there (bit i of `none`) cut the stage.
-template <int D, bool F8, int V>
-__device__ __forceinline__ void take_stage(Warp<D, V>& w, uint32_t stage, int pos,
+// Scores of a tile at position `pos` (of the lane's row) capped and biased: lim and slope of each
+// column, its query's position and its head's slope.
+template <int NC>
+__device__ __forceinline__ void shape_scores(float (&z)[NC][4], const BlockScoredArgs& a, int pos,
+                                             const int (&lim)[NC][2], const float (&slope)[NC][2]) {
+#pragma unroll
+  for (int n = 0; n < NC; ++n)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (a.shape.cap != 0.f) z[n][k] = capped(z[n][k], a.shape.cap, a.shape.over_cap);
+      if (a.shape.slopes)
+        z[n][k] = fmaf(slope[n][k & 1], (float)(pos + 8 * (k >> 1) - lim[n][k & 1]), z[n][k]);
+    }
+}
+
+// The TPI tiles of one stage, from position pos[i] each.  f: K scale * softmax scale * log2(e) of
+// each tile; lv: log2 of its V scale; lim: last position that each column attends; masked: whether
+// lim, lo (shaped scores: the window, outside the prefix) or a tile that is not there (bit i of
+// `none`) cut the stage.
+template <int D, bool F8, int V, class A>
+__device__ __forceinline__ void take_stage(Warp<D, V>& w, const A& a, uint32_t stage,
+                                           const int (&pos)[Shape<D>::TPI],
                                            const float (&f)[Shape<D>::TPI],
                                            const float (&lv)[Shape<D>::TPI], bool masked,
-                                           uint32_t none, int lo, const int (&lim)[Cols<V>::NC][2],
-                                           const Lane<D>& ln, uint32_t shared_q, int g, int t) {
+                                           uint32_t none, const Seen& seen,
+                                           const int (&lim)[Cols<V>::NC][2],
+                                           const float (&slope)[Cols<V>::NC][2], const Lane<D>& ln,
+                                           uint32_t shared_q, int g, int t) {
   using S = Shape<D>;
   constexpr int NC = Cols<V>::NC, TPI = S::TPI;
   float z[TPI][NC][4];
@@ -383,6 +446,7 @@ __device__ __forceinline__ void take_stage(Warp<D, V>& w, uint32_t stage, int po
     for (int n = 0; n < NC; ++n)
 #pragma unroll
       for (int k = 0; k < 4; ++k) z[i][n][k] *= f[i];
+    if constexpr (kScored<A>) shape_scores(z[i], a, pos[i] + position_of(g), lim, slope);
   }
   if (masked) {
 #pragma unroll
@@ -391,8 +455,13 @@ __device__ __forceinline__ void take_stage(Warp<D, V>& w, uint32_t stage, int po
       for (int n = 0; n < NC; ++n)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int at = pos + i * kTile + position_of(g) + 8 * (k >> 1);
-          if (at < lo || at > lim[n][k & 1] || (none >> i & 1)) z[i][n][k] = -INFINITY;
+          const int at = pos[i] + position_of(g) + 8 * (k >> 1), last = lim[n][k & 1];
+          bool hidden = at < seen.lo || at > last;
+          if constexpr (kScored<A>) {
+            hidden = at > last || (a.window > 0 && at <= last - a.window);
+            if (at < seen.pre && last >= 0) hidden = false;
+          }
+          if (hidden || (none >> i & 1)) z[i][n][k] = -INFINITY;
         }
   }
   bool over = false;
@@ -585,9 +654,9 @@ __device__ __forceinline__ int joined(int col, int d) {
   return col * D + (d ^ ((col >> 1 & 3) << 2));
 }
 
-template <int D, bool F8, int V>
+template <int D, bool F8, int V, class A>
 __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
-    decode_block_kernel(const BlockDecodeArgs a) {
+    decode_block_kernel(const A a) {
   using S = Shape<D>;
   constexpr int NC = Cols<V>::NC, N = Cols<V>::N, TPI = S::TPI;
   constexpr bool EARLY = N * D * 4 <= S::STAGE;
@@ -609,8 +678,7 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
     const int unit = blockIdx.x / a.cluster;
     seg.b = unit / per_seq;
     seg.u = unit % per_seq;
-    unit_range(a, seg.b, seg.lo, seg.hi);
-    seg.nt = unit_tiles(seg.lo, seg.hi);               // (none: zero rows)
+    seg.nt = unit_range(a, seg.b, seg);               // (none: zero rows)
     const int per = (seg.nt + a.cluster - 1) / a.cluster;
     seg.first = min(seg.nt, blockIdx.x % a.cluster * per);
     seg.last = min(seg.nt, seg.first + per);
@@ -633,7 +701,7 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
   auto issue = [&](int i) {
     const int kvh = seg.u / a.n_cg;
     const int tile = mine0 + ((i & ~(BATCH - 1)) + lane / TPI) * (S::NW * TPI) + lane % TPI;
-    const int at = (seg.lo / kTile + tile) * kTile;
+    const int at = seg.tile_at<A>(tile) * kTile;
     auto block_of = [&](int page) {
       return (((size_t)page * p.Hkv + kvh) << (p.ps_log2 - p.t_log2)) +
              ((at & ((1 << p.ps_log2) - 1)) >> p.t_log2);
@@ -649,7 +717,7 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
     }
     bool late = false;
     if (i < n) {
-      late = (seg.lo / kTile + mine0 + i * (S::NW * TPI) + TPI) * kTile > fresh;
+      late = (seg.lo / kTile + mine0 + i * (S::NW * TPI) + TPI) * kTile > fresh;      // (plain ones)
       if (late) {
         ptx::grid_dependency_wait();
         if (pages >= 0 && at >= fresh) {      // (written while this kernel may run: not through L1)
@@ -660,15 +728,21 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
 #pragma unroll
       for (int j = 0; j < TPI; ++j) {
         const int page = __shfl_sync(0xffffffffu, pages, (i & (BATCH - 1)) * TPI + j);
-        const int pos = (seg.lo / kTile + mine0 + i * (S::NW * TPI) + j) * kTile;
+        const int nth = mine0 + i * (S::NW * TPI) + j, pos = seg.tile_at<A>(nth) * kTile;
+        int from = seg.lo, to_pos = seg.hi;      // the rows that are there
+        if constexpr (kScored<A>)
+          if (seg.gap > 0 && nth < seg.gap_at) {
+            from = 0;
+            to_pos = seg.pre;
+          }
         const size_t row = ((((size_t)(page < 0 ? 0 : page) * p.Hkv + kvh) << p.ps_log2) +
                             (pos & ((1 << p.ps_log2) - 1))) * D + 16 * lane;
         const uint32_t to = ring + slot_in + j * S::TILE;
-        if (page >= 0 && pos >= seg.lo && pos + kTile <= seg.hi)
+        if (page >= 0 && pos >= from && pos + kTile <= to_pos)
           copy_tile<D, true>(p.k + row, p.v + row, to, ln, 0, kTile, lane);
         else      // rows behind the context, or of no page, become zeros
-          copy_tile<D, false>(p.k + row, p.v + row, to, ln, page < 0 ? kTile : seg.lo - pos,
-                              seg.hi - pos, lane);
+          copy_tile<D, false>(p.k + row, p.v + row, to, ln, page < 0 ? kTile : from - pos,
+                              to_pos - pos, lane);
       }
     }
     commit_copies();
@@ -697,14 +771,21 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
     if constexpr (!kSharedQ<D, V>) order_queries<D, F8, V>(w, cols, g);
     w.reset();
     int lim[NC][2];           // columns 2t, 2t + 1 of the fragments
+    float slope[NC][2];
 #pragma unroll
     for (int k = 0; k < NC; ++k)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int col = V == kPair ? (2 * t + c) & 3 : 8 * k + 2 * t + c;
         lim[k][c] = col < cols ? seg.hi - a.Q + (cg * a.width + col) / a.G : -1;
+        slope[k][c] = 0.f;
+        if constexpr (kScored<A>)
+          if (a.shape.slopes && col < cols)
+            slope[k][c] = __ldg(a.shape.slopes + kvh * a.G + (cg * a.width + col) % a.G) *
+                          1.4426950408889634f;
       }
     const int least = seg.hi - a.Q + (cg * a.width) / a.G;   // positions <= least: no column masks
+    [[maybe_unused]] const int most = seg.hi - a.Q + (cg * a.width + cols - 1) / a.G;
     int pages_now = -1;       // pages and scales of the stage being taken
     float fs_now = 0.f, ls_now = 0.f;
     for (int i = 0; i < n; ++i) {
@@ -727,9 +808,23 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
         f[j] = __shfl_sync(0xffffffffu, fs_now, (i & (BATCH - 1)) * TPI + j);
         lv[j] = __shfl_sync(0xffffffffu, ls_now, (i & (BATCH - 1)) * TPI + j);
       }
-      const int pos = (seg.lo / kTile + mine0 + i * (S::NW * TPI)) * kTile;
-      const bool masked = none || pos < seg.lo || pos + TPI * kTile - 1 > least;
-      take_stage<D, F8, V>(w, ring + slot_out, pos, f, lv, masked, none, seg.lo, lim, ln, shared_q, g, t);
+      int pos[TPI];
+      bool masked = none;
+      if constexpr (kScored<A>) {
+#pragma unroll
+        for (int j = 0; j < TPI; ++j) {
+          pos[j] = seg.tile_at<A>(mine0 + i * (S::NW * TPI) + j) * kTile;
+          masked |= (pos[j] + kTile - 1 > least || (a.window > 0 && pos[j] <= most - a.window)) &&
+                    (pos[j] + kTile > seg.pre || least < 0);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < TPI; ++j)
+          pos[j] = (seg.lo / kTile + mine0 + i * (S::NW * TPI)) * kTile + j * kTile;
+        masked |= pos[0] < seg.lo || pos[0] + TPI * kTile - 1 > least;
+      }
+      take_stage<D, F8, V>(w, a, ring + slot_out, pos, f, lv, masked, none, seg, lim, slope, ln,
+                           shared_q, g, t);
       slot_out = slot_out == (S::NS - 1) * S::STAGE ? 0 : slot_out + S::STAGE;
     }
     __syncwarp();
@@ -863,8 +958,8 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
   ptx::grid_dependency_wait();    // (the grid is not complete before the append is)
 }
 
-template <int D, bool F8, int V>
-cudaError_t launch_variant(const BlockDecodeArgs& a, cudaStream_t stream) {
+template <int D, bool F8, int V, class A>
+cudaError_t launch_variant(const A& a, cudaStream_t stream) {
   const long long units = (long long)a.B * a.pool.Hkv * a.n_cg;
   const long long grid = a.shares ? a.shares : units * a.cluster;
   if (grid > 0x7fffffffLL) return cudaErrorNotSupported;
@@ -881,23 +976,23 @@ cudaError_t launch_variant(const BlockDecodeArgs& a, cudaStream_t stream) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, decode_block_kernel<D, F8, V>, a);
+  return cudaLaunchKernelEx(&cfg, decode_block_kernel<D, F8, V, A>, a);
 }
 
 // Blocks per SM of one variant, with its shared-memory attribute set.
-template <int D, bool F8, int V>
+template <int D, bool F8, int V, class A>
 int variant_blocks() {
   int per_sm = 0;
-  if (cudaFuncSetAttribute(decode_block_kernel<D, F8, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(decode_block_kernel<D, F8, V, A>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            kSmem<D, V>) != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, decode_block_kernel<D, F8, V>,
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, decode_block_kernel<D, F8, V, A>,
                                                     Shape<D>::NW * 32, kSmem<D, V>) != cudaSuccess)
     return -1;
   return per_sm;
 }
 
 // Clusters of one variant that run at once, after variant_blocks.
-template <int D, bool F8, int V>
+template <int D, bool F8, int V, class A>
 int variant_clusters() {
   int n = 0;
   cudaLaunchConfig_t cfg = {};
@@ -910,49 +1005,54 @@ int variant_clusters() {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaOccupancyMaxActiveClusters(&n, decode_block_kernel<D, F8, V>, &cfg) == cudaSuccess ? n : -1;
+  return cudaOccupancyMaxActiveClusters(&n, decode_block_kernel<D, F8, V, A>, &cfg) == cudaSuccess ? n : -1;
 }
 
-template <int D, bool F8>
-cudaError_t launch_codes(const BlockDecodeArgs& a, cudaStream_t stream) {
+template <int D, bool F8, class A>
+cudaError_t launch_codes(const A& a, cudaStream_t stream) {
   if (a.width <= 4) return launch_variant<D, F8, kPair>(a, stream);
   if (a.width <= 8) return launch_variant<D, F8, kEight>(a, stream);
   return launch_variant<D, F8, kSixteen>(a, stream);
 }
 
-template <int D, bool F8>
+template <int D, bool F8, class A>
 int codes_blocks() {
-  return std::min({variant_blocks<D, F8, kPair>(), variant_blocks<D, F8, kEight>(),
-                   variant_blocks<D, F8, kSixteen>()});
+  return std::min({variant_blocks<D, F8, kPair, A>(), variant_blocks<D, F8, kEight, A>(),
+                   variant_blocks<D, F8, kSixteen, A>()});
 }
 
-template <int D, bool F8>
+template <int D, bool F8, class A>
 int codes_clusters() {
-  return std::min(variant_clusters<D, F8, kPair>(), variant_clusters<D, F8, kEight>());
+  return std::min(variant_clusters<D, F8, kPair, A>(), variant_clusters<D, F8, kEight, A>());
 }
 
 }  // namespace block
 
-// One head_dim's kernels, each in a translation unit of its own.
-#define INT8KV_DECODE_BLOCK_INSTANCE(D)                                                          \
-  cudaError_t launch_block_decode_##D(const BlockDecodeArgs& a, bool f8, cudaStream_t stream) {  \
+// One head_dim's kernels, plain and with shaped scores, each in a translation unit of its own.
+#define INT8KV_DECODE_BLOCK_KERNELS(NAME, ARGS, D)                                               \
+  cudaError_t launch_##NAME##_##D(const ARGS& a, bool f8, cudaStream_t stream) {                 \
     return f8 ? block::launch_codes<D, true>(a, stream) : block::launch_codes<D, false>(a, stream); \
   }                                                                                              \
-  int block_decode_blocks_##D(bool f8) {                                                         \
-    return f8 ? block::codes_blocks<D, true>() : block::codes_blocks<D, false>();                \
+  int NAME##_blocks_##D(bool f8) {                                                               \
+    return f8 ? block::codes_blocks<D, true, ARGS>() : block::codes_blocks<D, false, ARGS>();    \
   }                                                                                              \
-  int block_decode_clusters_##D(bool f8) {                                                       \
-    return f8 ? block::codes_clusters<D, true>() : block::codes_clusters<D, false>();            \
+  int NAME##_clusters_##D(bool f8) {                                                             \
+    return f8 ? block::codes_clusters<D, true, ARGS>() : block::codes_clusters<D, false, ARGS>(); \
   }
+#define INT8KV_DECODE_BLOCK_INSTANCE(D) \
+  INT8KV_DECODE_BLOCK_KERNELS(block_decode, BlockDecodeArgs, D)
+#define INT8KV_DECODE_SCORED_INSTANCE(D) \
+  INT8KV_DECODE_BLOCK_KERNELS(block_scored, BlockScoredArgs, D)
 
-cudaError_t launch_block_decode_64(const BlockDecodeArgs& a, bool f8, cudaStream_t stream);
-cudaError_t launch_block_decode_128(const BlockDecodeArgs& a, bool f8, cudaStream_t stream);
-cudaError_t launch_block_decode_256(const BlockDecodeArgs& a, bool f8, cudaStream_t stream);
-int block_decode_blocks_64(bool f8);
-int block_decode_blocks_128(bool f8);
-int block_decode_blocks_256(bool f8);
-int block_decode_clusters_64(bool f8);
-int block_decode_clusters_128(bool f8);
-int block_decode_clusters_256(bool f8);
+#define INT8KV_DECODE_BLOCK_DECLARED(NAME, ARGS, D)                                \
+  cudaError_t launch_##NAME##_##D(const ARGS& a, bool f8, cudaStream_t stream);    \
+  int NAME##_blocks_##D(bool f8);                                                  \
+  int NAME##_clusters_##D(bool f8);
+INT8KV_DECODE_BLOCK_DECLARED(block_decode, BlockDecodeArgs, 64)
+INT8KV_DECODE_BLOCK_DECLARED(block_decode, BlockDecodeArgs, 128)
+INT8KV_DECODE_BLOCK_DECLARED(block_decode, BlockDecodeArgs, 256)
+INT8KV_DECODE_BLOCK_DECLARED(block_scored, BlockScoredArgs, 64)
+INT8KV_DECODE_BLOCK_DECLARED(block_scored, BlockScoredArgs, 128)
+INT8KV_DECODE_BLOCK_DECLARED(block_scored, BlockScoredArgs, 256)
 
 }  // namespace int8kv

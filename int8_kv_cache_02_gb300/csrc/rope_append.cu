@@ -14,7 +14,7 @@
 // in pieces of four, and a piece of four pairs that go by one position is two 16-byte loads.
 #include <cmath>
 
-#include "block_common.cuh"
+#include "block_quant.cuh"
 #include "quant_row.cuh"
 #include "q4_row.cuh"
 
