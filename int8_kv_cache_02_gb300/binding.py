@@ -191,18 +191,38 @@ def kv_quant_append(pool, layer, k_new, v_new, seq_pos, page_table, stream=None)
                                  page_table.shape[1], _stream(stream)), "kv_quant_append")
 
 
-def _token_rows(t, n_heads, head_dim, name):
+def _ptr(t, dtype, shape, device, name):
+    """The address of a contiguous tensor of this dtype and shape on a device: one test where all is
+    well (a step's calls are short next to their checks), and what is wrong where it is not."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == device
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, dtype, name)
+    _shape(t, shape, name)
+    raise ValueError(f"{name} is on device {t.get_device()}, not on {device}")
+
+
+def _token_rows(t, shape, device, name):
     """Address and token stride of fp16 rows [n_seqs][n_new][n_heads][head_dim], evenly spaced (a part
     of a wider projection's rows will do)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device")
-    if t.dtype != torch.float16:
-        raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
-    _shape(t, (*t.shape[:2], n_heads, head_dim), name)
-    seqs, n_new = t.shape[:2]
-    if t.numel() == 0:
+    try:
+        there = t.dtype is torch.float16 and t.shape == shape and t.get_device() == device
+    except AttributeError:
+        there = False
+    if not there:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be on a CUDA device")
+        if t.dtype != torch.float16:
+            raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
+        _shape(t, shape, name)
+        raise ValueError(f"{name} is on device {t.get_device()}, not on {device}")
+    seqs, n_new, n_heads, head_dim = shape
+    if t.is_contiguous():
         return t.data_ptr(), n_heads * head_dim
     s0, s1, s2, s3 = t.stride()
     if n_new <= 1:
@@ -223,59 +243,67 @@ def kv_rope_append(pool, layer, k_new, v_new, seq_pos, page_table, rope_table, q
     [n_axes][n_seqs][n_new] or [n_seqs][n_new]; None: seq_pos[b] + i.  pair_axis: uint8
     [rope_dim / 2] on the HOST, the axis of each pair.  new_lens: int32 [n_seqs], tokens that each
     sequence brings.  q, k_new and v_new may be parts of one projection's rows."""
-    if k_new.dim() != 4 or v_new.shape != k_new.shape:
-        raise ValueError("k_new and v_new must have shape [n_seqs][n_new][n_kv_heads][head_dim]")
+    dev, i32 = pool.device_index, torch.int32
+    if k_new.dim() != 4 or page_table.dim() != 2 or rope_table.dim() != 2:
+        raise ValueError("k_new must have shape [n_seqs][n_new][n_kv_heads][head_dim], page_table "
+                         "[n_seqs][max_pages], rope_table [n_table][rope_dim]")
     n_seqs, n_new = k_new.shape[:2]
-    k, ks = _token_rows(k_new, pool.n_kv_heads, pool.head_dim, "k_new")
-    v, vs = _token_rows(v_new, pool.n_kv_heads, pool.head_dim, "v_new")
+    shape = (n_seqs, n_new, pool.n_kv_heads, pool.head_dim)
+    k, ks = _token_rows(k_new, shape, dev, "k_new")
+    v, vs = _token_rows(v_new, shape, dev, "v_new")
     qp = qo = axis = at = lens = None
     n_heads = qs = 0
     if q is not None:
-        if q.dim() != 4 or q.shape[:2] != k_new.shape[:2]:
+        if q.dim() != 4:
             raise ValueError("q must have shape [n_seqs][n_new][n_heads][head_dim]")
         n_heads = q.shape[2]
-        qp, qs = _token_rows(q, n_heads, pool.head_dim, "q")
-        qo = _dev(q_out, torch.float16, "q_out")
-        _shape(q_out, q.shape, "q_out")
-    table = _dev(rope_table, torch.float32, "rope_table")
-    if rope_table.dim() != 2 or (rope_dim is not None and rope_dim != rope_table.shape[1]):
-        raise ValueError("rope_table must have shape [n_table][rope_dim]")
-    n_table, rope_dim = rope_table.shape
+        shape = (n_seqs, n_new, n_heads, pool.head_dim)
+        qp, qs = _token_rows(q, shape, dev, "q")
+        qo = _ptr(q_out, torch.float16, shape, dev, "q_out")
+    n_table, dim = rope_table.shape
+    if rope_dim is not None and rope_dim != dim:
+        raise ValueError(f"rope_table must have shape [n_table][{rope_dim}]")
     n_axes = 1
     if positions is not None:
-        at = _dev(positions, torch.int32, "positions")
-        n_axes = positions.shape[0] if positions.dim() == 3 else 1
-        if positions.shape[-2:] != k_new.shape[:2] or positions.dim() not in (2, 3):
-            raise ValueError(f"positions must have shape [n_axes][{n_seqs}][{n_new}]")
+        if positions.dim() == 3:
+            n_axes = positions.shape[0]
+            at = _ptr(positions, i32, (n_axes, n_seqs, n_new), dev, "positions")
+        else:
+            at = _ptr(positions, i32, (n_seqs, n_new), dev, "positions")
     if pair_axis is not None:
         if pair_axis.is_cuda or pair_axis.dtype != torch.uint8 or not pair_axis.is_contiguous():
             raise TypeError("pair_axis must be a contiguous uint8 tensor on the host")
-        _shape(pair_axis, (rope_dim // 2,), "pair_axis")
+        _shape(pair_axis, (dim // 2,), "pair_axis")
         axis = pair_axis.data_ptr()
     if new_lens is not None:
-        lens = _dev(new_lens, torch.int32, "new_lens")
-        _shape(new_lens, (n_seqs,), "new_lens")
-    pos, pages = _dev(seq_pos, torch.int32, "seq_pos"), _dev(page_table, torch.int32, "page_table")
-    _shape(seq_pos, (n_seqs,), "seq_pos")
-    _shape(page_table, (n_seqs, page_table.shape[-1]), "page_table")
-    _here(pool, k_new, v_new, q, q_out, rope_table, positions, new_lens, seq_pos, page_table)
-    _check(lib().kv_rope_append(pool.handle, layer, qp, k, v, qs, ks, vs, n_seqs, n_new, n_heads,
-                                pos, lens, table, n_table, rope_dim, ROPE_STYLES[style], at, n_axes,
-                                axis, qo, pages, page_table.shape[1], _stream(stream)),
-           "kv_rope_append")
+        lens = _ptr(new_lens, i32, (n_seqs,), dev, "new_lens")
+    max_pages = page_table.shape[1]
+    _check((_lib or lib()).kv_rope_append(
+        pool.handle, layer, qp, k, v, qs, ks, vs, n_seqs, n_new, n_heads,
+        _ptr(seq_pos, i32, (n_seqs,), dev, "seq_pos"), lens,
+        _ptr(rope_table, torch.float32, (n_table, dim), dev, "rope_table"), n_table, dim,
+        ROPE_STYLES[style], at, n_axes, axis, qo,
+        _ptr(page_table, i32, (n_seqs, max_pages), dev, "page_table"), max_pages,
+        _stream(stream)), "kv_rope_append")
 
 
-def _prob_rows(t, shape, name):
+def _prob_rows(t, shape, device, name):
     """Address and row stride of fp32 probabilities [batch][rows][vocab], rows evenly spaced."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device")
-    if t.dtype != torch.float32:
-        raise TypeError(f"{name} must be {torch.float32}, got {t.dtype}")
-    _shape(t, shape, name)
+    try:
+        there = t.dtype is torch.float32 and t.shape == shape and t.get_device() == device
+    except AttributeError:
+        there = False
+    if not there:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be on a CUDA device")
+        if t.dtype != torch.float32:
+            raise TypeError(f"{name} must be {torch.float32}, got {t.dtype}")
+        _shape(t, shape, name)
+        raise ValueError(f"{name} is on device {t.get_device()}, not on {device}")
     batch, rows, vocab = shape
-    if t.numel() == 0:
+    if t.is_contiguous():
         return t.data_ptr(), vocab
     s0, s1, s2 = t.stride()
     if rows <= 1:
@@ -295,34 +323,31 @@ def kv_verify_drafts(target_probs, draft_tokens, accept_u, sample_u, tokens, n_a
     [batch][n_draft], sample_u fp32 [batch]; n_drafts int32 [batch], drafts of each sequence.
     Writes tokens (int32 [batch][n_draft + 1]) and n_accepted (int32 [batch]), and seq_lens less the
     refused drafts to seq_lens_out (int32 [batch] each).  Vocabularies may be padded: a slice of
-    wider rows will do."""
-    x, u = _dev(draft_tokens, torch.int32, "draft_tokens"), _dev(accept_u, torch.float32, "accept_u")
+    wider rows will do.  The tensors are on the current device."""
     if draft_tokens.dim() != 2 or target_probs.dim() != 3:
         raise ValueError("draft_tokens must have shape [batch][n_draft], target_probs "
                          "[batch][n_draft + 1][vocab]")
+    dev, i32, f32 = target_probs.get_device(), torch.int32, torch.float32
+    if dev < 0:
+        raise ValueError("target_probs must be on a CUDA device")
+    if dev != _device():
+        raise ValueError(f"target_probs is on device {dev}, the current one is {_device()}")
     batch, n = draft_tokens.shape
     vocab = target_probs.shape[2]
-    p, ps = _prob_rows(target_probs, (batch, n + 1, vocab), "target_probs")
-    q, qs = _prob_rows(draft_probs, (batch, n, vocab), "draft_probs") if draft_probs is not None \
-        else (None, 0)
-    _shape(accept_u, (batch, n), "accept_u")
-    s, t = _dev(sample_u, torch.float32, "sample_u"), _dev(tokens, torch.int32, "tokens")
-    acc = _dev(n_accepted, torch.int32, "n_accepted")
-    _shape(sample_u, (batch,), "sample_u")
-    _shape(tokens, (batch, n + 1), "tokens")
-    _shape(n_accepted, (batch,), "n_accepted")
-    optional = []
-    for name, v in (("n_drafts", n_drafts), ("seq_lens", seq_lens), ("seq_lens_out", seq_lens_out)):
-        optional.append(_dev(v, torch.int32, name) if v is not None else None)
-        if v is not None:
-            _shape(v, (batch,), name)
-    at = _device()
-    for v in (target_probs, draft_tokens, accept_u, sample_u, tokens, n_accepted, draft_probs,
-              n_drafts, seq_lens, seq_lens_out):
-        if v is not None and v.get_device() != at:
-            raise ValueError(f"a tensor is on device {v.get_device()}, the current one is {at}")
-    _check(lib().kv_verify_drafts(batch, n, vocab, p, ps, q, qs, x, optional[0], u, s, t, acc,
-                                  optional[1], optional[2], _stream(stream)), "kv_verify_drafts")
+    one = (batch,)
+    p, ps = _prob_rows(target_probs, (batch, n + 1, vocab), dev, "target_probs")
+    q, qs = (_prob_rows(draft_probs, (batch, n, vocab), dev, "draft_probs")
+             if draft_probs is not None else (None, 0))
+    _check((_lib or lib()).kv_verify_drafts(
+        batch, n, vocab, p, ps, q, qs, _ptr(draft_tokens, i32, (batch, n), dev, "draft_tokens"),
+        _ptr(n_drafts, i32, one, dev, "n_drafts") if n_drafts is not None else None,
+        _ptr(accept_u, f32, (batch, n), dev, "accept_u"),
+        _ptr(sample_u, f32, one, dev, "sample_u"),
+        _ptr(tokens, i32, (batch, n + 1), dev, "tokens"),
+        _ptr(n_accepted, i32, one, dev, "n_accepted"),
+        _ptr(seq_lens, i32, one, dev, "seq_lens") if seq_lens is not None else None,
+        _ptr(seq_lens_out, i32, one, dev, "seq_lens_out") if seq_lens_out is not None else None,
+        _stream(stream)), "kv_verify_drafts")
 
 
 def attn_decode_n_splits(pool, batch, max_ctx):
@@ -407,16 +432,22 @@ def attn_decode_multi_int8(pool, layer, q, seq_lens, page_table, out, workspace=
                                         _stream(stream)), "attn_decode_multi_int8")
 
 
-def _scored_call(pool, q, slopes, n_heads):
-    """Address of a call's slopes (fp32 [n_heads], or None)."""
+def _scored_args(pool, q, out, slopes, workspace):
+    """Addresses of a scored call's queries, output, slopes and workspace, and the workspace's size."""
     if not pool.block:
         raise ValueError("shaped scores want a block-scaled pool")
-    if slopes is None:
-        return None
-    s = _dev(slopes, torch.float32, "slopes")
-    _shape(slopes, (n_heads,), "slopes")
-    _here(pool, slopes)
-    return s
+    dev = pool.device_index
+    shape = q.shape
+    if shape[-1] != pool.head_dim:
+        raise ValueError(f"q must have shape [..., {pool.head_dim}], got {list(shape)}")
+    ws = None
+    nbytes = 0
+    if workspace is not None:
+        nbytes = workspace.numel()
+        ws = _ptr(workspace, torch.uint8, (nbytes,), dev, "workspace")
+    return (_ptr(q, torch.float16, shape, dev, "q"), _ptr(out, torch.float32, shape, dev, "out"),
+            _ptr(slopes, torch.float32, (shape[-2],), dev, "slopes") if slopes is not None else None,
+            ws, nbytes)
 
 
 def attn_decode_scored_int8(pool, layer, q, seq_lens, page_table, out, workspace=None, window=0,
@@ -427,25 +458,18 @@ def attn_decode_scored_int8(pool, layer, q, seq_lens, page_table, out, workspace
 
     q: fp16 [B][H][D], or a window of queries [B][q_len][H][D], the last of them at seq_lens[b] - 1;
     out: fp32, the same shape; block-scaled pools."""
-    B, H = q.shape[0], q.shape[-2]
-    Q = q.shape[1] if q.dim() == 4 else 1
-    if q.dim() not in (3, 4):
-        raise ValueError("q must have shape [B][H][D] or [B][q_len][H][D]")
-    s = _scored_call(pool, q, slopes, H)
-    _block_call(pool, q, seq_lens, page_table, out, workspace)
-    p = None
-    if prefix_lens is not None:
-        p = _dev(prefix_lens, torch.int32, "prefix_lens")
-        _shape(prefix_lens, (B,), "prefix_lens")
-        _here(pool, prefix_lens)
-    ws = _dev(workspace, torch.uint8, "workspace") if workspace is not None else None
-    nbytes = workspace.numel() if workspace is not None else 0
-    _check(lib().attn_decode_scored_int8(pool.handle, layer, _dev(q, torch.float16, "q"), B, Q, H,
-                                         _dev(seq_lens, torch.int32, "seq_lens"),
-                                         _dev(page_table, torch.int32, "page_table"),
-                                         page_table.shape[1], window, softmax_scale, softcap, s, p,
-                                         n_splits, _dev(out, torch.float32, "out"), ws, nbytes,
-                                         _stream(stream)), "attn_decode_scored_int8")
+    n = q.dim()
+    if n not in (3, 4) or page_table.dim() != 2:
+        raise ValueError("q must have shape [B][H][D] or [B][q_len][H][D], page_table [B][max_pages]")
+    qp, op, sp, ws, nbytes = _scored_args(pool, q, out, slopes, workspace)
+    dev, i32, B, max_pages = pool.device_index, torch.int32, q.shape[0], page_table.shape[1]
+    _check((_lib or lib()).attn_decode_scored_int8(
+        pool.handle, layer, qp, B, q.shape[1] if n == 4 else 1, q.shape[-2],
+        _ptr(seq_lens, i32, (B,), dev, "seq_lens"),
+        _ptr(page_table, i32, (B, max_pages), dev, "page_table"), max_pages, window, softmax_scale,
+        softcap, sp,
+        _ptr(prefix_lens, i32, (B,), dev, "prefix_lens") if prefix_lens is not None else None,
+        n_splits, op, ws, nbytes, _stream(stream)), "attn_decode_scored_int8")
 
 
 def attn_prefill_n_splits(pool, n_new, n_heads, start_pos):
@@ -486,22 +510,17 @@ def attn_prefill_chunk_scored_int8(pool, layer, q, start_pos, page_table, out, w
                                    softmax_scale=0.0, n_splits=0, stream=None):
     """attn_prefill_chunk_int8 with scores shaped as by attn_decode_scored_int8: q fp16 [n_new][H][D],
     query i at start_pos + i; positions below prefix_len are seen by all; block-scaled pools."""
-    n_new, H = q.shape[0], q.shape[1]
-    s = _scored_call(pool, q, slopes, H)
-    _shape(q, (n_new, H, pool.head_dim), "q")
-    _shape(out, q.shape, "out")
-    if page_table.numel() != page_table.shape[-1]:
+    if q.dim() != 3:
+        raise ValueError("q must have shape [n_new][H][D]")
+    qp, op, sp, ws, nbytes = _scored_args(pool, q, out, slopes, workspace)
+    row = page_table.shape
+    if page_table.numel() != row[-1]:
         raise ValueError("page_table must be one sequence's row")
-    _here(pool, q, page_table, out, workspace)
-    ws = _dev(workspace, torch.uint8, "workspace") if workspace is not None else None
-    nbytes = workspace.numel() if workspace is not None else 0
-    _check(lib().attn_prefill_chunk_scored_int8(pool.handle, layer, _dev(q, torch.float16, "q"), n_new,
-                                                H, start_pos,
-                                                _dev(page_table, torch.int32, "page_table"),
-                                                page_table.shape[-1], window, softmax_scale, softcap,
-                                                s, prefix_len, n_splits,
-                                                _dev(out, torch.float32, "out"), ws, nbytes,
-                                                _stream(stream)), "attn_prefill_chunk_scored_int8")
+    _check((_lib or lib()).attn_prefill_chunk_scored_int8(
+        pool.handle, layer, qp, q.shape[0], q.shape[1], start_pos,
+        _ptr(page_table, torch.int32, row, pool.device_index, "page_table"), row[-1], window,
+        softmax_scale, softcap, sp, prefix_len, n_splits, op, ws, nbytes, _stream(stream)),
+        "attn_prefill_chunk_scored_int8")
 
 
 def kv_pool_set_decode_kernel(pool, kind):

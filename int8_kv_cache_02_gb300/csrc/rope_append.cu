@@ -37,7 +37,7 @@ struct RopeArgs {
   int max_pages;
   int32_t* err;
   unsigned append_blocks;         // the blocks behind them rotate queries
-  int heads;                      // query heads that one of their threads takes
+  int heads, kv_heads;            // query heads that one of their threads takes, kv heads of a group
 };
 
 // Tokens that sequence b brings.
@@ -48,41 +48,46 @@ __device__ __forceinline__ int tokens_of(const RopeArgs& a, size_t b) {
   return max(0, min(n, a.n_new));
 }
 
-// The table's row of the position that token i of sequence b has on an axis; null (flagged)
-// outside the table.
-__device__ __forceinline__ const float* table_row(const RopeArgs& a, size_t b, int i, int axis) {
-  const long long at = a.positions
-                           ? __ldg(a.positions + ((size_t)axis * a.n_seqs + b) * a.n_new + i)
-                           : (long long)__ldg(a.seq_pos + b) + i;
-  if (at < 0 || at >= a.n_table) {
-    flag_error(a.err, INT8KV_DEVERR_LENGTH);
-    return nullptr;
+// The table's row of the position that token i of sequence b has on an axis; outside the table `ok`
+// is false and the row some other (loads go ahead without a branch, and in batches).
+struct TableRow {
+  const float* row;
+  bool ok;
+  __device__ __forceinline__ TableRow(const RopeArgs& a, size_t b, int i, int axis) {
+    const long long at = a.positions
+                             ? __ldg(a.positions + ((size_t)axis * a.n_seqs + b) * a.n_new + i)
+                             : (long long)__ldg(a.seq_pos + b) + i;
+    ok = at >= 0 && at < a.n_table;
+    row = a.table + (size_t)(ok ? at : 0) * a.R;
   }
-  return a.table + (size_t)at * a.R;
-}
+};
 
-// Cosines and sines of N consecutive pairs from pair i on (N a multiple of 4, i too).
+// Cosines and sines of N consecutive pairs from pair i on: 4 or 8 from a multiple of 4 on, else 1 or 2.
+// What lies outside the table is flagged by the caller (`bad`) and does not turn.
 template <int N>
 __device__ __forceinline__ void load_turns(const RopeArgs& a, size_t b, int tok, int i, float* c,
-                                           float* s) {
+                                           float* s, bool& bad) {
+  constexpr int STEP = N < 4 ? N : 4;
 #pragma unroll
-  for (int k = 0; k < N; k += 4) {
-    const unsigned by = a.axes[(i + k) >> 2], first = by & 3;
-    if (by == first * 0x55u) {
-      const float* row = table_row(a, b, tok, first);
-      float4 x = make_float4(1.f, 1.f, 1.f, 1.f), y = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (row) {
-        x = __ldg(reinterpret_cast<const float4*>(row + i + k));
-        y = __ldg(reinterpret_cast<const float4*>(row + a.R / 2 + i + k));
-      }
-      c[k] = x.x, c[k + 1] = x.y, c[k + 2] = x.z, c[k + 3] = x.w;
-      s[k] = y.x, s[k + 1] = y.y, s[k + 2] = y.z, s[k + 3] = y.w;
+  for (int k = 0; k < N; k += STEP) {
+    const unsigned by = a.axes[(i + k) >> 2] >> (N < 4 ? 2 * (i & 3) : 0), first = by & 3;
+    if (STEP == 4 && by == first * 0x55u) {
+      const TableRow r(a, b, tok, first);
+      const float4 x = __ldg(reinterpret_cast<const float4*>(r.row + i + k));
+      const float4 y = __ldg(reinterpret_cast<const float4*>(r.row + a.R / 2 + i + k));
+      bad |= !r.ok;
+      c[k] = r.ok ? x.x : 1.f, c[k + 1] = r.ok ? x.y : 1.f;
+      c[k + 2] = r.ok ? x.z : 1.f, c[k + 3] = r.ok ? x.w : 1.f;
+      s[k] = r.ok ? y.x : 0.f, s[k + 1] = r.ok ? y.y : 0.f;
+      s[k + 2] = r.ok ? y.z : 0.f, s[k + 3] = r.ok ? y.w : 0.f;
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float* row = table_row(a, b, tok, by >> (2 * e) & 3);
-        c[k + e] = row ? __ldg(row + i + k + e) : 1.f;
-        s[k + e] = row ? __ldg(row + a.R / 2 + i + k + e) : 0.f;
+      for (int e = 0; e < STEP; ++e) {
+        const TableRow r(a, b, tok, by >> (2 * e) & 3);
+        const float x = __ldg(r.row + i + k + e), y = __ldg(r.row + a.R / 2 + i + k + e);
+        bad |= !r.ok;
+        c[k + e] = r.ok ? x : 1.f;
+        s[k + e] = r.ok ? y : 0.f;
       }
     }
   }
@@ -119,12 +124,13 @@ __device__ __forceinline__ void twin_pieces(int t, int R, int& x, int& y) {
 struct Turns {
   float c[8], s[8];
 };
-__device__ __forceinline__ void twin_turns(const RopeArgs& a, size_t b, int tok, int t, Turns& w) {
+__device__ __forceinline__ void twin_turns(const RopeArgs& a, size_t b, int tok, int t, Turns& w,
+                                           bool& bad) {
   if (a.pairs) {
-    load_turns<4>(a, b, tok, 4 * t, w.c, w.s);
-    load_turns<4>(a, b, tok, a.R / 4 + 4 * t, w.c + 4, w.s + 4);
+    load_turns<4>(a, b, tok, 4 * t, w.c, w.s, bad);
+    load_turns<4>(a, b, tok, a.R / 4 + 4 * t, w.c + 4, w.s + 4, bad);
   } else {
-    load_turns<8>(a, b, tok, 8 * t, w.c, w.s);
+    load_turns<8>(a, b, tok, 8 * t, w.c, w.s, bad);
   }
 }
 __device__ __forceinline__ void turn_twin(bool pairs, const Turns& w, float (&x)[8], float (&y)[8]) {
@@ -140,12 +146,13 @@ __device__ __forceinline__ void turn_twin(bool pairs, const Turns& w, float (&x)
   }
 }
 
-// Queries: a thread takes one twin of a token for `a.heads` heads, whose turns it loads once.
+// Queries: a thread takes one twin of a token for `a.heads` heads, whose turns it loads once; the next
+// heads' values are under way while it turns the last ones'.
 // (q_out may be q: a value is read and written by one thread, in this order, so not through
 // the read-only path.)
 template <int D>
 __device__ __forceinline__ void rotate_queries(const RopeArgs& a, unsigned thread) {
-  constexpr int TW = D / 16, TOGETHER = 4;
+  constexpr int TW = D / 16, N = 2;
   const unsigned groups = (a.H + a.heads - 1) / a.heads;
   const int t = thread % TW;
   const unsigned job = thread / TW, tok = job / groups;
@@ -157,48 +164,67 @@ __device__ __forceinline__ void rotate_queries(const RopeArgs& a, unsigned threa
   int px, py;
   twin_pieces(t, a.R, px, py);
   const bool turned = t < a.R / 16;
-  Turns w;
   const int end = min(a.H, h0 + a.heads);
   const uint16_t* from = a.q + (size_t)tok * a.q_stride;
   uint16_t* to = a.q_out + (size_t)tok * a.H * D;
-  for (int h = h0; h < end; h += TOGETHER) {
-    uint4 x[TOGETHER], y[TOGETHER];
+  uint4 next[N][2];
+  const auto load = [&](int h) {
 #pragma unroll
-    for (int k = 0; k < TOGETHER; ++k)
+    for (int k = 0; k < N; ++k)
       if (h + k < end) {
-        x[k] = *reinterpret_cast<const uint4*>(from + (h + k) * D + 8 * px);
-        y[k] = *reinterpret_cast<const uint4*>(from + (h + k) * D + 8 * py);
+        next[k][0] = *reinterpret_cast<const uint4*>(from + (h + k) * D + 8 * px);
+        next[k][1] = *reinterpret_cast<const uint4*>(from + (h + k) * D + 8 * py);
       }
-    if (h == h0 && turned) twin_turns(a, b, i, t, w);
+  };
+  load(h0);
+  Turns w;
+  bool bad = false;
+  if (turned) twin_turns(a, b, i, t, w, bad);
+  if (bad) flag_error(a.err, INT8KV_DEVERR_LENGTH);
+  for (int h = h0; h < end; h += N) {
+    uint4 x[N][2];
 #pragma unroll
-    for (int k = 0; k < TOGETHER; ++k)
+    for (int k = 0; k < N; ++k) {
+      x[k][0] = next[k][0];
+      x[k][1] = next[k][1];
+    }
+    load(h + N);
+#pragma unroll
+    for (int k = 0; k < N; ++k)
       if (h + k < end) {
         if (turned) {
           float fx[8], fy[8];
-          halves_to_floats(x[k], fx);
-          halves_to_floats(y[k], fy);
+          halves_to_floats(x[k][0], fx);
+          halves_to_floats(x[k][1], fy);
           turn_twin(a.pairs, w, fx, fy);
-          x[k] = make_uint4(ptx::pack_f16x2(fx[0], fx[1]), ptx::pack_f16x2(fx[2], fx[3]),
-                            ptx::pack_f16x2(fx[4], fx[5]), ptx::pack_f16x2(fx[6], fx[7]));
-          y[k] = make_uint4(ptx::pack_f16x2(fy[0], fy[1]), ptx::pack_f16x2(fy[2], fy[3]),
-                            ptx::pack_f16x2(fy[4], fy[5]), ptx::pack_f16x2(fy[6], fy[7]));
+          x[k][0] = make_uint4(ptx::pack_f16x2(fx[0], fx[1]), ptx::pack_f16x2(fx[2], fx[3]),
+                               ptx::pack_f16x2(fx[4], fx[5]), ptx::pack_f16x2(fx[6], fx[7]));
+          x[k][1] = make_uint4(ptx::pack_f16x2(fy[0], fy[1]), ptx::pack_f16x2(fy[2], fy[3]),
+                               ptx::pack_f16x2(fy[4], fy[5]), ptx::pack_f16x2(fy[6], fy[7]));
         }
-        *reinterpret_cast<uint4*>(to + (h + k) * D + 8 * px) = x[k];
-        *reinterpret_cast<uint4*>(to + (h + k) * D + 8 * py) = y[k];
+        *reinterpret_cast<uint4*>(to + (h + k) * D + 8 * px) = x[k][0];
+        *reinterpret_cast<uint4*>(to + (h + k) * D + 8 * py) = x[k][1];
       }
   }
 }
 
 // ---- block-scaled pools ------------------------------------------------------
-// As in the append kernel, one group of threads (a warp, or a block of NT threads) owns a
-// (sequence, block, kv head, store): it loads the new rows once, turns K's, reduces the
-// largest magnitude, and writes codes and scale.  CH twins per thread, as fp32.
+// As in the append kernel, one group of threads (a warp, or a block of NT threads) owns blocks of
+// positions: it loads a block's new rows once, turns K's, reduces the largest magnitude, and writes
+// codes and scale.  Here it takes the same positions of a.kv_heads heads, one after the other: their
+// turns are the same, and loaded once (a row's are four times its own bytes), and the next head's
+// rows are under way meanwhile.  CH twins per thread, as fp32; beyond two of them the turns
+// are loaded again for each head, the registers holding no more.
+// Compiled for 768 threads an SM: a prompt of 2 x 16381 tokens (32 / 8 heads of D 128) takes 126 us,
+// 138 at 512 (128 registers) and 144 at 1024, whose spills the keys pay for.
+constexpr int kResident = 768;
 template <int D, bool F8, int NT, int GROUPS, int CH>
-__global__ void __launch_bounds__(NT* GROUPS)
+__global__ void __launch_bounds__(NT* GROUPS, kResident / (NT * GROUPS) ? kResident / (NT * GROUPS) : 1)
     rope_block_kernel(const __grid_constant__ RopeArgs a, const BlockView p, int nb) {
   constexpr int TW = D / 16;     // twins per row
+  constexpr bool KEEP = CH <= 2;
   static_assert(GROUPS == 1 || NT == 32, "groups of a block are single warps");
-  __shared__ float red[NT / 32];
+  __shared__ float red[2][NT / 32];
   ptx::grid_dependency_wait();
   ptx::grid_launch_dependents();
   if (blockIdx.x >= a.append_blocks) {
@@ -207,10 +233,11 @@ __global__ void __launch_bounds__(NT* GROUPS)
   }
   const int tid = threadIdx.x % NT;
   const unsigned unit = blockIdx.x * GROUPS + threadIdx.x / NT;     // (fewer than 2^31)
-  // unit = ((sequence * nb + block) * Hkv + kv head) * 2 + store
+  // unit = ((sequence * nb + block) * head groups + group) * 2 + store
   const bool is_v = unit & 1;
-  const int kvh = (unit >> 1) % (unsigned)p.Hkv;
-  const unsigned sb = (unit >> 1) / (unsigned)p.Hkv;
+  const unsigned groups = (p.Hkv + a.kv_heads - 1) / a.kv_heads;
+  const int h0 = (unit >> 1) % groups * a.kv_heads, end = min(p.Hkv, h0 + a.kv_heads);
+  const unsigned sb = (unit >> 1) / groups;
   const int j = sb % (unsigned)nb;
   const size_t b = sb / (unsigned)nb;
   if (b >= (size_t)a.n_seqs) return;
@@ -233,93 +260,266 @@ __global__ void __launch_bounds__(NT* GROUPS)
     return;
   }
   const long long stride = is_v ? a.v_stride : a.k_stride;
-  const uint16_t* src = (is_v ? a.v : a.k) + (size_t)(b * a.n_new + i0) * stride + kvh * D;
+  const uint16_t* src = (is_v ? a.v : a.k) + (size_t)(b * a.n_new + i0) * stride;
   uint4 raw[CH][2];
+  const auto load = [&](int h) {
 #pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const int n = tid + c * NT, r = n / TW;
-    int px, py;
-    twin_pieces(n % TW, a.R, px, py);
-    raw[c][0] = raw[c][1] = make_uint4(0, 0, 0, 0);
-    if (r < rows) {
-      raw[c][0] = ptx::ldg128(src + r * stride + 8 * px);
-      raw[c][1] = ptx::ldg128(src + r * stride + 8 * py);
+    for (int c = 0; c < CH; ++c) {
+      const int n = tid + c * NT, r = n / TW;
+      int px, py;
+      twin_pieces(n % TW, a.R, px, py);
+      raw[c][0] = raw[c][1] = make_uint4(0, 0, 0, 0);
+      if (r < rows && h < end) {
+        raw[c][0] = ptx::ldg128(src + r * stride + h * D + 8 * px);
+        raw[c][1] = ptx::ldg128(src + r * stride + h * D + 8 * py);
+      }
     }
-  }
+  };
+  load(h0);
   const int page = block_page(a.page_table + b * a.max_pages, (int)lp, p);
+  Turns turns[KEEP ? CH : 1];
+  bool bad = false;
+  const auto turns_of = [&](int c, Turns& w) {
+    const int n = tid + c * NT, r = n / TW, t = n % TW;
+    if (!is_v && t < a.R / 16 && r < rows) twin_turns(a, b, (int)i0 + r, t, w, bad);
+  };
+  if constexpr (KEEP)
+#pragma unroll
+    for (int c = 0; c < CH; ++c) turns_of(c, turns[c]);
   if (page < 0) return;
   const int slot = (int)(first & ((1 << p.ps_log2) - 1));
-  const size_t ph = (size_t)page * p.Hkv + kvh;
-  uint8_t* codes = (is_v ? p.v : p.k) + ((ph << p.ps_log2) + slot) * D;
-  float* scale = (is_v ? p.vs : p.ks) + (ph << (p.ps_log2 - p.t_log2)) + (slot >> p.t_log2);
-  const float s_old = r0 ? *scale : 0.f;
-
-  float x[CH][2][8], top = 0.f;
+  for (int h = h0; h < end; ++h) {
+    const size_t ph = (size_t)page * p.Hkv + h;
+    uint8_t* codes = (is_v ? p.v : p.k) + ((ph << p.ps_log2) + slot) * D;
+    float* scale = (is_v ? p.vs : p.ks) + (ph << (p.ps_log2 - p.t_log2)) + (slot >> p.t_log2);
+    const float s_old = r0 ? *scale : 0.f;
+    float x[CH][2][8], top = 0.f;
 #pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const int n = tid + c * NT, r = n / TW, t = n % TW;
-    halves_to_floats(raw[c][0], x[c][0]);
-    halves_to_floats(raw[c][1], x[c][1]);
-    if (!is_v && t < a.R / 16 && r < rows) {
-      Turns w;
-      twin_turns(a, b, (int)i0 + r, t, w);
-      turn_twin(a.pairs, w, x[c][0], x[c][1]);
+    for (int c = 0; c < CH; ++c) {
+      halves_to_floats(raw[c][0], x[c][0]);
+      halves_to_floats(raw[c][1], x[c][1]);
+    }
+    load(h + 1);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int n = tid + c * NT, r = n / TW, t = n % TW;
+      if constexpr (!KEEP) turns_of(c, turns[0]);
+      if (!is_v && t < a.R / 16 && r < rows) turn_twin(a.pairs, turns[KEEP ? c : 0], x[c][0], x[c][1]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, fmaxf(fabsf(x[c][0][e]), fabsf(x[c][1][e])));
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = fmaxf(top, fmaxf(fabsf(x[c][0][e]), fabsf(x[c][1][e])));
-  }
+    for (int off = 16; off > 0; off >>= 1)
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    if constexpr (NT > 32) {      // (two places in turn: one barrier a head)
+      float* at = red[h & 1];
+      if ((tid & 31) == 0) at[tid >> 5] = top;
+      __syncthreads();
+      top = at[0];
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1)
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  if constexpr (NT > 32) {
-    if ((tid & 31) == 0) red[tid >> 5] = top;
-    __syncthreads();
-    top = red[0];
+      for (int w = 1; w < NT / 32; ++w) top = fmaxf(top, at[w]);
+    }
+    float s;
+    if (s_old > 0.f) {
+      float shrink;
+      s = grown_scale<F8>(s_old, top, shrink);
+      if (shrink != 1.f) shrink_codes<F8>(codes, r0 * D, shrink, tid, NT);
+    } else {
+      s = __fdiv_rn(top, Codes<F8>::kMax);
+    }
+    // (every thread has read the old scale: by the barrier, or by the warp's reduction)
+    if (tid == 0) *scale = s;
+    // (products with a small sine may be far below what fp16 holds, where 1 / s has no fp32 value)
+    const bool tiny = s < 0x1p-100f;
+    const float inv = tiny ? 0.f : __frcp_rn(s);
 #pragma unroll
-    for (int w = 1; w < NT / 32; ++w) top = fmaxf(top, red[w]);
-  }
-  float s;
-  if (s_old > 0.f) {
-    float shrink;
-    s = grown_scale<F8>(s_old, top, shrink);
-    if (shrink != 1.f) shrink_codes<F8>(codes, r0 * D, shrink, tid, NT);
-  } else {
-    s = __fdiv_rn(top, Codes<F8>::kMax);
-  }
-  if (tid == 0) *scale = s;
-  // (products with a small sine may be far below what fp16 holds, where 1 / s has no fp32 value)
-  const bool tiny = s < 0x1p-100f;
-  const float inv = tiny ? 0.f : __frcp_rn(s);
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const int n = tid + c * NT, r = n / TW;
-    int px, py;
-    twin_pieces(n % TW, a.R, px, py);
-    if (r < rows) {
-      uint8_t* row = codes + (size_t)(r0 + r) * D;
-      *reinterpret_cast<uint2*>(row + 8 * px) =
-          s > 0.f ? quantize8<F8>(x[c][0], s, inv, tiny) : make_uint2(0, 0);
-      *reinterpret_cast<uint2*>(row + 8 * py) =
-          s > 0.f ? quantize8<F8>(x[c][1], s, inv, tiny) : make_uint2(0, 0);
+    for (int c = 0; c < CH; ++c) {
+      const int n = tid + c * NT, r = n / TW;
+      int px, py;
+      twin_pieces(n % TW, a.R, px, py);
+      if (r < rows) {
+        uint8_t* row = codes + (size_t)(r0 + r) * D;
+        *reinterpret_cast<uint2*>(row + 8 * px) =
+            s > 0.f ? quantize8<F8>(x[c][0], s, inv, tiny) : make_uint2(0, 0);
+        *reinterpret_cast<uint2*>(row + 8 * py) =
+            s > 0.f ? quantize8<F8>(x[c][1], s, inv, tiny) : make_uint2(0, 0);
+      }
     }
   }
+  if (bad) flag_error(p.err, INT8KV_DEVERR_LENGTH);
 }
 
 // ---- pools with a scale for each row --------------------------------------
-// A warp takes a (sequence, token, kv head), lane l values [l VPL, (l + 1) VPL) of K and V, as
-// the append kernel of these pools; a value's partner is in the lane R/2 values further.
+// int8 and fp16 stores: D / 16 lanes take a row, a twin each, for a.kv_heads heads in turn; a scale's
+// values are those of several pieces, whose largest magnitudes meet in shared memory.
+constexpr int kRowThreads = 256;
+
+// Eight codes under scale s (fp16's, as fp32); 1 / s and the products as in quantize8, but a scale
+// rounded to a subnormal leaves quotients beyond 127: saturated first.
+__device__ __forceinline__ uint2 quantize8_row(const float (&v)[8], float s, float inv) {
+  float y[8];
+  bool near = false;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    y[e] = fminf(fmaxf(v[e] * inv, -127.f), 127.f);
+    near |= fabsf(y[e] - ((y[e] + kRoundToInt) - kRoundToInt)) > 0.5f - 1.0e-4f;
+  }
+  if (near)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = fminf(fmaxf(__fdiv_rn(v[e], s), -127.f), 127.f);
+  return round_codes8<false>(y);
+}
+
+__device__ __forceinline__ float largest(const float (&x)[8]) {
+  float m = fabsf(x[0]);
+#pragma unroll
+  for (int e = 1; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
+  return m;
+}
+
+// A row's twin (px: x, py: y) into a store.  tops: the warp's places, D / 8 for this row; all lanes
+// of the warp take part.
+template <int D>
+__device__ __forceinline__ void store_twin(const PoolView& p, bool is_v, bool i8, size_t row, int px,
+                                           int py, const float (&x)[8], const float (&y)[8],
+                                           float* tops, bool there) {
+  char* store = (char*)(is_v ? p.v : p.k);
+  if (!i8) {
+    if (there) {
+      *reinterpret_cast<uint4*>(store + (row * D + 8 * px) * 2) =
+          make_uint4(ptx::pack_f16x2(x[0], x[1]), ptx::pack_f16x2(x[2], x[3]),
+                     ptx::pack_f16x2(x[4], x[5]), ptx::pack_f16x2(x[6], x[7]));
+      *reinterpret_cast<uint4*>(store + (row * D + 8 * py) * 2) =
+          make_uint4(ptx::pack_f16x2(y[0], y[1]), ptx::pack_f16x2(y[2], y[3]),
+                     ptx::pack_f16x2(y[4], y[5]), ptx::pack_f16x2(y[6], y[7]));
+    }
+    return;
+  }
+  uint16_t* scales = (uint16_t*)(is_v ? p.vs : p.ks) + row * p.ng;
+  float top[2] = {largest(x), largest(y)};
+  const int per = p.gs / 8;      // pieces of a scale: 2 or more
+  if (p.ng == 1) {
+    top[0] = fmaxf(top[0], top[1]);
+#pragma unroll
+    for (int off = D / 32; off > 0; off >>= 1)
+      top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], off));
+    top[1] = top[0];
+  } else {
+    __syncwarp();      // (the last row's have been read)
+    tops[px] = top[0];
+    tops[py] = top[1];
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float* from = tops + (k ? py : px) / per * per;
+      float m = 0.f;
+      for (int e = 0; e < per; e += 2) {
+        const float2 f = *reinterpret_cast<const float2*>(from + e);
+        m = fmaxf(m, fmaxf(f.x, f.y));
+      }
+      top[k] = m;
+    }
+  }
+  if (!there) return;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int piece = k ? py : px;
+    const __half s16 = __float2half_rn(__fdiv_rn(top[k], 127.f));
+    const float s = __half2float(s16);
+    *reinterpret_cast<uint2*>(store + row * D + 8 * piece) =
+        s > 0.f ? quantize8_row(k ? y : x, s, __frcp_rn(s)) : make_uint2(0, 0);
+    if (piece % per == 0) scales[piece / per] = __half_as_ushort(s16);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kRowThreads, 3)
+    rope_rows_kernel(const __grid_constant__ RopeArgs a, const PoolView p, bool k8, bool v8) {
+  constexpr int TW = D / 16;
+  __shared__ float tops[kRowThreads / TW][D / 8];
+  ptx::grid_dependency_wait();
+  ptx::grid_launch_dependents();
+  if (blockIdx.x >= a.append_blocks) {
+    rotate_queries<D>(a, (blockIdx.x - a.append_blocks) * kRowThreads + threadIdx.x);
+    return;
+  }
+  const int t = threadIdx.x % TW;
+  const unsigned n = blockIdx.x * (kRowThreads / TW) + threadIdx.x / TW;
+  const unsigned groups = (p.Hkv + a.kv_heads - 1) / a.kv_heads;
+  const unsigned tokens = (unsigned)a.n_seqs * a.n_new;
+  unsigned tok = n / groups;
+  const int h0 = n % groups * a.kv_heads;
+  bool there = tok < tokens;      // (a warp's lanes stay together)
+  if (!there) tok = 0;
+  const size_t b = tok / (unsigned)a.n_new;
+  const int i = tok % (unsigned)a.n_new;
+  there = there && i < tokens_of(a, b);
+  const int end = there ? min(p.Hkv, h0 + a.kv_heads) : 0;
+  const long long pos = (long long)__ldg(a.seq_pos + b) + i;
+  if (there && (pos < 0 || pos / p.ps >= a.max_pages)) {
+    if (t == 0) flag_error(p.err, INT8KV_DEVERR_LENGTH);
+    there = false;
+  }
+  int px, py;
+  twin_pieces(t, a.R, px, py);
+  const uint16_t* from_k = a.k + (size_t)tok * a.k_stride;
+  const uint16_t* from_v = a.v + (size_t)tok * a.v_stride;
+  uint4 raw[4] = {};
+  const auto load = [&](int h) {
+    if (there && h < end) {
+      raw[0] = ptx::ldg128(from_k + h * D + 8 * px);
+      raw[1] = ptx::ldg128(from_k + h * D + 8 * py);
+      raw[2] = ptx::ldg128(from_v + h * D + 8 * px);
+      raw[3] = ptx::ldg128(from_v + h * D + 8 * py);
+    }
+  };
+  load(h0);
+  const int page = there ? check_page(__ldg(a.page_table + b * a.max_pages + (int)(pos / p.ps)), p) : -1;
+  const bool turned = t < a.R / 16 && there;
+  Turns w;
+  bool bad = false;
+  if (turned) twin_turns(a, b, i, t, w, bad);
+  if (bad) flag_error(p.err, INT8KV_DEVERR_LENGTH);
+  there = there && page >= 0;
+  for (int k = 0; k < a.kv_heads; ++k) {
+    const int h = h0 + k;
+    float kx[8], ky[8], vx[8], vy[8];
+    halves_to_floats(raw[0], kx);
+    halves_to_floats(raw[1], ky);
+    halves_to_floats(raw[2], vx);
+    halves_to_floats(raw[3], vy);
+    load(h + 1);
+    if (turned) turn_twin(a.pairs, w, kx, ky);
+    const bool now = there && h < end;
+    const size_t row = now ? row_index(p, page, h, (int)(pos % p.ps)) : 0;
+    float* mine = tops[threadIdx.x / TW];
+    store_twin<D>(p, false, k8, row, px, py, kx, ky, mine, now);
+    store_twin<D>(p, true, v8, row, px, py, vx, vy, mine, now);
+  }
+}
+
+// Pools with a 4-bit store: a warp takes a (sequence, token), lane l values [l VPL, (l + 1) VPL) of K
+// and V, as their append kernel (whose transform runs over a whole row); a value's partner is in the
+// lane R/2 values further.
 template <int VPL>
-__device__ __forceinline__ void turn_row(const RopeArgs& a, size_t b, int tok, int lane,
-                                         float (&x)[VPL]) {
+__device__ __forceinline__ void row_turns(const RopeArgs& a, size_t b, int tok, int lane,
+                                          float (&c)[VPL], float (&s)[VPL], bool& bad) {
+  const int at = lane * VPL, half = a.R / 2;
+  if (at >= a.R) return;
+  if (a.pairs)
+    load_turns<VPL / 2>(a, b, tok, at / 2, c, s, bad);
+  else
+    load_turns<VPL>(a, b, tok, at >= half ? at - half : at, c, s, bad);
+}
+
+template <int VPL>
+__device__ __forceinline__ void turn_row(const RopeArgs& a, int lane, float (&x)[VPL],
+                                         const float (&c)[VPL], const float (&s)[VPL]) {
   const int at = lane * VPL, half = a.R / 2;
   if (a.pairs) {
     if (at < a.R) {
 #pragma unroll
-      for (int e = 0; e < VPL; e += 2) {
-        const int i = (at + e) / 2;
-        const float* row = table_row(a, b, tok, a.axes[i >> 2] >> (2 * (i & 3)) & 3);
-        if (row) turn(x[e], x[e + 1], __ldg(row + i), __ldg(row + half + i));
-      }
+      for (int e = 0; e < VPL; e += 2) turn(x[e], x[e + 1], c[e / 2], s[e / 2]);
     }
     return;
   }
@@ -330,15 +530,21 @@ __device__ __forceinline__ void turn_row(const RopeArgs& a, size_t b, int tok, i
   for (int e = 0; e < VPL; ++e) {
     float mine = x[e], other = __shfl_sync(0xffffffffu, x[e], partner);
     if (at < a.R) {
-      const int i = (second ? at - half : at) + e;
-      const float* row = table_row(a, b, tok, a.axes[i >> 2] >> (2 * (i & 3)) & 3);
-      if (row) {
-        float& first = second ? other : mine;
-        float& last = second ? mine : other;
-        turn(first, last, __ldg(row + i), __ldg(row + half + i));
-        x[e] = mine;
-      }
+      if (second) turn(other, mine, c[e], s[e]);
+      else turn(mine, other, c[e], s[e]);
+      x[e] = mine;
     }
+  }
+}
+
+template <int VPL>
+__device__ __forceinline__ void halves_of(const typename Vec<VPL>::H& raw, float (&x)[VPL]) {
+  const __half2* h = reinterpret_cast<const __half2*>(&raw);
+#pragma unroll
+  for (int e = 0; e < VPL / 2; ++e) {
+    const float2 f = __half22float2(h[e]);
+    x[2 * e] = f.x;
+    x[2 * e + 1] = f.y;
   }
 }
 
@@ -374,18 +580,19 @@ __device__ __forceinline__ void store_row(const PoolView& p, bool is_v, bool i8,
 constexpr int kRowWarps = 8;
 template <int VPL>
 __global__ void __launch_bounds__(kRowWarps * 32)
-    rope_rows_kernel(const __grid_constant__ RopeArgs a, const PoolView p, bool k8, bool v8,
-                     float norm) {
+    rope_q4_kernel(const __grid_constant__ RopeArgs a, const PoolView p, bool k8, bool v8,
+                   float norm) {
   ptx::grid_dependency_wait();
   ptx::grid_launch_dependents();
   if (blockIdx.x >= a.append_blocks) {
     rotate_queries<32 * VPL>(a, (blockIdx.x - a.append_blocks) * (kRowWarps * 32) + threadIdx.x);
     return;
   }
+  // a warp: one token, a.kv_heads heads, whose turns are the same
   const int lane = threadIdx.x & 31;
   const unsigned n = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-  const unsigned tok = n / (unsigned)p.Hkv;
-  const int kvh = n % (unsigned)p.Hkv;
+  const unsigned groups = (p.Hkv + a.kv_heads - 1) / a.kv_heads, tok = n / groups;
+  const int h0 = n % groups * a.kv_heads, end = min(p.Hkv, h0 + a.kv_heads);
   const size_t b = tok / (unsigned)a.n_new;
   const int i = tok % (unsigned)a.n_new;
   if (b >= (size_t)a.n_seqs || i >= tokens_of(a, b)) return;
@@ -394,15 +601,43 @@ __global__ void __launch_bounds__(kRowWarps * 32)
     if (lane == 0) flag_error(p.err, INT8KV_DEVERR_LENGTH);
     return;
   }
-  float k[VPL], v[VPL];
-  load_halves<VPL>(a.k + (size_t)tok * a.k_stride + kvh * p.D + lane * VPL, k);
-  load_halves<VPL>(a.v + (size_t)tok * a.v_stride + kvh * p.D + lane * VPL, v);
+  const uint16_t* from_k = a.k + (size_t)tok * a.k_stride + lane * VPL;
+  const uint16_t* from_v = a.v + (size_t)tok * a.v_stride + lane * VPL;
+  using H = typename Vec<VPL>::H;
+  constexpr int N = 2;      // heads under way
+  H next_k[N], next_v[N];
+  const auto load = [&](int h) {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (h + e < end) {
+        next_k[e] = __ldg(reinterpret_cast<const H*>(from_k + (h + e) * p.D));
+        next_v[e] = __ldg(reinterpret_cast<const H*>(from_v + (h + e) * p.D));
+      }
+  };
+  load(h0);
   const int page = check_page(__ldg(a.page_table + b * a.max_pages + (int)(pos / p.ps)), p);
+  float c[VPL], s[VPL];
+  bool bad = false;
+  row_turns<VPL>(a, b, i, lane, c, s, bad);
+  if (bad) flag_error(p.err, INT8KV_DEVERR_LENGTH);
   if (page < 0) return;
-  turn_row<VPL>(a, b, i, lane, k);
-  const size_t row = row_index(p, page, kvh, (int)(pos % p.ps));
-  store_row<VPL>(p, false, k8, p.k4, row, k, lane, norm);
-  store_row<VPL>(p, true, v8, p.v4, row, v, lane, norm);
+  for (int h = h0; h < end; h += N) {
+    float k[N][VPL], v[N][VPL];
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      halves_of<VPL>(next_k[e], k[e]);
+      halves_of<VPL>(next_v[e], v[e]);
+    }
+    load(h + N);
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (h + e < end) {
+        turn_row<VPL>(a, lane, k[e], c, s);
+        const size_t row = row_index(p, page, h + e, (int)(pos % p.ps));
+        store_row<VPL>(p, false, k8, p.k4, row, k[e], lane, norm);
+        store_row<VPL>(p, true, v8, p.v4, row, v[e], lane, norm);
+      }
+  }
 }
 
 // ---- launches ------------------------------------------------------------
@@ -414,6 +649,14 @@ unsigned query_blocks(RopeArgs& a, int D, int threads, int sms) {
   const long long twins = (long long)a.n_seqs * a.n_new * (D / 16);
   while (a.heads < 8 && twins * ((a.H + 2 * a.heads - 1) / (2 * a.heads)) >= 512LL * sms) a.heads *= 2;
   return (unsigned)((twins * ((a.H + a.heads - 1) / a.heads) + threads - 1) / threads);
+}
+
+// Heads that a group of threads takes in turn, of `threads` that one head wants: up to eight, while
+// there are two blocks' threads for every SM.
+int heads_of_a_group(long long threads, int heads, int sms) {
+  int n = 1;
+  while (n < 8 && n < heads && threads * ((heads + 2 * n - 1) / (2 * n)) >= 1024LL * sms) n *= 2;
+  return n;
 }
 
 struct RopeLaunch {
@@ -443,7 +686,9 @@ cudaError_t launch_blocks(const RopeLaunch& c) {
   const BlockView p = block_view(c.pool, c.layer);
   const int T = 1 << p.t_log2;
   const int nb = (int)(((long long)c.a.n_new + T - 2) / T + 1);   // blocks that n_new tokens may touch
-  const long long units = (long long)c.a.n_seqs * nb * p.Hkv * 2;
+  const long long blocks = (long long)c.a.n_seqs * nb * 2;
+  c.a.kv_heads = heads_of_a_group(blocks * NT, p.Hkv, c.pool->num_sms);
+  const long long units = blocks * ((p.Hkv + c.a.kv_heads - 1) / c.a.kv_heads);
   if (units > 0x3fffff00LL) return cudaErrorNotSupported;
   c.a.append_blocks = (unsigned)((units + GROUPS - 1) / GROUPS);
   const unsigned q = query_blocks(c.a, D, NT * GROUPS, c.pool->num_sms);
@@ -457,26 +702,34 @@ cudaError_t dispatch_blocks(const RopeLaunch& c) {
   const int twins = (c.a.n_new < T ? c.a.n_new : T) * (D / 16);   // most new twins of a block
   if (twins <= 32) return launch_blocks<D, F8, 32, 4, 1>(c);
   if (twins <= 64) return launch_blocks<D, F8, 32, 4, 2>(c);
-  if (twins <= 128) return launch_blocks<D, F8, 32, 4, 4>(c);
-  if (twins <= 256) return launch_blocks<D, F8, 64, 1, 4>(c);
-  if (twins <= 512) return launch_blocks<D, F8, 128, 1, 4>(c);
+  if (twins <= 128) return launch_blocks<D, F8, 64, 1, 2>(c);
+  if (twins <= 256) return launch_blocks<D, F8, 128, 1, 2>(c);
+  if (twins <= 512) return launch_blocks<D, F8, 256, 1, 2>(c);
   if constexpr (D >= 128)
-    if (twins <= 1024) return launch_blocks<D, F8, 256, 1, 4>(c);
+    if (twins <= 1024) return launch_blocks<D, F8, 512, 1, 2>(c);
   if constexpr (D >= 256)
     if (twins <= 2048) return launch_blocks<D, F8, 512, 1, 4>(c);
   return cudaErrorNotSupported;
 }
 
-template <int VPL>
+template <int D>
 cudaError_t launch_rows(const RopeLaunch& c) {
   const PoolView p = layer_view(c.pool, c.layer);
-  const long long rows = (long long)c.a.n_seqs * c.a.n_new * p.Hkv;
+  const bool q4 = p.k4 || p.v4;
+  const int threads = q4 ? kRowWarps * 32 : kRowThreads, lanes = q4 ? 32 : D / 16;
+  const long long tokens = (long long)c.a.n_seqs * c.a.n_new;
+  c.a.kv_heads = heads_of_a_group(tokens * lanes, p.Hkv, c.pool->num_sms);
+  const long long rows = tokens * ((p.Hkv + c.a.kv_heads - 1) / c.a.kv_heads);
   if (rows > 0x3fffff00LL) return cudaErrorNotSupported;
-  c.a.append_blocks = (unsigned)((rows + kRowWarps - 1) / kRowWarps);
-  const unsigned q = query_blocks(c.a, 32 * VPL, kRowWarps * 32, c.pool->num_sms);
-  return launch_early(rope_rows_kernel<VPL>, c.a.append_blocks + q, kRowWarps * 32, c.stream,
-                      (const RopeArgs)c.a, p, c.pool->k_int8, c.pool->v_int8,
-                      (float)(1.0 / std::sqrt((double)p.D)));
+  const int per = threads / lanes;
+  c.a.append_blocks = (unsigned)((rows + per - 1) / per);
+  const unsigned q = query_blocks(c.a, D, threads, c.pool->num_sms);
+  if (q4)
+    return launch_early(rope_q4_kernel<D / 32>, c.a.append_blocks + q, threads, c.stream,
+                        (const RopeArgs)c.a, p, c.pool->k_int8, c.pool->v_int8,
+                        (float)(1.0 / std::sqrt((double)D)));
+  return launch_early(rope_rows_kernel<D>, c.a.append_blocks + q, threads, c.stream,
+                      (const RopeArgs)c.a, p, c.pool->k_int8, c.pool->v_int8);
 }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
@@ -549,7 +802,7 @@ extern "C" int kv_rope_append(const int8kv_pool* pool, int layer, const uint16_t
         : D == 128 ? f8 ? dispatch_blocks<128, true>(c) : dispatch_blocks<128, false>(c)
                    : f8 ? dispatch_blocks<256, true>(c) : dispatch_blocks<256, false>(c);
   } else {
-    e = D == 64 ? launch_rows<2>(c) : D == 128 ? launch_rows<4>(c) : launch_rows<8>(c);
+    e = D == 64 ? launch_rows<64>(c) : D == 128 ? launch_rows<128>(c) : launch_rows<256>(c);
   }
   if (e == cudaErrorNotSupported) return INT8KV_ERR_UNSUPPORTED;
   return e == cudaSuccess ? INT8KV_OK : INT8KV_ERR_CUDA;

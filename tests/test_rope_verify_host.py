@@ -83,37 +83,49 @@ class _Pool:
 def test_the_binding_refuses(L):
     i, f = torch.zeros(4, dtype=torch.int32), torch.zeros(4)
     k = torch.zeros((1, 4, 2, 64), dtype=torch.float16)
-    with pytest.raises(ValueError, match="k_new and v_new must have shape"):
-        b.kv_rope_append(_Pool(), 0, k, k[:, :2], i[:1], i.view(1, 4), f)
+    with pytest.raises(ValueError, match="k_new must have shape"):
+        b.kv_rope_append(_Pool(), 0, k[0], k[0], i[:1], i.view(1, 4), f.view(1, 4))
     with pytest.raises(ValueError, match="CUDA"):
-        b.kv_rope_append(_Pool(), 0, k, k, i[:1], i.view(1, 4), f)
+        b.kv_rope_append(_Pool(), 0, k, k, i[:1], i.view(1, 4), f.view(1, 4))
     with pytest.raises(ValueError, match="CUDA"):
         b.kv_verify_drafts(f.view(1, 2, 2), i[:1].view(1, 1), f[:1].view(1, 1), f[:1],
                            i[:2].view(1, 2), i[:1])
 
 
-def test_token_and_row_strides(monkeypatch):
-    """What counts as evenly apart (addresses are not looked at here)."""
-    real = torch.Tensor.is_cuda
-    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True))
-    try:
-        wide = torch.zeros((3, 5, 12, 64), dtype=torch.float16)
-        assert b._token_rows(wide[:, :, 2:4], 2, 64, "k")[1] == 12 * 64
-        assert b._token_rows(wide[:, :1, :2], 2, 64, "k")[1] == 5 * 12 * 64
-        assert b._token_rows(wide[:1, 1:4, :2], 2, 64, "k")[1] == 12 * 64
-        assert b._token_rows(wide[:1, :1, :2], 2, 64, "k")[1] == 128
+def test_token_and_row_strides():
+    """What counts as evenly apart (on the host's device, -1; addresses are not looked at here)."""
+    def tokens(t, heads=2, device=-1):
+        return b._token_rows(t, (*t.shape[:2], heads, 64), device, "k")[1]
+
+    def rows(t, *shape, device=-1):
+        return b._prob_rows(t, shape, device, "p")[1]
+    wide = torch.zeros((3, 5, 12, 64), dtype=torch.float16)
+    assert tokens(wide[:, :, 2:4]) == 12 * 64
+    assert tokens(wide[:, :1, :2]) == 5 * 12 * 64
+    assert tokens(wide[:1, 1:4, :2]) == 12 * 64
+    assert tokens(wide[:1, :1, :2]) == 128
+    assert tokens(wide, 12) == 12 * 64 and tokens(wide[:, :0, :2]) == 128
+    for t in (wide[:, :3, :2], wide.transpose(0, 1)[:, :, :2], wide[:, :, ::2][:, :, :2]):
         with pytest.raises(ValueError, match="evenly"):
-            b._token_rows(wide[:, :3, :2], 2, 64, "k")
-        with pytest.raises(ValueError, match="evenly"):
-            b._token_rows(wide.transpose(0, 1)[:, :, :2], 2, 64, "k")
-        with pytest.raises(ValueError, match="evenly"):
-            b._token_rows(wide[:, :, ::2][:, :, :2], 2, 64, "k")
-        with pytest.raises(ValueError, match="shape"):
-            b._token_rows(wide, 2, 64, "k")
-        p = torch.zeros((2, 4, 40))
-        assert b._prob_rows(p[..., :33], (2, 4, 33), "p")[1] == 40
-        assert b._prob_rows(p[:, :1, :33], (2, 1, 33), "p")[1] == 160
-        with pytest.raises(ValueError, match="evenly"):
-            b._prob_rows(p[:, :3], (2, 3, 40), "p")
-    finally:
-        monkeypatch.setattr(torch.Tensor, "is_cuda", real)
+            tokens(t)
+    p = torch.zeros((2, 4, 40))
+    assert rows(p[..., :33], 2, 4, 33) == 40 and rows(p[:, :1, :33], 2, 1, 33) == 160
+    assert rows(p, 2, 4, 40) == 40 and rows(p[:, :0], 2, 0, 40) == 40
+    with pytest.raises(ValueError, match="evenly"):
+        rows(p[:, :3], 2, 3, 40)
+    for call in (lambda: tokens(wide, device=0), lambda: rows(p, 2, 4, 40, device=0)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    for call in (lambda: b._token_rows(None, (1, 1, 1, 64), 0, "k"),
+                 lambda: b._prob_rows([1.0], (1, 1, 1), 0, "p"),
+                 lambda: b._ptr(3, torch.int32, (1,), 0, "n")):
+        with pytest.raises(TypeError, match="torch tensor"):
+            call()
+
+
+def test_one_test_where_all_is_well():
+    i = torch.zeros((2, 6), dtype=torch.int32)
+    assert b._ptr(i, torch.int32, (2, 6), -1, "i") == i.data_ptr()
+    for t, dtype in ((i, torch.float32), (i[:, ::2], torch.int32), (i, torch.int32)):
+        with pytest.raises(ValueError, match="i must be on a CUDA device"):
+            b._ptr(t, dtype, (3, 6) if t is i else (2, 3), -1, "i")
