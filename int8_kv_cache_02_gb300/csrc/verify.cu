@@ -11,9 +11,11 @@
 //
 // One cluster of kCluster blocks per sequence.  Each finds r by itself (three short dependent
 // loads), sums its slice of the row (or of the two), a run of consecutive values for each
-// warp, and reads the others' sums from their shared memory.  The warp whose run holds the place looks
-// it up there; its values come from L2 the second time.  So a row is read once and nothing
-// is written but the results.
+// warp, and writes its sum to the others' shared memory.  The warp whose run holds the place looks it
+// up there: 32 equal parts of the run, then 32 of the part, their values from L2.  So a row is
+// read once and nothing is written but the results.
+#include <utility>
+
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -23,7 +25,7 @@ namespace int8kv {
 namespace {
 
 constexpr int kCluster = 8;
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
 struct VerifyArgs {
@@ -41,58 +43,108 @@ struct VerifyArgs {
   int n_draft, vocab;
 };
 
+using u64 = unsigned long long;
+
 // A probability in units of 2^-60, rounded down; outside [0, 1] the nearest of the two, NaN 0.
-__device__ __forceinline__ unsigned long long fixed60(float p) {
-  const uint32_t b = __float_as_uint(fminf(fmaxf(p, 0.f), 1.f));
-  // 24 bits of mantissa at the top of 61, down by the exponent (a subnormal is below 2^-60)
-  const unsigned long long m = (unsigned long long)((b & 0x7fffffu) | 0x800000u) << 37;
-  return m >> min(127 - (int)(b >> 23), 63);
+__device__ __forceinline__ u64 fixed60(float p) {
+  const uint32_t b = __float_as_uint(__saturatef(p));
+  // 24 bits of mantissa at the top of 61, down by the exponent: a shift of 64 and more leaves 0 in
+  // PTX (a subnormal value is below 2^-60)
+  const u64 m = (u64)((b << 5 & 0x0fffffe0u) | 0x10000000u) << 32;
+  u64 w;
+  asm("shr.u64 %0, %1, %2;" : "=l"(w) : "l"(m), "r"(127u - (b >> 23)));
+  return w;
 }
 
-// The weight of a value: what the draft's probability leaves of the target's.
+// The weights of a row: what the draft's probabilities leave of the target's.
 struct Row {
   const float *p, *q;      // q null: p alone
   int without;             // this value's weight is 0 (a draft without probabilities); or -1
-  __device__ __forceinline__ unsigned long long weight(int v, float pv, float qv) const {
-    unsigned long long w = fixed60(pv);
-    if (q) {
-      const unsigned long long o = fixed60(qv);
-      w = w > o ? w - o : 0;
-    }
-    return v == without ? 0 : w;
-  }
 };
+template <bool TWO>
+__device__ __forceinline__ u64 weight(float p, float q) {
+  if constexpr (!TWO) return fixed60(p);
+  const u64 w = fixed60(p) - fixed60(q);
+  return (long long)w > 0 ? w : 0;      // (both are at most 2^60)
+}
 
-__device__ __forceinline__ unsigned long long warp_sum64(unsigned long long x) {
+__device__ __forceinline__ u64 warp_sum64(u64 x) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
   return x;
 }
 
-// The sum of a lane's weights of values [a, z), a warp's lanes 4 bytes apart, 32 * K at a time.
-template <bool TWO>
-__device__ __forceinline__ unsigned long long sum_run(const Row& r, int a, int z, int lane) {
-  constexpr int K = 8;
-  unsigned long long sum = 0;
-  for (int v0 = a + lane; v0 < z; v0 += 32 * K) {
-    float p[K], q[K];
+// The sum of the weights of values [a, z) that fall to a lane of `lanes`, each taking VEC together.
+template <bool TWO, int VEC>
+__device__ __forceinline__ u64 sum_lane(const Row& r, int a, int z, int lane, int lanes) {
+  constexpr int K = VEC == 4 ? 4 : 8;
+  const int step = lanes * VEC;
+  u64 sum = 0;
+  for (int v0 = a + lane * VEC; v0 < z; v0 += step * K) {
+    float p[K][VEC], q[K][VEC];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int v = v0 + 32 * k;
-      p[k] = v < z ? __ldg(r.p + v) : 0.f;
-      q[k] = TWO && v < z ? __ldg(r.q + v) : 0.f;
+      const int v = v0 + step * k;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) p[k][e] = q[k][e] = 0.f;
+      if (v < z) {      // (VEC 4: z and the rows are multiples of 4)
+        if constexpr (VEC == 4) {
+          const float4 x = __ldg(reinterpret_cast<const float4*>(r.p + v));
+          p[k][0] = x.x, p[k][1] = x.y, p[k][2] = x.z, p[k][3] = x.w;
+          if constexpr (TWO) {
+            const float4 y = __ldg(reinterpret_cast<const float4*>(r.q + v));
+            q[k][0] = y.x, q[k][1] = y.y, q[k][2] = y.z, q[k][3] = y.w;
+          }
+        } else {
+          p[k][0] = __ldg(r.p + v);
+          if constexpr (TWO) q[k][0] = __ldg(r.q + v);
+        }
+      }
     }
 #pragma unroll
-    for (int k = 0; k < K; ++k) sum += r.weight(v0 + 32 * k, p[k], q[k]);
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) sum += weight<TWO>(p[k][e], q[k][e]);
   }
   return sum;
 }
 
+// The weight that the sum of [a, z) has too much: that of `without`, if it is among them.
+__device__ __forceinline__ u64 left_out(const Row& r, int a, int z) {
+  return r.without >= a && r.without < z ? fixed60(__ldg(r.p + r.without)) : 0;
+}
+
+// The place-th unit of the weights of [a, z) (fewer than they sum to) is this value's; a warp together.
+template <bool TWO, int VEC>
+__device__ __forceinline__ int look_up(const Row& r, int a, int z, u64 place, int lane) {
+  for (;;) {
+    const bool last = z - a <= 32;      // (else a part is a multiple of VEC)
+    const int per = last ? 1 : ((z - a + 31) / 32 + VEC - 1) / VEC * VEC;
+    const int from = min(z, a + lane * per), to = min(z, from + per);
+    u64 inc = (last ? sum_lane<TWO, 1>(r, from, to, 0, 1) : sum_lane<TWO, VEC>(r, from, to, 0, 1)) -
+              left_out(r, from, to);
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const u64 o = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += o;
+    }
+    const int at = __ffs(__ballot_sync(0xffffffffu, inc > place)) - 1;
+    const u64 before = __shfl_sync(0xffffffffu, inc, at ? at - 1 : 0);
+    if (at > 0) place -= before;
+    a = a + at * per;
+    z = min(z, a + per);
+    if (last) return a;
+  }
+}
+
+// VEC: rows are read 16 bytes at a time, where every row begins at such a boundary.
+template <int VEC>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     verify_kernel(const VerifyArgs a) {
   namespace cg = cooperative_groups;
-  __shared__ unsigned long long runs[kWarps], total_s;
+  __shared__ u64 runs[kWarps], totals[2][kCluster];
   const cg::cluster_group cluster = cg::this_cluster();
+  auto started = cluster.barrier_arrive();      // (all blocks run before one writes to another)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = blockIdx.x % kCluster;
   const size_t b = blockIdx.x / kCluster;
@@ -108,11 +160,12 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     bool refused = false;
     if (i < count) {
       const int x = __ldg(a.x + b * a.n_draft + i);
+      const float u = __ldg(a.u + b * a.n_draft + i);
       refused = true;
       if (x >= 0 && x < a.vocab) {
         const float p = __ldg(a.target + (b * (a.n_draft + 1) + i) * a.target_stride + x);
         const float q = a.draft ? __ldg(a.draft + (b * a.n_draft + i) * a.draft_stride + x) : 1.f;
-        refused = !((double)__ldg(a.u + b * a.n_draft + i) * (double)q < (double)p);
+        refused = !((double)u * (double)q < (double)p);
       }
     }
     const unsigned any = __ballot_sync(0xffffffffu, refused);
@@ -130,64 +183,53 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
       if (a.seq_lens_out) a.seq_lens_out[b] = a.seq_lens[b] - (max(count, 0) - taken);
     }
   }
-  if (given < 0) return;      // (the cluster's blocks all do)
-
+  const float sample = __ldg(a.sample_u + b);
   const bool refused = taken < count;
   Row row;
   row.p = a.target + (b * (a.n_draft + 1) + taken) * a.target_stride;
   row.q = refused && a.draft ? a.draft + (b * a.n_draft + taken) * a.draft_stride : nullptr;
   row.without = refused && !a.draft ? __ldg(a.x + b * a.n_draft + taken) : -1;
   // runs of consecutive values: warp `rank * kWarps + warp` has [from, to)
-  const int per = ((a.vocab + kCluster * kWarps - 1) / (kCluster * kWarps) + 31) & ~31;
-  const int from = (int)min((long long)a.vocab, (long long)(rank * kWarps + warp) * per);
-  const int to = min(a.vocab, from + per);
-  unsigned long long total = 0, before = 0, mine = 0;
+  const int per = (int)(((long long)a.vocab + kCluster * kWarps - 1) / (kCluster * kWarps) + 31) & ~31;
+  const int from = given < 0 ? 0 : (int)min((long long)a.vocab, (long long)(rank * kWarps + warp) * per);
+  const int to = given < 0 ? 0 : min(a.vocab, from + per);
+  u64 total = 0, before = 0, mine = 0;
+  cluster.barrier_wait(std::move(started));
   for (int round = 0; round < 2; ++round) {
-    mine = warp_sum64(row.q ? sum_run<true>(row, from, to, lane) : sum_run<false>(row, from, to, lane));
+    mine = warp_sum64(row.q ? sum_lane<true, VEC>(row, from, to, lane, 32)
+                            : sum_lane<false, VEC>(row, from, to, lane, 32)) -
+           left_out(row, from, to);
     if (lane == 0) runs[warp] = mine;
     __syncthreads();
-    if (threadIdx.x == 0) {
-      unsigned long long t = 0;
-      for (int w = 0; w < kWarps; ++w) t += runs[w];
-      total_s = t;
+    if (warp == 0) {
+      const u64 t = warp_sum64(lane < kWarps ? runs[lane] : 0);
+      if (lane < kCluster) *cluster.map_shared_rank(&totals[round][rank], lane) = t;
     }
     cluster.sync();
     total = before = 0;
+#pragma unroll
     for (int k = 0; k < kCluster; ++k) {
-      const unsigned long long t = *cluster.map_shared_rank(&total_s, k);
+      const u64 t = totals[round][k];
       before += k < rank ? t : 0;
       total += t;
     }
-    cluster.sync();      // (others' sums have been read)
     if (total || !(row.q || row.without >= 0)) break;
     row.q = nullptr;      // nothing is left of the target's: its own probabilities
     row.without = -1;
   }
-  if (total == 0) {
-    if (rank == 0 && threadIdx.x == 0) a.tokens[b * (a.n_draft + 1) + taken] = -1;
+  if (total == 0) {      // (or a sequence that takes no part, whose tokens are there)
+    if (given >= 0 && rank == 0 && threadIdx.x == 0) a.tokens[b * (a.n_draft + 1) + taken] = -1;
     return;
   }
   // u in units of 2^-64; the place is the first whose sum is above u * total
-  const unsigned long long u64 = fixed60(fminf(fmaxf(__ldg(a.sample_u + b), 0.f), 0x1.fffffep-1f)) << 4;
-  const unsigned long long place = __umul64hi(u64, total);
-  for (int w = 0; w < warp; ++w) before += runs[w];
-  if (place < before || place - before >= mine) return;
-  for (int v0 = from; v0 < to; v0 += 32) {
-    const int v = v0 + lane;
-    unsigned long long inc =
-        v < to ? row.weight(v, __ldg(row.p + v), row.q ? __ldg(row.q + v) : 0.f) : 0;
+  const u64 u = fixed60(fminf(fmaxf(sample, 0.f), 0x1.fffffep-1f)) << 4;
+  const u64 place = __umul64hi(u, total);
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const unsigned long long o = __shfl_up_sync(0xffffffffu, inc, off);
-      if (lane >= off) inc += o;
-    }
-    const unsigned above = __ballot_sync(0xffffffffu, before + inc > place);
-    if (above) {
-      if (lane == 0) a.tokens[b * (a.n_draft + 1) + taken] = v0 + __ffs(above) - 1;
-      return;
-    }
-    before += __shfl_sync(0xffffffffu, inc, 31);
-  }
+  for (int w = 0; w < kWarps; ++w) before += w < warp ? runs[w] : 0;
+  if (place < before || place - before >= mine) return;
+  const int token = row.q ? look_up<true, VEC>(row, from, to, place - before, lane)
+                          : look_up<false, VEC>(row, from, to, place - before, lane);
+  if (lane == 0) a.tokens[b * (a.n_draft + 1) + taken] = token;
 }
 
 }  // namespace
@@ -233,5 +275,12 @@ extern "C" int kv_verify_drafts(int batch, int n_draft, int vocab, const float* 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, verify_kernel, a) == cudaSuccess ? INT8KV_OK : INT8KV_ERR_CUDA;
+  const auto fits = [&](const float* p, long long stride) {
+    return ((uintptr_t)p & 15u) == 0 && stride % 4 == 0;
+  };
+  const bool vec = vocab % 4 == 0 && fits(target_probs, target_stride) &&
+                   (!draft_probs || fits(draft_probs, draft_stride));
+  const cudaError_t e = vec ? cudaLaunchKernelEx(&cfg, verify_kernel<4>, a)
+                            : cudaLaunchKernelEx(&cfg, verify_kernel<1>, a);
+  return e == cudaSuccess ? INT8KV_OK : INT8KV_ERR_CUDA;
 }
