@@ -511,14 +511,23 @@ int attn_decode_int8_noalloc(const int8kv_pool* pool, int layer, const uint16_t*
  *   seq_lens, seq_lens_out  device int32 [batch], both or neither: seq_lens_out[b] = seq_lens[b] less
  *                 the drafts that were not taken, for a cache that holds the whole window (it may be
  *                 seq_lens; kv_pages_resize takes the pages back).
- * Probabilities outside [0, 1] count as the nearest of the two, NaN as 0; below 2^-37 they are cut
- * to multiples of 2^-60.  n_draft may be 0: plain sampling.
+ * Probabilities outside [0, 1] count as the nearest of the two, NaN as 0; below 2^-37 they are
+ * rounded to multiples of 2^-60.  A row of the target sums to less than 16 (else the token is some
+ * value of the vocabulary, or -1).  n_draft may be 0: plain sampling.
  * Errors: NULL_PTR, INVALID_ARG (vocab beyond 2^30, too), UNSUPPORTED (a batch of 2^28 and more), CUDA. */
 int kv_verify_drafts(int batch, int n_draft, int vocab, const float* target_probs,
                      long long target_stride, const float* draft_probs, long long draft_stride,
                      const int32_t* draft_tokens, const int32_t* n_drafts, const float* accept_u,
                      const float* sample_u, int32_t* tokens, int32_t* n_accepted,
                      const int32_t* seq_lens, int32_t* seq_lens_out, void* stream);
+
+/* The calls above that a decoding step makes, with their arguments in order as one host array of
+ * 64-bit words (integers sign-extended, pointers, a float as the bits of a double; `stream` last): for
+ * callers to whom every argument is a cost of its own.  The same checks, results and errors. */
+int kv_rope_append_packed(const int64_t* words);                  /* 24 */
+int attn_decode_scored_int8_packed(const int64_t* words);         /* 19 */
+int attn_prefill_chunk_scored_int8_packed(const int64_t* words);  /* 18 */
+int kv_verify_drafts_packed(const int64_t* words);                /* 16 */
 
 /* ---- saved pool images ------------------------------------------------
  * The used positions 0 .. L_b - 1 of each sequence, every layer, with the int8

@@ -11,6 +11,7 @@ device regions (allocated with torch, which only provides memory).
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -39,6 +40,10 @@ _SIGS = {
     "kv_rope_append": (_c_int, [_vp, _c_int, _vp, _vp, _vp, _c_ll, _c_ll, _c_ll, _c_int, _c_int,
                                 _c_int, _vp, _vp, _vp, _c_int, _c_int, _c_int, _vp, _c_int, _vp,
                                 _vp, _vp, _c_int, _vp]),
+    "kv_rope_append_packed": (_c_int, [ctypes.c_char_p]),
+    "attn_decode_scored_int8_packed": (_c_int, [ctypes.c_char_p]),
+    "attn_prefill_chunk_scored_int8_packed": (_c_int, [ctypes.c_char_p]),
+    "kv_verify_drafts_packed": (_c_int, [ctypes.c_char_p]),
     "kv_verify_drafts": (_c_int, [_c_int, _c_int, _c_int, _vp, _c_ll, _vp, _c_ll, _vp, _vp, _vp,
                                   _vp, _vp, _vp, _vp, _vp, _vp]),
     "attn_decode_scored_int8": (_c_int, [_vp, _c_int, _vp, _c_int, _c_int, _c_int, _vp, _vp, _c_int,
@@ -79,6 +84,12 @@ _SIGS = {
 }
 
 _lib = None
+
+# Arguments of the packed calls as 64-bit words (ctypes takes 70 ns and more for each of its own).
+_pack_rope = struct.Struct("24q").pack
+_pack_decode = struct.Struct("10q2d7q").pack
+_pack_chunk = struct.Struct("9q2d7q").pack
+_pack_verify = struct.Struct("16q").pack
 
 
 class Int8KVError(RuntimeError):
@@ -191,6 +202,11 @@ def kv_quant_append(pool, layer, k_new, v_new, seq_pos, page_table, stream=None)
                                  page_table.shape[1], _stream(stream)), "kv_quant_append")
 
 
+def _handle(pool):
+    h = pool.handle
+    return (h.value or 0) if h is not None else 0
+
+
 def _ptr(t, dtype, shape, device, name):
     """The address of a contiguous tensor of this dtype and shape on a device: one test where all is
     well (a step's calls are short next to their checks), and what is wrong where it is not."""
@@ -251,8 +267,7 @@ def kv_rope_append(pool, layer, k_new, v_new, seq_pos, page_table, rope_table, q
     shape = (n_seqs, n_new, pool.n_kv_heads, pool.head_dim)
     k, ks = _token_rows(k_new, shape, dev, "k_new")
     v, vs = _token_rows(v_new, shape, dev, "v_new")
-    qp = qo = axis = at = lens = None
-    n_heads = qs = 0
+    qp = qo = axis = at = lens = n_heads = qs = 0
     if q is not None:
         if q.dim() != 4:
             raise ValueError("q must have shape [n_seqs][n_new][n_heads][head_dim]")
@@ -278,13 +293,13 @@ def kv_rope_append(pool, layer, k_new, v_new, seq_pos, page_table, rope_table, q
     if new_lens is not None:
         lens = _ptr(new_lens, i32, (n_seqs,), dev, "new_lens")
     max_pages = page_table.shape[1]
-    _check((_lib or lib()).kv_rope_append(
-        pool.handle, layer, qp, k, v, qs, ks, vs, n_seqs, n_new, n_heads,
+    _check((_lib or lib()).kv_rope_append_packed(_pack_rope(
+        _handle(pool), layer, qp, k, v, qs, ks, vs, n_seqs, n_new, n_heads,
         _ptr(seq_pos, i32, (n_seqs,), dev, "seq_pos"), lens,
         _ptr(rope_table, torch.float32, (n_table, dim), dev, "rope_table"), n_table, dim,
         ROPE_STYLES[style], at, n_axes, axis, qo,
         _ptr(page_table, i32, (n_seqs, max_pages), dev, "page_table"), max_pages,
-        _stream(stream)), "kv_rope_append")
+        _stream(stream))), "kv_rope_append")
 
 
 def _prob_rows(t, shape, device, name):
@@ -337,17 +352,17 @@ def kv_verify_drafts(target_probs, draft_tokens, accept_u, sample_u, tokens, n_a
     one = (batch,)
     p, ps = _prob_rows(target_probs, (batch, n + 1, vocab), dev, "target_probs")
     q, qs = (_prob_rows(draft_probs, (batch, n, vocab), dev, "draft_probs")
-             if draft_probs is not None else (None, 0))
-    _check((_lib or lib()).kv_verify_drafts(
+             if draft_probs is not None else (0, 0))
+    _check((_lib or lib()).kv_verify_drafts_packed(_pack_verify(
         batch, n, vocab, p, ps, q, qs, _ptr(draft_tokens, i32, (batch, n), dev, "draft_tokens"),
-        _ptr(n_drafts, i32, one, dev, "n_drafts") if n_drafts is not None else None,
+        _ptr(n_drafts, i32, one, dev, "n_drafts") if n_drafts is not None else 0,
         _ptr(accept_u, f32, (batch, n), dev, "accept_u"),
         _ptr(sample_u, f32, one, dev, "sample_u"),
         _ptr(tokens, i32, (batch, n + 1), dev, "tokens"),
         _ptr(n_accepted, i32, one, dev, "n_accepted"),
-        _ptr(seq_lens, i32, one, dev, "seq_lens") if seq_lens is not None else None,
-        _ptr(seq_lens_out, i32, one, dev, "seq_lens_out") if seq_lens_out is not None else None,
-        _stream(stream)), "kv_verify_drafts")
+        _ptr(seq_lens, i32, one, dev, "seq_lens") if seq_lens is not None else 0,
+        _ptr(seq_lens_out, i32, one, dev, "seq_lens_out") if seq_lens_out is not None else 0,
+        _stream(stream))), "kv_verify_drafts")
 
 
 def attn_decode_n_splits(pool, batch, max_ctx):
@@ -440,13 +455,12 @@ def _scored_args(pool, q, out, slopes, workspace):
     shape = q.shape
     if shape[-1] != pool.head_dim:
         raise ValueError(f"q must have shape [..., {pool.head_dim}], got {list(shape)}")
-    ws = None
-    nbytes = 0
+    ws = nbytes = 0
     if workspace is not None:
         nbytes = workspace.numel()
         ws = _ptr(workspace, torch.uint8, (nbytes,), dev, "workspace")
     return (_ptr(q, torch.float16, shape, dev, "q"), _ptr(out, torch.float32, shape, dev, "out"),
-            _ptr(slopes, torch.float32, (shape[-2],), dev, "slopes") if slopes is not None else None,
+            _ptr(slopes, torch.float32, (shape[-2],), dev, "slopes") if slopes is not None else 0,
             ws, nbytes)
 
 
@@ -463,13 +477,13 @@ def attn_decode_scored_int8(pool, layer, q, seq_lens, page_table, out, workspace
         raise ValueError("q must have shape [B][H][D] or [B][q_len][H][D], page_table [B][max_pages]")
     qp, op, sp, ws, nbytes = _scored_args(pool, q, out, slopes, workspace)
     dev, i32, B, max_pages = pool.device_index, torch.int32, q.shape[0], page_table.shape[1]
-    _check((_lib or lib()).attn_decode_scored_int8(
-        pool.handle, layer, qp, B, q.shape[1] if n == 4 else 1, q.shape[-2],
+    _check((_lib or lib()).attn_decode_scored_int8_packed(_pack_decode(
+        _handle(pool), layer, qp, B, q.shape[1] if n == 4 else 1, q.shape[-2],
         _ptr(seq_lens, i32, (B,), dev, "seq_lens"),
         _ptr(page_table, i32, (B, max_pages), dev, "page_table"), max_pages, window, softmax_scale,
         softcap, sp,
-        _ptr(prefix_lens, i32, (B,), dev, "prefix_lens") if prefix_lens is not None else None,
-        n_splits, op, ws, nbytes, _stream(stream)), "attn_decode_scored_int8")
+        _ptr(prefix_lens, i32, (B,), dev, "prefix_lens") if prefix_lens is not None else 0,
+        n_splits, op, ws, nbytes, _stream(stream))), "attn_decode_scored_int8")
 
 
 def attn_prefill_n_splits(pool, n_new, n_heads, start_pos):
@@ -516,10 +530,10 @@ def attn_prefill_chunk_scored_int8(pool, layer, q, start_pos, page_table, out, w
     row = page_table.shape
     if page_table.numel() != row[-1]:
         raise ValueError("page_table must be one sequence's row")
-    _check((_lib or lib()).attn_prefill_chunk_scored_int8(
-        pool.handle, layer, qp, q.shape[0], q.shape[1], start_pos,
+    _check((_lib or lib()).attn_prefill_chunk_scored_int8_packed(_pack_chunk(
+        _handle(pool), layer, qp, q.shape[0], q.shape[1], start_pos,
         _ptr(page_table, torch.int32, row, pool.device_index, "page_table"), row[-1], window,
-        softmax_scale, softcap, sp, prefix_len, n_splits, op, ws, nbytes, _stream(stream)),
+        softmax_scale, softcap, sp, prefix_len, n_splits, op, ws, nbytes, _stream(stream))),
         "attn_prefill_chunk_scored_int8")
 
 

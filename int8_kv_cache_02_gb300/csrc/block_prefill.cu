@@ -47,6 +47,7 @@
 
 #include "block_prefill.h"
 #include "decode_common.cuh"
+#include "packed.cuh"
 #include "tc_common.cuh"
 
 namespace int8kv {
@@ -64,7 +65,11 @@ constexpr uint64_t kPatience = 2000000000;      // ns after which a wait has run
 constexpr float kUnset = -1e30f;
 constexpr float kLazy = 8.f;
 constexpr float kWeightShift = 6.f;        // w <= 2^14 in fp16
-constexpr int kChain = 80;                 // tiles that one sum in tensor memory takes
+// Tiles that one sum in tensor memory takes.  Shaped scores, all within a cap, leave no row to one
+// position, and what is lost shows beside their error: 256 queries over 33,024 positions (D 256) are
+// 7.0e-6 off with 80 tiles, 4.5e-6 with 40 and 3.1e-6 with 24, in 260, 270 and 280 us.
+template <bool SHAPED>
+constexpr int kChainOf = SHAPED ? 40 : 80;
 constexpr float kNear = 64.f;              // |m| up to here: c - m is one summand
 
 template <int D>
@@ -128,26 +133,6 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* failed
   }
   if (failed) *(volatile int*)failed = 1;
   return false;
-}
-
-// Two fp32 values in one operation.
-__device__ __forceinline__ uint64_t pack2(float x, float y) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
-  return v;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
 }
 
 __device__ __forceinline__ void tmem_scale(uint32_t ta, int n, float f) {
@@ -240,16 +225,47 @@ struct Sums {
 };
 
 // Sixteen scores in units of 1 / f, capped and biased; ahead: how far the first one's position is
-// ahead of the query's.
+// ahead of the query's.  Two at a time go through the polynomial of capped(); a piece in which one
+// is beyond the cap goes through it one by one.
 __device__ __forceinline__ void shape_piece(uint32_t (&v)[16], float f, const Shaping& shape,
                                             float slope, int ahead) {
+  if (shape.cap != 0.f) {
+    float most = 0.f;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    float z = __uint_as_float(v[k]) * f;
-    if (shape.cap != 0.f) z = capped(z, shape.cap, shape.over_cap);
-    if (shape.slopes) z = fmaf(slope, (float)(ahead + k), z);
-    v[k] = __float_as_uint(z);
+    for (int k = 0; k < 16; ++k) most = fmaxf(most, fabsf(__uint_as_float(v[k])));
+    if (most * f <= shape.cap) {
+      const uint64_t f2 = pack2(f, f), over = pack2(shape.over_cap, shape.over_cap);
+#pragma unroll
+      for (int k = 0; k < 16; k += 2) {
+        float y0, y1;
+        unpack2(capped2(mul2(pack2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), f2), over), y0,
+                y1);
+        v[k] = __float_as_uint(y0);
+        v[k + 1] = __float_as_uint(y1);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        v[k] = __float_as_uint(capped(__uint_as_float(v[k]) * f, shape.cap, shape.over_cap));
+    }
+    f = 1.f;
   }
+  if (shape.slopes) {
+    const uint64_t s2 = pack2(slope, slope), f2 = pack2(f, f);
+    const float first = (float)ahead;      // (exact, and so are its successors: below 2^24 or far off)
+#pragma unroll
+    for (int k = 0; k < 16; k += 2) {
+      float y0, y1;
+      unpack2(fma2(s2, pack2(first + k, first + (k + 1)),
+                   mul2(pack2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), f2)), y0, y1);
+      v[k] = __float_as_uint(y0);
+      v[k + 1] = __float_as_uint(y1);
+    }
+    f = 1.f;
+  }
+  if (f != 1.f)
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
 }
 
 // Sixteen codes as fp16 in the order codes_to_h2 gives (int8: dims 0 2 1 3 of every four).
@@ -264,7 +280,7 @@ __device__ __forceinline__ void halves_of(const uint4 w, uint4& lo, uint4& hi) {
 template <int D, bool F8, bool SHAPED>
 __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const PrefillBlockArgs a) {
   using L = Layout<D>;
-  constexpr int CH = L::CH, CPR = D / 16;
+  constexpr int CH = L::CH, CPR = D / 16, kChain = kChainOf<SHAPED>;
   extern __shared__ unsigned char raw[];
   __shared__ Shared s;
   unsigned char* smem = raw + ((1024u - (ptx::smem_u32(raw) & 1023u)) & 1023u);
@@ -285,10 +301,14 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
     gap_at = (pre + kKeys - 1) / kKeys;
     gap = max(0, lo / kKeys - gap_at);
   }
-  const auto position = [&](int tile) {
-    return (SHAPED && tile >= gap_at ? tile + gap : tile) * kKeys;
-  };
   const int tiles = (hi + kKeys - 1) / kKeys - gap;
+  // The last tile first: a bias that falls with the distance then has its largest scores early,
+  // and the references hardly move.
+  const auto position = [&](int tile) {
+    if constexpr (!SHAPED) return tile * kKeys;
+    const int back = tiles - 1 - tile;
+    return (back >= gap_at ? back + gap : back) * kKeys;
+  };
   const int t0 = (int)((long long)tiles * split / a.splits);
   const int n = (int)((long long)tiles * (split + 1) / a.splits) - t0;
 
@@ -567,21 +587,24 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
     bool bad = false;
     // A position that some row sees, or one of its 16 does: pages that none sees need not be there.
     auto needed = [&](int pos) {
-      if constexpr (SHAPED) return pos < hi && ((pos & ~15) < pre || (pos | 15) >= lo);
+      if constexpr (SHAPED) return pos >= 0 && pos < hi && ((pos & ~15) < pre || (pos | 15) >= lo);
       return pos < hi;
     };
     auto entry = [&](int pos) { return needed(pos) ? __ldg(a.page_table + (pos >> p.ps_log2)) : -1; };
+    int found = 0;      // where the tile begins that was looked for last
     auto find = [&](int tile) {
-      const int pos = position(t0 + tile) + row;
+      found = position(t0 + tile);
+      const int pos = found + row;
       // (a tile in one page: a position of its end that is there, or its first)
-      page[0] = !one_page ? entry(pos) : pos - row < hi ? __ldg(a.page_table + ((pos - row) >> p.ps_log2)) : -1;
+      const bool in = pos - row < hi && (!SHAPED || pos >= 0);
+      page[0] = !one_page ? entry(pos) : in ? __ldg(a.page_table + ((pos - row) >> p.ps_log2)) : -1;
       if (!one_page)
 #pragma unroll
         for (int x = 1; x < CH; ++x) page[x] = entry(pos + STEP * x);
-      if (tables) table_page = entry(position(t0 + tile) + (lane & 3) * 16);
+      if (tables) table_page = entry(found + (lane & 3) * 16);
     };
-    auto locate = [&](int tile) {      // (the page ids have come by then)
-      const int pos = position(t0 + tile) + row;
+    auto locate = [&]() {      // (the page ids have come by then)
+      const int pos = found + row;
       have = 0;
       if (one_page) {
         const bool there = (unsigned)page[0] < (unsigned)p.n_pages;
@@ -619,9 +642,9 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
         }
       }
     };
-    auto load_scale = [&](int tile) {
+    auto load_scale = [&]() {
       if (!tables) return;
-      const int pos = position(t0 + tile) + (lane & 3) * 16;
+      const int pos = found + (lane & 3) * 16;
       none = (unsigned)table_page >= (unsigned)p.n_pages;
       scale = 0.f;
       if (!none)
@@ -641,10 +664,10 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
     };
     if (n > 0) {
       find(0);
-      locate(0);
+      locate();
       load(p.k, k);
       load(p.v, v);
-      load_scale(0);
+      load_scale();
       find(1);
     }
     for (int i = 0; i < n; ++i) {
@@ -668,9 +691,9 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
         ptx::mbar_arrive(&s.k_full[b]);
       }
       if (i + 1 < n) {
-        locate(i + 1);
+        locate();
         load(p.k, k);
-        load_scale(i + 1);
+        load_scale();
         find(i + 2);
       }
       ok = i < 2 || wait(&s.o_done[b], before, &s.failed, a.patience);

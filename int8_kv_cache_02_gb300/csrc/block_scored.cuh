@@ -3,6 +3,7 @@
 #pragma once
 
 #include "block_common.cuh"
+#include "packed.cuh"
 
 namespace int8kv {
 
@@ -18,21 +19,35 @@ struct Shaping {
 // roundings 1.3 * 2^-24): scores far below the cap, where all the weights can lie, keep
 // fp32's relative precision, which 1 - 2 / (e^2x + 1) loses there, and nothing but
 // multiply-adds is issued.  Larger ones are rare: a branch.
+__device__ constexpr float cap_poly(int c) {
+  return c == 0   ? -3.3333296e-1f
+         : c == 1 ? 1.3332345e-1f
+         : c == 2 ? -5.3879801e-2f
+         : c == 3 ? 2.1486657e-2f
+         : c == 4 ? -7.9461057e-3f
+         : c == 5 ? 2.3013644e-3f
+                  : -3.5845194e-4f;
+}
 __device__ __forceinline__ float capped(float z, float cap, float over_cap) {
   const float x = z * over_cap, s = x * x;
-  float p = -3.5845194e-4f;
-  p = fmaf(p, s, 2.3013644e-3f);
-  p = fmaf(p, s, -7.9461057e-3f);
-  p = fmaf(p, s, 2.1486657e-2f);
-  p = fmaf(p, s, -5.3879801e-2f);
-  p = fmaf(p, s, 1.3332345e-1f);
-  p = fmaf(p, s, -3.3333296e-1f);
+  float p = cap_poly(6);
+#pragma unroll
+  for (int c = 5; c >= 0; --c) p = fmaf(p, s, cap_poly(c));
   float y = fmaf(z, s * p, z);
   if (s > 1.f) {
     const float e = ptx::ex2(fabsf(x) * 2.8853900817779268f);      // e^2|x|; beyond fp32: tanh is 1
     y = copysignf(cap - cap * __fdividef(2.f, fminf(e, 1e30f) + 1.f), z);
   }
   return y;
+}
+
+// Two scores, neither beyond the cap; over: the pair of 1 / cap.
+__device__ __forceinline__ uint64_t capped2(uint64_t z, uint64_t over) {
+  const uint64_t x = mul2(z, over), s = mul2(x, x);
+  uint64_t p = pack2(cap_poly(6), cap_poly(6));
+#pragma unroll
+  for (int c = 5; c >= 0; --c) p = fma2(p, s, pack2(cap_poly(c), cap_poly(c)));
+  return fma2(z, mul2(s, p), z);
 }
 
 // attn_decode_scored_int8's arguments beside those of a plain decode call.

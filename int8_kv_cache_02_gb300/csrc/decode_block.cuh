@@ -142,14 +142,18 @@ __device__ __forceinline__ int unit_tiles(int lo, int hi) {
 }
 
 // The positions of a sequence that some query of it attends: [lo, hi), and with shaped scores
-// [0, pre) too.  Its tiles in the order in which they are taken: from tile `gap_at` on, `gap`
-// tiles are left out.
+// [0, pre) too: from tile `gap_at` on, `gap` tiles are left out, and the last one is taken first
+// (a bias that falls with the distance has its largest scores there: the references hardly
+// move).  tile_at: the tile that is taken as the t-th of nt.
 struct Seen {
-  int lo, hi;
+  int lo, hi, nt;
   int pre, gap_at, gap;
   template <class A>
   __device__ __forceinline__ int tile_at(int t) const {
-    if constexpr (kScored<A>) return t + (t >= gap_at ? gap : 0);
+    if constexpr (kScored<A>) {
+      const int back = nt - 1 - t;
+      return back + (back >= gap_at ? gap : 0);
+    }
     return lo / kTile + t;
   }
 };
@@ -158,7 +162,7 @@ __device__ __forceinline__ int prefix_of(const BlockScoredArgs& a, int b) {
   return a.prefix_lens ? __ldg(a.prefix_lens + b) : a.prefix;
 }
 
-// From the length of a sequence (at most what its row holds) -> its number of tiles.
+// From the length of a sequence (at most what its row holds) -> its number of tiles, nt.
 template <class A>
 __device__ __forceinline__ int seen_tiles(const A& a, int b, int hi, Seen& s) {
   s.hi = hi;
@@ -168,11 +172,12 @@ __device__ __forceinline__ int seen_tiles(const A& a, int b, int hi, Seen& s) {
     s.gap_at = (s.pre + kTile - 1) / kTile;
     s.gap = s.lo / kTile - s.gap_at;
     if (s.gap <= 0) s.lo = s.gap = 0;
-    return unit_tiles(0, hi) - s.gap;
+    s.nt = unit_tiles(0, hi) - s.gap;
   } else {
     s.lo = a.window > 0 && hi > a.window ? hi - a.window : 0;
-    return unit_tiles(s.lo, hi);
+    s.nt = unit_tiles(s.lo, hi);
   }
+  return s.nt;
 }
 // The same for sequence b; a length beyond its row is flagged.
 template <class A>
@@ -245,7 +250,7 @@ __device__ __forceinline__ Place find_share(const A& a, int per_seq, int start, 
 // The part of a unit that one block takes: tiles [first, last) of unit u of sequence b.
 // pieces: how many shares the unit lies in, from this one on.
 struct Segment : Seen {
-  int b, u, nt, first, last, pieces;
+  int b, u, first, last, pieces;
 };
 
 // The segment at p.at, and p behind it; false at the share's end.
@@ -253,7 +258,7 @@ template <class A>
 __device__ __forceinline__ bool next_segment(const A& a, Place& p, int per_seq, int start,
                                              Segment& s) {
   while (p.at < p.end) {
-    s.nt = unit_range(a, p.b, s);
+    unit_range(a, p.b, s);
     const int len = s.nt + start;
     s.u = s.nt ? (int)((unsigned)(p.at - p.base) / (unsigned)len) : per_seq;
     if (s.u >= per_seq) {     // past this sequence's units
@@ -412,14 +417,33 @@ __device__ __forceinline__ void score_tile(const Warp<D, V>& w, uint32_t tile, c
 template <int NC>
 __device__ __forceinline__ void shape_scores(float (&z)[NC][4], const BlockScoredArgs& a, int pos,
                                              const int (&lim)[NC][2], const float (&slope)[NC][2]) {
+  if (a.shape.cap != 0.f) {
+    float most = 0.f;
 #pragma unroll
-  for (int n = 0; n < NC; ++n)
+    for (int n = 0; n < NC; ++n)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (a.shape.cap != 0.f) z[n][k] = capped(z[n][k], a.shape.cap, a.shape.over_cap);
-      if (a.shape.slopes)
-        z[n][k] = fmaf(slope[n][k & 1], (float)(pos + 8 * (k >> 1) - lim[n][k & 1]), z[n][k]);
+      for (int k = 0; k < 4; ++k) most = fmaxf(most, fabsf(z[n][k]));
+    if (most <= a.shape.cap) {
+      const uint64_t over = pack2(a.shape.over_cap, a.shape.over_cap);
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; k += 2)
+          unpack2(capped2(pack2(z[n][k], z[n][k + 1]), over), z[n][k], z[n][k + 1]);
+    } else {
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[n][k] = capped(z[n][k], a.shape.cap, a.shape.over_cap);
     }
+  }
+  if (a.shape.slopes) {
+#pragma unroll
+    for (int n = 0; n < NC; ++n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        z[n][k] = fmaf(slope[n][k & 1], (float)(pos + 8 * (k >> 1) - lim[n][k & 1]), z[n][k]);
+  }
 }
 
 // The TPI tiles of one stage, from position pos[i] each.  f: K scale * softmax scale * log2(e) of
@@ -678,7 +702,7 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
     const int unit = blockIdx.x / a.cluster;
     seg.b = unit / per_seq;
     seg.u = unit % per_seq;
-    seg.nt = unit_range(a, seg.b, seg);               // (none: zero rows)
+    unit_range(a, seg.b, seg);               // (no tiles: zero rows)
     const int per = (seg.nt + a.cluster - 1) / a.cluster;
     seg.first = min(seg.nt, blockIdx.x % a.cluster * per);
     seg.last = min(seg.nt, seg.first + per);
@@ -731,7 +755,7 @@ __global__ void __launch_bounds__(Shape<D>::NW * 32, Shape<D>::BLOCKS)
         const int nth = mine0 + i * (S::NW * TPI) + j, pos = seg.tile_at<A>(nth) * kTile;
         int from = seg.lo, to_pos = seg.hi;      // the rows that are there
         if constexpr (kScored<A>)
-          if (seg.gap > 0 && nth < seg.gap_at) {
+          if (seg.gap > 0 && pos < seg.pre) {
             from = 0;
             to_pos = seg.pre;
           }

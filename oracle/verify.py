@@ -1,6 +1,6 @@
 """Oracle: verification of drafted tokens (test infrastructure only), in whole numbers.
 
-A probability is floor(p * 2^60), p taken into [0, 1] (NaN: 0); a draft is taken while
+A probability is p * 2^60 rounded to a whole number, p taken into [0, 1] (NaN: 0); a draft is taken while
 u q(x) < p(x) as fractions; the token behind the drafts taken is the lowest v whose weights
 0 .. v sum to more than u times all weights.
 """
@@ -15,7 +15,7 @@ ONE = 1 << 60
 def fixed(p):
     """fp32 array -> whole multiples of 2^-60 (exact in fp64: 24 bits and a power of two)."""
     p = np.nan_to_num(np.asarray(p, np.float32).astype(np.float64), nan=0.0)
-    return np.floor(np.clip(p, 0.0, 1.0) * 2.0 ** 60).astype(np.uint64)
+    return np.rint(np.clip(p, 0.0, 1.0) * 2.0 ** 60).astype(np.uint64)
 
 
 def one(target, draft, x, u, sample_u):
@@ -46,7 +46,7 @@ def one(target, draft, x, u, sample_u):
         return taken, -1
     c = np.cumsum(w, dtype=np.uint64)
     su = 0.0 if np.isnan(sample_u) else min(max(float(sample_u), 0.0), 1.0 - 2.0 ** -24)
-    place = (int(su * 2.0 ** 60) << 4) * int(c[-1]) >> 64
+    place = (int(fixed(su)) << 4) * int(c[-1]) >> 64
     return taken, int(np.searchsorted(c, np.uint64(place), side="right"))
 
 

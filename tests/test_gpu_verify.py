@@ -177,3 +177,29 @@ def test_replayed_on_another_stream():
             assert np.array_equal(acc.cpu().numpy(), want[1])
             total -= 4 - want[1]
             assert np.array_equal(lens.cpu().numpy(), total)
+
+
+def test_rows_that_are_no_probabilities():
+    """Sums of 16 and more: some value of the vocabulary, or -1; the drafts before it stand."""
+    for V in (40, 5000, 33001):
+        p = torch.ones((3, 2, V))
+        p[1] *= 0.01
+        x = torch.zeros((3, 1), dtype=torch.int32)
+        for n in (None, [0, 0, 0]):
+            got = _call(p, None, x, torch.full((3, 1), 0.5), torch.rand(3), n_drafts=n)
+            assert ((got[0] >= -1) & (got[0] < V)).all()
+            assert got[1].tolist() == ([1, 0, 1] if n is None else [0, 0, 0])
+
+
+def test_every_exponent_is_exact():
+    """Values of random mantissas at every exponent, alone in their rows and against another's."""
+    g = torch.Generator().manual_seed(13)
+    V, B = 64, 140
+    p = torch.zeros((B, 2, V))
+    e = torch.arange(B).float()[:, None]
+    p[:, 0] = (1 + torch.rand((B, V), generator=g)) * 2.0 ** (-1 - e) / V
+    p[:, 1] = (1 + torch.rand((B, V), generator=g)) * 2.0 ** (-1 - e) / V
+    q = (1 + torch.rand((B, 1, V), generator=g)) * 2.0 ** (-1 - e[..., None]) / V
+    x = torch.randint(0, V, (B, 1), generator=g, dtype=torch.int32)
+    for u in (0.0, 1.0):
+        _check(p, q, x, torch.full((B, 1), u), torch.rand(B, generator=g))

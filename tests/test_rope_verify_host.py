@@ -36,7 +36,10 @@ def _rope(L, **kw):
              out=P, pages=P, max_pages=4)
     a.update(kw)
     f = _Fake(1, 2, 128, 128, 1, 64, 4, 0)
-    return L.kv_rope_append(ctypes.byref(f), *a.values(), None)
+    status = L.kv_rope_append(ctypes.byref(f), *a.values(), None)
+    words = [ctypes.addressof(x) if isinstance(x, ctypes.Array) else x or 0 for x in a.values()]
+    assert L.kv_rope_append_packed(b._pack_rope(ctypes.addressof(f), *words, 0)) == status
+    return status
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -61,7 +64,9 @@ def _verify(L, **kw):
     a = dict(batch=2, n_draft=3, vocab=100, target=P, ts=100, draft=P, ds=100, x=P, n=None, u=P, s=P,
              tokens=P, acc=P, lens=None, out=None)
     a.update(kw)
-    return L.kv_verify_drafts(*a.values(), None)
+    status = L.kv_verify_drafts(*a.values(), None)
+    assert L.kv_verify_drafts_packed(b._pack_verify(*(x or 0 for x in a.values()), 0)) == status
+    return status
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -73,6 +78,25 @@ def _verify(L, **kw):
 ])
 def test_verify_refusals(L, kw, status):
     assert _verify(L, **kw) == status
+
+
+def test_packed_calls_refuse_null_and_read_floats(L):
+    """The caps that are none are told by their value, so that a float's word is seen to arrive."""
+    for f in (L.kv_rope_append_packed, L.kv_verify_drafts_packed, L.attn_decode_scored_int8_packed,
+              L.attn_prefill_chunk_scored_int8_packed):
+        assert f(None) == -2
+    f = _Fake(1, 2, 128, 64, 1, 64, 4, 8)
+    at = ctypes.addressof(f)
+    for cap, status in ((1.0, 0), (-1.0, -1), (2.0 ** 65, -1), (float("nan"), -1), (0.0, 0)):
+        words = b._pack_decode(at, 0, 0, 0, 1, 2, 0, 0, 4, 0, 0.0, cap, 0, 0, 1, 0, 0, 0, 0)
+        assert L.attn_decode_scored_int8_packed(words) == status        # (a batch of none)
+        words = b._pack_chunk(at, 0, 0, 0, 2, 0, 0, 4, 0, 0.0, cap, 0, 0, 1, 0, 0, 0, 0)
+        assert L.attn_prefill_chunk_scored_int8_packed(words) == status
+    words = b._pack_decode(at, 0, 0, 0, 1, 2, 0, 0, 4, 0, float("inf"), 1.0, 0, 0, 1, 0, 0, 0, 0)
+    assert L.attn_decode_scored_int8_packed(words) == -1
+    f.variant = 0
+    words = b._pack_decode(at, 0, 0, 0, 1, 2, 0, 0, 4, 0, 0.0, 1.0, 0, 0, 1, 0, 0, 0, 0)
+    assert L.attn_decode_scored_int8_packed(words) == -6        # not block-scaled
 
 
 class _Pool:
