@@ -2,8 +2,15 @@
 #pragma once
 
 #include "block_common.cuh"
+#include "packed.cuh"
 
 namespace int8kv {
+
+__device__ __forceinline__ void scale8(const float (&v)[8], float f, float (&y)[8]) {
+  const uint64_t f2 = pack2(f, f);
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) unpack2(mul2(pack2(v[e], v[e + 1]), f2), y[e], y[e + 1]);
+}
 
 // Codes of eight values.  A code is decided by the IEEE quotient v / s; v * inv (inv = 1 / s) is
 // within 2^-22 of it (two roundings, and the quotient's own).  Only where a rounding
@@ -18,20 +25,16 @@ __device__ __forceinline__ uint2 quantize8(const float (&v)[8], float s, float i
   float y[8];
   uint2 w;
   if constexpr (F8) {
-    const float below = inv * (1.f - 0x1p-21f), above = inv * (1.f + 0x1p-21f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = v[e] * below;
+    scale8(v, inv * (1.f - 0x1p-21f), y);
     w = round_codes8<F8>(y);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = v[e] * above;
+    scale8(v, inv * (1.f + 0x1p-21f), y);
     const uint2 u = round_codes8<F8>(y);
     near |= w.x != u.x || w.y != u.y;
   } else {
+    scale8(v, inv, y);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      y[e] = v[e] * inv;
+    for (int e = 0; e < 8; ++e)
       near |= fabsf(y[e] - ((y[e] + kRoundToInt) - kRoundToInt)) > 0.5f - 1.0e-4f;
-    }
     w = round_codes8<F8>(y);
   }
   if (near) {

@@ -260,38 +260,52 @@ __global__ void __launch_bounds__(NT* GROUPS, kResident / (NT * GROUPS) ? kResid
     return;
   }
   const long long stride = is_v ? a.v_stride : a.k_stride;
-  const uint16_t* src = (is_v ? a.v : a.k) + (size_t)(b * a.n_new + i0) * stride;
+  const uint16_t* src = (is_v ? a.v : a.k) + (size_t)(b * a.n_new + i0) * stride + h0 * D;
+  // What a thread's twins are: where they come from (in the next head: D values on) and go to, how far
+  // apart their pieces are, which are there, and which turn.
+  const uint16_t* from[CH];
+  int to[CH], apart[CH];
+  unsigned there = 0, turned = 0;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int n = tid + c * NT, r = n / TW, t = n % TW;
+    int px, py;
+    twin_pieces(t, a.R, px, py);
+    apart[c] = 8 * (py - px);
+    from[c] = src + r * stride + 8 * px;
+    to[c] = (r0 + r) * D + 8 * px;
+    there |= (r < rows) << c;
+    turned |= (r < rows && !is_v && t < a.R / 16) << c;
+  }
   uint4 raw[CH][2];
-  const auto load = [&](int h) {
+  const auto load = [&](bool more) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int n = tid + c * NT, r = n / TW;
-      int px, py;
-      twin_pieces(n % TW, a.R, px, py);
       raw[c][0] = raw[c][1] = make_uint4(0, 0, 0, 0);
-      if (r < rows && h < end) {
-        raw[c][0] = ptx::ldg128(src + r * stride + h * D + 8 * px);
-        raw[c][1] = ptx::ldg128(src + r * stride + h * D + 8 * py);
+      if (more && (there >> c & 1)) {
+        raw[c][0] = ptx::ldg128(from[c]);
+        raw[c][1] = ptx::ldg128(from[c] + apart[c]);
       }
+      from[c] += D;
     }
   };
-  load(h0);
+  load(true);
   const int page = block_page(a.page_table + b * a.max_pages, (int)lp, p);
   Turns turns[KEEP ? CH : 1];
   bool bad = false;
   const auto turns_of = [&](int c, Turns& w) {
-    const int n = tid + c * NT, r = n / TW, t = n % TW;
-    if (!is_v && t < a.R / 16 && r < rows) twin_turns(a, b, (int)i0 + r, t, w, bad);
+    const int n = tid + c * NT;
+    if (turned >> c & 1) twin_turns(a, b, (int)i0 + n / TW, n % TW, w, bad);
   };
   if constexpr (KEEP)
 #pragma unroll
     for (int c = 0; c < CH; ++c) turns_of(c, turns[c]);
   if (page < 0) return;
   const int slot = (int)(first & ((1 << p.ps_log2) - 1));
+  const size_t ph = (size_t)page * p.Hkv + h0;
+  uint8_t* codes = (is_v ? p.v : p.k) + ((ph << p.ps_log2) + slot) * D;
+  float* scale = (is_v ? p.vs : p.ks) + (ph << (p.ps_log2 - p.t_log2)) + (slot >> p.t_log2);
   for (int h = h0; h < end; ++h) {
-    const size_t ph = (size_t)page * p.Hkv + h;
-    uint8_t* codes = (is_v ? p.v : p.k) + ((ph << p.ps_log2) + slot) * D;
-    float* scale = (is_v ? p.vs : p.ks) + (ph << (p.ps_log2 - p.t_log2)) + (slot >> p.t_log2);
     const float s_old = r0 ? *scale : 0.f;
     float x[CH][2][8], top = 0.f;
 #pragma unroll
@@ -299,12 +313,11 @@ __global__ void __launch_bounds__(NT* GROUPS, kResident / (NT * GROUPS) ? kResid
       halves_to_floats(raw[c][0], x[c][0]);
       halves_to_floats(raw[c][1], x[c][1]);
     }
-    load(h + 1);
+    load(h + 1 < end);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int n = tid + c * NT, r = n / TW, t = n % TW;
       if constexpr (!KEEP) turns_of(c, turns[0]);
-      if (!is_v && t < a.R / 16 && r < rows) turn_twin(a.pairs, turns[KEEP ? c : 0], x[c][0], x[c][1]);
+      if (turned >> c & 1) turn_twin(a.pairs, turns[KEEP ? c : 0], x[c][0], x[c][1]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) top = fmaxf(top, fmaxf(fabsf(x[c][0][e]), fabsf(x[c][1][e])));
     }
@@ -333,18 +346,15 @@ __global__ void __launch_bounds__(NT* GROUPS, kResident / (NT * GROUPS) ? kResid
     const bool tiny = s < 0x1p-100f;
     const float inv = tiny ? 0.f : __frcp_rn(s);
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int n = tid + c * NT, r = n / TW;
-      int px, py;
-      twin_pieces(n % TW, a.R, px, py);
-      if (r < rows) {
-        uint8_t* row = codes + (size_t)(r0 + r) * D;
-        *reinterpret_cast<uint2*>(row + 8 * px) =
+    for (int c = 0; c < CH; ++c)
+      if (there >> c & 1) {
+        *reinterpret_cast<uint2*>(codes + to[c]) =
             s > 0.f ? quantize8<F8>(x[c][0], s, inv, tiny) : make_uint2(0, 0);
-        *reinterpret_cast<uint2*>(row + 8 * py) =
+        *reinterpret_cast<uint2*>(codes + to[c] + apart[c]) =
             s > 0.f ? quantize8<F8>(x[c][1], s, inv, tiny) : make_uint2(0, 0);
       }
-    }
+    codes += (size_t)D << p.ps_log2;
+    scale += 1 << (p.ps_log2 - p.t_log2);
   }
   if (bad) flag_error(p.err, INT8KV_DEVERR_LENGTH);
 }
