@@ -25,6 +25,10 @@
  *  4. attn_decode_multi_int8: decode of a window of queries per sequence,
  *     causal within the window (Strata #2698 "What it does": the verify
  *     windows of speculative decoding go through the decode kernels).
+ *  5. Around these: kv_rope_append rotates queries and keys by their positions on
+ *     the way into the cache; attn_decode_scored_int8 and
+ *     attn_prefill_chunk_scored_int8 cap scores, bias them by distance and show
+ *     every query a prefix; kv_verify_drafts takes or refuses drafted tokens.
  *
  * Store variants (Strata #2698 "What it does": k8v8, and one-store variants;
  * "Not in this PR": k8v4 with the Hadamard rotation over head_dim 256):
@@ -507,7 +511,7 @@ int attn_decode_int8_noalloc(const int8kv_pool* pool, int layer, const uint16_t*
  *   accept_u      device fp32 [batch][n_draft], sample_u device fp32 [batch]: in [0, 1)
  *   tokens        device int32 [batch][n_draft + 1]: the drafts that are taken, the token behind
  *                 them, then -1.  That token is -1 where the target's row has no positive value.
- *   n_accepted    device int32 [batch]: drafts taken
+ *   n_accepted    device int32 [batch]: drafts taken.  (Neither overlaps an input.)
  *   seq_lens, seq_lens_out  device int32 [batch], both or neither: seq_lens_out[b] = seq_lens[b] less
  *                 the drafts that were not taken, for a cache that holds the whole window (it may be
  *                 seq_lens; kv_pages_resize takes the pages back).

@@ -278,6 +278,46 @@ def test_a_prefix_that_only_the_chunk_sees_and_replays():
                             z_max=Z)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_an_expired_wait_of_a_chunk_is_reported(kind):
+    """As for plain chunks: the call completes, its rows count for nothing, and later ones are whole."""
+    from int8_kv_cache_02_gb300 import binding as b
+    n, G, D = 700, 8, 128
+    g, pt, dev, orc = _filled(kind, 13, [n], 1, D, 64, 64)
+    q = torch.randn((64, G, D), generator=g).half()
+    args = (dev, q, n - 64, pt[0], 200, 9.0, _slopes(G), 70)
+    for n_splits in (1, 3):
+        want = _chunk(*args, n_splits)
+        b.kv_pool_test_expire_prefill_waits(dev, 1000)
+        got = _chunk(*args, n_splits)
+        assert b.kv_pool_read_device_error(dev) == b.DEVERR_TIMEOUT and not got.any()
+        b.kv_pool_test_expire_prefill_waits(dev, 0)
+        assert np.array_equal(_chunk(*args, n_splits), want)
+
+
+def test_two_streams_at_once():
+    """Calls that share a pool and nothing else, on two streams: the bits of each alone."""
+    from int8_kv_cache_02_gb300 import binding as b
+    lens, D, H = [3000, 2999], 128, 8
+    g, pt, dev, orc = _filled("int8", 14, lens, 2, D, 64, 64)
+    q = torch.randn((2, 4, H, D), generator=g).half().cuda()
+    alone = [_decode(dev, q.cpu(), lens, pt, 500, 20.0, _slopes(H), [7, 9], n_splits=n)
+             for n in (5, 8)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ws = [dev.decode_workspace(8, H, 8) for _ in range(2)]
+    out = [torch.empty((2, 4, H, D), device="cuda") for _ in range(2)]
+    dl, dpt, sl, pre = _dev(lens), pt.cuda(), _slopes(H).cuda(), _dev([7, 9])
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for k in range(2):
+            b.attn_decode_scored_int8(dev, 0, q, dl, dpt, out[k], ws[k], window=500, softcap=20.0,
+                                      slopes=sl, prefix_lens=pre, n_splits=(5, 8)[k],
+                                      stream=streams[k])
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert np.array_equal(out[k].cpu().numpy(), alone[k])
+
+
 def test_refusals():
     from int8_kv_cache_02_gb300 import binding as b
     g, pt, dev, orc = _filled("int8", 11, [64], 2, 64, 16, 16)
