@@ -12,6 +12,9 @@
 // that one thread takes, pieces t and t + R/16 for t < R/16, and neighbours behind the
 // rotated part.  In either pairing a twin's eight pairs use eight cosines and eight sines
 // in pieces of four, and a piece of four pairs that go by one position is two 16-byte loads.
+//
+// Bound by HBM for prompts (rows in, queries and codes out; half of the issue slots are taken), by
+// the launch and three dependent loads for single tokens (64 sequences: 3.7 us).
 #include <cmath>
 
 #include "block_quant.cuh"
@@ -215,8 +218,9 @@ __device__ __forceinline__ void rotate_queries(const RopeArgs& a, unsigned threa
 // turns are the same, and loaded once (a row's are four times its own bytes), and the next head's
 // rows are under way meanwhile.  CH twins per thread, as fp32; beyond two of them the turns
 // are loaded again for each head, the registers holding no more.
-// Compiled for 768 threads an SM: a prompt of 2 x 16381 tokens (32 / 8 heads of D 128) takes 126 us,
-// 138 at 512 (128 registers) and 144 at 1024, whose spills the keys pay for.
+// Compiled for 768 threads an SM: a prompt of 2 x 16381 tokens (32 / 8 heads of D 128, one axis) takes
+// 124 us (89 % of the copy rate); when the three were measured it took 126, 138 with 512
+// threads (128 registers), and 144 with 1024, whose spills the keys pay for.
 constexpr int kResident = 768;
 template <int D, bool F8, int NT, int GROUPS, int CH>
 __global__ void __launch_bounds__(NT* GROUPS, kResident / (NT * GROUPS) ? kResident / (NT * GROUPS) : 1)
@@ -651,8 +655,11 @@ __global__ void __launch_bounds__(kRowWarps * 32)
 }
 
 // ---- launches ------------------------------------------------------------
-// Query heads per thread: a thread's turns cost twice its twin's bytes of one head, so a thread takes
-// up to eight heads, but not fewer than two blocks of threads an SM are made of them.
+// Query heads per thread: a thread's turns are twice its twin's bytes of one head, so it takes up to
+// eight heads, but two blocks of threads an SM are made of them at least.  A prompt of 2 x 16381 tokens
+// (32 / 8 heads of D 128, one axis) with 1, 2, 4, 8, 16 heads a thread: 197, 140, 128, 124, 126 us,
+// with three axes 302, 205, 149, 133, 129; 16 heads of D 256, 64 values turned: 92, 64, 58, 56, 59;
+// 2 x 1000 tokens, where the rule stops at four: 14.1 with one, 9.9.
 unsigned query_blocks(RopeArgs& a, int D, int threads, int sms) {
   a.heads = 1;
   if (!a.q) return 0;
@@ -662,7 +669,8 @@ unsigned query_blocks(RopeArgs& a, int D, int threads, int sms) {
 }
 
 // Heads that a group of threads takes in turn, of `threads` that one head wants: up to eight, while
-// there are two blocks' threads for every SM.
+// two blocks' threads are left for every SM.  Keys and values of the prompt above with 1 and 8 heads a
+// group: 76 and 57 us, with three axes 102 and 60.
 int heads_of_a_group(long long threads, int heads, int sms) {
   int n = 1;
   while (n < 8 && n < heads && threads * ((heads + 2 * n - 1) / (2 * n)) >= 1024LL * sms) n *= 2;
