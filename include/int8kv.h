@@ -252,6 +252,8 @@ int kv_quant_append(const int8kv_pool* pool, int layer, const uint16_t* k_new,
  *                 returns; NULL for one axis
  *   q_out         device fp16 [n_seqs][n_new][n_heads][head_dim]; may be q itself where q_stride is
  *                 n_heads * head_dim, but overlaps nothing else
+ * A turned value can be 1.42 times the larger of its pair: beyond 65504 it becomes infinite where it
+ * is kept as fp16 (queries, fp16 stores).
  * A position outside the table is flagged (INT8KV_DEVERR_LENGTH) and its pairs are not turned; so is
  * a new_lens[b] beyond n_new, which counts as n_new.  Tokens without a place in the cache are flagged
  * and left out as by kv_quant_append; their queries are turned all the same.

@@ -223,6 +223,43 @@ def test_many_query_heads_and_tokens(n):
     bu.assert_same(dev, orc)
 
 
+@pytest.mark.parametrize("kind", KINDS + ["rows"])
+def test_layers_and_pages_past_4_gb(kind):
+    """The second layer's last pages, more than 2^32 bytes into either store; what comes to lie there is
+    what a small pool gets, the first layer stays as it was, and shaped scores read it back."""
+    from int8_kv_cache_02_gb300 import binding as b
+    g = torch.Generator().manual_seed(9)
+    D, ps, n_pages, n = 256, 128, 72000, 150
+    variant = {"int8": "k8v8_block", "e4m3": "f8_block", "rows": "k8v8"}[kind]
+    gs = 256 if kind == "rows" else 32
+    far = b.KVPool(2, 1, D, gs, ps, n_pages, variant)
+    near = b.KVPool(1, 1, D, gs, ps, 2, variant)
+    assert far.k_store[1].numel() * 2 > 1 << 32
+    q, k, v = (t.cuda() for t in _rows(g, 1, n, 8, 1, D))
+    tab = torch.from_numpy(rope.table(n, D)).cuda()
+    out = [torch.empty_like(q) for _ in range(2)]
+    ft, nt = _dev([[n_pages - 1, n_pages - 2]]), _dev([[0, 1]])
+    for pool, layer, table, o in ((far, 1, ft, out[0]), (near, 0, nt, out[1])):
+        b.kv_rope_append(pool, layer, k, v, _dev([0]), table, tab, q=q, q_out=o)
+    assert torch.equal(out[0], out[1])
+    for name in ("k_store", "v_store", "k_scales", "v_scales"):
+        x, y = (getattr(p, name).view(torch.uint8) for p in (far, near))
+        assert torch.equal(x[1, [n_pages - 1, n_pages - 2]], y[0])
+        assert not x[0, -4:].any() and not x[1, -6:-2].any()
+    if kind == "rows":
+        return
+    lens = _dev([n])
+    got = [torch.empty((1, 4, 8, D), device="cuda") for _ in range(2)]
+    chunk = [torch.empty((n, 8, D), device="cuda") for _ in range(2)]
+    for pool, layer, table, o, c in ((far, 1, ft, got[0], chunk[0]), (near, 0, nt, got[1], chunk[1])):
+        b.attn_decode_scored_int8(pool, layer, q[:, -4:].contiguous(), lens, table, o, None,
+                                  softcap=20.0, n_splits=1)
+        b.attn_prefill_chunk_scored_int8(pool, layer, q[0], 0, table[0], c, None, softcap=20.0,
+                                         n_splits=1)
+    assert got[0].any() and torch.equal(got[0], got[1]) and torch.equal(chunk[0], chunk[1])
+    assert b.kv_pool_read_device_error(far) == 0
+
+
 def test_replayed_on_another_stream():
     """Captured once, replayed as positions and lengths move on, on a stream of its own."""
     from int8_kv_cache_02_gb300 import binding
