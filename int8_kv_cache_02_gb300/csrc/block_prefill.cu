@@ -65,11 +65,11 @@ constexpr uint64_t kPatience = 2000000000;      // ns after which a wait has run
 constexpr float kUnset = -1e30f;
 constexpr float kLazy = 8.f;
 constexpr float kWeightShift = 6.f;        // w <= 2^14 in fp16
-// Tiles that one sum in tensor memory takes.  Shaped scores, all within a cap, leave no row to one
-// position, and what is lost shows beside their error: 256 queries over 33,024 positions (D 256) are
-// 7.0e-6 off with 80 tiles, 4.5e-6 with 40 and 3.1e-6 with 24, in 260, 270 and 280 us.
-template <bool SHAPED>
-constexpr int kChainOf = SHAPED ? 40 : 80;
+constexpr int kChain = 80;                 // tiles that one sum in tensor memory takes
+// Shaped scores, all within a cap, leave no row to one position, and what is lost shows beside their
+// error: 256 queries over 33,024 positions (D 256, 57 tiles a block) are 7.0e-6 off as one chain and
+// 3.8e-6 as two of 29, which take 10 us.  So at most 40 tiles, in chains of about the same length.
+constexpr int kShapedChain = 40;
 
 // Scores of the kernel: plain, shaped, and capped without a bias, which is most of what is capped and
 // takes 6 % less time at D 256 for knowing it (257 against 273 us when it was made; nothing at D 128).
@@ -109,7 +109,7 @@ struct Shared {
   int failed;
   float k_scale[4][4], v_log2[4][4];       // of a tile's 16-position pieces; four tiles
   int none[4][4];                          // piece without a page
-  float2 top[2][2][kRows];                 // largest z of a thread's two pieces, by tile and half
+  float2 top[2][2][kRows];                 // by half: largest z of a thread's two pieces; its sum
 };
 
 __device__ __forceinline__ int swizzled(int row, int c) { return row * 128 + ((c ^ (row & 7)) << 4); }
@@ -137,6 +137,19 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* failed
   }
   if (failed) *(volatile int*)failed = 1;
   return false;
+}
+
+// Whether the condition holds for a thread of those (whole warps, `count` of them) that meet at
+// barrier `id`.
+__device__ __forceinline__ bool barrier_or(int id, int count, bool condition) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+      "bar.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(count), "r"((uint32_t)condition)
+      : "memory");
+  return any != 0;
 }
 
 __device__ __forceinline__ void tmem_scale(uint32_t ta, int n, float f) {
@@ -287,7 +300,7 @@ template <int D, bool F8, int SCORES>
 __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const PrefillBlockArgs a) {
   using L = Layout<D>;
   constexpr bool SHAPED = SCORES != kPlain;
-  constexpr int CH = L::CH, CPR = D / 16, kChain = kChainOf<SHAPED>;
+  constexpr int CH = L::CH, CPR = D / 16;
   extern __shared__ unsigned char raw[];
   __shared__ Shared s;
   unsigned char* smem = raw + ((1024u - (ptx::smem_u32(raw) & 1023u)) & 1023u);
@@ -318,6 +331,9 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
   };
   const int t0 = (int)((long long)tiles * split / a.splits);
   const int n = (int)((long long)tiles * (split + 1) / a.splits) - t0;
+
+  const int chains = SHAPED && n > 0 ? (n + kShapedChain - 1) / kShapedChain : 1;
+  const int chain = SHAPED ? max(1, (n + chains - 1) / chains) : kChain;
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -392,23 +408,23 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
     float m = kUnset, e = kUnset, l = 0.f, e_sum = kUnset;      // (e_sum: e of that sum)
     bool far = false;    // whether a row of the warp has |m| > kNear
     bool ok = true;      // (once it is false the warp only keeps the barrier's count)
-    for (int from = 0; from < n; from += kChain) {
+    for (int from = 0; from < n; from += chain) {
       if (from > 0) {      // the sum in tensor memory starts anew with the next product
         ok = ok && wait(&s.o_done[(from - 1) & 1], ((from - 1) >> 1) & 1, &s.failed, a.patience);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
           tc::fence_after();
           const Sums<D> sum = sums();
-          if (from == kChain) {
+          if (from == chain) {
             e_sum = e;
           } else if (__any_sync(0xffffffffu, e - e_sum > 64.f)) {      // (else O grows to it)
             sum.scale(ptx::ex2(e_sum - e));
             e_sum = e;
           }
-          sum.take(my_o, ptx::ex2(e - e_sum), from == kChain);
+          sum.take(my_o, ptx::ex2(e - e_sum), from == chain);
         }
       }
-      const int behind = min(n, from + kChain);
+      const int behind = min(n, from + chain);
       for (int i = from; i < behind; ++i) {
         const int pos = position(t0 + i) + half * 32, tab = i & 3;
         ok = ok && wait(&s.t_full[tab], (i >> 2) & 1, &s.failed, a.patience);
@@ -416,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
         ok = __all_sync(0xffffffffu, ok);
         const uint32_t sc = lanes + (i % 3) * kKeys + half * 32;
         uint32_t v[2][16];
-        float f[2], lv[2], lo[2], most[2] = {-INFINITY, -INFINITY};
+        float f[2], lv[2], most[2] = {-INFINITY, -INFINITY};
         if (ok) {
           tc::fence_after();
           tc::ld16(sc, v[0]);
@@ -426,7 +442,6 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
           for (int j = 0; j < 2; ++j) {
             f[j] = s.k_scale[tab][2 * half + j];
             lv[j] = s.v_log2[tab][2 * half + j];
-            lo[j] = s.v_log2[tab][2 * (half ^ 1) + j];      // (the other thread's)
             none[j] = s.none[tab][2 * half + j];
           }
           tc::wait_ld();
@@ -462,18 +477,26 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
             most[j] = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * f[j];
           }
         }
-        s.top[i & 1][half][R] = make_float2(most[0], most[1]);
-        // a row's two warps alone (also once a wait has failed); all eight together: the capped chunk
-        // 258 us instead of 250
-        ptx::named_barrier_sync(1 + (warp & 3), 64);
+        // Whether a reference of the row has to move; its two warps alone ask each other (all eight
+        // together: the capped chunk 258 us, 250 so), and tell each other why only if it has (the same
+        // chunk with 32 / 8 heads of D 128: 417 us, 407 so).
+        // (Both meet at both barriers, also once a wait of one of them has failed.)
+        const bool over = ok && (fmaxf(most[0], most[1]) > m + kLazy ||
+                                 fmaxf(most[0] - m + lv[0], most[1] - m + lv[1]) > e + kLazy);
+        const bool moves = barrier_or(1 + (warp & 3), 64, over);
+        if (moves) {
+          s.top[0][half][R] = make_float2(most[0], most[1]);
+          ptx::named_barrier_sync(1 + (warp & 3), 64);
+        }
         if (!ok) continue;
-        const float2 other = s.top[i & 1][half ^ 1][R];
-        const float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(other.x, other.y));
-        const auto above_m = [&]() {      // the tile's largest z - m + log2 sv
-          return fmaxf(fmaxf(most[0] - m + lv[0], most[1] - m + lv[1]),
-                       fmaxf(other.x - m + lo[0], other.y - m + lo[1]));
-        };
-        if (__any_sync(0xffffffffu, top > m + kLazy || above_m() > e + kLazy)) {
+        if (moves) {
+          const float2 other = s.top[0][half ^ 1][R];
+          const float lo[2] = {s.v_log2[tab][2 * (half ^ 1)], s.v_log2[tab][2 * (half ^ 1) + 1]};
+          const float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(other.x, other.y));
+          const auto above_m = [&]() {      // the tile's largest z - m + log2 sv
+            return fmaxf(fmaxf(most[0] - m + lv[0], most[1] - m + lv[1]),
+                         fmaxf(other.x - m + lo[0], other.y - m + lo[1]));
+          };
           if (top > m + kLazy) {
             l *= ptx::ex2(m - top);
             e += m - top;      // (the same references, from the new m)
@@ -539,9 +562,9 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
         if (lane == 0) ptx::mbar_arrive(&s.w_full[i & 1]);
       }
     }
-    s.top[n & 1][half][R] = make_float2(l, 0.f);      // (the last tile's may still be read)
+    s.top[1][half][R] = make_float2(l, 0.f);      // (the last tile's may still be read)
     ptx::named_barrier_sync(1 + (warp & 3), 64);
-    l += s.top[n & 1][half ^ 1][R].x;
+    l += s.top[1][half ^ 1][R].x;
     ok = __all_sync(0xffffffffu, wait(&s.drain, 0, &s.failed, a.patience));
     tc::fence_after();
     if (!ok && tid == 0) flag_error(p.err, INT8KV_DEVERR_TIMEOUT);
@@ -549,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
       const bool live = ok && n > 0 && l > 0.f;      // (a block that failed counts for nothing)
       float f = live ? ptx::ex2(e - kWeightShift) : 0.f;
       float* const out = row_out(gc);
-      if (n > kChain) {
+      if (n > chain) {
         sums().give(my_o, ptx::ex2(e_sum - e));
         __syncwarp();      // (other lanes' sums lay where this lane's row goes)
       }
@@ -748,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
         for (int j = 0; j < kKeys / 16; ++j) {
           const uint64_t d = dv + (((i & 1) * L::TILE + j * 2048) >> 4);
           const uint32_t w = tmem + i % 3 * kKeys + j * 16;
-          tc::mma_ts(tmem + L::O, w, d, id_o, i % kChain > 0 || j > 0);
+          tc::mma_ts(tmem + L::O, w, d, id_o, i % chain > 0 || j > 0);
           tc::mma_ts(tmem + L::O, w + 8, d, id_o, true);
         }
         tc::mma_commit(&s.o_done[i & 1]);
