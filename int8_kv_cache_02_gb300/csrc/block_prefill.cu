@@ -242,8 +242,11 @@ struct Sums {
 };
 
 // Sixteen scores in units of 1 / f, capped and biased; ahead: how far the first one's position is
-// ahead of the query's.  Two at a time go through the polynomial of capped(); a piece in which one
-// is beyond the cap goes through it one by one.
+// ahead of the query's.  Two at a time go through the polynomial of capped().  A piece in which one
+// is beyond the cap takes the exponential for all: what that loses of its small scores, 2^-22 of the
+// cap, meets weights that are the smaller for it (they are one row's).  With a cap of 5
+// and scores up to 20 the chunk of 33,024 positions (D 256) takes 293 us instead of 251, one by one
+// it took 361 (D 128: 466, 377, 580).
 template <int SCORES>
 __device__ __forceinline__ void shape_piece(uint32_t (&v)[16], float f, const Shaping& shape,
                                             float slope, int ahead) {
@@ -262,9 +265,10 @@ __device__ __forceinline__ void shape_piece(uint32_t (&v)[16], float f, const Sh
         v[k + 1] = __float_as_uint(y1);
       }
     } else {
+      const float over = f * shape.over_cap;
 #pragma unroll
       for (int k = 0; k < 16; ++k)
-        v[k] = __float_as_uint(capped(__uint_as_float(v[k]) * f, shape.cap, shape.over_cap));
+        v[k] = __float_as_uint(beyond_cap(__uint_as_float(v[k]) * over, shape.cap));
     }
     f = 1.f;
   }

@@ -28,6 +28,7 @@ __device__ constexpr float cap_poly(int c) {
          : c == 5 ? 2.3013644e-3f
                   : -3.5845194e-4f;
 }
+constexpr float kTwoLog2E = 2.8853900817779268f;
 __device__ __forceinline__ float capped(float z, float cap, float over_cap) {
   const float x = z * over_cap, s = x * x;
   float p = cap_poly(6);
@@ -35,10 +36,16 @@ __device__ __forceinline__ float capped(float z, float cap, float over_cap) {
   for (int c = 5; c >= 0; --c) p = fmaf(p, s, cap_poly(c));
   float y = fmaf(z, s * p, z);
   if (s > 1.f) {
-    const float e = ptx::ex2(fabsf(x) * 2.8853900817779268f);      // e^2|x|; beyond fp32: tanh is 1
+    const float e = ptx::ex2(fabsf(x) * kTwoLog2E);
     y = copysignf(cap - cap * __fdividef(2.f, fminf(e, 1e30f) + 1.f), z);
   }
   return y;
+}
+
+// The exponential's form alone, for x = z / cap.
+__device__ __forceinline__ float beyond_cap(float x, float cap) {
+  const float e = ptx::ex2(fabsf(x) * kTwoLog2E);      // e^2|x|; infinite: tanh is 1
+  return copysignf(cap - __fdividef(2.f * cap, e + 1.f), x);
 }
 
 // Two scores, neither beyond the cap; over: the pair of 1 / cap.
