@@ -70,29 +70,30 @@ struct TableRow {
 template <int N>
 __device__ __forceinline__ void load_turns(const RopeArgs& a, size_t b, int tok, int i, float* c,
                                            float* s, bool& bad) {
-  constexpr int STEP = N < 4 ? N : 4;
-#pragma unroll
-  for (int k = 0; k < N; k += STEP) {
-    const unsigned by = a.axes[(i + k) >> 2] >> (N < 4 ? 2 * (i & 3) : 0), first = by & 3;
-    if (STEP == 4 && by == first * 0x55u) {
+  if constexpr (N >= 4) {      // (mostly by one position)
+    const unsigned by = a.axes[i >> 2], first = by & 3;
+    if (by == first * 0x55u && (N == 4 || a.axes[(i >> 2) + 1] == by)) {
       const TableRow r(a, b, tok, first);
-      const float4 x = __ldg(reinterpret_cast<const float4*>(r.row + i + k));
-      const float4 y = __ldg(reinterpret_cast<const float4*>(r.row + a.R / 2 + i + k));
       bad |= !r.ok;
-      c[k] = r.ok ? x.x : 1.f, c[k + 1] = r.ok ? x.y : 1.f;
-      c[k + 2] = r.ok ? x.z : 1.f, c[k + 3] = r.ok ? x.w : 1.f;
-      s[k] = r.ok ? y.x : 0.f, s[k + 1] = r.ok ? y.y : 0.f;
-      s[k + 2] = r.ok ? y.z : 0.f, s[k + 3] = r.ok ? y.w : 0.f;
-    } else {
 #pragma unroll
-      for (int e = 0; e < STEP; ++e) {
-        const TableRow r(a, b, tok, by >> (2 * e) & 3);
-        const float x = __ldg(r.row + i + k + e), y = __ldg(r.row + a.R / 2 + i + k + e);
-        bad |= !r.ok;
-        c[k + e] = r.ok ? x : 1.f;
-        s[k + e] = r.ok ? y : 0.f;
+      for (int k = 0; k < N; k += 4) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(r.row + i + k));
+        const float4 y = __ldg(reinterpret_cast<const float4*>(r.row + a.R / 2 + i + k));
+        c[k] = r.ok ? x.x : 1.f, c[k + 1] = r.ok ? x.y : 1.f;
+        c[k + 2] = r.ok ? x.z : 1.f, c[k + 3] = r.ok ? x.w : 1.f;
+        s[k] = r.ok ? y.x : 0.f, s[k + 1] = r.ok ? y.y : 0.f;
+        s[k + 2] = r.ok ? y.z : 0.f, s[k + 3] = r.ok ? y.w : 0.f;
       }
+      return;
     }
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const TableRow r(a, b, tok, a.axes[(i + k) >> 2] >> (2 * ((i + k) & 3)) & 3);
+    const float x = __ldg(r.row + i + k), y = __ldg(r.row + a.R / 2 + i + k);
+    bad |= !r.ok;
+    c[k] = r.ok ? x : 1.f;
+    s[k] = r.ok ? y : 0.f;
   }
 }
 
