@@ -173,6 +173,42 @@ def test_scores_beyond_the_cap(kind, size):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("size", [60.0, 2000.0])
+@pytest.mark.parametrize("D,Hkv,G", [(64, 1, 8), (128, 2, 4), (256, 1, 8)])
+def test_large_scores(kind, size, D, Hkv, G):
+    """Scores of 4e4 to 9e7 in base 2, windowed, with a prefix and (too small to be seen beside them)
+    slopes: one position in the prefix wins by half its score, and the output is its V row; or all
+    are alike, below a cap or beyond it, and it is the mean of the V rows that are seen."""
+    lens, prefix, window, n_new = [700, 2500], 900, 300, 130
+    g = torch.Generator().manual_seed(D)
+    pt, n_pages = inputs.page_table(lens, 64, seed=D)
+    sign = torch.where(torch.rand((Hkv, D), generator=g) < 0.5, -1.0, 1.0)
+    q = (size * sign).repeat_interleave(G, 0).half().expand(n_new, Hkv * G, D).contiguous()
+    for winner in (True, False):
+        dev, orc = bu.make_pools(kind, Hkv, D, 16, 64, n_pages)
+        for b, n in enumerate(lens):
+            k = (sign * size).expand(1, n, Hkv, D).clone()
+            if winner:
+                k *= 0.5 * (torch.arange(n) % 2).view(1, n, 1, 1)
+                k[:, n // 3] = sign * size
+            v = torch.randn((1, n, Hkv, D), generator=g).half()
+            bu.append(dev, orc, 0, k.half(), v, [0], pt[b:b + 1])
+        caps = (0.0,) if winner else (0.0, 2.0 ** 30, 100.0)
+        slopes = torch.full((Hkv * G,), 1e-6) if winner else None
+        for cap in caps:
+            q3 = q[None, :3].expand(2, 3, Hkv * G, D).contiguous()
+            ref = _reference(orc, q3, lens, pt, window, cap, slopes, [prefix] * 2)
+            for n_splits in (0, 1, 3):
+                got = _decode(dev, q3, lens, pt, window, cap, slopes, [prefix] * 2, n_splits)
+                bu.assert_close(got, ref, what=f"{winner} {cap} {n_splits}")
+            for b, n in enumerate(lens):
+                ref = _reference(orc, q[None], [n], pt[b:b + 1], window, cap, slopes, [prefix])[0]
+                for n_splits in (0, 1, 3):
+                    got = _chunk(dev, q, n - n_new, pt[b], window, cap, slopes, prefix, n_splits)
+                    bu.assert_close(got, ref, what=f"chunk {winner} {cap} {n} {n_splits}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_negative_scales_and_slopes(kind):
     """softmax_scale below 0; slopes of both signs and 0."""
     lens = [150, 31]
