@@ -220,7 +220,7 @@ __device__ __forceinline__ void rotate_queries(const RopeArgs& a, unsigned threa
 // rows are under way meanwhile.  CH twins per thread, as fp32; beyond two of them the turns
 // are loaded again for each head, the registers holding no more.
 // Compiled for 768 threads an SM: a prompt of 2 x 16381 tokens (32 / 8 heads of D 128, one axis) takes
-// 124 us (89 % of the copy rate); when the three were measured it took 126, 138 with 512
+// 123 us (90 % of the copy rate); when the three were measured it took 126, 138 with 512
 // threads (128 registers), and 144 with 1024, whose spills the keys pay for.
 constexpr int kResident = 768;
 template <int D, bool F8, int NT, int GROUPS, int CH>
