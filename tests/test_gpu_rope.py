@@ -190,6 +190,28 @@ def test_tokens_without_a_place(kind):
     assert binding.kv_pool_read_device_error(dev) == binding.DEVERR_LENGTH | binding.DEVERR_PAGE_ID
 
 
+@pytest.mark.parametrize("kind", KINDS + ["rows"])
+@pytest.mark.parametrize("n", [2, 5, 17, 40])
+def test_positions_at_the_ends_of_int32(kind, n):
+    """INT32_MIN and its successors, whose distance to a block's first token is beyond 32 bits; INT32_MAX;
+    one sequence among them that has a place."""
+    from int8_kv_cache_02_gb300 import binding
+    g = torch.Generator().manual_seed(n)
+    D, pos = 64, [-2 ** 31, 3, 2 ** 31 - 1, -2 ** 31 + 1, -2 ** 31 + n, 2 ** 31 - n]
+    pt = torch.arange(24, dtype=torch.int32).view(6, 4)
+    if kind == "rows":
+        gu.lib_ready()
+        dev, orc = gu.make_pools(1, 2, D, D, 16, 24, opool.K8V8)
+    else:
+        dev, orc = bu.make_pools(kind, 2, D, 16, 16, 24)
+    tab = rope.table(60, D)
+    q, k, v = _rows(g, 6, n, 2, 2, D)
+    want = _oracle(orc, q, k, v, pos, pt, tab, "halves")
+    _same(_call(dev, q, k, v, pos, pt, tab), want)
+    (gu.regions_equal if kind == "rows" else bu.assert_same)(dev, orc)
+    assert binding.kv_pool_read_device_error(dev) == binding.DEVERR_LENGTH
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_scales_from_tiny_products(kind):
     """A sine of 2^-110 leaves keys whose scale has no reciprocal in fp32; zeros leave scale 0."""
