@@ -72,8 +72,9 @@ __global__ void __launch_bounds__(NT* GROUPS) block_append_kernel(
   const long long first = ((pos >> p.t_log2) + j) << p.t_log2;   // the block's first position
   const int r0 = j == 0 ? (int)(pos & (T - 1)) : 0;              // rows it held before
   const long long i0 = first + r0 - pos + skip;                  // its first new token
-  const int rows = (int)min((long long)(T - r0), (long long)n_new - i0);
-  if (rows <= 0) return;
+  const long long left = (long long)n_new - i0;                  // (below INT_MIN, it may be)
+  if (left <= 0) return;
+  const int rows = (int)min((long long)(T - r0), left);
   const long long lp = first >> p.ps_log2;
   if (lp >= max_pages) {
     if (tid == 0) flag_error(p.err, INT8KV_DEVERR_LENGTH);

@@ -94,6 +94,22 @@ def test_append_rounds_ties_and_extremes_like_the_oracle(kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n_new", [1, 2, 5, 17, 40])
+def test_append_at_the_ends_of_int32(kind, n_new):
+    """INT32_MIN and its successors, whose distance to a block's first token is beyond 32 bits, and
+    INT32_MAX; one sequence among them that has a place."""
+    from int8_kv_cache_02_gb300 import binding as b
+    D, pos = 64, [-2 ** 31, 3, 2 ** 31 - 1, -2 ** 31 + 1, -2 ** 31 + n_new, 2 ** 31 - n_new]
+    g = torch.Generator().manual_seed(n_new)
+    pt = torch.arange(24, dtype=torch.int32).view(6, 4)
+    dev, orc = bu.make_pools(kind, 2, D, 16, 16, 24)
+    k, v = (torch.randn((6, n_new, 2, D), generator=g).half() for _ in range(2))
+    bu.append(dev, orc, 0, k, v, pos, pt)
+    bu.assert_same(dev, orc)
+    assert b.kv_pool_read_device_error(dev) == b.DEVERR_LENGTH
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_append_leaves_everything_else_alone(kind):
     from int8_kv_cache_02_gb300 import binding as b
     g = torch.Generator().manual_seed(3)
