@@ -520,7 +520,8 @@ int attn_decode_int8_noalloc(const int8kv_pool* pool, int layer, const uint16_t*
  * Probabilities outside [0, 1] count as the nearest of the two, NaN as 0; below 2^-37 they are
  * rounded to multiples of 2^-60.  A row of the target sums to less than 16 (else the token is some
  * value of the vocabulary, or -1).  n_draft may be 0: plain sampling.
- * Errors: NULL_PTR, INVALID_ARG (vocab beyond 2^30, too), UNSUPPORTED (a batch of 2^28 and more), CUDA. */
+ * Errors: NULL_PTR, INVALID_ARG (vocab or n_draft beyond 2^30, too), UNSUPPORTED (a batch of 2^28 and
+ * more), CUDA. */
 int kv_verify_drafts(int batch, int n_draft, int vocab, const float* target_probs,
                      long long target_stride, const float* draft_probs, long long draft_stride,
                      const int32_t* draft_tokens, const int32_t* n_drafts, const float* accept_u,

@@ -299,8 +299,9 @@ extern "C" int kv_verify_drafts(int batch, int n_draft, int vocab, const float* 
                                 const int32_t* n_drafts, const float* accept_u,
                                 const float* sample_u, int32_t* tokens, int32_t* n_accepted,
                                 const int32_t* seq_lens, int32_t* seq_lens_out, void* stream) {
-  if (batch < 0 || n_draft < 0 || vocab <= 0 || vocab > (1 << 30) || target_stride < vocab ||
-      (draft_probs && draft_stride < vocab))
+  // (the kernel counts drafts and values in 32 bits, by steps of a block's threads)
+  if (batch < 0 || n_draft < 0 || n_draft > (1 << 30) || vocab <= 0 || vocab > (1 << 30) ||
+      target_stride < vocab || (draft_probs && draft_stride < vocab))
     return INT8KV_ERR_INVALID_ARG;
   if (batch == 0) return INT8KV_OK;
   if (!target_probs || !sample_u || !tokens || !n_accepted || !seq_lens != !seq_lens_out ||

@@ -80,6 +80,13 @@ def test_verify_refusals(L, kw, status):
     assert _verify(L, **kw) == status
 
 
+@pytest.mark.parametrize("n", [(1 << 30) + 1, (1 << 31) - 256, (1 << 31) - 1])
+def test_more_drafts_than_32_bits_count(L, n):
+    """Indexes that step over 2^31 would never reach such a count.  (A batch of none: nothing runs.)"""
+    assert _verify(L, batch=0, n_draft=n) == -1
+    assert _verify(L, batch=0, n_draft=1 << 30) == 0
+
+
 def test_packed_calls_refuse_null_and_read_floats(L):
     """The caps that are none are told by their value, so that a float's word is seen to arrive."""
     for f in (L.kv_rope_append_packed, L.kv_verify_drafts_packed, L.attn_decode_scored_int8_packed,
