@@ -517,8 +517,8 @@ int attn_decode_int8_noalloc(const int8kv_pool* pool, int layer, const uint16_t*
  *   seq_lens, seq_lens_out  device int32 [batch], both or neither: seq_lens_out[b] = seq_lens[b] less
  *                 the drafts that were not taken, for a cache that holds the whole window (it may be
  *                 seq_lens; kv_pages_resize takes the pages back).
- * Probabilities outside [0, 1] count as the nearest of the two, NaN as 0; below 2^-37 they are
- * rounded to multiples of 2^-60.  A row of the target sums to less than 16 (else the token is some
+ * Probabilities outside [0, 1] count as the nearest of the two, NaN as 0; in the weights those below
+ * 2^-37 are rounded to multiples of 2^-60.  A row of the target sums to less than 16 (else the token is some
  * value of the vocabulary, or -1).  n_draft may be 0: plain sampling.
  * Errors: NULL_PTR, INVALID_ARG (vocab or n_draft beyond 2^30, too), UNSUPPORTED (a batch of 2^28 and
  * more), CUDA. */

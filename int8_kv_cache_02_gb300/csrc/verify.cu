@@ -222,8 +222,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
       const float u = __ldg(a.u + b * a.n_draft + i);
       refused = true;
       if (x >= 0 && x < a.vocab) {
-        const float p = __ldg(a.target + (b * (a.n_draft + 1) + i) * a.target_stride + x);
-        const float q = a.draft ? __ldg(a.draft + (b * a.n_draft + i) * a.draft_stride + x) : 1.f;
+        const float p = __saturatef(__ldg(a.target + (b * (a.n_draft + 1) + i) * a.target_stride + x));
+        const float q =      // (both as the weights take them: NaN is 0)
+            a.draft ? __saturatef(__ldg(a.draft + (b * a.n_draft + i) * a.draft_stride + x)) : 1.f;
         refused = !((double)u * (double)q < (double)p);
       }
     }

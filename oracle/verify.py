@@ -1,7 +1,7 @@
 """Oracle: verification of drafted tokens (test infrastructure only), in whole numbers.
 
-A probability is p * 2^60 rounded to a whole number, p taken into [0, 1] (NaN: 0); a draft is taken while
-u q(x) < p(x) as fractions; the token behind the drafts taken is the lowest v whose weights
+Probabilities are taken into [0, 1] (NaN: 0); a draft is taken while u q(x) < p(x) as fractions; in the
+weights a probability is p * 2^60 rounded to a whole number; the token behind the drafts taken is the lowest v whose weights
 0 .. v sum to more than u times all weights.
 """
 
@@ -18,6 +18,11 @@ def fixed(p):
     return np.rint(np.clip(p, 0.0, 1.0) * 2.0 ** 60).astype(np.uint64)
 
 
+def nearest(p):
+    """An fp32 number as the nearest of [0, 1] (NaN: 0)."""
+    return Fraction(0) if np.isnan(p) else Fraction(min(max(float(p), 0.0), 1.0))
+
+
 def one(target, draft, x, u, sample_u):
     """One sequence: target [n + 1][V], draft [n][V] or None, x [n], u [n] -> (taken, token)."""
     V, n = target.shape[1], len(x)
@@ -26,10 +31,9 @@ def one(target, draft, x, u, sample_u):
         v = int(x[taken])
         if not 0 <= v < V:
             break
-        q = Fraction(1) if draft is None else Fraction(float(draft[taken, v]))
-        p = float(target[taken, v])
-        p = min(p, 2.0 ** 100)      # (an infinity is above every product, too)
-        if np.isnan(p) or np.isnan(u[taken]) or not Fraction(float(u[taken])) * q < Fraction(p):
+        q = Fraction(1) if draft is None else nearest(draft[taken, v])
+        p = nearest(target[taken, v])
+        if np.isnan(u[taken]) or not Fraction(float(u[taken])) * q < p:
             break
         taken += 1
     p = fixed(target[taken])

@@ -203,3 +203,27 @@ def test_every_exponent_is_exact():
     x = torch.randint(0, V, (B, 1), generator=g, dtype=torch.int32)
     for u in (0.0, 1.0):
         _check(p, q, x, torch.full((B, 1), u), torch.rand(B, generator=g))
+
+
+def test_drafts_of_no_probability():
+    """The drafted token's own entries outside [0, 1] and NaN, in either row: they count as the nearest
+    of the two, NaN as 0.  Each pair's verdict is written out, not the oracle's alone."""
+    inf, nan = float("inf"), float("nan")
+    #        p, q, u, taken: u q < p with both in [0, 1]
+    rows = [(1.0, 3.0, 0.9, 1), (1.0, inf, 0.999, 1), (0.5, 3.0, 0.4, 1), (0.5, 3.0, 0.5, 0),
+            (0.0, -0.5, 0.5, 0), (-0.5, -1.0, 0.9, 0), (nan, -1.0, 0.9, 0), (0.25, nan, 0.999, 1),
+            (0.0, nan, 0.5, 0), (nan, 0.5, 0.0, 0), (nan, nan, 0.0, 0), (7.0, 1.0, 0.999, 1),
+            (inf, inf, 0.999, 1), (-inf, -inf, 0.5, 0), (2.0 ** -140, -1.0, 0.9, 1),
+            (2.0 ** -149, 0.0, 0.5, 1), (0.0, 0.0, 0.0, 0)]
+    B, V, at = len(rows), 70, 37
+    g = torch.Generator().manual_seed(15)
+    target = torch.rand((B, 2, V), generator=g) / V
+    draft = torch.rand((B, 1, V), generator=g) / V
+    x = torch.full((B, 1), at, dtype=torch.int32)
+    u = torch.zeros((B, 1))
+    for b, (p, q, r, _) in enumerate(rows):
+        target[b, 0, at], draft[b, 0, at], u[b, 0] = p, q, r
+    got = _check(target, draft, x, u, torch.rand(B, generator=g))
+    assert got[1].tolist() == [r[3] for r in rows]
+    got = _check(target, None, x, u, torch.rand(B, generator=g))        # (q is 1)
+    assert got[1].tolist() == [int(r[2] < min(max(r[0], 0.0), 1.0)) if r[0] == r[0] else 0 for r in rows]
