@@ -249,6 +249,7 @@ __global__ void __launch_bounds__(NT* GROUPS, kResident / (NT * GROUPS) ? kResid
   const int T = 1 << p.t_log2;
   long long pos = __ldg(a.seq_pos + b), skip = 0;
   const int count = tokens_of(a, b);
+  if (count == 0) return;      // (of a sequence that brings none the position does not matter)
   if (pos < 0) {     // tokens at negative positions have no place
     skip = -pos;
     pos = 0;

@@ -212,6 +212,30 @@ def test_positions_at_the_ends_of_int32(kind, n):
     assert binding.kv_pool_read_device_error(dev) == binding.DEVERR_LENGTH
 
 
+@pytest.mark.parametrize("kind", KINDS + ["rows", "q4_0"])
+def test_sequences_without_tokens_are_no_error(kind):
+    """Entries that pad a batch: any position and page table row, no tokens.  Nothing is flagged, and the
+    others' rows are there."""
+    from int8_kv_cache_02_gb300 import binding
+    g = torch.Generator().manual_seed(16)
+    n, D = 5, 64
+    pos, lens = [-1, 3, -2 ** 31, 2 ** 31 - 1, 10 ** 6, 0], [0, 5, 0, 0, -3, 2]
+    pt = torch.tensor([[-1, -1], [0, 1], [99, 99], [-1, -1], [-7, -1], [2, 3]], dtype=torch.int32)
+    if kind in KINDS:
+        dev, orc = bu.make_pools(kind, 2, D, 16, 16, 4)
+    else:
+        gu.lib_ready()
+        dev, orc = gu.make_pools(1, 2, D, D, 16, 4, opool.K8V8 if kind == "rows" else opool.Q4_0)
+    tab = rope.table(40, D)
+    q, k, v = _rows(g, 6, n, 2, 2, D)
+    want = _oracle(orc, q, k, v, pos, pt, tab, "halves", lens)
+    got = _call(dev, q, k, v, pos, pt, tab, lens=lens)
+    for b in (1, 5):
+        _same(got[b, :lens[b]], want[b, :lens[b]])
+    (bu.assert_same if kind in KINDS else gu.regions_equal)(dev, orc)
+    assert binding.kv_pool_read_device_error(dev) == 0
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_scales_from_tiny_products(kind):
     """A sine of 2^-110 leaves keys whose scale has no reciprocal in fp32; zeros leave scale 0."""
