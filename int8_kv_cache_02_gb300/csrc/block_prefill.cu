@@ -242,11 +242,10 @@ struct Sums {
 };
 
 // Sixteen scores in units of 1 / f, capped and biased; ahead: how far the first one's position is
-// ahead of the query's.  Two at a time go through the polynomial of capped().  A piece in which one
-// is beyond the cap takes the exponential for all: what that loses of its small scores, 2^-22 of the
-// cap, meets weights that are the smaller for it (they are one row's).  With a cap of 5
-// and scores up to 20 the chunk of 33,024 positions (D 256) takes 293 us instead of 251, one by one
-// it took 361 (D 128: 466, 377, 580).
+// ahead of the query's; whole warps.  Two at a time go through the polynomial of the cap.  Where one of
+// the warp's is beyond the cap all take both of its forms, and each keeps its own: with a cap of 5 and
+// scores up to 20 the chunk of 33,024 positions (D 256) takes 288 us instead of 238, D 128 480 instead
+// of 377.
 template <int SCORES>
 __device__ __forceinline__ void shape_piece(uint32_t (&v)[16], float f, const Shaping& shape,
                                             float slope, int ahead) {
@@ -254,8 +253,8 @@ __device__ __forceinline__ void shape_piece(uint32_t (&v)[16], float f, const Sh
     float most = 0.f;
 #pragma unroll
     for (int k = 0; k < 16; ++k) most = fmaxf(most, fabsf(__uint_as_float(v[k])));
-    if (most * f <= shape.cap) {
-      const uint64_t f2 = pack2(f, f), over = pack2(shape.over_cap, shape.over_cap);
+    const uint64_t f2 = pack2(f, f), over = pack2(shape.over_cap, shape.over_cap);
+    if (!__any_sync(0xffffffffu, most * f > shape.cap)) {
 #pragma unroll
       for (int k = 0; k < 16; k += 2) {
         float y0, y1;
@@ -265,10 +264,24 @@ __device__ __forceinline__ void shape_piece(uint32_t (&v)[16], float f, const Sh
         v[k + 1] = __float_as_uint(y1);
       }
     } else {
-      const float over = f * shape.over_cap;
+      // (Four a turn, and the others move up: unrolled, 16 scores' code cost the usual case 14 % at D 256,
+      // 272 us for 238, and helped this one at D 128 alone, 468 for 480.  Two: 326 and 546; eight: 246.)
+#pragma unroll 1
+      for (int turn = 0; turn < 4; ++turn) {
+        uint32_t y[4];
 #pragma unroll
-      for (int k = 0; k < 16; ++k)
-        v[k] = __float_as_uint(beyond_cap(__uint_as_float(v[k]) * over, shape.cap));
+        for (int k = 0; k < 4; k += 2) {
+          float y0, y1;
+          capped_any(mul2(pack2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), f2), shape.cap,
+                     shape.over_cap, y0, y1);
+          y[k] = __float_as_uint(y0);
+          y[k + 1] = __float_as_uint(y1);
+        }
+#pragma unroll
+        for (int k = 0; k < 12; ++k) v[k] = v[k + 4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[12 + k] = y[k];
+      }
     }
     f = 1.f;
   }
@@ -413,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
     };
     const uint32_t my_o = lanes + L::O + half * (D / 2);
     float m = kUnset, e = kUnset, l = 0.f, e_sum = kUnset;      // (e_sum: e of that sum)
-    bool far = false;    // whether a row of the warp has |m| > kNear
+    bool far = false;    // whether |m| > kNear, of the row (plain scores: of one of the warp's)
     bool ok = true;      // (once it is false the warp only keeps the barrier's count)
     for (int from = 0; from < n; from += chain) {
       if (from > 0) {      // the sum in tensor memory starts anew with the next product
@@ -516,7 +529,10 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
             r = ptx::ex2(e - topE);
             e = topE;
           }
-          far = __any_sync(0xffffffffu, fabsf(m) > kNear && m != kUnset);
+          far = fabsf(m) > kNear && m != kUnset;
+          // (Shaped scores: each row by itself, so that none depends on what others see.  Plain ones by
+          // warps, as they were.)
+          if constexpr (!SHAPED) far = __any_sync(0xffffffffu, far);
           if (i > 0 && __any_sync(0xffffffffu, r != 1.f)) {
             ok = wait(&s.o_done[(i - 1) & 1], ((i - 1) >> 1) & 1, &s.failed, a.patience);
             ok = __all_sync(0xffffffffu, ok);

@@ -17,8 +17,9 @@ struct Shaping {
 // c tanh(z / c).  Up to |z| = c the odd polynomial x + x x^2 P(x^2), P fitted to
 // (tanh(x) / x - 1) / x^2 on [0, 1] for the least relative error of tanh (4.6e-9; with its
 // roundings 1.3 * 2^-24): scores far below the cap, where all the weights can lie, keep
-// fp32's relative precision, which 1 - 2 / (e^2x + 1) loses there, and nothing but
-// multiply-adds is issued.  Larger ones are rare: a branch.
+// fp32's relative precision, which c - 2 c / (e^2x + 1) loses there (2^-22 of the cap), and nothing
+// but multiply-adds is issued.  Larger ones are rare: both forms, of which each score takes its own.
+// A score's bits are its own matter so, whatever stands around it, hidden or seen.
 __device__ constexpr float cap_poly(int c) {
   return c == 0   ? -3.3333296e-1f
          : c == 1 ? 1.3332345e-1f
@@ -29,24 +30,6 @@ __device__ constexpr float cap_poly(int c) {
                   : -3.5845194e-4f;
 }
 constexpr float kTwoLog2E = 2.8853900817779268f;
-__device__ __forceinline__ float capped(float z, float cap, float over_cap) {
-  const float x = z * over_cap, s = x * x;
-  float p = cap_poly(6);
-#pragma unroll
-  for (int c = 5; c >= 0; --c) p = fmaf(p, s, cap_poly(c));
-  float y = fmaf(z, s * p, z);
-  if (s > 1.f) {
-    const float e = ptx::ex2(fabsf(x) * kTwoLog2E);
-    y = copysignf(cap - cap * __fdividef(2.f, fminf(e, 1e30f) + 1.f), z);
-  }
-  return y;
-}
-
-// The exponential's form alone, for x = z / cap.
-__device__ __forceinline__ float beyond_cap(float x, float cap) {
-  const float e = ptx::ex2(fabsf(x) * kTwoLog2E);      // e^2|x|; infinite: tanh is 1
-  return copysignf(cap - __fdividef(2.f * cap, e + 1.f), x);
-}
 
 // Two scores, neither beyond the cap; over: the pair of 1 / cap.
 __device__ __forceinline__ uint64_t capped2(uint64_t z, uint64_t over) {
@@ -55,6 +38,24 @@ __device__ __forceinline__ uint64_t capped2(uint64_t z, uint64_t over) {
 #pragma unroll
   for (int c = 5; c >= 0; --c) p = fma2(p, s, pack2(cap_poly(c), cap_poly(c)));
   return fma2(z, mul2(s, p), z);
+}
+
+// One beyond it; per: 2 log2(e) / cap.  (e^2|x| + 1 is 1 and more, or infinite: tanh is 1 then.)
+__device__ __forceinline__ float beyond_cap(float z, float cap, float per) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ptx::ex2(fabsf(z) * per) + 1.f));
+  return copysignf(fmaf(-2.f * cap, r, cap), z);
+}
+
+// Two of any size.
+__device__ __forceinline__ void capped_any(uint64_t z, float cap, float over_cap, float& y0, float& y1) {
+  float z0, z1;
+  unpack2(z, z0, z1);
+  unpack2(capped2(z, pack2(over_cap, over_cap)), y0, y1);
+  const float per = over_cap * kTwoLog2E;
+  const float far0 = beyond_cap(z0, cap, per), far1 = beyond_cap(z1, cap, per);
+  y0 = fabsf(z0) > cap ? far0 : y0;
+  y1 = fabsf(z1) > cap ? far1 : y1;
 }
 
 // attn_decode_scored_int8's arguments beside those of a plain decode call.

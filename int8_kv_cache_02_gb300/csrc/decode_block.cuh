@@ -434,7 +434,8 @@ __device__ __forceinline__ void shape_scores(float (&z)[NC][4], const BlockScore
 #pragma unroll
       for (int n = 0; n < NC; ++n)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) z[n][k] = capped(z[n][k], a.shape.cap, a.shape.over_cap);
+        for (int k = 0; k < 4; k += 2)
+          capped_any(pack2(z[n][k], z[n][k + 1]), a.shape.cap, a.shape.over_cap, z[n][k], z[n][k + 1]);
     }
   }
   if (a.shape.slopes) {

@@ -463,3 +463,87 @@ def test_a_speculative_step(kind):
         at = lens.tolist()
         assert int(refs.sum()) == sum(math.ceil(a / ps) for a in at)
     assert b.kv_pool_read_device_error(dev) == 0
+
+
+def _outliers(kind, n, D, seed, sign):
+    """Keys [1][n][1][D], and the value that all of a query's dims have: every 16th key is the sign
+    throughout (0: the two in turn), its score sign * value * D, and the others' scores are small
+    beside it.  The value is a power of two and the codes are whole (e4m3: multiples of 2^-18 of their
+    range), so that the sum of a row, and with it every score, is exact in fp32 whatever cancels in it."""
+    g = torch.Generator().manual_seed(seed)
+    size = 1024.0 if kind == "int8" else 128.0       # (e4m3 rounds codes to 2^-4, int8 to 1/254)
+    k = 2 * torch.rand((1, n, 1, D), generator=g) - 1
+    k[..., 0], k[..., 1] = 1.0, -1.0                 # (blocks of one scale)
+    k -= k.mean(-1, keepdim=True)
+    k = k.clamp(-1, 1)
+    k[..., 0] = 1.0
+    out = torch.arange(n) % 16 == seed % 16
+    s = torch.ones(n) * sign if sign else 1.0 - 2.0 * (torch.arange(n) // 16 % 2)
+    k[:, out] = s[out].view(1, -1, 1, 1)
+    return k.half(), size
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("sign", [-1, 0])
+def test_small_scores_beside_ones_beyond_the_cap(kind, D, sign):
+    """One score in 16 is far beyond the cap, all negative or of both signs: those below -cap have no
+    weight, and the others keep their precision beside them.  Chunk and decode of the same rows, against
+    fp64."""
+    n, G, n_new = 600, 8, 64
+    k, size = _outliers(kind, n, D, 5, sign)
+    g = torch.Generator().manual_seed(D)
+    v = torch.randn((1, n, 1, D), generator=g).half()
+    pt, n_pages = inputs.page_table([n], 64, seed=1)
+    dev, orc = bu.make_pools(kind, 1, D, 64, 64, n_pages)
+    bu.append(dev, orc, 0, k, v, [0], pt)
+    q = torch.full((n_new, G, D), size).half()
+    kh, _ = orc.gather(0, pt[0].numpy(), n)
+    z = (kh.sum(-1)[:, 0] * size / math.sqrt(D)).astype(np.float64)
+    out = np.arange(n) % 16 == 5
+    far, near = np.abs(z[out]).min(), np.abs(z[~out]).max()
+    scale = 10.0 / near / math.sqrt(D)             # small scores up to 10 (14.4 in base 2)
+    for part in (1.3, 20.0, 500.0):                # the outliers in caps
+        cap = float(far * 10.0 / near / part)
+        assert cap > 0.5
+        ref = _reference(orc, q[None], [n], pt, cap=cap, scale=scale)[0]
+        for n_splits in (1, 3):
+            got = _chunk(dev, q, n - n_new, pt[0], cap=cap, n_splits=n_splits, scale=scale)
+            bu.assert_close(got, ref, z_max=Z, what=f"chunk, cap {cap}, {n_splits}")
+        for Q in (1, 5, 64):
+            got = _decode(dev, q[None, -Q:].contiguous(), [n], pt, cap=cap, scale=scale)[0]
+            bu.assert_close(got, ref[-Q:], z_max=Z, what=f"decode of {Q}, cap {cap}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("slopes", [False, True])
+@pytest.mark.parametrize("top", [10.0, 150.0])
+def test_hidden_scores_change_no_bit(kind, D, slopes, top):
+    """The keys of later tokens, or of ones that have left the window, are beyond the cap, or are not
+    (with codes and scales of all others the same): the rows that do not see them have the same bits."""
+    n, G, at, window = 300, 8, [40, 255, 299], 180
+    k, size = _outliers(kind, n, D, 99, 1)
+    k[:, 99 % 16::16] = k[:, :1]                    # (the outliers are set below)
+    g = torch.Generator().manual_seed(D)
+    v = torch.randn((1, n, 1, D), generator=g).half()
+    q = torch.full((n, G, D), size).half()
+    pt, n_pages = inputs.page_table([n], 64, seed=1)
+    out, scale = [], None
+    for big in (False, True):
+        dev, orc = bu.make_pools(kind, 1, D, 16, 64, n_pages)
+        kk = k.clone()
+        if big:
+            kk[:, at] = 1.0
+        bu.append(dev, orc, 0, kk, v, [0], pt)
+        z = np.abs(orc.gather(0, pt[0].numpy(), n)[0].sum(-1)[:, 0])
+        if scale is None:
+            scale = float(top / (z.max() * size))
+        assert (z[at] * size * scale > 3 * top).all() if big else z.max() * size * scale < 1.1 * top
+        out.append(_chunk(dev, q, 0, pt[0], window=window, cap=1.5 * top,
+                          slopes=_slopes(G) if slopes else None, n_splits=1, scale=scale))
+    P = np.arange(n)
+    hidden = ~np.logical_or.reduce([(P >= a) & (P < a + window) for a in at])
+    assert hidden[:40].all() and hidden[220:255].all() and hidden.sum() == 75
+    assert np.array_equal(out[0][hidden], out[1][hidden])
+    assert not np.array_equal(out[0][~hidden], out[1][~hidden])
