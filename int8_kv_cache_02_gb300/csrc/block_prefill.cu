@@ -242,7 +242,7 @@ struct Sums {
 };
 
 // Sixteen scores in units of 1 / f, capped and biased; ahead: how far the first one's position is
-// ahead of the query's; whole warps.  Two at a time go through the polynomial of the cap.  Where one of
+// ahead of the row's origin; whole warps.  Two at a time go through the polynomial of the cap.  Where one of
 // the warp's is beyond the cap all take both of its forms, and each keeps its own: with a cap of 5 and
 // scores up to 20 the chunk of 33,024 positions (D 256) takes 288 us instead of 238, D 128 480 instead
 // of 377.
@@ -384,9 +384,12 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
     const int least = a.start + row0 / a.G;                    // of the block's first row
     [[maybe_unused]] const int most_last = a.start + (min(row0 + kRows, rows) - 1) / a.G;
     float slope = 0.f;
+    [[maybe_unused]] int origin = 0;
     if constexpr (SCORES == kShaped)
-      if (a.shape.slopes && gc < rows)
+      if (a.shape.slopes && gc < rows) {
         slope = __ldg(a.shape.slopes + kvh * a.G + gc % a.G) * 1.4426950408889634f;
+        origin = bias_origin(slope, last, pre, a.window);
+      }
     // the queries, while the first codes come
     constexpr int PIECES = kRows * (D / 8) / kSoftmax, BATCH = PIECES < 8 ? PIECES : 8;
     for (int x0 = 0; x0 < PIECES; x0 += BATCH) {
@@ -473,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             if constexpr (SHAPED) {      // (f is in the score then)
-              shape_piece<SCORES>(v[j], f[j], a.shape, slope, pos + 16 * j - last);
+              shape_piece<SCORES>(v[j], f[j], a.shape, slope, pos + 16 * j - origin);
               f[j] = 1.f;
               if (masked) {
                 const int to = last - pos - 16 * j, from = a.window > 0 ? to - a.window : -1;

@@ -14,6 +14,16 @@ struct Shaping {
   const float* slopes;          // [H], in natural units; or null
 };
 
+// The position that a row's bias is counted from, of those that a query at `last` sees (itself, the
+// `window` positions up to it, 0: all, and the prefix).  A softmax is the same whatever is added to a
+// whole row, so it is the one with the largest bias: the heaviest positions then have biases near 0,
+// and nothing of their scores is rounded away.  (Counted from the query itself, as the formula has it,
+// queries up to 3500 positions ahead of their prefix's end were 1.6e-4 off at slopes near 1.)
+__device__ __forceinline__ int bias_origin(float slope, int last, int pre, int window) {
+  if (slope < 0.f) return pre > 0 || window == 0 ? 0 : max(0, last - window + 1);
+  return max(last, pre - 1);
+}
+
 // c tanh(z / c).  Up to |z| = c the odd polynomial x + x x^2 P(x^2), P fitted to
 // (tanh(x) / x - 1) / x^2 on [0, 1] for the least relative error of tanh (4.6e-9; with its
 // roundings 1.3 * 2^-24): scores far below the cap, where all the weights can lie, keep

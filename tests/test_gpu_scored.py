@@ -547,3 +547,42 @@ def test_hidden_scores_change_no_bit(kind, D, slopes, top):
     assert hidden[:40].all() and hidden[220:255].all() and hidden.sum() == 75
     assert np.array_equal(out[0][hidden], out[1][hidden])
     assert not np.array_equal(out[0][~hidden], out[1][~hidden])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("prefix,cap", [(3500, 0.0), (9999, 20.0), (2111, 0.0)])
+def test_biases_of_thousands_of_positions(kind, prefix, cap):
+    """Queries thousands of positions ahead of a prefix's end, with slopes near 1 and of both signs: the
+    biases are in the thousands where the weight is, and scores keep their precision beside them.  (A
+    bias counted from the heaviest position is below 40 where a weight is above 2^-40, as above.)"""
+    n, D, G = 3500, 64, 4
+    g, pt, dev, orc = _filled(kind, 17, [n], 1, D, 64, 64)
+    slopes = torch.tensor([0.84, 1.0, 0.2, -0.84])
+    q = torch.randn((n, G, D), generator=g).half()
+    ref = _reference(orc, q[None], [n], pt, 0, cap, slopes, [prefix])[0]
+    for n_splits in (0, 1, 7):
+        got = _chunk(dev, q, 0, pt[0], 0, cap, slopes, prefix, n_splits)
+        bu.assert_close(got, ref, z_max=Z, what=f"{n_splits} splits")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,G", [(64, 1), (128, 4), (256, 8)])
+@pytest.mark.parametrize("window,prefix", [(0, 0), (0, 40), (3000, 0), (3000, 5), (900, 3200)])
+def test_biases_that_grow_with_the_distance(kind, D, G, window, prefix):
+    """Slopes below 0: the weight is at the first position that a query sees, thousands behind it; and
+    above 0, with prefixes that a window does not reach."""
+    lens = [4000, 3301, 17]
+    g, pt, dev, orc = _filled(kind, 18, lens, 1, D, 32, 32)
+    slopes = torch.tensor([-0.84, -1.0, 0.5, -0.03, 0.0, 1.0, -0.3, 2.0])[:G]
+    for Q in (1, 3, 20):
+        q = torch.randn((3, Q, G, D), generator=g).half()
+        ref = _reference(orc, q, lens, pt, window, 30.0, slopes, [prefix] * 3)
+        for n_splits in (0, 1, 3):
+            got = _decode(dev, q, lens, pt, window, 30.0, slopes, [prefix] * 3, n_splits)
+            bu.assert_close(got, ref, z_max=Z, what=f"{Q} queries, {n_splits} splits")
+    n_new = 600 // G                    # (in tiles of rows)
+    q = torch.randn((n_new, G, D), generator=g).half()
+    for b in (0, 1):
+        ref = _reference(orc, q[None], lens[b:b + 1], pt[b:b + 1], window, 0.0, slopes, [prefix])[0]
+        got = _chunk(dev, q, lens[b] - n_new, pt[b], window, 0.0, slopes, prefix)
+        bu.assert_close(got, ref, z_max=Z, what=f"chunk {b}")
