@@ -530,7 +530,8 @@ int kv_verify_drafts(int batch, int n_draft, int vocab, const float* target_prob
 
 /* The calls above that a decoding step makes, with their arguments in order as one host array of
  * 64-bit words (integers sign-extended, pointers, a float as the bits of a double; `stream` last): for
- * callers to whom every argument is a cost of its own.  The same checks, results and errors. */
+ * callers to whom every argument is a cost of its own.  The same checks, results and errors, and
+ * INVALID_ARG for an integer beyond its argument's type. */
 int kv_rope_append_packed(const int64_t* words);                  /* 24 */
 int attn_decode_scored_int8_packed(const int64_t* words);         /* 19 */
 int attn_prefill_chunk_scored_int8_packed(const int64_t* words);  /* 18 */

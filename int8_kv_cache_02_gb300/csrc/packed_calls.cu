@@ -21,8 +21,16 @@ T word(const int64_t* at) {
   }
 }
 
+// Whether a word is a value of the type: an integer that does not fit would become another one.
+template <class T>
+bool fits(int64_t x) {
+  if constexpr (std::is_integral_v<T>) return static_cast<T>(x) == x;
+  return true;
+}
+
 template <class... A, size_t... I>
 int call(int (*f)(A...), const int64_t* words, std::index_sequence<I...>) {
+  if (!(fits<A>(words[I]) && ...)) return INT8KV_ERR_INVALID_ARG;
   return f(word<A>(words + I)...);
 }
 

@@ -106,6 +106,28 @@ def test_packed_calls_refuse_null_and_read_floats(L):
     assert L.attn_decode_scored_int8_packed(words) == -6        # not block-scaled
 
 
+def test_packed_integers_beyond_32_bits_are_refused(L):
+    """A window of 2^32 is not a window of 0: each integer in turn, one period of its type away from what
+    the call would take (batches of none: nothing runs)."""
+    f = _Fake(1, 2, 128, 64, 1, 64, 4, 8)
+    at = ctypes.addressof(f)
+    rope = [at, 0, 0, P, P, 1024, 256, 256, 0, 3, 8, P, 0, P, 10, 64, 0, 0, 1, 0, P, P, 4, 0]
+    decode = [at, 0, 0, 0, 1, 2, 0, 0, 4, 0, 0.0, 1.0, 0, 0, 1, 0, 0, 0, 0]
+    chunk = [at, 0, 0, 0, 2, 0, 0, 4, 0, 0.0, 1.0, 0, 0, 1, 0, 0, 0, 0]
+    verify = [0, 3, 100, P, 100, 0, 0, P, 0, P, P, P, P, 0, 0, 0]
+    for call, pack, words, ints in (
+            (L.kv_rope_append_packed, b._pack_rope, rope, (1, 8, 9, 10, 14, 15, 16, 18, 22)),
+            (L.attn_decode_scored_int8_packed, b._pack_decode, decode, (1, 3, 4, 5, 8, 9, 14)),
+            (L.attn_prefill_chunk_scored_int8_packed, b._pack_chunk, chunk, (1, 3, 4, 5, 7, 8, 12, 13)),
+            (L.kv_verify_drafts_packed, b._pack_verify, verify, (0, 1, 2))):
+        assert call(pack(*words)) == 0
+        for i in ints:
+            for period in (1 << 32, -1 << 32, 5 << 32):
+                off = list(words)
+                off[i] += period
+                assert call(pack(*off)) == -1, (call.__name__, i, period)
+
+
 class _Pool:
     handle = None
     block, n_kv_heads, head_dim, n_pages, device_index = True, 2, 64, 4, 0
