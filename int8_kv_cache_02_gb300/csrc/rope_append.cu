@@ -14,7 +14,7 @@
 // in pieces of four, and a piece of four pairs that go by one position is two 16-byte loads.
 //
 // Bound by HBM for prompts (rows in, queries and codes out; half of the issue slots are taken), by
-// the launch and three dependent loads for single tokens (64 sequences: 3.7 us).
+// the launch and three dependent loads for single tokens (64 sequences: 3.3 us).
 #include <cmath>
 
 #include "block_quant.cuh"
@@ -368,7 +368,9 @@ __global__ void __launch_bounds__(NT* GROUPS, kResident / (NT * GROUPS) ? kResid
 
 // ---- pools with a scale for each row --------------------------------------
 // int8 and fp16 stores: D / 16 lanes take a row, a twin each, for a.kv_heads heads in turn; a scale's
-// values are those of several pieces, whose largest magnitudes meet in shared memory.
+// values are those of several pieces, whose largest magnitudes meet in shared memory.  The prompt of
+// 2 x 16381 tokens (32 / 8 heads of D 128): 144 us with two int8 stores (109 at the copy rate), 132 with
+// one of them fp16 (113); 16 / 2 heads of D 256, all values turned: 124 and 118 (94, 96).
 constexpr int kRowThreads = 256;
 
 // Eight codes under scale s (fp16's, as fp32); 1 / s and the products as in quantize8, but a scale
@@ -517,7 +519,11 @@ __global__ void __launch_bounds__(kRowThreads, 3)
 
 // Pools with a 4-bit store: a warp takes a (sequence, token), lane l values [l VPL, (l + 1) VPL) of K
 // and V, as their append kernel (whose transform runs over a whole row); a value's partner is in the
-// lane R/2 values further.
+// lane R/2 values further.  Bound by issue: the transform's butterflies, the search for a block's first
+// largest value and single-byte stores make 182 M warp-instructions of the prompt of 2 x 16381 tokens
+// (32 / 8 heads of D 128; 82 M in block-scaled pools), at 2.6 a cycle and SM: 224 us with k8v4, 208
+// with q4_0 (106 and 104 at the copy rate); keys and values alone 154 and 137, kv_quant_append's 158
+// and 153.  64 single tokens: 3.9 and 3.7 us.
 template <int VPL>
 __device__ __forceinline__ void row_turns(const RopeArgs& a, size_t b, int tok, int lane,
                                           float (&c)[VPL], float (&s)[VPL], bool& bad) {

@@ -22,10 +22,14 @@
 // up there: 32 equal parts of the run, then 32 of the part, their values from L2.  So a row is
 // read once and nothing is written but the results.
 //
-// 64 sequences of 131072 tokens, 63 MB: 19.7 us (47 % of the copy rate); one of 32000: 5.1 us.  Before
-// and behind the stream lie the launch, three dependent loads, the cluster's barriers and two
-// look-ups.  Clusters of 16 blocks of 128 threads: 19.6 and 4.9, and a size that not every device
-// grants; of 4 blocks of 512: 29.0 (without loads ahead, 8 x 256 took 23.2).
+// 64 sequences of 131072 tokens, 63 MB: 19.7 us (47 % of the copy rate); one of 32000: 5.1 us.  What
+// stands beside the stream is a sequence's own chain: the launch, three dependent loads, eight
+// batches of a block's slice one after another, the cluster's barriers and two look-ups.  One
+// sequence of 131072 takes 9.8 us with two rows (7.8 with one), 19 (a block an SM) 11.8, 38 14.4, 76
+// 20.7, 128 33.5: all blocks of a wave are at the same point of the chain, so that none hides
+// another's.  Whether sequences read one row or two is not what costs: all drafts refused takes
+// 19.9, all taken 12.3.  Clusters of 16 blocks of 128 threads: 19.6 and 4.9, and a size that not
+// every device grants; of 4 blocks of 512: 29.0 (without loads ahead, 8 x 256 took 23.2).
 #include <utility>
 
 #include <cooperative_groups.h>
