@@ -72,8 +72,9 @@ constexpr int kChain = 80;                 // tiles that one sum in tensor memor
 constexpr int kShapedChain = 40;
 
 // Scores of the kernel: plain, shaped, and capped without a bias, which is most of what is capped and
-// takes 5 to 9 % less time for knowing it (256 queries over 33,024 positions, a cap of 50: D 256 237
-// against 259 us, D 128 e4m3 375 against 395, int8 388 against 411, one kv head of D 64 99 against 109).
+// takes 5 to 9 % less time for knowing it (256 queries over 33,024 positions, a cap of 50, measured side
+// by side: D 256 237 against 259 us, D 128 e4m3 375 against 395, int8 388 against 411, one kv head of
+// D 64 99 against 109).
 enum Scores { kPlain = 0, kShaped = 1, kCapped = 2 };
 constexpr float kNear = 64.f;              // |m| up to here: c - m is one summand
 
@@ -245,8 +246,8 @@ struct Sums {
 // Sixteen scores in units of 1 / f, capped and biased; ahead: how far the first one's position is
 // ahead of the row's origin; whole warps.  Two at a time go through the polynomial of the cap.  Where one of
 // the warp's is beyond the cap all take both of its forms, and each keeps its own: with a cap of 5 and
-// scores up to 20 the chunk of 33,024 positions (D 256) takes 288 us instead of 238, D 128 480 instead
-// of 377.
+// scores up to 20 the chunk of 33,024 positions (D 256) takes 288 us instead of 239, D 128 483 instead
+// of 378.
 template <int SCORES>
 __device__ __forceinline__ void shape_piece(uint32_t (&v)[16], float f, const Shaping& shape,
                                             float slope, int ahead) {
@@ -430,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
     };
     const uint32_t my_o = lanes + L::O + half * (D / 2);
     float m = kUnset, e = kUnset, l = 0.f, e_sum = kUnset;      // (e_sum: e of that sum)
-    bool far = false;    // whether |m| > kNear, of the row (plain scores: of one of the warp's)
+    bool far = false;    // whether a row of the warp has |m| > kNear
     bool ok = true;      // (once it is false the warp only keeps the barrier's count)
     for (int from = 0; from < n; from += chain) {
       if (from > 0) {      // the sum in tensor memory starts anew with the next product
@@ -533,10 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
             r = ptx::ex2(e - topE);
             e = topE;
           }
-          far = fabsf(m) > kNear && m != kUnset;
-          // (Shaped scores: each row by itself, so that none depends on what others see.  Plain ones by
-          // warps, as they were.)
-          if constexpr (!SHAPED) far = __any_sync(0xffffffffu, far);
+          far = __any_sync(0xffffffffu, fabsf(m) > kNear && m != kUnset);
           if (i > 0 && __any_sync(0xffffffffu, r != 1.f)) {
             ok = wait(&s.o_done[(i - 1) & 1], ((i - 1) >> 1) & 1, &s.failed, a.patience);
             ok = __all_sync(0xffffffffu, ok);
@@ -547,14 +545,18 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
         }
         float to = m;
         if (far) {      // scores, rounded like m, less m, which is exact
+          // (Shaped ones by rows, so that no row's bits depend on what others see.  Plain ones by warps.)
+          const bool takes = !SHAPED || (fabsf(m) > kNear && m != kUnset);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              v[j][k] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(v[j][k]), f[j]), m));
-            f[j] = 1.f;
+            for (int k = 0; k < 16; ++k) {
+              const float z = __uint_as_float(v[j][k]);
+              v[j][k] = __float_as_uint(takes ? __fsub_rn(__fmul_rn(z, f[j]), m) : z);
+            }
+            f[j] = takes ? 1.f : f[j];
           }
-          to = 0.f;
+          to = takes ? 0.f : m;
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
