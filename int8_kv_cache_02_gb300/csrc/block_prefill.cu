@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefill_kernel(const Prefil
         }
         float to = m;
         if (far) {      // scores, rounded like m, less m, which is exact
-          // (Shaped ones by rows, so that no row's bits depend on what others see.  Plain ones by warps.)
+          // (Shaped ones by rows, whatever references others have.  Plain ones by warps.)
           const bool takes = !SHAPED || (fabsf(m) > kNear && m != kUnset);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
